@@ -420,6 +420,104 @@ int emeans_fp8_encode(const float* X, int64_t n, int32_t d, const float* shift, 
 int emeans_fp8_decode(const float* C, int64_t k, int32_t d, const float* shift, double scale,
                       float* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Block codes: 8-bit codes with one power-of-two scale for each block of
+ * values (the converters above have one factor for all data). The scale of a
+ * block whose largest finite magnitude is a is s = 2^e, the smallest power of
+ * two with a <= L s (L = 448 for E4M3, 127 for int8), e clamped to
+ * [-127, 127]; s = 1 where a = 0. It is stored as the byte e + 127 (E8M0). A
+ * code is the nearest representable value of x / s, ties to even; infinities
+ * saturate, NaN becomes the E4M3 NaN, or int8 0. Number types are EMEANS_F32,
+ * EMEANS_BF16 and EMEANS_F16. Leading dimensions (ld...) are the distance of
+ * consecutive rows, in elements. All calls are asynchronous on `stream` and
+ * may be captured into a graph.
+ * ------------------------------------------------------------------------- */
+
+/* E4M3 codes of X with blocks of 128, in either or both orders:
+ *   codes    n x d, scales n x ceil(d/128): blocks along the rows
+ *   codes_t  d x n, scales_t d x ceil(n/128): the transpose, blocks along it
+ * With tiles != 0 a block is a 128 x 128 tile, both orders hold the same codes,
+ * scales is ceil(n/128) x ceil(d/128) and scales_t its transpose.
+ * codes and scales may be NULL together, so may codes_t and scales_t; not all
+ * four. Bytes of a row past its values are left as they are.
+ *   X  device, n x d, dtype
+ * Errors: EINVAL (n < 0, n >= 2^31, d < 1, a leading dimension below the row
+ * length, no output, codes without scales), EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int64_t ldx,
+                        int32_t tiles, uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
+                        uint8_t* codes_t, int64_t ldct, uint8_t* scales_t, int64_t ldst,
+                        void* stream);
+
+/* out[i][j] = sum_l A[i][l] B[j][l] over the values that E4M3 codes and their
+ * scales stand for (the product of A with the transpose of B): products exact,
+ * sums in fp32, one rounding to out_dtype.
+ *   A    device, m x k codes      As  device, m x ceil(k/128) scales
+ *   B    device, n x k codes      Bs  device, n x ceil(k/128) scales, or with
+ *        b_tiles != 0 ceil(n/128) x ceil(k/128)
+ *   out  device, m x n, out_dtype
+ * A NaN code or a scale byte of 255 makes the outputs it enters NaN. k = 0
+ * gives zeros. Any alignment and any leading dimension is right; rows that
+ * start at multiples of 16 bytes are read fastest.
+ * Errors: EINVAL (m, n or k < 0, m or n >= 2^31, a leading dimension below
+ * the row length, NULL), EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
+                        const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
+                        int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
+                        int32_t out_dtype, int64_t ldo, void* stream);
+
+/* The same product with A given as numbers: X (m x k, dtype) is encoded as
+ * emeans_block_encode does along its rows, and multiplied with B. A few rows
+ * are encoded inside the product's own launch; more are encoded first, into
+ *   work  device, emeans_block_linear_work(m, k) bytes, 16-byte aligned
+ * which may be NULL (the library then allocates it stream-ordered).
+ * Errors: as emeans_block_matmul, and ENOMEM. */
+int64_t emeans_block_linear_work(int64_t m, int32_t k);
+int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
+                        const uint8_t* Bs, int64_t ldbs, int32_t b_tiles, int64_t m, int64_t n,
+                        int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
+                        void* stream);
+
+/* A store ("cache") of `rows` rows of d codes (contiguous, EMEANS_F8 or
+ * EMEANS_I8) with one scale for each block of `block` values along the row (a
+ * multiple of 16, at most 256; the last block of a row may be short).
+ *
+ * emeans_cache_write encodes n rows into the rows that `slots` names: row r to
+ * slots[r], and to none where slots[r] is outside [0, rows). Slots of one call
+ * must be distinct (of rows with the same slot one wins, block by block).
+ *   X       device; row r is heads * width = d values, value c of head h at
+ *           X[r * row_stride + h * head_stride + c]; with more than one head
+ *           width must be a multiple of block unless head_stride = width
+ *   slots   device, n integers of slot_bytes (4 or 8)
+ *   codes   device, rows x d      scales  device, rows x ceil(d/block)
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,
+                       int64_t row_stride, int64_t head_stride, const void* slots,
+                       int32_t slot_bytes, void* codes, uint8_t* scales, int64_t rows,
+                       int32_t block, int32_t fmt, void* stream);
+
+/* out[i] = row slots[i] of the store as numbers (code * scale, one rounding to
+ * out_dtype); a slot outside [0, rows) reads as zeros.
+ *   slots  device, n integers of slot_bytes (4 or 8)
+ *   out    device, n x d, out_dtype, rows ldo elements apart
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d,
+                      int32_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
+                      int64_t n, void* out, int32_t out_dtype, int64_t ldo, void* stream);
+
+/* Ragged sequences read through a page table into packed rows: the store is
+ * `pages` pages of page_rows rows; sequence s is rows starts[s] .. starts[s+1]
+ * of out, and its row p lies in page table[s][p / page_rows] at p % page_rows.
+ * Rows of out (n of them) outside every sequence, past a table row's
+ * table_pages entries or in a page outside [0, pages) are zeros.
+ *   table   device, seqs x table_pages int32, rows table_ld entries apart
+ *   starts  device, seqs + 1 int32, not decreasing
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pages,
+                            int32_t page_rows, int32_t d, int32_t block, int32_t fmt,
+                            const int32_t* table, int64_t table_ld, int32_t table_pages,
+                            const int32_t* starts, int32_t seqs, int64_t n, void* out,
+                            int32_t out_dtype, int64_t ldo, void* stream);
+
 /* Message for the last non-zero return on this thread ("" if none). */
 const char* emeans_last_error(void);
 

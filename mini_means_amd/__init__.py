@@ -94,6 +94,24 @@ def lib() -> ctypes.CDLL:
         for f in ("emeans_fp8_calibrate", "emeans_fp8_encode", "emeans_fp8_decode"):
             getattr(L, f).argtypes = getattr(L, f.replace("fp8", "int8")).argtypes
             getattr(L, f).restype = ctypes.c_int
+        L.emeans_block_encode.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64,
+                                          c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]
+        L.emeans_block_matmul.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
+                                          c_i32, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp]
+        L.emeans_block_linear_work.argtypes = [c_i64, c_i32]
+        L.emeans_block_linear_work.restype = c_i64
+        L.emeans_block_linear.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
+                                          c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_vp]
+        L.emeans_cache_write.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i32, c_i64, c_i64, c_vp,
+                                         c_i32, c_vp, c_vp, c_i64, c_i32, c_i32, c_vp]
+        L.emeans_cache_read.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32,
+                                        c_i64, c_vp, c_i32, c_i64, c_vp]
+        L.emeans_cache_read_pages.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp,
+                                              c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_i32,
+                                              c_i64, c_vp]
+        for f in ("emeans_block_encode", "emeans_block_matmul", "emeans_block_linear",
+                  "emeans_cache_write", "emeans_cache_read", "emeans_cache_read_pages"):
+            getattr(L, f).restype = ctypes.c_int
         L.emeans_last_error.restype = ctypes.c_char_p
         L.emeans_last_error.argtypes = []
         L.emeans_version.argtypes = []
@@ -112,7 +130,7 @@ def declared_functions() -> list:
     """Function names the C header declares."""
     with open(HEADER) as f:
         text = f.read()
-    return re.findall(r"^\s*(?:int|void|const char\*)\s+(emeans_\w+)\s*\(", text, flags=re.M)
+    return re.findall(r"^\s*(?:int|int64_t|void|const char\*)\s+(emeans_\w+)\s*\(", text, flags=re.M)
 
 
 def _check(rc: int) -> None:
@@ -408,6 +426,416 @@ def fp8_encode(X, shift, scale: float, stream=None):
 def fp8_decode(C, shift, scale: float, stream=None):
     """Code-space centroids back to data space: C / scale + shift."""
     return _decode(C, shift, scale, stream, "emeans_fp8_decode")
+
+
+# ---- block codes: 8-bit codes with one power-of-two scale per block ----------
+
+BLOCK = 128  # values per scale of the matrix codes
+
+
+def _types():
+    """(number types, code formats) by torch dtype, made on first use."""
+    global _NUMBERS, _FORMATS
+    import torch
+    _NUMBERS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    _FORMATS = {torch.float8_e4m3fn: F8, torch.int8: I8}
+    return _NUMBERS, _FORMATS
+
+
+_NUMBERS = _FORMATS = None
+
+
+def _number(dtype, what: str) -> int:
+    code = (_NUMBERS or _types()[0]).get(dtype)
+    if code is None:
+        raise EmeansError(f"EDTYPE: {what} {dtype} not supported (float32, bfloat16 or float16)")
+    return code
+
+
+class _queue:
+    """Where a call runs: the tensor's device made current, new tensors
+    allocated on the stream that the library works on (.ptr)."""
+
+    def __init__(self, X, stream, what="X"):
+        import torch
+        if not getattr(X, "is_cuda", False):
+            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU")
+        i = X.device.index
+        self._on = None
+        if stream is not None:
+            self._on = torch.cuda.stream(stream)
+            self.ptr = stream.cuda_stream
+        else:
+            if i != torch.cuda.current_device():
+                self._on = torch.cuda.device(i)
+            self.ptr = torch._C._cuda_getCurrentRawStream(i)
+        self.index = i
+
+    def __enter__(self):
+        if self._on is not None:
+            self._on.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._on is not None:
+            self._on.__exit__(*exc)
+
+    def matrix(self, A, what, dtypes, names):
+        """A 2-D tensor on this device whose rows are runs of values; its row
+        distance."""
+        if not getattr(A, "is_cuda", False) or A.device.index != self.index:
+            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
+        if A.dtype not in dtypes:
+            raise EmeansError(f"EDTYPE: {what} must be {names} (got {A.dtype})")
+        if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1 and A.numel()):
+            raise EmeansError(f"EINVAL: {what} must be 2-D with adjacent values in a row")
+        return A.stride(0)
+
+
+def _byte_types():
+    import torch
+    return (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _codes_room(n: int, d: int, device):
+    """Codes n x d with rows a multiple of 16 bytes apart, and the scales
+    n_s x ceil(d/128) made by _scales_room: what the product reads fastest."""
+    import torch
+    pitch = (d + 15) // 16 * 16
+    room = torch.empty((n, pitch), dtype=torch.float8_e4m3fn, device=device)
+    return room if pitch == d else room[:, :d]
+
+
+def _scales_room(n: int, nb: int, device):
+    import torch
+    pitch = (nb + 3) // 4 * 4
+    room = torch.empty((n, pitch), dtype=torch.float8_e8m0fnu, device=device)
+    return room if pitch == nb else room[:, :nb]
+
+
+def block_encode(X, *, tiles: bool = False, rows: bool = True, cols: bool = False, stream=None):
+    """E4M3 codes of X (n x d float32, bfloat16 or float16 tensor on the GPU,
+    rows any distance apart) with one power-of-two scale for each 128 values
+    (float8_e8m0fnu): the smallest s with max |x| <= 448 s, codes the nearest
+    E4M3 values of x / s.
+
+    Returns (codes n x d, scales n x ceil(d/128)), blocks along the rows; with
+    cols=True (codes, scales, codes_t, scales_t), where codes_t (d x n) and
+    scales_t (d x ceil(n/128)) are the transpose with blocks along its rows, made
+    from the same read of X (rows=False: the first two are None). tiles=True:
+    a block is a 128 x 128 tile, scales ceil(n/128) x ceil(d/128), and both
+    orders hold the same codes (the form for weights). Rows of codes start at
+    multiples of 16 bytes: for other d the tensors are views of wider ones."""
+    with _queue(X, stream) as q:
+        dt = _number(X.dtype, "X")
+        ldx = q.matrix(X, "X", (X.dtype,), "")
+        if not rows and not cols:
+            raise EmeansError("EINVAL: block_encode makes rows, cols or both")
+        n, d = X.shape
+        if X.stride(0) < d and n > 1:
+            raise EmeansError("EINVAL: the rows of X overlap")
+        nb, db = -(-n // BLOCK), -(-d // BLOCK)
+        out = [None] * 4
+        args = [None, 0, None, 0, None, 0, None, 0]
+        if rows:
+            out[0], out[1] = _codes_room(n, d, X.device), \
+                _scales_room(nb if tiles else n, db, X.device)
+        if cols:
+            out[2], out[3] = _codes_room(d, n, X.device), \
+                _scales_room(db if tiles else d, nb, X.device)
+        if n and d:
+            for i, t in enumerate(out):
+                if t is not None:
+                    args[2 * i], args[2 * i + 1] = t.data_ptr(), t.stride(0)
+            _check(lib().emeans_block_encode(X.data_ptr(), dt, n, d, ldx, 1 if tiles else 0,
+                                             *args, q.ptr))
+    return tuple(out) if cols else (out[0], out[1])
+
+
+def _product_side(q, codes, scales, what):
+    """Arguments of one side of the product; True if its scales stand per tile."""
+    import torch
+    ld = q.matrix(codes, what, (torch.float8_e4m3fn,), "float8_e4m3fn codes")
+    lds = q.matrix(scales, f"{what}_scales", _byte_types(), "float8_e8m0fnu or uint8 scales")
+    n, k = codes.shape
+    kb = -(-k // BLOCK)
+    if scales.shape[1] != kb or scales.shape[0] not in (n, -(-n // BLOCK)):
+        raise EmeansError(f"EINVAL: {what}_scales must be {n} x {kb} (rows) or {-(-n // BLOCK)} x "
+                          f"{kb} (tiles), got {tuple(scales.shape)}")
+    return ld, lds, scales.shape[0] != n
+
+
+def _product_out(m, n, out, out_dtype, device):
+    import torch
+    if out is None:
+        return torch.empty((m, n), dtype=out_dtype, device=device)
+    if not (getattr(out, "is_cuda", False) and out.device == device and out.dtype == out_dtype
+            and out.shape == (m, n) and (out.stride(1) == 1 or n <= 1)):
+        raise EmeansError(f"EINVAL: out must be an {m} x {n} {out_dtype} GPU tensor with adjacent "
+                          "values in a row")
+    return out
+
+
+def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=None):
+    """a b^T (m x n) of block codes: a m x k and b n x k float8_e4m3fn tensors
+    with scales per row and 128 values (as block_encode makes them); b_scales
+    may instead stand per 128 x 128 tile. Products are exact, sums fp32, rounded
+    once to out_dtype (float32, bfloat16, the default, or float16). out: a
+    tensor to write into."""
+    import torch
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    ot = _number(out_dtype, "out_dtype")
+    with _queue(a, stream, "a") as q:
+        lda, ldas, a_tiles = _product_side(q, a, a_scales, "a")
+        ldb, ldbs, b_tiles = _product_side(q, b, b_scales, "b")
+        m, k = a.shape
+        n = b.shape[0]
+        if b.shape[1] != k:
+            raise EmeansError(f"EINVAL: a has {k} columns, b has {b.shape[1]}")
+        if a_tiles:
+            raise EmeansError("EINVAL: a_scales must stand per row (tiles are for b)")
+        out = _product_out(m, n, out, out_dtype, a.device)
+        if m and n:
+            _check(lib().emeans_block_matmul(a.data_ptr(), lda, a_scales.data_ptr(), ldas,
+                                             b.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
+                                             1 if b_tiles else 0, m, n, k, out.data_ptr(), ot,
+                                             out.stride(0), q.ptr))
+    return out
+
+
+def _linear_codes(x, w, w_scales, out_dtype, stream):
+    """x (m x k numbers) times the transpose of codes: one library call."""
+    import torch
+    with _queue(x, stream) as q:
+        dt = _number(x.dtype, "X")
+        ldx = q.matrix(x, "X", (x.dtype,), "")
+        ldb, ldbs, tiles = _product_side(q, w, w_scales, "w")
+        m, k = x.shape
+        n = w.shape[0]
+        if w.shape[1] != k:
+            raise EmeansError(f"EINVAL: X has {k} columns, w has {w.shape[1]}")
+        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+        if m and n:
+            L = lib()
+            need = L.emeans_block_linear_work(m, k)
+            work = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
+            _check(L.emeans_block_linear(x.data_ptr(), dt, ldx, w.data_ptr(), ldb,
+                                         w_scales.data_ptr(), ldbs, 1 if tiles else 0, m, n, k,
+                                         out.data_ptr(), _number(out_dtype, "out_dtype"),
+                                         out.stride(0), work.data_ptr() if need else None, q.ptr))
+    return out
+
+
+def _rows(t):
+    """t as a matrix whose rows are runs that do not overlap (a copy if it is
+    not one: an expanded gradient, say)."""
+    if (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1):
+        return t
+    return t.contiguous()
+
+
+_linear_function = None
+
+
+def _linear_fn():
+    global _linear_function
+    if _linear_function is None:
+        import torch
+
+        class BlockLinear(torch.autograd.Function):
+            """y = Q(x) Q(w)^T; the rounding passes gradients straight through."""
+
+            @staticmethod
+            def forward(ctx, x, w, frozen, out_dtype, stream):
+                need_x, need_w = ctx.needs_input_grad[:2]
+                xr, xs, xc, xcs = block_encode(x, cols=True, stream=stream) if need_w else \
+                    (*block_encode(x, stream=stream), None, None)
+                if frozen is not None:
+                    wr, ws, wc, wcs = frozen
+                elif need_x:
+                    wr, ws, wc, wcs = block_encode(w, tiles=True, cols=True, stream=stream)
+                else:
+                    wr, ws, wc, wcs = *block_encode(w, tiles=True, stream=stream), None, None
+                ctx.save_for_backward(xc, xcs, wc if need_x else None, wcs if need_x else None)
+                ctx.types = x.dtype, None if w is None else w.dtype, stream
+                return block_matmul(xr, xs, wr, ws, out_dtype=out_dtype, stream=stream)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                xc, xcs, wc, wcs = ctx.saved_tensors
+                x_type, w_type, stream = ctx.types
+                dy = _rows(dy)
+                need_x, need_w = ctx.needs_input_grad[:2]
+                dx = dw = None
+                gr, gs, gc, gcs = block_encode(dy, rows=need_x, cols=True, stream=stream) \
+                    if need_w else (*block_encode(dy, stream=stream), None, None)
+                if need_x:
+                    dx = block_matmul(gr, gs, wc, wcs, out_dtype=x_type, stream=stream)
+                if need_w:
+                    dw = block_matmul(gc, gcs, xc, xcs, out_dtype=w_type, stream=stream)
+                return dx, dw, None, None, None
+
+        _linear_function = BlockLinear
+    return _linear_function
+
+
+def block_linear(X, w, *, out_dtype=None, stream=None):
+    """y = X w^T (X (..., k), w n x k) with both sides as block codes: X encoded
+    along its rows, w in 128 x 128 tiles; y in out_dtype (X's by default).
+
+    w a float32, bfloat16 or float16 tensor: encoded in the call; gradients of
+    X and w pass straight through the rounding, dX = Q(dY) Q(w) and dw =
+    Qt(dY) Qt(X)^T (Qt: the transpose, blocks along the rows of X), with the codes
+    of X and w kept for the backward pass instead of the numbers.
+    w a tuple (codes, scales), as block_encode(w, tiles=True) gives: serving,
+    where a few rows of X are encoded inside the product's launch. With the
+    tuple of four of block_encode(w, tiles=True, cols=True), X has a gradient
+    and the frozen w none.
+
+    On `stream` (the current one by default) the backward pass runs too; its
+    caller orders the gradients' use, as for any work on another stream."""
+    import torch
+    if not getattr(X, "is_cuda", False):
+        raise EmeansError("ENOTDEVICE: X must be a tensor on the GPU")
+    out_dtype = out_dtype or X.dtype
+    lead = X.shape[:-1]
+    x = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
+    frozen = w if isinstance(w, (tuple, list)) else None
+    if frozen is not None and len(frozen) not in (2, 4):
+        raise EmeansError("EINVAL: w must be a tensor, (codes, scales) or the four of "
+                          "block_encode(w, tiles=True, cols=True)")
+    grad = torch.is_grad_enabled() and (X.requires_grad or (frozen is None and w.requires_grad))
+    if grad:
+        if frozen is not None and len(frozen) != 4:
+            raise EmeansError("EINVAL: the gradient of X needs the transposed codes of w: pass "
+                              "the four of block_encode(w, tiles=True, cols=True)")
+        wt = None if frozen is not None else w
+        if wt is not None and (wt.dim() != 2 or wt.shape[1] != x.shape[1]):
+            raise EmeansError(f"EINVAL: w must be n x {x.shape[1]}")
+        y = _linear_fn().apply(_rows(x), wt if wt is None else _rows(wt), frozen, out_dtype, stream)
+    else:
+        codes, scales = frozen[:2] if frozen is not None else \
+            block_encode(w, tiles=True, stream=stream)
+        y = _linear_codes(_rows(x), codes, scales, out_dtype, stream)
+    return y if X.dim() == 2 else y.view(*lead, y.shape[1])
+
+
+def cache_new(rows, d: int, *, block: int = BLOCK, dtype=None, device="cuda"):
+    """An empty store of codes: (codes, scales) of shape rows + (d,) and rows +
+    (ceil(d / block),), rows a number or a shape such as (pages, rows per
+    page). dtype float8_e4m3fn (default) or int8. Its rows read as zeros."""
+    import torch
+    shape = (rows,) if isinstance(rows, int) else tuple(rows)
+    dtype = dtype or torch.float8_e4m3fn
+    if dtype not in (_FORMATS or _types()[1]):
+        raise EmeansError(f"EDTYPE: {dtype} not supported (float8_e4m3fn or int8)")
+    codes = torch.zeros((*shape, d), dtype=torch.uint8, device=device).view(dtype)
+    scales = torch.full((*shape, -(-d // block)), 127, dtype=torch.uint8, device=device)
+    return codes, scales.view(torch.float8_e8m0fnu)
+
+
+def _store(q, codes, scales, block):
+    fmt = (_FORMATS or _types()[1]).get(codes.dtype)
+    if fmt is None:
+        raise EmeansError(f"EDTYPE: codes must be float8_e4m3fn or int8 (got {codes.dtype})")
+    if scales.dtype not in _byte_types():
+        raise EmeansError(f"EDTYPE: scales must be float8_e8m0fnu or uint8 (got {scales.dtype})")
+    for t, what in ((codes, "codes"), (scales, "scales")):
+        if not getattr(t, "is_cuda", False) or t.device.index != q.index:
+            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
+        if not t.is_contiguous() or t.dim() < 2:
+            raise EmeansError(f"EINVAL: {what} must be contiguous, rows last but one")
+    d = codes.shape[-1]
+    if block < 1 or codes.shape[:-1] != scales.shape[:-1] or scales.shape[-1] != -(-d // block):
+        raise EmeansError(f"EINVAL: scales must be {tuple(codes.shape[:-1])} x ceil({d} / {block}),"
+                          f" got {tuple(scales.shape)}")
+    return fmt, codes.numel() // d if d else 0, d
+
+
+def _slots(q, slots, n=None):
+    import torch
+    if not getattr(slots, "is_cuda", False) or slots.device.index != q.index:
+        raise EmeansError("ENOTDEVICE: slots must be a tensor on the GPU of the others")
+    if slots.dtype not in (torch.int32, torch.int64):
+        raise EmeansError(f"EDTYPE: slots must be int32 or int64 (got {slots.dtype})")
+    if slots.dim() != 1 or not slots.is_contiguous() or (n is not None and slots.numel() != n):
+        raise EmeansError("EINVAL: slots must be one contiguous number per row")
+    return slots.element_size()
+
+
+def cache_write(X, slots, codes, scales, *, block: int = BLOCK, stream=None) -> None:
+    """Encode the rows of X (n x d, or n x heads x width with any distance
+    between rows and between heads; float32, bfloat16 or float16) into the rows
+    of a store (cache_new) that slots (n int32 or int64, distinct) names, with
+    one scale for each `block` values of a row. The store may have any shape
+    rows x d, pages x page rows x d, ...: a slot counts its rows in order.
+    Negative slots and slots past its end are skipped."""
+    with _queue(X, stream) as q:
+        dt = _number(X.dtype, "X")
+        fmt, rows, d = _store(q, codes, scales, block)
+        if X.dim() not in (2, 3) or (X.stride(-1) != 1 and X.shape[-1] > 1):
+            raise EmeansError("EINVAL: X must be n x d or n x heads x width with adjacent values")
+        n = X.shape[0]
+        heads, width = (1, X.shape[1]) if X.dim() == 2 else X.shape[1:]
+        if heads * width != d:
+            raise EmeansError(f"EINVAL: X has rows of {heads * width} values, the store of {d}")
+        size = _slots(q, slots, n)
+        if n and rows:
+            _check(lib().emeans_cache_write(X.data_ptr(), dt, n, heads, width, X.stride(0),
+                                            X.stride(1) if X.dim() == 3 else width,
+                                            slots.data_ptr(), size, codes.data_ptr(),
+                                            scales.data_ptr(), rows, block, fmt, q.ptr))
+
+
+def cache_read(codes, scales, slots, *, block: int = BLOCK, out_dtype=None, out=None, stream=None):
+    """Rows slots (int32 or int64) of a store as numbers (len(slots) x d,
+    out_dtype: bfloat16 by default, float32 or float16). A slot outside the
+    store reads as zeros. out: a tensor to write into."""
+    import torch
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    ot = _number(out_dtype, "out_dtype")
+    with _queue(codes, stream, "codes") as q:
+        fmt, rows, d = _store(q, codes, scales, block)
+        size = _slots(q, slots)
+        n = slots.numel()
+        out = _product_out(n, d, out, out_dtype, codes.device)
+        if n:
+            _check(lib().emeans_cache_read(codes.data_ptr(), scales.data_ptr(), rows, d, block,
+                                           fmt, slots.data_ptr(), size, n, out.data_ptr(), ot,
+                                           out.stride(0), q.ptr))
+    return out
+
+
+def cache_read_pages(codes, scales, table, starts, total: int, *, block: int = BLOCK,
+                     out_dtype=None, out=None, stream=None):
+    """Ragged sequences of a paged store (codes pages x page rows x d) packed
+    into total x d numbers: sequence s is rows starts[s] .. starts[s + 1] of the
+    result (starts: seqs + 1 int32), its row p in page table[s, p // page rows]
+    (table: seqs x pages of the longest, int32). Rows of the result outside
+    every sequence, and rows whose page is negative or past the end, are zeros.
+    total is the host's number: nothing is read back."""
+    import torch
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    ot = _number(out_dtype, "out_dtype")
+    with _queue(codes, stream, "codes") as q:
+        fmt, _, d = _store(q, codes, scales, block)
+        if codes.dim() != 3:
+            raise EmeansError("EINVAL: codes must be pages x page rows x d")
+        ldt = q.matrix(table, "table", (torch.int32,), "int32")
+        if not getattr(starts, "is_cuda", False) or starts.device.index != q.index:
+            raise EmeansError("ENOTDEVICE: starts must be a tensor on the GPU of the others")
+        if starts.dtype != torch.int32 or not starts.is_contiguous() \
+                or starts.shape != (table.shape[0] + 1,):
+            raise EmeansError(f"EINVAL: starts must be {table.shape[0] + 1} contiguous int32")
+        total = int(total)
+        out = _product_out(total, d, out, out_dtype, codes.device)
+        if total:
+            _check(lib().emeans_cache_read_pages(
+                codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1], d, block,
+                fmt, table.data_ptr(), ldt, table.shape[1], starts.data_ptr(), table.shape[0],
+                total, out.data_ptr(), ot, out.stride(0), q.ptr))
+    return out
 
 
 def batch_rows(n: int, seed: int, pass_: int, start: int, count: int, device="cuda", stream=None):

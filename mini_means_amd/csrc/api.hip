@@ -1181,4 +1181,263 @@ int emeans_fp8_decode(const float* C, int64_t k, int32_t d, const float* shift, 
   return emeans_int8_decode(C, k, d, shift, scale, out, stream);
 }
 
+// ---- block codes ------------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 31;
+
+bool number_type(int32_t dt) { return dt == EMEANS_F32 || dt == EMEANS_BF16 || dt == EMEANS_F16; }
+
+int check_number_type(int32_t dt, const char* name) {
+  return number_type(dt) ? EMEANS_OK
+                         : fail(EMEANS_EDTYPE, "%s %d not supported (fp32 = 0, bf16 = 1, fp16 = 4)",
+                                name, dt);
+}
+
+int64_t blocks_of(int64_t n, int64_t block) { return (n + block - 1) / block; }
+
+int check_ld(int64_t ld, int64_t row, int64_t rows, const char* name) {
+  return rows > 1 && ld < row ? fail(EMEANS_EINVAL, "%s must be at least %lld (got %lld)", name,
+                                     (long long)row, (long long)ld)
+                              : EMEANS_OK;
+}
+
+int check_count(int64_t n, const char* name) {
+  return n < 0 || n >= kMaxRows ? fail(EMEANS_EINVAL, "%s out of range (%lld)", name, (long long)n)
+                                : EMEANS_OK;
+}
+
+// Checks shared by the two products; b_rows: rows of Bs.
+int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs, bool b_tiles,
+                  int64_t m, int64_t n, int32_t k, const void* out, int32_t out_dtype,
+                  int64_t ldo) {
+  int rc;
+  if ((rc = check_count(m, "m")) || (rc = check_count(n, "n")) || (rc = check_count(k, "k")) ||
+      (rc = check_number_type(out_dtype, "out_dtype")))
+    return rc;
+  const int64_t kb = blocks_of(k, 128), sr = b_tiles ? blocks_of(n, 128) : n;
+  if ((rc = check_ld(ldb, k, n, "ldb")) || (rc = check_ld(ldbs, kb, sr, "ldbs")) ||
+      (rc = check_ld(ldo, n, m, "ldo")))
+    return rc;
+  if (m == 0 || n == 0) return EMEANS_OK;
+  if ((k > 0 && (!B || !Bs)) || !out)
+    return fail(EMEANS_EINVAL, "B, Bs and out must not be NULL");
+  return EMEANS_OK;
+}
+
+int check_store(const void* codes, const uint8_t* scales, int64_t rows, int64_t d, int32_t block,
+                int32_t fmt) {
+  if (rows < 0 || rows > ((int64_t)1 << 40))
+    return fail(EMEANS_EINVAL, "rows out of range (%lld)", (long long)rows);
+  if (d < 1 || d >= kMaxRows) return fail(EMEANS_EINVAL, "d out of range (%lld)", (long long)d);
+  if (block < 16 || block > 256 || block % 16)
+    return fail(EMEANS_EINVAL, "block must be a multiple of 16 in [16, 256] (got %d)", block);
+  if (fmt != EMEANS_F8 && fmt != EMEANS_I8)
+    return fail(EMEANS_EDTYPE, "fmt %d not supported (int8 = 2, fp8 = 3)", fmt);
+  if (rows > 0 && (!codes || !scales))
+    return fail(EMEANS_EINVAL, "codes and scales must not be NULL");
+  return EMEANS_OK;
+}
+
+int check_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d, int64_t n,
+               const void* out, int32_t out_dtype, int64_t ldo) {
+  int rc;
+  if ((rc = check_count(n, "n")) || (rc = check_number_type(out_dtype, "out_dtype")) ||
+      (rc = check_ld(ldo, d, n, "ldo")))
+    return rc;
+  if (n > 0 && !out) return fail(EMEANS_EINVAL, "out must not be NULL");
+  if (n == 0) return EMEANS_OK;
+  if (rows > 0 && ((rc = check_device(codes, "codes")) || (rc = check_device(scales, "scales"))))
+    return rc;
+  return check_device(out, "out");
+}
+
+int launched(hipError_t e, const char* what) {
+  return e == hipSuccess ? EMEANS_OK
+                         : fail(EMEANS_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+}
+
+}  // namespace
+
+int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int64_t ldx,
+                        int32_t tiles, uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
+                        uint8_t* codes_t, int64_t ldct, uint8_t* scales_t, int64_t ldst,
+                        void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_count(n, "n")) || (rc = check_number_type(dtype, "dtype"))) return rc;
+  if (d < 1) return fail(EMEANS_EINVAL, "d must be >= 1");
+  if (!codes && !codes_t) return fail(EMEANS_EINVAL, "codes and codes_t are both NULL");
+  if (!codes != !scales || !codes_t != !scales_t)
+    return fail(EMEANS_EINVAL, "codes and scales (codes_t and scales_t) come together");
+  const int64_t nb = blocks_of(n, 128), db = blocks_of(d, 128);
+  if ((rc = check_ld(ldx, d, n, "ldx"))) return rc;
+  if (codes && ((rc = check_ld(ldc, d, n, "ldc")) ||
+                (rc = check_ld(lds, db, tiles ? nb : n, "lds"))))
+    return rc;
+  if (codes_t && ((rc = check_ld(ldct, n, d, "ldct")) ||
+                  (rc = check_ld(ldst, nb, tiles ? db : d, "ldst"))))
+    return rc;
+  if (n == 0) return EMEANS_OK;
+  if (!X) return fail(EMEANS_EINVAL, "X must not be NULL");
+  if ((rc = check_device(X, "X"))) return rc;
+  if (codes && ((rc = check_device(codes, "codes")) || (rc = check_device(scales, "scales"))))
+    return rc;
+  if (codes_t &&
+      ((rc = check_device(codes_t, "codes_t")) || (rc = check_device(scales_t, "scales_t"))))
+    return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (!tiles && !codes_t)
+    return launched(launch_encode_rows({dtype, X, n, d, d, ldx, 0, 128, false, nullptr, 0, n,
+                                        codes, ldc, scales, lds}, st), "block encode");
+  return launched(launch_encode_tiles({dtype, X, ldx, n, d, tiles != 0, codes, ldc, scales, lds,
+                                       codes_t, ldct, scales_t, ldst}, st), "block encode");
+}
+
+int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
+                        const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
+                        int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
+                        int32_t out_dtype, int64_t ldo, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo)) ||
+      (rc = check_ld(lda, k, m, "lda")) || (rc = check_ld(ldas, blocks_of(k, 128), m, "ldas")))
+    return rc;
+  if (m == 0 || n == 0) return EMEANS_OK;
+  if (k > 0 && (!A || !As)) return fail(EMEANS_EINVAL, "A and As must not be NULL");
+  if (k > 0 && ((rc = check_device(A, "A")) || (rc = check_device(As, "As")) ||
+                (rc = check_device(B, "B")) || (rc = check_device(Bs, "Bs"))))
+    return rc;
+  if ((rc = check_device(out, "out"))) return rc;
+  return launched(launch_block_product({A, lda, As, ldas, B, ldb, Bs, ldbs, b_tiles != 0, m, n, k,
+                                        out_dtype, out, ldo}, static_cast<hipStream_t>(stream)),
+                  "block product");
+}
+
+// Codes of X with rows a multiple of 16 bytes apart, then their scales with
+// rows a multiple of 4 bytes apart.
+int64_t emeans_block_linear_work(int64_t m, int32_t k) {
+  if (m < 0 || m >= kMaxRows || k < 0) return 0;
+  return m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
+}
+
+int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
+                        const uint8_t* Bs, int64_t ldbs, int32_t b_tiles, int64_t m, int64_t n,
+                        int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
+                        void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_number_type(dtype, "dtype")) ||
+      (rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo)) ||
+      (rc = check_ld(ldx, k, m, "ldx")))
+    return rc;
+  if (m == 0 || n == 0) return EMEANS_OK;
+  if (k > 0 && !X) return fail(EMEANS_EINVAL, "X must not be NULL");
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
+  if (k > 0 && ((rc = check_device(X, "X")) || (rc = check_device(B, "B")) ||
+                (rc = check_device(Bs, "Bs"))))
+    return rc;
+  if ((rc = check_device(out, "out")) || (work && (rc = check_device(work, "work")))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  BlockProduct p{nullptr, blocks_of(k, 16) * 16, nullptr, blocks_of(blocks_of(k, 128), 4) * 4,
+                 B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo};
+  void* own = nullptr;
+  rc = EMEANS_OK;
+  if (k > 0) {
+    if (!work) HIP_TRY(hipMallocAsync(&own, emeans_block_linear_work(m, k), st));
+    uint8_t* codes = static_cast<uint8_t*>(work ? work : own);
+    uint8_t* scales = codes + m * p.lda;
+    p.A = codes;
+    p.As = scales;
+    HIP_TRY(launch_encode_rows({dtype, X, m, k, k, ldx, 0, 128, false, nullptr, 0, m, codes,
+                                p.lda, scales, p.ldas}, st));
+  }
+  HIP_TRY(launch_block_product(p, st));
+done:
+  if (own) {
+    const hipError_t e = hipFreeAsync(own, st);
+    if (e != hipSuccess && rc == EMEANS_OK)
+      rc = fail(EMEANS_EHIP, "hipFreeAsync: %s", hipGetErrorString(e));
+  }
+  return rc;
+}
+
+int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,
+                       int64_t row_stride, int64_t head_stride, const void* slots,
+                       int32_t slot_bytes, void* codes, uint8_t* scales, int64_t rows,
+                       int32_t block, int32_t fmt, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_count(n, "n")) || (rc = check_number_type(dtype, "dtype"))) return rc;
+  if (heads < 1 || width < 1)
+    return fail(EMEANS_EINVAL, "heads and width must be >= 1 (got %d and %d)", heads, width);
+  int64_t d = (int64_t)heads * width;
+  if ((rc = check_store(codes, scales, rows, d, block, fmt))) return rc;
+  if (row_stride < 0 || head_stride < 0)
+    return fail(EMEANS_EINVAL, "strides must not be negative");
+  if (slot_bytes != 4 && slot_bytes != 8)
+    return fail(EMEANS_EINVAL, "slot_bytes must be 4 or 8 (got %d)", slot_bytes);
+  if (heads == 1 || head_stride == width)
+    width = (int32_t)d;  // one run of values
+  else if (width % block)
+    return fail(EMEANS_EINVAL, "heads apart from each other need a width (%d) that is a multiple "
+                "of block (%d)", width, block);
+  if (n == 0 || rows == 0) return EMEANS_OK;
+  if (!X || !slots) return fail(EMEANS_EINVAL, "X and slots must not be NULL");
+  if ((rc = check_device(X, "X")) || (rc = check_device(slots, "slots")) ||
+      (rc = check_device(codes, "codes")) || (rc = check_device(scales, "scales")))
+    return rc;
+  return launched(launch_encode_rows({dtype, X, n, (int)d, width, row_stride, head_stride, block,
+                                      fmt == EMEANS_I8, slots, slot_bytes, rows,
+                                      static_cast<uint8_t*>(codes), d, scales,
+                                      blocks_of(d, block)}, static_cast<hipStream_t>(stream)),
+                  "cache write");
+}
+
+int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d,
+                      int32_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
+                      int64_t n, void* out, int32_t out_dtype, int64_t ldo, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_store(codes, scales, rows, d, block, fmt))) return rc;
+  if (slot_bytes != 4 && slot_bytes != 8)
+    return fail(EMEANS_EINVAL, "slot_bytes must be 4 or 8 (got %d)", slot_bytes);
+  if (n > 0 && !slots) return fail(EMEANS_EINVAL, "slots must not be NULL");
+  if ((rc = check_read(codes, scales, rows, d, n, out, out_dtype, ldo))) return rc;
+  if (n == 0) return EMEANS_OK;
+  if ((rc = check_device(slots, "slots"))) return rc;
+  return launched(launch_decode_rows({static_cast<const uint8_t*>(codes), scales, rows, d, block,
+                                      fmt == EMEANS_I8, slots, slot_bytes, nullptr, 0, 0, nullptr,
+                                      0, 1, n, out_dtype, out, ldo},
+                                     static_cast<hipStream_t>(stream)), "cache read");
+}
+
+int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pages,
+                            int32_t page_rows, int32_t d, int32_t block, int32_t fmt,
+                            const int32_t* table, int64_t table_ld, int32_t table_pages,
+                            const int32_t* starts, int32_t seqs, int64_t n, void* out,
+                            int32_t out_dtype, int64_t ldo, void* stream) {
+  g_err.clear();
+  int rc;
+  if (page_rows < 1) return fail(EMEANS_EINVAL, "page_rows must be >= 1 (got %d)", page_rows);
+  if ((rc = check_count(pages, "pages")) || (rc = check_count(seqs, "seqs"))) return rc;
+  if ((rc = check_store(codes, scales, pages * page_rows, d, block, fmt))) return rc;
+  if (table_pages < 0 || (rc = check_ld(table_ld, table_pages, seqs, "table_ld")))
+    return fail(EMEANS_EINVAL, "table_pages or table_ld out of range (%d, %lld)", table_pages,
+                (long long)table_ld);
+  if (n > 0 && (!starts || (seqs > 0 && table_pages > 0 && !table)))
+    return fail(EMEANS_EINVAL, "table and starts must not be NULL");
+  if ((rc = check_read(codes, scales, pages * page_rows, d, n, out, out_dtype, ldo))) return rc;
+  if (n == 0) return EMEANS_OK;
+  if ((rc = check_device(starts, "starts")) ||
+      (seqs > 0 && table_pages > 0 && (rc = check_device(table, "table"))))
+    return rc;
+  return launched(launch_decode_rows({static_cast<const uint8_t*>(codes), scales,
+                                      pages * page_rows, d, block, fmt == EMEANS_I8, nullptr, 4,
+                                      table, table_ld, table_pages, starts, seqs, page_rows, n,
+                                      out_dtype, out, ldo},
+                                     static_cast<hipStream_t>(stream)), "cache read");
+}
+
 }  // extern "C"

@@ -218,4 +218,101 @@ hipError_t launch_encode(const float* X, int64_t n, int d, const float* shift, f
 hipError_t launch_decode(const float* C, int64_t k, int d, const float* shift, double scale,
                          float* out, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Block-scaled 8-bit codes (block_codes.hip): one E8M0 scale byte for each
+// block of values; number types dt / ot: 0 fp32, 1 bf16, 4 fp16.
+// ---------------------------------------------------------------------------
+
+// Codes and scales of n rows, blocks of `block` values along the row (a
+// multiple of 16, at most 256; the last of a row may be short). Value (h, c)
+// of row r sits at X[r rs + h hs + c], c < width, and d = heads * width; with
+// more than one head, width is a multiple of block. Row r goes to row r of
+// codes / scales (rows ldc / lds bytes apart), or with slots to row slots[r],
+// and is skipped where slots[r] is outside [0, cap).
+struct EncodeRows {
+  int dt;
+  const void* X;
+  int64_t n;
+  int d, width;
+  int64_t rs, hs;
+  int block;
+  bool i8;
+  const void* slots;  // NULL, or n entries of slot_bytes (4 or 8)
+  int slot_bytes;
+  int64_t cap;
+  uint8_t* codes;
+  int64_t ldc;
+  uint8_t* scales;
+  int64_t lds;
+};
+hipError_t launch_encode_rows(const EncodeRows& a, hipStream_t st);
+
+// E4M3 codes of the n x d matrix X in either or both orders (NULL: not made):
+// codes n x d with scales per row and 128 columns, codes_t d x n with scales_t
+// per column and 128 rows; `tiles`: one scale per 128 x 128 tile instead, in
+// both orders (scales[i][j] = scales_t[j][i]).
+struct EncodeTiles {
+  int dt;
+  const void* X;
+  int64_t ldx;
+  int64_t n;
+  int d;
+  bool tiles;
+  uint8_t* codes;
+  int64_t ldc;
+  uint8_t* scales;
+  int64_t lds;
+  uint8_t* codes_t;
+  int64_t ldct;
+  uint8_t* scales_t;
+  int64_t ldst;
+};
+hipError_t launch_encode_tiles(const EncodeTiles& a, hipStream_t st);
+
+// n rows of a store of `cap` rows of d codes (contiguous; scales contiguous,
+// one per block), decoded to ot: row i from slots[i], or (slots NULL) from the
+// place that the page table gives packed row i: sequence s with starts[s] <=
+// i < starts[s + 1], page table[s][(i - starts[s]) / page]. Rows whose place
+// is outside the store, the table or the sequences are zeros.
+struct DecodeRows {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t cap;
+  int d, block;
+  bool i8;
+  const void* slots;
+  int slot_bytes;
+  const int32_t* table;
+  int64_t table_ld;
+  int table_pages;
+  const int32_t* starts;
+  int seqs, page;
+  int64_t n;
+  int ot;
+  void* out;
+  int64_t ldo;
+};
+hipError_t launch_decode_rows(const DecodeRows& a, hipStream_t st);
+
+// out[m][n] = sum_k A[m][k] B[n][k] over E4M3 codes with scales per row and
+// 128 values of k (B: per 128 x 128 tile with b_tiles), fp32 sums, rounded
+// once to ot (block_matmul.hip).
+struct BlockProduct {
+  const uint8_t* A;
+  int64_t lda;
+  const uint8_t* As;
+  int64_t ldas;
+  const uint8_t* B;
+  int64_t ldb;
+  const uint8_t* Bs;
+  int64_t ldbs;
+  bool b_tiles;
+  int64_t m, n;
+  int k;
+  int ot;
+  void* out;
+  int64_t ldo;
+};
+hipError_t launch_block_product(const BlockProduct& p, hipStream_t st);
+
 }  // namespace emk
