@@ -449,29 +449,33 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
                         void* stream);
 
 /* out[i][j] = sum_l A[i][l] B[j][l] over the values that E4M3 codes and their
- * scales stand for (the product of A with the transpose of B): products exact,
- * sums in fp32, one rounding to out_dtype.
+ * scales stand for (the product of A with the transpose of B), rounded once to
+ * out_dtype. Products are exact. An fp32 result is a sum in fp32; for results
+ * of 16 bits the FP8 matrix unit sums, which adds products in groups of eight
+ * with 14 bits kept below the largest (about 1.5e-5 of the result's norm).
  *   A    device, m x k codes      As  device, m x ceil(k/128) scales
  *   B    device, n x k codes      Bs  device, n x ceil(k/128) scales, or with
  *        b_tiles != 0 ceil(n/128) x ceil(k/128)
  *   out  device, m x n, out_dtype
+ *   work device, emeans_block_matmul_work(m, n, k) bytes (0 for many sizes),
+ *        16-byte aligned, or NULL: the library then allocates it stream-ordered
  * A NaN code or a scale byte of 255 makes the outputs it enters NaN. k = 0
- * gives zeros. Any alignment and any leading dimension is right; rows that
- * start at multiples of 16 bytes are read fastest.
+ * gives zeros. Any alignment and any leading dimension is right; codes whose
+ * rows start at multiples of 16 bytes are read fastest.
  * Errors: EINVAL (m, n or k < 0, m or n >= 2^31, a leading dimension below
- * the row length, NULL), EDTYPE, ENOTDEVICE, EHIP. */
+ * the row length, work not aligned, NULL), EDTYPE, ENOTDEVICE, ENOMEM, EHIP. */
+int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k);
 int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
                         const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
                         int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
-                        int32_t out_dtype, int64_t ldo, void* stream);
+                        int32_t out_dtype, int64_t ldo, void* work, void* stream);
 
 /* The same product with A given as numbers: X (m x k, dtype) is encoded as
  * emeans_block_encode does along its rows, and multiplied with B. A few rows
  * are encoded inside the product's own launch; more are encoded first, into
- *   work  device, emeans_block_linear_work(m, k) bytes, 16-byte aligned
- * which may be NULL (the library then allocates it stream-ordered).
- * Errors: as emeans_block_matmul, and ENOMEM. */
-int64_t emeans_block_linear_work(int64_t m, int32_t k);
+ * work (emeans_block_linear_work(m, n, k) bytes, 16-byte aligned, or NULL).
+ * Errors: as emeans_block_matmul. */
+int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k);
 int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
                         const uint8_t* Bs, int64_t ldbs, int32_t b_tiles, int64_t m, int64_t n,
                         int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,

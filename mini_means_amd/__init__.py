@@ -97,9 +97,11 @@ def lib() -> ctypes.CDLL:
         L.emeans_block_encode.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64,
                                           c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]
         L.emeans_block_matmul.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
-                                          c_i32, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp]
-        L.emeans_block_linear_work.argtypes = [c_i64, c_i32]
-        L.emeans_block_linear_work.restype = c_i64
+                                          c_i32, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp,
+                                          c_vp]
+        for f in ("emeans_block_matmul_work", "emeans_block_linear_work"):
+            getattr(L, f).argtypes = [c_i64, c_i64, c_i32]
+            getattr(L, f).restype = c_i64
         L.emeans_block_linear.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
                                           c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_vp]
         L.emeans_cache_write.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i32, c_i64, c_i64, c_vp,
@@ -576,12 +578,26 @@ def _product_out(m, n, out, out_dtype, device):
     return out
 
 
+class _Work:
+    """Working memory of one call, allocated where the call runs."""
+
+    def __init__(self, need, device):
+        import torch
+        self.room = torch.empty((need,), dtype=torch.uint8, device=device)
+        self.data_ptr = self.room.data_ptr
+
+
+def _work(need: int, device):
+    return _Work(need, device) if need else None
+
+
 def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=None):
     """a b^T (m x n) of block codes: a m x k and b n x k float8_e4m3fn tensors
     with scales per row and 128 values (as block_encode makes them); b_scales
-    may instead stand per 128 x 128 tile. Products are exact, sums fp32, rounded
-    once to out_dtype (float32, bfloat16, the default, or float16). out: a
-    tensor to write into."""
+    may instead stand per 128 x 128 tile. Rounded once to out_dtype: float32
+    (sums in fp32), bfloat16 (the default) or float16 (sums of the FP8 matrix
+    unit, off by about 1.5e-5 of the result's norm). out: a tensor to write
+    into."""
     import torch
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
     ot = _number(out_dtype, "out_dtype")
@@ -596,10 +612,12 @@ def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=N
             raise EmeansError("EINVAL: a_scales must stand per row (tiles are for b)")
         out = _product_out(m, n, out, out_dtype, a.device)
         if m and n:
-            _check(lib().emeans_block_matmul(a.data_ptr(), lda, a_scales.data_ptr(), ldas,
-                                             b.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
-                                             1 if b_tiles else 0, m, n, k, out.data_ptr(), ot,
-                                             out.stride(0), q.ptr))
+            L = lib()
+            work = _work(L.emeans_block_matmul_work(m, n, k), a.device)
+            _check(L.emeans_block_matmul(a.data_ptr(), lda, a_scales.data_ptr(), ldas,
+                                         b.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
+                                         1 if b_tiles else 0, m, n, k, out.data_ptr(), ot,
+                                         out.stride(0), work and work.data_ptr(), q.ptr))
     return out
 
 
@@ -617,12 +635,11 @@ def _linear_codes(x, w, w_scales, out_dtype, stream):
         out = torch.empty((m, n), dtype=out_dtype, device=x.device)
         if m and n:
             L = lib()
-            need = L.emeans_block_linear_work(m, k)
-            work = torch.empty((need,), dtype=torch.uint8, device=x.device) if need else None
+            work = _work(L.emeans_block_linear_work(m, n, k), x.device)
             _check(L.emeans_block_linear(x.data_ptr(), dt, ldx, w.data_ptr(), ldb,
                                          w_scales.data_ptr(), ldbs, 1 if tiles else 0, m, n, k,
                                          out.data_ptr(), _number(out_dtype, "out_dtype"),
-                                         out.stride(0), work.data_ptr() if need else None, q.ptr))
+                                         out.stride(0), work and work.data_ptr(), q.ptr))
     return out
 
 

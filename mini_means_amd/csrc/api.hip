@@ -1208,10 +1208,10 @@ int check_count(int64_t n, const char* name) {
                                 : EMEANS_OK;
 }
 
-// Checks shared by the two products; b_rows: rows of Bs.
+// Checks shared by the two products.
 int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs, bool b_tiles,
                   int64_t m, int64_t n, int32_t k, const void* out, int32_t out_dtype,
-                  int64_t ldo) {
+                  int64_t ldo, const void* work) {
   int rc;
   if ((rc = check_count(m, "m")) || (rc = check_count(n, "n")) || (rc = check_count(k, "k")) ||
       (rc = check_number_type(out_dtype, "out_dtype")))
@@ -1223,6 +1223,7 @@ int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs
   if (m == 0 || n == 0) return EMEANS_OK;
   if ((k > 0 && (!B || !Bs)) || !out)
     return fail(EMEANS_EINVAL, "B, Bs and out must not be NULL");
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
   return EMEANS_OK;
 }
 
@@ -1251,6 +1252,15 @@ int check_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d
   if (rows > 0 && ((rc = check_device(codes, "codes")) || (rc = check_device(scales, "scales"))))
     return rc;
   return check_device(out, "out");
+}
+
+// Stream-ordered release of a call's own working memory; the call's status.
+int release(void* own, hipStream_t st, int rc) {
+  if (!own) return rc;
+  const hipError_t e = hipFreeAsync(own, st);
+  if (e != hipSuccess && rc == EMEANS_OK)
+    return fail(EMEANS_EHIP, "hipFreeAsync: %s", hipGetErrorString(e));
+  return rc;
 }
 
 int launched(hipError_t e, const char* what) {
@@ -1295,13 +1305,26 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
                                        codes_t, ldct, scales_t, ldst}, st), "block encode");
 }
 
+int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k) {
+  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1) return 0;
+  return (int64_t)block_product_work(m, n, k);
+}
+
+// The product's own working memory, then codes of X with rows a multiple of 16
+// bytes apart, then their scales with rows a multiple of 4 bytes apart.
+int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k) {
+  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1) return 0;
+  return emeans_block_matmul_work(m, n, k) +
+         m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
+}
+
 int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
                         const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
                         int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
-                        int32_t out_dtype, int64_t ldo, void* stream) {
+                        int32_t out_dtype, int64_t ldo, void* work, void* stream) {
   g_err.clear();
   int rc;
-  if ((rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo)) ||
+  if ((rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo, work)) ||
       (rc = check_ld(lda, k, m, "lda")) || (rc = check_ld(ldas, blocks_of(k, 128), m, "ldas")))
     return rc;
   if (m == 0 || n == 0) return EMEANS_OK;
@@ -1309,17 +1332,20 @@ int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_
   if (k > 0 && ((rc = check_device(A, "A")) || (rc = check_device(As, "As")) ||
                 (rc = check_device(B, "B")) || (rc = check_device(Bs, "Bs"))))
     return rc;
-  if ((rc = check_device(out, "out"))) return rc;
-  return launched(launch_block_product({A, lda, As, ldas, B, ldb, Bs, ldbs, b_tiles != 0, m, n, k,
-                                        out_dtype, out, ldo}, static_cast<hipStream_t>(stream)),
-                  "block product");
-}
-
-// Codes of X with rows a multiple of 16 bytes apart, then their scales with
-// rows a multiple of 4 bytes apart.
-int64_t emeans_block_linear_work(int64_t m, int32_t k) {
-  if (m < 0 || m >= kMaxRows || k < 0) return 0;
-  return m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
+  if ((rc = check_device(out, "out")) || (work && (rc = check_device(work, "work")))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  BlockProduct p{A, lda, As, ldas, B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo,
+                 work};
+  const int64_t need = emeans_block_matmul_work(m, n, k);
+  void* own = nullptr;
+  rc = EMEANS_OK;
+  if (need > 0 && !work) {
+    HIP_TRY(hipMallocAsync(&own, need, st));
+    p.work = own;
+  }
+  HIP_TRY(launch_block_product(p, st));
+done:
+  return release(own, st, rc);
 }
 
 int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
@@ -1329,24 +1355,26 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
   g_err.clear();
   int rc;
   if ((rc = check_number_type(dtype, "dtype")) ||
-      (rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo)) ||
+      (rc = check_product(B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out, out_dtype, ldo, work)) ||
       (rc = check_ld(ldx, k, m, "ldx")))
     return rc;
   if (m == 0 || n == 0) return EMEANS_OK;
   if (k > 0 && !X) return fail(EMEANS_EINVAL, "X must not be NULL");
-  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
   if (k > 0 && ((rc = check_device(X, "X")) || (rc = check_device(B, "B")) ||
                 (rc = check_device(Bs, "Bs"))))
     return rc;
   if ((rc = check_device(out, "out")) || (work && (rc = check_device(work, "work")))) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   BlockProduct p{nullptr, blocks_of(k, 16) * 16, nullptr, blocks_of(blocks_of(k, 128), 4) * 4,
-                 B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo};
+                 B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo, work};
   void* own = nullptr;
   rc = EMEANS_OK;
   if (k > 0) {
-    if (!work) HIP_TRY(hipMallocAsync(&own, emeans_block_linear_work(m, k), st));
-    uint8_t* codes = static_cast<uint8_t*>(work ? work : own);
+    if (!work) {
+      HIP_TRY(hipMallocAsync(&own, emeans_block_linear_work(m, n, k), st));
+      p.work = own;
+    }
+    uint8_t* codes = static_cast<uint8_t*>(p.work) + emeans_block_matmul_work(m, n, k);
     uint8_t* scales = codes + m * p.lda;
     p.A = codes;
     p.As = scales;
@@ -1355,12 +1383,7 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
   }
   HIP_TRY(launch_block_product(p, st));
 done:
-  if (own) {
-    const hipError_t e = hipFreeAsync(own, st);
-    if (e != hipSuccess && rc == EMEANS_OK)
-      rc = fail(EMEANS_EHIP, "hipFreeAsync: %s", hipGetErrorString(e));
-  }
-  return rc;
+  return release(own, st, rc);
 }
 
 int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,

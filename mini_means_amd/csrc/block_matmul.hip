@@ -257,11 +257,230 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, bool v
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tiles of 32 MI x 32 NI outputs, four waves of 16 MI x 16 NI each, one k-step
+// (128 codes) per stage, two stages in LDS, loaded straight from memory
+// (global_load_lds) a step ahead. Rows of codes must start at multiples of 16
+// bytes. Layout in LDS as above: row r's chunk c at c ^ (r % 8), arranged by
+// the source address of each lane. The scales of a stage come with it, one
+// byte per row. The codes past k in the last stage are read singly and
+// replaced by zeros: what a row holds beyond its values does not matter.
+//
+// Workgroups go round the eight XCDs in launch order, so XCD x takes the x-th
+// run of tiles, and a run walks kGroup tile rows at a time: the tiles that
+// share an L2 at one time form a compact patch of the output.
+//
+// SPLIT: blockIdx.y takes `per` k-steps and writes fp32 sums to part[y], which
+// join_kernel adds in order.
+// ---------------------------------------------------------------------------
+constexpr int kGroup = 4;
+
+struct TileMap {
+  unsigned tiles_m, tiles_n;
+  int per;        // k-steps of one split
+  float* part;    // splits x m x part_ld
+  int64_t part_ld;
+};
+
+__device__ __forceinline__ void tile_of(unsigned id, const TileMap& t, unsigned& tm, unsigned& tn) {
+  const unsigned total = t.tiles_m * t.tiles_n;
+  const unsigned x = id & 7, each = total >> 3, more = total & 7;
+  const unsigned j = x * each + min(x, more) + (id >> 3);
+  const unsigned group = j / (kGroup * t.tiles_n), in = j - group * (kGroup * t.tiles_n);
+  const unsigned rows = min((unsigned)kGroup, t.tiles_m - group * kGroup);
+  tn = in / rows;
+  tm = group * kGroup + (in - tn * rows);
+}
+
+template <int MI, int NI, int OT, bool SPLIT>
+__global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kernel(BlockProduct p,
+                                                                                 TileMap t,
+                                                                                 bool vec_o) {
+  constexpr bool F8 = OT != 0;
+  constexpr int BM = 32 * MI, BN = 32 * NI, R = BM + BN;
+  constexpr int Q = (R / 64 + 3) / 4;  // scale loads per wave and stage, at most
+  __shared__ __attribute__((aligned(1024))) uint8_t lc[2][R * kStep];
+  __shared__ __attribute__((aligned(256))) uint32_t ls[2][R];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  unsigned tm, tn;
+  tile_of(blockIdx.x, t, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int mrows = (int)min((int64_t)BM, p.m - m0), nrows = (int)min((int64_t)BN, p.n - n0);
+  const int steps = (p.k + kStep - 1) / kStep;
+  const int s0 = SPLIT ? (int)blockIdx.y * t.per : 0;
+  const int s1 = SPLIT ? min(steps, s0 + t.per) : steps;
+
+  // Window w of the stage is rows 8 w .. 8 w + 7 (A's rows, then B's): lane l
+  // loads position l % 8 of row l / 8, which holds chunk (l % 8) ^ (l / 8).
+  const uint8_t* a0 = p.A + m0 * p.lda;
+  const uint8_t* b0 = p.B + n0 * p.ldb;
+  const int lr = lane >> 3, lx = 16 * ((lane & 7) ^ lr);
+  uint32_t off[MI + NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+    off[i] = (uint32_t)min(8 * (wave * MI + i) + lr, mrows - 1) * (uint32_t)p.lda + lx;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    off[MI + i] = (uint32_t)min(8 * (wave * NI + i) + lr, nrows - 1) * (uint32_t)p.ldb + lx;
+  const uint8_t* sp[Q];  // scales of rows 64 q' .. + 63, q' = wave + 4 q
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int r = 64 * (wave + 4 * q) + lane;
+    if (r < BM) {
+      sp[q] = p.As + (m0 + min(r, mrows - 1)) * p.ldas;
+    } else {
+      const int64_t n = n0 + min(r - BM, nrows - 1);
+      sp[q] = p.Bs + (p.b_tiles ? n / kStep : n) * p.ldbs;
+    }
+  }
+  auto issue = [&](int s, int buf) {
+    const int64_t k0 = (int64_t)s * kStep;
+    uint8_t* da = lc[buf] + wave * MI * 1024;
+    uint8_t* db = lc[buf] + BM * kStep + wave * NI * 1024;
+    if (k0 + kStep <= p.k) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) lds_load16_at(a0 + k0, off[i], da + i * 1024);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) lds_load16_at(b0 + k0, off[MI + i], db + i * 1024);
+    } else {
+      const int left = p.k - (int)k0 - lx;
+#pragma unroll 1
+      for (int i = 0; i < MI; ++i) {
+        const uint32_t o = (uint32_t)min(8 * (wave * MI + i) + lr, mrows - 1) * (uint32_t)p.lda + lx;
+        *reinterpret_cast<u32x4*>(da + i * 1024 + 16 * lane) = load16(a0 + k0 + o, left, true);
+      }
+#pragma unroll 1
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t o = (uint32_t)min(8 * (wave * NI + i) + lr, nrows - 1) * (uint32_t)p.ldb + lx;
+        *reinterpret_cast<u32x4*>(db + i * 1024 + 16 * lane) = load16(b0 + k0 + o, left, true);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (wave + 4 * q < R / 64) lds_load1(sp[q] + s, &ls[buf][64 * (wave + 4 * q)]);
+  };
+
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const int ra = (wave & 1) * 16 * MI + col, rb = BM + (wave >> 1) * 16 * NI + col;
+  const int fx = 16 * (grp ^ (col & 7));
+  if (s0 < s1) issue(s0, 0);
+  for (int s = s0; s < s1; ++s) {
+    const int buf = (s - s0) & 1;
+    EMK_WAIT_VMCNT(0);
+    lds_barrier();
+    if (s + 1 < s1) issue(s + 1, buf ^ 1);
+    const uint8_t* L = lc[buf];
+    auto frag = [&](Operand<F8>& o, int row) {
+      const uint8_t* r = L + row * kStep;
+      o.set(*reinterpret_cast<const u32x4*>(r + fx), *reinterpret_cast<const u32x4*>(r + (fx ^ 64)),
+            ls[buf][row]);
+    };
+    Operand<F8> b[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) frag(b[j], rb + 16 * j);
+    const bool eb = any_rest(b);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      Operand<F8> a[1];
+      frag(a[0], ra + 16 * i);
+      const bool ea = eb || any_rest(a);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = add_step(b[j], a[0], acc[i][j], ea);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t m = m0 + ra + 16 * i;
+    if (m >= p.m) continue;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      const int64_t n = n0 + (rb - BM) - col + 16 * j + 4 * grp;
+      if constexpr (SPLIT) {
+        if (n < p.n)
+          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4, true);
+      } else {
+        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n), vec_o);
+      }
+    }
+  }
+}
+
+// out = the sum of the splits' parts, in order, rounded once.
+template <int OT>
+__global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int splits,
+                                                   int64_t m, int64_t n, int64_t part_ld,
+                                                   void* __restrict__ out, int64_t ldo,
+                                                   bool vec_o) {
+  const int64_t per = part_ld / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= m * per) return;
+  const int64_t row = i / per, c = 4 * (i - row * per);
+  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < splits; ++s)
+    y += *reinterpret_cast<const f32x4*>(part + (s * m + row) * part_ld + c);
+  store4<OT>(out, row * ldo + c, y, (int)min((int64_t)4, n - c), vec_o);
+}
+
+constexpr int kCUs = 256;
+
+struct Plan {
+  int tile;       // 0: any alignment, 4: 128 x 128, 8: 256 x 256
+  int splits, per;
+};
+
+// Which kernel and how many splits of k. vec: rows of codes start at multiples
+// of 16 bytes, offsets inside a tile fit 31 bits.
+Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec) {
+  const int steps = (k + kStep - 1) / kStep;
+  if (!vec || steps == 0) return {0, 1, steps};
+  auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
+  if (tiles(256) >= kCUs) return {8, 1, steps};
+  const int64_t t = tiles(128);
+  int64_t s = t > 0 ? kCUs / t : 1;
+  s = s < 1 ? 1 : s > 16 ? 16 : s;
+  const int64_t most = steps / 4 < 1 ? 1 : steps / 4;  // at least four k-steps each
+  if (s > most) s = most;
+  const int per = (int)((steps + s - 1) / s);
+  return {4, (int)((steps + per - 1) / (per < 1 ? 1 : per)), per};
+}
+
+int64_t part_pitch(int64_t n) { return (n + 3) / 4 * 4; }
+
+template <int MI, int NI, int OT>
+hipError_t product_tiles(const BlockProduct& p, const Plan& plan, bool vec_o, hipStream_t st) {
+  constexpr int BM = 32 * MI, BN = 32 * NI;
+  const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
+  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+  TileMap t{(unsigned)tm, (unsigned)tn, plan.per, static_cast<float*>(p.work), part_pitch(p.n)};
+  const dim3 grid((unsigned)(tm * tn), (unsigned)plan.splits);
+  if (plan.splits == 1) {
+    product_tile_kernel<MI, NI, OT, false><<<grid, 256, 0, st>>>(p, t, vec_o);
+    return hipGetLastError();
+  }
+  product_tile_kernel<MI, NI, OT, true><<<grid, 256, 0, st>>>(p, t, vec_o);
+  const int64_t threads = p.m * (t.part_ld / 4);
+  join_kernel<OT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
+      t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo, vec_o);
+  return hipGetLastError();
+}
+
 template <int OT>
 hipError_t product_t(const BlockProduct& p, hipStream_t st) {
   const bool vec_a = (uintptr_t)p.A % 16 == 0 && p.lda % 16 == 0;
   const bool vec_b = (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0;
   const bool vec_o = (uintptr_t)p.out % (OT == 0 ? 16 : 8) == 0 && p.ldo % 4 == 0;
+  const bool vec = vec_a && vec_b && p.lda < (1 << 22) && p.ldb < (1 << 22);
+  const Plan plan = plan_of(p.m, p.n, p.k, vec);
+  if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, vec_o, st);
+  if (plan.tile == 4) return product_tiles<4, 4, OT>(p, plan, vec_o, st);
   const int64_t tm = (p.m + kAT - 1) / kAT, tn = (p.n + kAT - 1) / kAT;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, vec_a, vec_b, vec_o, (unsigned)tn);
@@ -269,6 +488,11 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
 }
 
 }  // namespace
+
+size_t block_product_work(int64_t m, int64_t n, int32_t k) {
+  const Plan plan = plan_of(m, n, k, true);
+  return plan.splits > 1 ? (size_t)plan.splits * m * part_pitch(n) * sizeof(float) : 0;
+}
 
 hipError_t launch_block_product(const BlockProduct& p, hipStream_t st) {
   if (p.m <= 0 || p.n <= 0) return hipSuccess;

@@ -296,7 +296,8 @@ hipError_t launch_decode_rows(const DecodeRows& a, hipStream_t st);
 
 // out[m][n] = sum_k A[m][k] B[n][k] over E4M3 codes with scales per row and
 // 128 values of k (B: per 128 x 128 tile with b_tiles), fp32 sums, rounded
-// once to ot (block_matmul.hip).
+// once to ot (block_matmul.hip). work: block_product_work() bytes, 16-byte
+// aligned (NULL where that is 0).
 struct BlockProduct {
   const uint8_t* A;
   int64_t lda;
@@ -312,7 +313,9 @@ struct BlockProduct {
   int ot;
   void* out;
   int64_t ldo;
+  void* work;
 };
+size_t block_product_work(int64_t m, int64_t n, int32_t k);
 hipError_t launch_block_product(const BlockProduct& p, hipStream_t st);
 
 }  // namespace emk

@@ -66,7 +66,7 @@ def test_encode_refuses(L, change, code, word):
 
 def _matmul(L, **kw):
     a = dict(A=FAKE, lda=256, As=FAKE, ldas=2, B=FAKE, ldb=256, Bs=FAKE, ldbs=2, tiles=0,
-             m=4, n=5, k=200, out=FAKE, ot=0, ldo=5)
+             m=4, n=5, k=200, out=FAKE, ot=0, ldo=5, work=None)
     a.update(kw)
     return L.emeans_block_matmul(*a.values(), None)
 
@@ -76,6 +76,7 @@ def _matmul(L, **kw):
     (dict(ot=3), -2, b"out_dtype"), (dict(lda=199), -1, b"lda"), (dict(ldas=1), -1, b"ldas"),
     (dict(ldb=10), -1, b"ldb"), (dict(ldbs=0), -1, b"ldbs"), (dict(ldo=4), -1, b"ldo"),
     (dict(A=None), -1, b"NULL"), (dict(Bs=None), -1, b"NULL"), (dict(out=None), -1, b"NULL"),
+    (dict(work=8), -1, b"aligned"),
 ])
 def test_matmul_refuses(L, change, code, word):
     assert _matmul(L, **change) == code
@@ -102,9 +103,14 @@ def test_linear_refuses(L, change, code, word):
     assert word in L.emeans_last_error()
 
 
-def test_linear_work(L):
-    assert L.emeans_block_linear_work(3, 200) == 3 * (208 + 4)
-    assert L.emeans_block_linear_work(0, 200) == 0 and L.emeans_block_linear_work(3, 0) == 0
+def test_work_sizes(L):
+    """Codes and scales of X come on top of the product's own working memory."""
+    for m, n, k in ((300, 200, 200), (100, 100, 8192), (40, 256, 1000)):
+        own = L.emeans_block_matmul_work(m, n, k)
+        assert own % 16 == 0 and own >= 0
+        assert L.emeans_block_linear_work(m, n, k) == own + m * (-(-k // 16) * 16
+                                                                + -(-(-(-k // 128)) // 4) * 4)
+    assert L.emeans_block_linear_work(0, 5, 200) == 0 and L.emeans_block_matmul_work(3, 5, 0) == 0
 
 
 def _write(L, **kw):
