@@ -1314,6 +1314,7 @@ int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k) {
 // bytes apart, then their scales with rows a multiple of 4 bytes apart.
 int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k) {
   if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1) return 0;
+  if (block_product_encodes(m, k)) return 0;
   return emeans_block_matmul_work(m, n, k) +
          m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
 }
@@ -1367,6 +1368,11 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
   hipStream_t st = static_cast<hipStream_t>(stream);
   BlockProduct p{nullptr, blocks_of(k, 16) * 16, nullptr, blocks_of(blocks_of(k, 128), 4) * 4,
                  B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo, work};
+  if (block_product_encodes(m, k)) {
+    p.A = static_cast<const uint8_t*>(X);
+    p.lda = ldx;
+    return launched(launch_encode_product(dtype, p, st), "block linear");
+  }
   void* own = nullptr;
   rc = EMEANS_OK;
   if (k > 0) {

@@ -23,19 +23,15 @@
 // The first operand is B's rows (n), the second A's (m): the result then has
 // n = 4 (l / 16) + v, v < 4, and m = l % 16 in lane l, four consecutive
 // values of an output row.
+#include "block.hpp"
 #include "kernels.hpp"
 
 namespace emk {
 
 namespace {
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStep = 128;  // codes of k per MFMA, and per scale
 
@@ -55,8 +51,6 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p, int cnt, bool vec) {
     if (i < cnt) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
   return w;
 }
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // One lane's 32 codes of a k-step as an MFMA operand, with its scale byte: as
 // they are for the FP8 unit, decoded for the bf16 unit.
@@ -147,14 +141,6 @@ __device__ __forceinline__ bool any_rest(const Operand<false> (&o)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) r |= o[i].rest;
   return __any(r != 0);
-}
-
-template <int OT>  // 1 bf16, 4 fp16
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (OT == 1)
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-  else
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
 }
 
 // Four consecutive values of an output row, of which the first cnt exist;
@@ -429,10 +415,145 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   store4<OT>(out, row * ldo + c, y, (int)min((int64_t)4, n - c), vec_o);
 }
 
+// ---------------------------------------------------------------------------
+// Up to 16 rows of A (a few tokens): bound by reading B once. A workgroup of
+// eight waves takes 16 * 8 / wk rows of B; wk waves share their k-steps and
+// add their sums through LDS in order. Fragments of B go straight from memory
+// to registers, kAhead k-steps at a time.
+//
+// XT >= 0: A is given as numbers (that dt) and encoded by every workgroup into
+// LDS while its first codes of B are on their way; block rows of m * k bytes
+// are small beside B, and it saves a launch.
+// ---------------------------------------------------------------------------
+constexpr int kFew = 16;
+constexpr int kFewWaves = 8;
+constexpr int kAhead = 4;
+
+template <int OT, int XT>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduct p, int wk_log,
+                                                                     bool vec_a, bool vec_b,
+                                                                     bool vec_o) {
+  constexpr bool F8 = OT != 0;
+  constexpr bool kEncode = XT >= 0;
+  __shared__ f32x4 part[kFewWaves][64];
+  extern __shared__ __attribute__((aligned(16))) uint8_t room[];  // m x kb * 128 codes, m x kb scales
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wk = 1 << wk_log, kw = wave & (wk - 1);
+  const int col = lane & 15, grp = lane >> 4;
+  const int m = (int)p.m;
+  const int steps = (p.k + kStep - 1) / kStep;
+  const int64_t nb = ((int64_t)blockIdx.x * (kFewWaves >> wk_log) + (wave >> wk_log)) * 16;
+  const int64_t bn = min(nb + col, p.n - 1);
+  const uint8_t* bp = p.B + bn * p.ldb + 16 * grp;
+  const uint8_t* bs = p.Bs + (p.b_tiles ? bn / kStep : bn) * p.ldbs;
+  const int am = min(col, m - 1);
+  const uint8_t* ap = p.A + am * p.lda + 16 * grp;
+  const uint8_t* as = p.As + am * p.ldas;
+
+  u32x4 lo[kAhead], hi[kAhead];
+  uint32_t sc[kAhead];
+  auto load_b = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = s + (u << wk_log);
+      if (t < steps) {
+        const int64_t k0 = (int64_t)t * kStep;
+        if (k0 + kStep <= p.k && vec_b) {
+          lo[u] = *reinterpret_cast<const u32x4*>(bp + k0);
+          hi[u] = *reinterpret_cast<const u32x4*>(bp + k0 + 64);
+        } else {
+          const int left = p.k - (int)k0 - 16 * grp;
+          lo[u] = load16(bp + k0, left, vec_b);
+          hi[u] = load16(bp + k0 + 64, left - 64, vec_b);
+        }
+        sc[u] = bs[t];
+      }
+    }
+  };
+  load_b(kw);
+  uint8_t* scales = room + m * steps * kStep;
+  if constexpr (kEncode) {
+    const int sub = threadIdx.x & 15;
+    const int items = m * steps;
+    for (int i = threadIdx.x >> 4; i < items; i += 64 * kFewWaves / 16) {
+      const int r = i / steps, b = i - r * steps;
+      const int c = b * kStep + 8 * sub;
+      const int cnt = min(8, p.k - c);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      if (vec_a && cnt == 8)
+        load8<XT < 0 ? 0 : XT, true>(p.A, r * p.lda + c, 8, v);
+      else if (cnt > 0)
+        load8<XT < 0 ? 0 : XT, false>(p.A, r * p.lda + c, cnt, v);
+      uint32_t a = group_max<16>(amax8(v));
+      const bool odd = a >= kInfBits;
+      if (odd) a = group_max<16>(amax8_finite(v));
+      const uint32_t byte = scale_byte<false>(a);
+      *reinterpret_cast<u32x2*>(room + r * steps * kStep + b * kStep +
+                                16 * ((sub >> 1) ^ (r & 7)) + 8 * (sub & 1)) =
+          codes8<false>(v, inv_scale(byte), odd);
+      if (sub == 0) scales[r * steps + b] = (uint8_t)byte;
+    }
+    __syncthreads();
+  }
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = kw; s < steps; s += kAhead << wk_log) {
+    if (s != kw) load_b(s);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int t = s + (u << wk_log);
+      if (t >= steps) break;
+      Operand<F8> a[1], b[1];
+      if constexpr (kEncode) {
+        const uint8_t* q = room + (am * steps + t) * kStep;
+        const int x = 16 * (grp ^ (am & 7));
+        a[0].set(*reinterpret_cast<const u32x4*>(q + x), *reinterpret_cast<const u32x4*>(q + (x ^ 64)),
+                 scales[am * steps + t]);
+      } else {
+        const int64_t k0 = (int64_t)t * kStep;
+        const int left = p.k - (int)k0 - 16 * grp;
+        a[0].set(load16(ap + k0, left, vec_a), load16(ap + k0 + 64, left - 64, vec_a), as[t]);
+      }
+      b[0].set(lo[u], hi[u], sc[u]);
+      acc = add_step(b[0], a[0], acc, any_rest(a) || any_rest(b));
+    }
+  }
+  const int64_t n = nb + 4 * grp;
+  if (wk > 1) {
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (kw) return;
+    for (int w = 1; w < wk; ++w) acc += part[wave + w][lane];
+  }
+  if (col < m) store4<OT>(p.out, col * p.ldo + n, acc, (int)min((int64_t)4, p.n - n), vec_o);
+}
+
+constexpr size_t kFewRoom = 48 << 10;  // LDS for the codes made in product_few_kernel
+
+size_t few_room(int64_t m, int32_t k) {
+  const int64_t steps = (k + kStep - 1) / kStep;
+  return (size_t)(m * steps * (kStep + 1));
+}
+
+template <int OT, int XT>
+hipError_t product_few(const BlockProduct& p, bool vec_a, bool vec_b, bool vec_o, hipStream_t st) {
+  const int steps = (p.k + kStep - 1) / kStep;
+  int wk_log = 0;
+  while (wk_log < 3 && (2 << wk_log) <= steps) ++wk_log;
+  const int64_t per = 16 * (kFewWaves >> wk_log);
+  const int64_t wgs = (p.n + per - 1) / per;
+  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  product_few_kernel<OT, XT><<<(unsigned)wgs, 64 * kFewWaves, XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(
+      p, wk_log, vec_a, vec_b, vec_o);
+  return hipGetLastError();
+}
+
 constexpr int kCUs = 256;
 
 struct Plan {
-  int tile;       // 0: any alignment, 4: 128 x 128, 8: 256 x 256
+  int tile;       // 0: any alignment, 1: few rows, 4: 128 x 128, 8: 256 x 256
   int splits, per;
 };
 
@@ -440,7 +561,9 @@ struct Plan {
 // of 16 bytes, offsets inside a tile fit 31 bits.
 Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec) {
   const int steps = (k + kStep - 1) / kStep;
-  if (!vec || steps == 0) return {0, 1, steps};
+  if (steps == 0) return {0, 1, steps};
+  if (m <= kFew) return {1, 1, steps};
+  if (!vec) return {0, 1, steps};
   auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
   if (tiles(256) >= kCUs) return {8, 1, steps};
   const int64_t t = tiles(128);
@@ -479,15 +602,48 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
   const bool vec_o = (uintptr_t)p.out % (OT == 0 ? 16 : 8) == 0 && p.ldo % 4 == 0;
   const bool vec = vec_a && vec_b && p.lda < (1 << 22) && p.ldb < (1 << 22);
   const Plan plan = plan_of(p.m, p.n, p.k, vec);
-  if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, vec_o, st);
-  if (plan.tile == 4) return product_tiles<4, 4, OT>(p, plan, vec_o, st);
+  if (plan.tile == 1) return product_few<OT, -1>(p, vec_a, vec_b, vec_o, st);
+  if constexpr (OT != 0)  // decoded operands do not fit beside 256 accumulators
+    if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, vec_o, st);
+  if (plan.tile >= 4) return product_tiles<4, 4, OT>(p, plan, vec_o, st);
   const int64_t tm = (p.m + kAT - 1) / kAT, tn = (p.n + kAT - 1) / kAT;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, vec_a, vec_b, vec_o, (unsigned)tn);
   return hipGetLastError();
 }
 
+// A's rows as numbers of type XT, encoded inside the product.
+template <int OT, int XT>
+hipError_t encoded_t(const BlockProduct& p, hipStream_t st) {
+  const bool vec_a = (uintptr_t)p.A % 16 == 0 && p.lda % (XT == 0 ? 4 : 8) == 0;
+  const bool vec_b = (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0;
+  const bool vec_o = (uintptr_t)p.out % (OT == 0 ? 16 : 8) == 0 && p.ldo % 4 == 0;
+  return product_few<OT, XT>(p, vec_a, vec_b, vec_o, st);
+}
+
 }  // namespace
+
+bool block_product_encodes(int64_t m, int32_t k) {
+  return m <= kFew && k > 0 && few_room(m, k) <= kFewRoom;
+}
+
+hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) {
+  if (p.m <= 0 || p.n <= 0) return hipSuccess;
+#define EMK_XT(OT)                                \
+  switch (dt) {                                   \
+    case 0: return encoded_t<OT, 0>(p, st);       \
+    case 1: return encoded_t<OT, 1>(p, st);       \
+    case 4: return encoded_t<OT, 4>(p, st);       \
+  }                                               \
+  break
+  switch (p.ot) {
+    case 0: EMK_XT(0);
+    case 1: EMK_XT(1);
+    case 4: EMK_XT(4);
+  }
+#undef EMK_XT
+  return hipErrorInvalidValue;
+}
 
 size_t block_product_work(int64_t m, int64_t n, int32_t k) {
   const Plan plan = plan_of(m, n, k, true);

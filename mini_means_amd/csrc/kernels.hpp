@@ -318,4 +318,10 @@ struct BlockProduct {
 size_t block_product_work(int64_t m, int64_t n, int32_t k);
 hipError_t launch_block_product(const BlockProduct& p, hipStream_t st);
 
+// The same with A as numbers of type dt (p.A, lda elements apart; As unused),
+// encoded along their rows inside the product's launch: for the few rows that
+// block_product_encodes() takes.
+bool block_product_encodes(int64_t m, int32_t k);
+hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st);
+
 }  // namespace emk
