@@ -320,66 +320,115 @@ __device__ __forceinline__ int64_t source_row(const RowsFrom& f, int64_t row, in
   }
 }
 
-// E values per lane: 4 (fp32 out) or 8 (16-bit out); VEC: every lane's codes
-// and outputs are whole and aligned (d a multiple of E, no block border
-// inside a lane: the host checks it). Rows outside the store are zero.
+// A workgroup takes R rows: their places are found first, one thread per row
+// (a page table costs a chain of dependent reads, paid once per R rows), then
+// the threads go over the rows' pieces of E values, E = 4 (fp32 out) or 8
+// (16-bit out). VEC: pieces are whole and aligned (d a multiple of E, no block
+// border inside a piece). Rows outside the store are zeros. The quotients by
+// the pieces per row and by the block are products by `inv` = 2^32 / divisor,
+// rounded up (exact while dividend x divisor < 2^32, which the host checks).
+constexpr int kReadRows = 64;  // R at most
+
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t div, uint32_t inv) {
+  return inv ? __umulhi(a, inv) : a / div;
+}
+
+struct Divisors {
+  uint32_t per, per_inv, block, block_inv;
+};
+
 template <int OT, bool I8, bool VEC, bool PAGES>
 __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
-                                                          int64_t cap, int d, int block, int nb,
-                                                          RowsFrom from, int64_t n,
-                                                          void* __restrict__ out, int64_t ldo) {
+                                                          int64_t cap, int d, int nb,
+                                                          RowsFrom from, int64_t n, int R,
+                                                          Divisors dv, void* __restrict__ out,
+                                                          int64_t ldo) {
   constexpr int E = OT == 0 ? 4 : 8;
-  const int per = (d + E - 1) / E;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = i / per;
-  if (row >= n) return;
-  const int c = (int)(i - row * per) * E;
-  const int64_t src = source_row<PAGES>(from, row, cap);
-  float y[E];
-  const int cnt = min(E, d - c);
-  if (src < 0) {
+  constexpr int U = VEC ? 4 : 1;  // pieces in flight per thread
+  __shared__ int64_t place[kReadRows];
+  const int64_t row0 = (int64_t)blockIdx.x * R;
+  const int rows = (int)min((int64_t)R, n - row0);
+  if ((int)threadIdx.x < rows)
+    place[threadIdx.x] = source_row<PAGES>(from, row0 + threadIdx.x, cap);
+  __syncthreads();
+  const uint32_t items = (uint32_t)rows * dv.per;
+  for (uint32_t i0 = threadIdx.x; i0 < items; i0 += 256 * U) {
+    u32x2 w[U];
+    uint32_t sb[U];
+    int r[U], c[U];
+    bool in[U];
 #pragma unroll
-    for (int q = 0; q < E; ++q) y[q] = 0.0f;
-  } else if constexpr (VEC) {
-    const uint8_t* p = codes + src * d + c;
-    const float s = scale_value(scales[src * nb + c / block]);
-#pragma unroll
-    for (int q = 0; q < E; q += 4) {
-      float z[4];
-      values4<I8>(*reinterpret_cast<const uint32_t*>(p + q), s, z);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[q + e] = z[e];
-    }
-  } else {
-#pragma unroll
-    for (int q = 0; q < E; ++q) {
-      y[q] = 0.0f;
-      if (q < cnt) {
-        float z[4];
-        values4<I8>(codes[src * d + c + q], scale_value(scales[src * nb + (c + q) / block]), z);
-        y[q] = z[0];
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + 256 * u;
+      w[u] = u32x2{0u, 0u};
+      sb[u] = 0;
+      in[u] = false;
+      if (i < items) {
+        r[u] = (int)quotient(i, dv.per, dv.per_inv);
+        c[u] = (int)(i - r[u] * dv.per) * E;
+        const int64_t src = place[r[u]];
+        in[u] = src >= 0;
+        if (VEC && in[u]) {
+          const uint8_t* p = codes + src * d + c[u];
+          w[u][0] = *reinterpret_cast<const uint32_t*>(p);
+          if constexpr (E == 8) w[u][1] = *reinterpret_cast<const uint32_t*>(p + 4);
+          sb[u] = scales[src * nb + quotient(c[u], dv.block, dv.block_inv)];
+        }
       }
     }
-  }
-  if constexpr (OT == 0) {
-    float* o = static_cast<float*>(out) + row * ldo + c;
-    if constexpr (VEC) {
-      *reinterpret_cast<f32x4*>(o) = f32x4{y[0], y[1], y[2], y[3]};
-    } else {
 #pragma unroll
-      for (int q = 0; q < E; ++q)
-        if (q < cnt) o[q] = y[q];
-    }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(out) + row * ldo + c;
-    if constexpr (VEC) {
-      *reinterpret_cast<u32x4*>(o) = u32x4{pack2<OT>(y[0], y[1]), pack2<OT>(y[2], y[3]),
-                                           pack2<OT>(y[4], y[5]), pack2<OT>(y[6], y[7])};
-    } else {
+    for (int u = 0; u < U; ++u) {
+      if (i0 + 256 * u >= items) break;
+      float y[8];
 #pragma unroll
-      for (int q = 0; q < E; ++q)
-        if (q < cnt) o[q] = (uint16_t)pack2<OT>(y[q], 0.0f);
+      for (int q = 0; q < 8; ++q) y[q] = 0.0f;
+      const int cnt = min(E, d - c[u]);
+      if constexpr (VEC) {
+        if (in[u]) {
+          const float s = scale_value(sb[u]);
+          float z[4];
+#pragma unroll
+          for (int q = 0; q < E; q += 4) {
+            values4<I8>(w[u][q >> 2], s, z);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[q + e] = z[e];
+          }
+        }
+      } else if (in[u]) {
+        const int64_t src = place[r[u]];
+#pragma unroll
+        for (int q = 0; q < E; ++q)
+          if (q < cnt) {
+            float z[4];
+            values4<I8>(codes[src * d + c[u] + q],
+                        scale_value(scales[src * nb + quotient(c[u] + q, dv.block, dv.block_inv)]),
+                        z);
+            y[q] = z[0];
+          }
+      }
+      const int64_t at = (row0 + r[u]) * ldo + c[u];
+      if constexpr (OT == 0) {
+        float* o = static_cast<float*>(out) + at;
+        if constexpr (VEC) {
+          __builtin_nontemporal_store(f32x4{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4*>(o));
+        } else {
+#pragma unroll
+          for (int q = 0; q < E; ++q)
+            if (q < cnt) o[q] = y[q];
+        }
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(out) + at;
+        if constexpr (VEC) {
+          __builtin_nontemporal_store(u32x4{pack2<OT>(y[0], y[1]), pack2<OT>(y[2], y[3]),
+                                            pack2<OT>(y[4], y[5]), pack2<OT>(y[6], y[7])},
+                                      reinterpret_cast<u32x4*>(o));
+        } else {
+#pragma unroll
+          for (int q = 0; q < E; ++q)
+            if (q < cnt) o[q] = (uint16_t)pack2<OT>(y[q], 0.0f);
+        }
+      }
     }
   }
 }
@@ -458,21 +507,31 @@ hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
   return hipSuccess;
 }
 
+uint32_t inverse(uint64_t div, uint64_t most) {  // 0: divide
+  return div > 1 && most * div < (1ull << 32) ? (uint32_t)((1ull << 32) / div + 1) : 0;
+}
+
 template <int OT, bool I8>
 hipError_t decode_rows_t(const DecodeRows& a, hipStream_t st) {
   constexpr int E = OT == 0 ? 4 : 8;
   const int nb = (a.d + a.block - 1) / a.block;
-  const int64_t threads = a.n * ((a.d + E - 1) / E);
-  const int64_t blocks = (threads + 255) / 256;
+  const uint32_t per = (uint32_t)((a.d + E - 1) / E);
+  // rows per workgroup: about 4096 pieces, fewer where that leaves CUs idle
+  int64_t R = 4096 / per;
+  if (R > a.n / 2048) R = a.n / 2048;
+  R = R < 1 ? 1 : R > kReadRows ? kReadRows : R;
+  const int64_t blocks = (a.n + R - 1) / R;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const Divisors dv{per, inverse(per, (uint64_t)R * per), (uint32_t)a.block,
+                    inverse(a.block, a.d)};
   const bool vec = a.d % E == 0 && (uintptr_t)a.codes % 4 == 0 && (uintptr_t)a.out % 16 == 0 &&
                    a.ldo % E == 0;
   const dim3 grid((unsigned)blocks), wg(256);
   const RowsFrom f{a.slots, a.slot_bytes, a.table, a.table_ld, a.table_pages, a.starts, a.seqs,
                    a.page};
 #define EMK_GO(V, P)                                                                       \
-  decode_rows_kernel<OT, I8, V, P><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d,       \
-                                                        a.block, nb, f, a.n, a.out, a.ldo)
+  decode_rows_kernel<OT, I8, V, P><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, \
+                                                        a.n, (int)R, dv, a.out, a.ldo)
   if (a.slots) {
     if (vec) EMK_GO(true, false);
     else EMK_GO(false, false);
