@@ -14,15 +14,29 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Eight consecutive values as fp32 (dt 0 fp32, 1 bf16, 4 fp16). VEC: p is
-// 16-byte aligned and holds all eight; else only the first `cnt` are read.
-template <int DT, bool VEC>
+// A vector at any address: one load or store instruction, as the hardware takes
+// global accesses of any alignment.
+template <typename V>
+__device__ __forceinline__ V load_any(const void* p) {
+  V v;
+  __builtin_memcpy(&v, p, sizeof v);
+  return v;
+}
+
+template <typename V>
+__device__ __forceinline__ void store_any(void* p, V v) {
+  __builtin_memcpy(p, &v, sizeof v);
+}
+
+// The cnt <= 8 values from base[at] on (dt 0 fp32, 1 bf16, 4 fp16) as fp32,
+// zeros after them.
+template <int DT>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int cnt, float (&v)[8]) {
   if constexpr (DT == 0) {
     const float* p = static_cast<const float*>(base) + at;
-    if constexpr (VEC) {
-      const f32x4 a = *reinterpret_cast<const f32x4*>(p);
-      const f32x4 b = *reinterpret_cast<const f32x4*>(p + 4);
+    if (cnt >= 8) {
+      const f32x4 a = load_any<f32x4>(p);
+      const f32x4 b = load_any<f32x4>(p + 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[i] = a[i];
@@ -34,17 +48,16 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int cnt, flo
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-    uint16_t h[8];
-    if constexpr (VEC) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    u32x4 w = {0u, 0u, 0u, 0u};
+    if (cnt >= 8) {
+      w = load_any<u32x4>(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = i < cnt ? p[i] : (uint16_t)0;
+      for (int i = 0; i < 8; ++i)
+        if (i < cnt) w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = half_to_f32(h[i], DT == 4);
+    for (int i = 0; i < 8; ++i) v[i] = half_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))), DT == 4);
   }
 }
 
@@ -123,11 +136,39 @@ __device__ __forceinline__ u32x2 codes8(const float (&v)[8], float inv, bool odd
                codes4<I8>(v[4], v[5], v[6], v[7], inv, odd)};
 }
 
-// The largest of m over the G consecutive lanes of a group (G a power of two).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t m) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, CTRL, 0xF, 0xF, false);
+}
+
+// max of m over lanes l and l ^ 16, and over l and l ^ 32 (MAX: any maximum).
+template <typename MAX>
+__device__ __forceinline__ uint32_t max_xor16(uint32_t m, MAX mx) {
+  const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return mx(r[0], r[1]);
+}
+
+template <typename MAX>
+__device__ __forceinline__ uint32_t max_xor32(uint32_t m, MAX mx) {
+  const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return mx(r[0], r[1]);
+}
+
+struct MaxU32 {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
+
+// The largest of m over the G consecutive lanes of a group (G a power of two):
+// lane moves within rows of 16 (quad permutations and mirrors), then swaps of
+// rows, all without an LDS round trip.
 template <int G>
 __device__ __forceinline__ uint32_t group_max(uint32_t m) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+  if constexpr (G >= 2) m = max(m, dpp_u32<0xB1>(m));   // lane ^ 1
+  if constexpr (G >= 4) m = max(m, dpp_u32<0x4E>(m));   // lane ^ 2
+  if constexpr (G >= 8) m = max(m, dpp_u32<0x141>(m));  // mirror of 8: the other four
+  if constexpr (G >= 16) m = max(m, dpp_u32<0x140>(m));  // mirror of 16: the other eight
+  if constexpr (G >= 32) m = max_xor16(m, MaxU32());
+  if constexpr (G >= 64) m = max_xor32(m, MaxU32());
   return m;
 }
 

@@ -11,6 +11,8 @@
 //
 // All kernels here move bytes: a few VALU operations per value, bound by HBM
 // at large sizes and by the launch at small ones.
+#include <type_traits>
+
 #include "block.hpp"
 #include "kernels.hpp"
 
@@ -18,10 +20,10 @@ namespace emk {
 
 namespace {
 
-// Store up to eight code bytes; wide when `vec` (8-byte aligned and whole).
-__device__ __forceinline__ void store_codes(uint8_t* p, u32x2 w, int cnt, bool vec) {
-  if (vec && cnt >= 8) {
-    *reinterpret_cast<u32x2*>(p) = w;
+// Store the first cnt <= 8 code bytes of w.
+__device__ __forceinline__ void store_codes(uint8_t* p, u32x2 w, int cnt) {
+  if (cnt >= 8) {
+    store_any(p, w);
     return;
   }
 #pragma unroll
@@ -46,14 +48,14 @@ struct RowsIn {
   int width;
 };
 
-template <int DT, bool I8, int G, bool VEC, int SLOTS>  // SLOTS 0 none, 4 int32, 8 int64
+template <int DT, bool I8, int G, int SLOTS>  // SLOTS 0 none, 4 int32, 8 int64
 __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, int d, int block,
                                                           int nb, const void* __restrict__ slots,
                                                           int64_t cap,
                                                           uint8_t* __restrict__ codes,
                                                           int64_t ldc,
                                                           uint8_t* __restrict__ scales,
-                                                          int64_t lds, bool vec_out) {
+                                                          int64_t lds) {
   const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
   if (item >= n * nb) return;  // whole groups leave together
   const int64_t row = item / nb;
@@ -74,16 +76,13 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, 
   if (cnt > 0) {
     const int h = c0 / in.width;
     const int64_t at = row * in.rs + h * in.hs + (c0 - h * in.width);
-    if (VEC && cnt == 8)
-      load8<DT, true>(in.X, at, 8, v);
-    else
-      load8<DT, false>(in.X, at, cnt, v);
+    load8<DT>(in.X, at, cnt, v);
   }
   uint32_t m = group_max<G>(amax8(v));
   const bool odd = m >= kInfBits;
   if (odd) m = group_max<G>(amax8_finite(v));
   const uint32_t byte = scale_byte<I8>(m);
-  if (cnt > 0) store_codes(codes + to * ldc + c0, codes8<I8>(v, inv_scale(byte), odd), cnt, vec_out);
+  if (cnt > 0) store_codes(codes + to * ldc + c0, codes8<I8>(v, inv_scale(byte), odd), cnt);
   if (sub == 0) scales[to * lds + b] = (uint8_t)byte;
 }
 
@@ -96,16 +95,126 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, 
 // consecutive bytes of the transposed output. TILES: one scale for the tile,
 // and both orders hold the same codes.
 // ---------------------------------------------------------------------------
+// Magnitudes are compared as the bits of the number type (16-bit types two at
+// a time, in packed registers that also hold the values until they are used).
 constexpr int kT = 128;
 constexpr int kTPitch = kT + 8;  // bytes per transposed row in LDS: 8-byte aligned
 
-template <int DT, bool TILES, bool VEC>
-__global__ __launch_bounds__(256) void encode_tile_kernel(
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+struct MaxU16x2 {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+  }
+};
+
+// An 8 x 8 patch of a thread. Keys are magnitude bits: one per word for fp32,
+// two per word for the 16-bit types.
+template <int DT>
+struct Patch {
+  static constexpr int W = DT == 0 ? 8 : 4;  // words of a row
+  static constexpr uint32_t kAbs = DT == 0 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+  static constexpr uint32_t kInf = DT == 0 ? kInfBits : DT == 1 ? 0x7F80u : 0x7C00u;
+  uint32_t w[8][W];
+
+  __device__ __forceinline__ static uint32_t kmax(uint32_t a, uint32_t b) {
+    if constexpr (DT == 0)
+      return max(a, b);
+    else
+      return MaxU16x2()(a, b);
+  }
+  __device__ __forceinline__ static uint32_t finite(uint32_t k) {  // non-finite keys as 0
+    if constexpr (DT == 0) return k < kInf ? k : 0u;
+    const uint32_t lo = k & 0xFFFFu, hi = k >> 16;
+    return (lo < kInf ? lo : 0u) | (hi < kInf ? hi << 16 : 0u);
+  }
+  __device__ __forceinline__ static uint32_t widest(uint32_t k) {  // of a word's keys
+    if constexpr (DT == 0) return k;
+    return max(k & 0xFFFFu, k >> 16);
+  }
+  __device__ __forceinline__ static uint32_t key(uint32_t k, int i) {  // of value i of two
+    if constexpr (DT == 0) return k;
+    return i ? k >> 16 : k & 0xFFFFu;
+  }
+  __device__ __forceinline__ static uint32_t bits(uint32_t key) {  // key as fp32 bits
+    if constexpr (DT == 0) return key;
+    return __float_as_uint(half_to_f32((uint16_t)key, DT == 4));
+  }
+  __device__ __forceinline__ float at(int p, int i) const {
+    if constexpr (DT == 0) return __uint_as_float(w[p][i]);
+    if constexpr (DT == 1)
+      return __uint_as_float(i & 1 ? w[p][i >> 1] & 0xFFFF0000u : w[p][i >> 1] << 16);
+    return f16_to_f32((uint16_t)(w[p][i >> 1] >> (16 * (i & 1))));
+  }
+  // row p from memory: the cnt <= 8 values from base[at0] on, zeros after them
+  __device__ __forceinline__ void load(int p, const void* base, int64_t at0, int cnt) {
+#pragma unroll
+    for (int q = 0; q < W; ++q) w[p][q] = 0u;
+    if (cnt >= 8) {
+      const char* v = static_cast<const char*>(base) + at0 * (DT == 0 ? 4 : 2);
+#pragma unroll
+      for (int h = 0; h < W / 4; ++h) {
+        const u32x4 x = load_any<u32x4>(v + 16 * h);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[p][4 * h + q] = x[q];
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < cnt) {
+        if constexpr (DT == 0)
+          w[p][i] = static_cast<const uint32_t*>(base)[at0 + i];
+        else
+          w[p][i >> 1] |= (uint32_t) static_cast<const uint16_t*>(base)[at0 + i] << (16 * (i & 1));
+      }
+  }
+  // Keeps the compiler from holding unpacked values across this point: 64
+  // registers more, which would spill.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int q = 0; q < W; ++q) asm volatile("" : "+v"(w[p][q]));
+  }
+  template <bool FINITE>
+  __device__ __forceinline__ uint32_t row_key(int p) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < W; ++q) m = kmax(m, FINITE ? finite(w[p][q] & kAbs) : w[p][q] & kAbs);
+    return widest(m);
+  }
+  template <bool FINITE>
+  __device__ __forceinline__ uint32_t col_key(int q) const {  // of word q's column(s)
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) m = kmax(m, FINITE ? finite(w[p][q] & kAbs) : w[p][q] & kAbs);
+    return m;
+  }
+  __device__ __forceinline__ u32x2 row_codes(int p, float inv, bool odd) const {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = at(p, i);
+    return codes8<false>(y, inv, odd);
+  }
+  __device__ __forceinline__ u32x2 col_codes(int i, float inv, bool odd) const {
+    float y[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) y[p] = at(p, i);
+    return codes8<false>(y, inv, odd);
+  }
+};
+
+template <int DT, bool TILES>
+__global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
     const void* __restrict__ X, int64_t ldx, int64_t n, int d, uint8_t* __restrict__ codes,
     int64_t ldc, uint8_t* __restrict__ scales, int64_t lds, uint8_t* __restrict__ codes_t,
-    int64_t ldct, uint8_t* __restrict__ scales_t, int64_t ldst, bool vec_out, bool vec_t) {
+    int64_t ldct, uint8_t* __restrict__ scales_t, int64_t ldst) {
+  using P = Patch<DT>;
+  constexpr int CW = P::W * 16;  // key words of a tile's columns
   __shared__ __attribute__((aligned(16))) uint8_t tr[kT * kTPitch];
-  __shared__ uint32_t cmax[4][kT];
+  __shared__ uint32_t kmax[4][CW];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int rg = t >> 4, cg = t & 15;
   const int64_t r0 = (int64_t)blockIdx.y * kT;
@@ -113,133 +222,98 @@ __global__ __launch_bounds__(256) void encode_tile_kernel(
   const int rows = (int)min((int64_t)kT, n - r0), cols = min(kT, d - c0);
   const int ccnt = min(8, cols - 8 * cg);  // columns of this thread (may be <= 0)
 
-  float v[8][8];
+  P x;
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
     const int r = 8 * rg + p;
-    if (r < rows && ccnt > 0) {
-      const int64_t at = (r0 + r) * ldx + c0 + 8 * cg;
-      if (VEC && ccnt == 8)
-        load8<DT, true>(X, at, 8, v[p]);
-      else
-        load8<DT, false>(X, at, ccnt, v[p]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-    }
+    x.load(p, X, (r0 + min(r, rows - 1)) * ldx + c0 + 8 * cg, r < rows ? ccnt : 0);
   }
 
   if constexpr (TILES) {
     uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) m = max(m, amax8(v[p]));
+    for (int p = 0; p < 8; ++p) m = max(m, x.template row_key<false>(p));
     m = group_max<64>(m);
-    if (lane == 0) cmax[0][wave] = m;
+    if (lane == 0) kmax[0][wave] = m;
     __syncthreads();
-    m = max(max(cmax[0][0], cmax[0][1]), max(cmax[0][2], cmax[0][3]));
-    const bool odd = m >= kInfBits;
+    m = max(max(kmax[0][0], kmax[0][1]), max(kmax[0][2], kmax[0][3]));
+    const bool odd = m >= P::kInf;
     if (odd) {  // the same answer in every thread of the workgroup
       m = 0;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) m = max(m, amax8_finite(v[p]));
+      for (int p = 0; p < 8; ++p) m = max(m, x.template row_key<true>(p));
       m = group_max<64>(m);
-      if (lane == 0) cmax[1][wave] = m;
+      if (lane == 0) kmax[1][wave] = m;
       __syncthreads();
-      m = max(max(cmax[1][0], cmax[1][1]), max(cmax[1][2], cmax[1][3]));
+      m = max(max(kmax[1][0], kmax[1][1]), max(kmax[1][2], kmax[1][3]));
     }
-    const uint32_t byte = scale_byte<false>(m);
+    const uint32_t byte = scale_byte<false>(P::bits(m));
     const float inv = inv_scale(byte);
-    uint32_t w[8][2];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const u32x2 q = codes8<false>(v[p], inv, odd);
-      w[p][0] = q[0];
-      w[p][1] = q[1];
-      if (codes && 8 * rg + p < rows && ccnt > 0)
-        store_codes(codes + (r0 + 8 * rg + p) * ldc + c0 + 8 * cg, q, ccnt, vec_out);
-    }
     if (t == 0) {
       if (codes) scales[(int64_t)blockIdx.y * lds + blockIdx.x] = (uint8_t)byte;
       if (codes_t) scales_t[(int64_t)blockIdx.x * ldst + blockIdx.y] = (uint8_t)byte;
     }
-    if (!codes_t) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      u32x2 q = {0u, 0u};
+    if (codes) {
 #pragma unroll
       for (int p = 0; p < 8; ++p)
-        q[p >> 2] |= ((w[p][i >> 2] >> (8 * (i & 3))) & 0xFFu) << (8 * (p & 3));
-      *reinterpret_cast<u32x2*>(&tr[(8 * cg + i) * kTPitch + 8 * rg]) = q;
+        if (8 * rg + p < rows && ccnt > 0)
+          store_codes(codes + (r0 + 8 * rg + p) * ldc + c0 + 8 * cg, x.row_codes(p, inv, odd), ccnt);
     }
+    if (!codes_t) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<u32x2*>(&tr[(8 * cg + i) * kTPitch + 8 * rg]) = x.col_codes(i, inv, odd);
   } else {
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      if (!codes) break;
-      uint32_t m = group_max<16>(amax8(v[p]));
-      const bool odd = m >= kInfBits;
-      if (odd) m = group_max<16>(amax8_finite(v[p]));
-      const uint32_t byte = scale_byte<false>(m);
-      const int r = 8 * rg + p;
-      if (r < rows) {
-        if (ccnt > 0)
-          store_codes(codes + (r0 + r) * ldc + c0 + 8 * cg,
-                      codes8<false>(v[p], inv_scale(byte), odd), ccnt, vec_out);
-        if (cg == 0) scales[(r0 + r) * lds + blockIdx.x] = (uint8_t)byte;
-      }
-    }
     // columns: the thread's rows, the four row groups of the wave, the waves.
-    // Column maxima in LDS carry the non-finite mark; a column that has one
-    // takes its finite maximum in a second round.
+    // A column that holds a non-finite value takes its finite maximum in a
+    // second round.
+    uint32_t ck[P::W];
+    auto columns = [&](auto fin) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int p = 0; p < 8; ++p) m = max(m, abs_bits(v[p][i]));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      if (lane < 16) cmax[wave][8 * cg + i] = m;
-    }
-    __syncthreads();
-    uint32_t cm[8];
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = 8 * cg + i;
-      cm[i] = max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c]));
-      any |= cm[i] >= kInfBits;
-    }
-    uint32_t fm[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) fm[i] = cm[i];
-    if (__syncthreads_or(any)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const uint32_t b = abs_bits(v[p][i]);
-          m = max(m, b < kInfBits ? b : 0u);
-        }
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-        if (lane < 16) cmax[wave][8 * cg + i] = m;
+      for (int q = 0; q < P::W; ++q) {
+        uint32_t m = x.template col_key<decltype(fin)::value>(q);
+        auto mx = [](uint32_t a, uint32_t b) { return P::kmax(a, b); };
+        m = max_xor32(max_xor16(m, mx), mx);
+        if (lane < 16) kmax[wave][P::W * cg + q] = m;
       }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = 8 * cg + i;
-        fm[i] = max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c]));
+      for (int q = 0; q < P::W; ++q) {
+        const int c = P::W * cg + q;
+        ck[q] = P::kmax(P::kmax(kmax[0][c], kmax[1][c]), P::kmax(kmax[2][c], kmax[3][c]));
       }
-    }
+    };
+    columns(std::false_type());
+    bool odd = false;
+#pragma unroll
+    for (int q = 0; q < P::W; ++q) odd |= P::widest(ck[q]) >= P::kInf;
+    odd = __syncthreads_or(odd);
+    if (odd) columns(std::true_type());
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t byte = scale_byte<false>(fm[i]);
-      float y[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) y[p] = v[p][i];
+      const uint32_t byte = scale_byte<false>(
+          P::bits(DT == 0 ? ck[i] : P::key(ck[DT == 0 ? i : i >> 1], i & 1)));
       *reinterpret_cast<u32x2*>(&tr[(8 * cg + i) * kTPitch + 8 * rg]) =
-          codes8<false>(y, inv_scale(byte), cm[i] >= kInfBits);
-      if (rg == 0 && i < ccnt) scales_t[(int64_t)(c0 + 8 * cg + i) * ldst + blockIdx.y] = (uint8_t)byte;
+          x.col_codes(i, inv_scale(byte), odd);
+      if (rg == 0 && i < ccnt)
+        scales_t[(int64_t)(c0 + 8 * cg + i) * ldst + blockIdx.y] = (uint8_t)byte;
+    }
+    x.forget();
+    if (codes) {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        uint32_t m = group_max<16>(x.template row_key<false>(p));
+        const bool bad = m >= P::kInf;
+        if (bad) m = group_max<16>(x.template row_key<true>(p));
+        const uint32_t byte = scale_byte<false>(P::bits(m));
+        const int r = 8 * rg + p;
+        if (r < rows) {
+          if (ccnt > 0)
+            store_codes(codes + (r0 + r) * ldc + c0 + 8 * cg, x.row_codes(p, inv_scale(byte), bad),
+                        ccnt);
+          if (cg == 0) scales[(r0 + r) * lds + blockIdx.x] = (uint8_t)byte;
+        }
+      }
     }
   }
   __syncthreads();
@@ -253,11 +327,11 @@ __global__ __launch_bounds__(256) void encode_tile_kernel(
     const u32x2 hi = *reinterpret_cast<const u32x2*>(&tr[c * kTPitch + 16 * ch + 8]);
     uint8_t* p = codes_t + (int64_t)(c0 + c) * ldct + r0 + 16 * ch;
     const int cnt = rows - 16 * ch;
-    if (vec_t && cnt >= 16) {
-      *reinterpret_cast<u32x4*>(p) = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    if (cnt >= 16) {
+      store_any(p, u32x4{lo[0], lo[1], hi[0], hi[1]});
     } else {
-      store_codes(p, lo, cnt, false);
-      store_codes(p + 8, hi, cnt - 8, false);
+      store_codes(p, lo, cnt);
+      store_codes(p + 8, hi, cnt - 8);
     }
   }
 }
@@ -323,8 +397,8 @@ __device__ __forceinline__ int64_t source_row(const RowsFrom& f, int64_t row, in
 // A workgroup takes R rows: their places are found first, one thread per row
 // (a page table costs a chain of dependent reads, paid once per R rows), then
 // the threads go over the rows' pieces of E values, E = 4 (fp32 out) or 8
-// (16-bit out). VEC: pieces are whole and aligned (d a multiple of E, no block
-// border inside a piece). Rows outside the store are zeros. The quotients by
+// (16-bit out; block borders are at multiples of 16). Only a row's last piece
+// may be short. Rows outside the store are zeros. The quotients by
 // the pieces per row and by the block are products by `inv` = 2^32 / divisor,
 // rounded up (exact while dividend x divisor < 2^32, which the host checks).
 constexpr int kReadRows = 64;  // R at most
@@ -333,11 +407,35 @@ __device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t div, uint32_t 
   return inv ? __umulhi(a, inv) : a / div;
 }
 
+// The first cnt values of a piece of output: read once by whoever comes next,
+// so they are not kept in the caches on their way.
+__device__ __forceinline__ void store_out(float* o, f32x4 v, int cnt) {
+  typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+  if (cnt >= 4) {
+    __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(o));
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    if (q < cnt) o[q] = v[q];
+}
+
+__device__ __forceinline__ void store_out(uint16_t* o, u32x4 v, int cnt) {
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+  if (cnt >= 8) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(o));
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < 7; ++q)
+    if (q < cnt) o[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
+}
+
 struct Divisors {
   uint32_t per, per_inv, block, block_inv;
 };
 
-template <int OT, bool I8, bool VEC, bool PAGES>
+template <int OT, bool I8, bool PAGES>
 __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
                                                           int64_t cap, int d, int nb,
@@ -345,7 +443,7 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restr
                                                           Divisors dv, void* __restrict__ out,
                                                           int64_t ldo) {
   constexpr int E = OT == 0 ? 4 : 8;
-  constexpr int U = VEC ? 4 : 1;  // pieces in flight per thread
+  constexpr int U = 4;  // pieces in flight per thread
   __shared__ int64_t place[kReadRows];
   const int64_t row0 = (int64_t)blockIdx.x * R;
   const int rows = (int)min((int64_t)R, n - row0);
@@ -357,22 +455,28 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restr
     u32x2 w[U];
     uint32_t sb[U];
     int r[U], c[U];
-    bool in[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t i = i0 + 256 * u;
       w[u] = u32x2{0u, 0u};
       sb[u] = 0;
-      in[u] = false;
       if (i < items) {
         r[u] = (int)quotient(i, dv.per, dv.per_inv);
         c[u] = (int)(i - r[u] * dv.per) * E;
         const int64_t src = place[r[u]];
-        in[u] = src >= 0;
-        if (VEC && in[u]) {
+        if (src >= 0) {
           const uint8_t* p = codes + src * d + c[u];
-          w[u][0] = *reinterpret_cast<const uint32_t*>(p);
-          if constexpr (E == 8) w[u][1] = *reinterpret_cast<const uint32_t*>(p + 4);
+          const int cnt = d - c[u];
+          if (cnt >= E) {
+            if constexpr (E == 8)
+              w[u] = load_any<u32x2>(p);
+            else
+              w[u][0] = load_any<uint32_t>(p);
+          } else {
+#pragma unroll
+            for (int q = 0; q < E - 1; ++q)
+              if (q < cnt) w[u][q >> 2] |= (uint32_t)p[q] << (8 * (q & 3));
+          }
           sb[u] = scales[src * nb + quotient(c[u], dv.block, dv.block_inv)];
         }
       }
@@ -380,105 +484,61 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restr
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + 256 * u >= items) break;
-      float y[8];
+      float y[E];
+      const float s = scale_value(sb[u]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = 0.0f;
-      const int cnt = min(E, d - c[u]);
-      if constexpr (VEC) {
-        if (in[u]) {
-          const float s = scale_value(sb[u]);
-          float z[4];
+      for (int q = 0; q < E; q += 4) {
+        float z[4];
+        values4<I8>(w[u][q >> 2], s, z);
 #pragma unroll
-          for (int q = 0; q < E; q += 4) {
-            values4<I8>(w[u][q >> 2], s, z);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[q + e] = z[e];
-          }
-        }
-      } else if (in[u]) {
-        const int64_t src = place[r[u]];
-#pragma unroll
-        for (int q = 0; q < E; ++q)
-          if (q < cnt) {
-            float z[4];
-            values4<I8>(codes[src * d + c[u] + q],
-                        scale_value(scales[src * nb + quotient(c[u] + q, dv.block, dv.block_inv)]),
-                        z);
-            y[q] = z[0];
-          }
+        for (int e = 0; e < 4; ++e) y[q + e] = z[e];
       }
       const int64_t at = (row0 + r[u]) * ldo + c[u];
+      const int cnt = d - c[u];
       if constexpr (OT == 0) {
-        float* o = static_cast<float*>(out) + at;
-        if constexpr (VEC) {
-          __builtin_nontemporal_store(f32x4{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4*>(o));
-        } else {
-#pragma unroll
-          for (int q = 0; q < E; ++q)
-            if (q < cnt) o[q] = y[q];
-        }
+        store_out(static_cast<float*>(out) + at, f32x4{y[0], y[1], y[2], y[3]}, cnt);
       } else {
-        uint16_t* o = static_cast<uint16_t*>(out) + at;
-        if constexpr (VEC) {
-          __builtin_nontemporal_store(u32x4{pack2<OT>(y[0], y[1]), pack2<OT>(y[2], y[3]),
-                                            pack2<OT>(y[4], y[5]), pack2<OT>(y[6], y[7])},
-                                      reinterpret_cast<u32x4*>(o));
-        } else {
-#pragma unroll
-          for (int q = 0; q < E; ++q)
-            if (q < cnt) o[q] = (uint16_t)pack2<OT>(y[q], 0.0f);
-        }
+        store_out(static_cast<uint16_t*>(out) + at,
+                  u32x4{pack2<OT>(y[0], y[1]), pack2<OT>(y[2], y[3]), pack2<OT>(y[4], y[5]),
+                        pack2<OT>(y[6], y[7])}, cnt);
       }
     }
   }
 }
 
 template <int DT, bool I8, int G>
-hipError_t encode_rows_g(const EncodeRows& a, bool vec, bool vec_out, hipStream_t st) {
+hipError_t encode_rows_g(const EncodeRows& a, hipStream_t st) {
   const int nb = (a.d + a.block - 1) / a.block;
   const int64_t groups = a.n * nb;
   const int64_t blocks = (groups * G + 255) / 256;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), wg(256);
   const RowsIn in{a.X, a.rs, a.hs, a.width};
-#define EMK_GO(V, S)                                                                          \
-  encode_rows_kernel<DT, I8, G, V, S><<<grid, wg, 0, st>>>(in, a.n, a.d, a.block, nb, a.slots, \
-                                                           a.cap, a.codes, a.ldc, a.scales,   \
-                                                           a.lds, vec_out)
-  if (!a.slots) {
-    if (vec) EMK_GO(true, 0);
-    else EMK_GO(false, 0);
-  } else if (a.slot_bytes == 8) {
-    if (vec) EMK_GO(true, 8);
-    else EMK_GO(false, 8);
-  } else {
-    if (vec) EMK_GO(true, 4);
-    else EMK_GO(false, 4);
-  }
+#define EMK_GO(S)                                                                          \
+  encode_rows_kernel<DT, I8, G, S><<<grid, wg, 0, st>>>(in, a.n, a.d, a.block, nb, a.slots, \
+                                                        a.cap, a.codes, a.ldc, a.scales, a.lds)
+  if (!a.slots)
+    EMK_GO(0);
+  else if (a.slot_bytes == 8)
+    EMK_GO(8);
+  else
+    EMK_GO(4);
 #undef EMK_GO
   return hipGetLastError();
 }
 
 template <int DT, bool I8>
 hipError_t encode_rows_t(const EncodeRows& a, hipStream_t st) {
-  const int64_t unit = DT == 0 ? 4 : 8;  // elements of 16 bytes
-  const bool vec = (uintptr_t)a.X % 16 == 0 && a.rs % unit == 0 &&
-                   (a.width == a.d || (a.hs % unit == 0 && a.width % 8 == 0));
-  const bool vec_out = (uintptr_t)a.codes % 8 == 0 && a.ldc % 8 == 0;
-  if (a.block <= 16) return encode_rows_g<DT, I8, 2>(a, vec, vec_out, st);
-  if (a.block <= 32) return encode_rows_g<DT, I8, 4>(a, vec, vec_out, st);
-  if (a.block <= 64) return encode_rows_g<DT, I8, 8>(a, vec, vec_out, st);
-  if (a.block <= 128) return encode_rows_g<DT, I8, 16>(a, vec, vec_out, st);
-  return encode_rows_g<DT, I8, 32>(a, vec, vec_out, st);
+  if (a.block <= 16) return encode_rows_g<DT, I8, 2>(a, st);
+  if (a.block <= 32) return encode_rows_g<DT, I8, 4>(a, st);
+  if (a.block <= 64) return encode_rows_g<DT, I8, 8>(a, st);
+  if (a.block <= 128) return encode_rows_g<DT, I8, 16>(a, st);
+  return encode_rows_g<DT, I8, 32>(a, st);
 }
 
 template <int DT>
 hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
   const int64_t gx = (a.d + kT - 1) / kT, gy = (a.n + kT - 1) / kT;
-  const int64_t unit = DT == 0 ? 4 : 8;
-  const bool vec = (uintptr_t)a.X % 16 == 0 && a.ldx % unit == 0;
-  const bool vec_out = (uintptr_t)a.codes % 8 == 0 && a.ldc % 8 == 0;
-  const bool vec_t = (uintptr_t)a.codes_t % 16 == 0 && a.ldct % 16 == 0;
   // rows in launches of at most 65535 tiles (the grid's y limit)
   for (int64_t y0 = 0; y0 < gy; y0 += 65535) {
     const int64_t ny = gy - y0 < 65535 ? gy - y0 : 65535;
@@ -489,18 +549,12 @@ hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
     uint8_t* scales = a.scales ? a.scales + (a.tiles ? y0 : r) * a.lds : nullptr;
     uint8_t* ct = a.codes_t ? a.codes_t + r : nullptr;
     uint8_t* stt = a.scales_t ? a.scales_t + y0 : nullptr;
-#define EMK_GO(T, V)                                                                         \
-  encode_tile_kernel<DT, T, V><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, a.d, codes, a.ldc,     \
-                                                    scales, a.lds, ct, a.ldct, stt, a.ldst,  \
-                                                    vec_out, vec_t)
-    if (a.tiles) {
-      if (vec) EMK_GO(true, true);
-      else EMK_GO(true, false);
-    } else {
-      if (vec) EMK_GO(false, true);
-      else EMK_GO(false, false);
-    }
-#undef EMK_GO
+    if (a.tiles)
+      encode_tile_kernel<DT, true><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, a.d, codes, a.ldc, scales,
+                                                        a.lds, ct, a.ldct, stt, a.ldst);
+    else
+      encode_tile_kernel<DT, false><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, a.d, codes, a.ldc,
+                                                         scales, a.lds, ct, a.ldct, stt, a.ldst);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -524,22 +578,15 @@ hipError_t decode_rows_t(const DecodeRows& a, hipStream_t st) {
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const Divisors dv{per, inverse(per, (uint64_t)R * per), (uint32_t)a.block,
                     inverse(a.block, a.d)};
-  const bool vec = a.d % E == 0 && (uintptr_t)a.codes % 4 == 0 && (uintptr_t)a.out % 16 == 0 &&
-                   a.ldo % E == 0;
   const dim3 grid((unsigned)blocks), wg(256);
   const RowsFrom f{a.slots, a.slot_bytes, a.table, a.table_ld, a.table_pages, a.starts, a.seqs,
                    a.page};
-#define EMK_GO(V, P)                                                                       \
-  decode_rows_kernel<OT, I8, V, P><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, \
-                                                        a.n, (int)R, dv, a.out, a.ldo)
-  if (a.slots) {
-    if (vec) EMK_GO(true, false);
-    else EMK_GO(false, false);
-  } else {
-    if (vec) EMK_GO(true, true);
-    else EMK_GO(false, true);
-  }
-#undef EMK_GO
+  if (a.slots)
+    decode_rows_kernel<OT, I8, false><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, a.n,
+                                                           (int)R, dv, a.out, a.ldo);
+  else
+    decode_rows_kernel<OT, I8, true><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, a.n,
+                                                          (int)R, dv, a.out, a.ldo);
   return hipGetLastError();
 }
 

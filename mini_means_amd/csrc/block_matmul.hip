@@ -40,14 +40,12 @@ __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
-// 16 codes at p, of which the first cnt exist (the rest read as zeros);
-// wide when vec (p 16-byte aligned) and whole.
-__device__ __forceinline__ u32x4 load16(const uint8_t* p, int cnt, bool vec) {
-  if (vec && cnt >= 16) return *reinterpret_cast<const u32x4*>(p);
+// 16 codes at p (any address), of which the first cnt exist; the rest are zeros.
+__device__ __forceinline__ u32x4 load16(const uint8_t* p, int cnt) {
+  if (cnt >= 16) return load_any<u32x4>(p);
   u32x4 w = {0u, 0u, 0u, 0u};
-  if (cnt <= 0) return w;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < 15; ++i)
     if (i < cnt) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
   return w;
 }
@@ -143,28 +141,27 @@ __device__ __forceinline__ bool any_rest(const Operand<false> (&o)[N]) {
   return __any(r != 0);
 }
 
-// Four consecutive values of an output row, of which the first cnt exist;
-// wide when vec (the row's values are aligned to four) and whole.
+// The first cnt of four consecutive values of an output row.
 template <int OT>
-__device__ __forceinline__ void store4(void* out, int64_t at, f32x4 y, int cnt, bool vec) {
+__device__ __forceinline__ void store4(void* out, int64_t at, f32x4 y, int cnt) {
   if constexpr (OT == 0) {
     float* o = static_cast<float*>(out) + at;
-    if (vec && cnt >= 4) {
-      *reinterpret_cast<f32x4*>(o) = y;
+    if (cnt >= 4) {
+      store_any(o, y);
       return;
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < 3; ++v)
       if (v < cnt) o[v] = y[v];
   } else {
     uint16_t* o = static_cast<uint16_t*>(out) + at;
     const u32x2 w = {pack2<OT>(y[0], y[1]), pack2<OT>(y[2], y[3])};
-    if (vec && cnt >= 4) {
-      *reinterpret_cast<u32x2*>(o) = w;
+    if (cnt >= 4) {
+      store_any(o, w);
       return;
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int v = 0; v < 3; ++v)
       if (v < cnt) o[v] = (uint16_t)(w[v >> 1] >> (16 * (v & 1)));
   }
 }
@@ -178,8 +175,7 @@ __device__ __forceinline__ void store4(void* out, int64_t at, f32x4 y, int cnt, 
 constexpr int kAT = 64;
 
 template <int OT>
-__global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, bool vec_a, bool vec_b,
-                                                          bool vec_o, unsigned tiles_n) {
+__global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsigned tiles_n) {
   __shared__ __attribute__((aligned(16))) uint8_t la[kAT * kStep], lb[kAT * kStep];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -206,10 +202,10 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, bool v
   const int steps = (p.k + kStep - 1) / kStep;
   for (int s = 0; s < steps; ++s) {
     const int left = p.k - s * kStep - 16 * q;
-    const u32x4 a0 = load16(ap + (int64_t)s * kStep, left, vec_a);
-    const u32x4 a1 = load16(ap + (int64_t)s * kStep + 16, left - 16, vec_a);
-    const u32x4 b0 = load16(bp + (int64_t)s * kStep, left, vec_b);
-    const u32x4 b1 = load16(bp + (int64_t)s * kStep + 16, left - 16, vec_b);
+    const u32x4 a0 = load16(ap + (int64_t)s * kStep, left);
+    const u32x4 a1 = load16(ap + (int64_t)s * kStep + 16, left - 16);
+    const u32x4 b0 = load16(bp + (int64_t)s * kStep, left);
+    const u32x4 b1 = load16(bp + (int64_t)s * kStep + 16, left - 16);
     __syncthreads();
     *reinterpret_cast<u32x4*>(&la[r * kStep + 16 * (q ^ (r & 7))]) = a0;
     *reinterpret_cast<u32x4*>(&la[r * kStep + 16 * ((q + 1) ^ (r & 7))]) = a1;
@@ -238,7 +234,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, bool v
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int64_t n = n0 + wn + 16 * j + 4 * grp;
-      store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n), vec_o);
+      store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
     }
   }
 }
@@ -280,8 +276,7 @@ __device__ __forceinline__ void tile_of(unsigned id, const TileMap& t, unsigned&
 
 template <int MI, int NI, int OT, bool SPLIT>
 __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kernel(BlockProduct p,
-                                                                                 TileMap t,
-                                                                                 bool vec_o) {
+                                                                                 TileMap t) {
   constexpr bool F8 = OT != 0;
   constexpr int BM = 32 * MI, BN = 32 * NI, R = BM + BN;
   constexpr int Q = (R / 64 + 3) / 4;  // scale loads per wave and stage, at most
@@ -336,12 +331,12 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
 #pragma unroll 1
       for (int i = 0; i < MI; ++i) {
         const uint32_t o = (uint32_t)min(8 * (wave * MI + i) + lr, mrows - 1) * (uint32_t)p.lda + lx;
-        *reinterpret_cast<u32x4*>(da + i * 1024 + 16 * lane) = load16(a0 + k0 + o, left, true);
+        *reinterpret_cast<u32x4*>(da + i * 1024 + 16 * lane) = load16(a0 + k0 + o, left);
       }
 #pragma unroll 1
       for (int i = 0; i < NI; ++i) {
         const uint32_t o = (uint32_t)min(8 * (wave * NI + i) + lr, nrows - 1) * (uint32_t)p.ldb + lx;
-        *reinterpret_cast<u32x4*>(db + i * 1024 + 16 * lane) = load16(b0 + k0 + o, left, true);
+        *reinterpret_cast<u32x4*>(db + i * 1024 + 16 * lane) = load16(b0 + k0 + o, left);
       }
     }
 #pragma unroll
@@ -391,9 +386,9 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
       const int64_t n = n0 + (rb - BM) - col + 16 * j + 4 * grp;
       if constexpr (SPLIT) {
         if (n < p.n)
-          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4, true);
+          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4);
       } else {
-        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n), vec_o);
+        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
       }
     }
   }
@@ -403,8 +398,7 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
 template <int OT>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int splits,
                                                    int64_t m, int64_t n, int64_t part_ld,
-                                                   void* __restrict__ out, int64_t ldo,
-                                                   bool vec_o) {
+                                                   void* __restrict__ out, int64_t ldo) {
   const int64_t per = part_ld / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= m * per) return;
@@ -412,7 +406,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = 0; s < splits; ++s)
     y += *reinterpret_cast<const f32x4*>(part + (s * m + row) * part_ld + c);
-  store4<OT>(out, row * ldo + c, y, (int)min((int64_t)4, n - c), vec_o);
+  store4<OT>(out, row * ldo + c, y, (int)min((int64_t)4, n - c));
 }
 
 // ---------------------------------------------------------------------------
@@ -430,9 +424,7 @@ constexpr int kFewWaves = 8;
 constexpr int kAhead = 4;
 
 template <int OT, int XT>
-__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduct p, int wk_log,
-                                                                     bool vec_a, bool vec_b,
-                                                                     bool vec_o) {
+__global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduct p, int wk_log) {
   constexpr bool F8 = OT != 0;
   constexpr bool kEncode = XT >= 0;
   __shared__ f32x4 part[kFewWaves][64];
@@ -459,13 +451,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
       const int t = s + (u << wk_log);
       if (t < steps) {
         const int64_t k0 = (int64_t)t * kStep;
-        if (k0 + kStep <= p.k && vec_b) {
-          lo[u] = *reinterpret_cast<const u32x4*>(bp + k0);
-          hi[u] = *reinterpret_cast<const u32x4*>(bp + k0 + 64);
+        if (k0 + kStep <= p.k) {
+          lo[u] = load_any<u32x4>(bp + k0);
+          hi[u] = load_any<u32x4>(bp + k0 + 64);
         } else {
           const int left = p.k - (int)k0 - 16 * grp;
-          lo[u] = load16(bp + k0, left, vec_b);
-          hi[u] = load16(bp + k0 + 64, left - 64, vec_b);
+          lo[u] = load16(bp + k0, left);
+          hi[u] = load16(bp + k0 + 64, left - 64);
         }
         sc[u] = bs[t];
       }
@@ -483,10 +475,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      if (vec_a && cnt == 8)
-        load8<XT < 0 ? 0 : XT, true>(p.A, r * p.lda + c, 8, v);
-      else if (cnt > 0)
-        load8<XT < 0 ? 0 : XT, false>(p.A, r * p.lda + c, cnt, v);
+      if (cnt > 0) load8<XT < 0 ? 0 : XT>(p.A, r * p.lda + c, cnt, v);
       uint32_t a = group_max<16>(amax8(v));
       const bool odd = a >= kInfBits;
       if (odd) a = group_max<16>(amax8_finite(v));
@@ -514,7 +503,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
       } else {
         const int64_t k0 = (int64_t)t * kStep;
         const int left = p.k - (int)k0 - 16 * grp;
-        a[0].set(load16(ap + k0, left, vec_a), load16(ap + k0 + 64, left - 64, vec_a), as[t]);
+        a[0].set(load16(ap + k0, left), load16(ap + k0 + 64, left - 64), as[t]);
       }
       b[0].set(lo[u], hi[u], sc[u]);
       acc = add_step(b[0], a[0], acc, any_rest(a) || any_rest(b));
@@ -527,7 +516,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
     if (kw) return;
     for (int w = 1; w < wk; ++w) acc += part[wave + w][lane];
   }
-  if (col < m) store4<OT>(p.out, col * p.ldo + n, acc, (int)min((int64_t)4, p.n - n), vec_o);
+  if (col < m) store4<OT>(p.out, col * p.ldo + n, acc, (int)min((int64_t)4, p.n - n));
 }
 
 constexpr size_t kFewRoom = 48 << 10;  // LDS for the codes made in product_few_kernel
@@ -538,7 +527,7 @@ size_t few_room(int64_t m, int32_t k) {
 }
 
 template <int OT, int XT>
-hipError_t product_few(const BlockProduct& p, bool vec_a, bool vec_b, bool vec_o, hipStream_t st) {
+hipError_t product_few(const BlockProduct& p, hipStream_t st) {
   const int steps = (p.k + kStep - 1) / kStep;
   int wk_log = 0;
   while (wk_log < 3 && (2 << wk_log) <= steps) ++wk_log;
@@ -546,7 +535,7 @@ hipError_t product_few(const BlockProduct& p, bool vec_a, bool vec_b, bool vec_o
   const int64_t wgs = (p.n + per - 1) / per;
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   product_few_kernel<OT, XT><<<(unsigned)wgs, 64 * kFewWaves, XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(
-      p, wk_log, vec_a, vec_b, vec_o);
+      p, wk_log);
   return hipGetLastError();
 }
 
@@ -578,47 +567,36 @@ Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec) {
 int64_t part_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 
 template <int MI, int NI, int OT>
-hipError_t product_tiles(const BlockProduct& p, const Plan& plan, bool vec_o, hipStream_t st) {
+hipError_t product_tiles(const BlockProduct& p, const Plan& plan, hipStream_t st) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   TileMap t{(unsigned)tm, (unsigned)tn, plan.per, static_cast<float*>(p.work), part_pitch(p.n)};
   const dim3 grid((unsigned)(tm * tn), (unsigned)plan.splits);
   if (plan.splits == 1) {
-    product_tile_kernel<MI, NI, OT, false><<<grid, 256, 0, st>>>(p, t, vec_o);
+    product_tile_kernel<MI, NI, OT, false><<<grid, 256, 0, st>>>(p, t);
     return hipGetLastError();
   }
-  product_tile_kernel<MI, NI, OT, true><<<grid, 256, 0, st>>>(p, t, vec_o);
+  product_tile_kernel<MI, NI, OT, true><<<grid, 256, 0, st>>>(p, t);
   const int64_t threads = p.m * (t.part_ld / 4);
   join_kernel<OT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
-      t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo, vec_o);
+      t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo);
   return hipGetLastError();
 }
 
 template <int OT>
 hipError_t product_t(const BlockProduct& p, hipStream_t st) {
-  const bool vec_a = (uintptr_t)p.A % 16 == 0 && p.lda % 16 == 0;
-  const bool vec_b = (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0;
-  const bool vec_o = (uintptr_t)p.out % (OT == 0 ? 16 : 8) == 0 && p.ldo % 4 == 0;
-  const bool vec = vec_a && vec_b && p.lda < (1 << 22) && p.ldb < (1 << 22);
+  const bool vec = (uintptr_t)p.A % 16 == 0 && p.lda % 16 == 0 && p.lda < (1 << 22) &&
+                   (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0 && p.ldb < (1 << 22);
   const Plan plan = plan_of(p.m, p.n, p.k, vec);
-  if (plan.tile == 1) return product_few<OT, -1>(p, vec_a, vec_b, vec_o, st);
+  if (plan.tile == 1) return product_few<OT, -1>(p, st);
   if constexpr (OT != 0)  // decoded operands do not fit beside 256 accumulators
-    if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, vec_o, st);
-  if (plan.tile >= 4) return product_tiles<4, 4, OT>(p, plan, vec_o, st);
+    if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, st);
+  if (plan.tile >= 4) return product_tiles<4, 4, OT>(p, plan, st);
   const int64_t tm = (p.m + kAT - 1) / kAT, tn = (p.n + kAT - 1) / kAT;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
-  product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, vec_a, vec_b, vec_o, (unsigned)tn);
+  product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, (unsigned)tn);
   return hipGetLastError();
-}
-
-// A's rows as numbers of type XT, encoded inside the product.
-template <int OT, int XT>
-hipError_t encoded_t(const BlockProduct& p, hipStream_t st) {
-  const bool vec_a = (uintptr_t)p.A % 16 == 0 && p.lda % (XT == 0 ? 4 : 8) == 0;
-  const bool vec_b = (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0;
-  const bool vec_o = (uintptr_t)p.out % (OT == 0 ? 16 : 8) == 0 && p.ldo % 4 == 0;
-  return product_few<OT, XT>(p, vec_a, vec_b, vec_o, st);
 }
 
 }  // namespace
@@ -631,9 +609,9 @@ hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) 
   if (p.m <= 0 || p.n <= 0) return hipSuccess;
 #define EMK_XT(OT)                                \
   switch (dt) {                                   \
-    case 0: return encoded_t<OT, 0>(p, st);       \
-    case 1: return encoded_t<OT, 1>(p, st);       \
-    case 4: return encoded_t<OT, 4>(p, st);       \
+    case 0: return product_few<OT, 0>(p, st);       \
+    case 1: return product_few<OT, 1>(p, st);       \
+    case 4: return product_few<OT, 4>(p, st);       \
   }                                               \
   break
   switch (p.ot) {
