@@ -48,51 +48,81 @@ struct RowsIn {
   int width;
 };
 
-template <int DT, bool I8, int G, int SLOTS>  // SLOTS 0 none, 4 int32, 8 int64
+// A workgroup takes (256 / G) U consecutive blocks, a group every 256 / G'th of
+// them, all U loaded before the first is encoded: U = 4 keeps enough loads in
+// flight at large sizes, U = 1 spreads small calls over the CUs.
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t div, uint32_t inv) {
+  return inv ? __umulhi(a, inv) : a / div;  // inv = 2^32 / div rounded up, or 0
+}
+
+uint32_t inverse(uint64_t div, uint64_t most) {  // exact for dividends up to most; 0: divide
+  return div > 1 && most * div < (1ull << 32) ? (uint32_t)((1ull << 32) / div + 1) : 0;
+}
+
+template <int DT, bool I8, int G, int SLOTS, int U>
 __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, int d, int block,
-                                                          int nb, const void* __restrict__ slots,
+                                                          uint32_t nb, uint32_t nb_inv,
+                                                          const void* __restrict__ slots,
                                                           int64_t cap,
                                                           uint8_t* __restrict__ codes,
                                                           int64_t ldc,
                                                           uint8_t* __restrict__ scales,
                                                           int64_t lds) {
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) / G;
-  if (item >= n * nb) return;  // whole groups leave together
-  const int64_t row = item / nb;
-  const int b = (int)(item - row * nb);
+  constexpr int kGroups = 256 / G;
+  const int64_t first = (int64_t)blockIdx.x * (kGroups * U);
+  const int64_t row0 = first / nb;
+  const uint32_t skip = (uint32_t)(first - row0 * nb) + threadIdx.x / G;
   const int sub = threadIdx.x & (G - 1);
-  int64_t to = row;
-  if constexpr (SLOTS != 0) {
-    to = SLOTS == 8 ? static_cast<const int64_t*>(slots)[row]
-                    : (int64_t) static_cast<const int32_t*>(slots)[row];
-    if (to < 0 || to >= cap) return;
-  }
-  const int c0 = b * block + 8 * sub;  // first column of the lane
-  const int end = min(d, (b + 1) * block);
-  const int cnt = 8 * sub < block ? min(8, end - c0) : 0;
-  float v[8];
+  float v[U][8];
+  int64_t to[U];
+  int cnt[U], c0[U], blk[U];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (cnt > 0) {
-    const int h = c0 / in.width;
-    const int64_t at = row * in.rs + h * in.hs + (c0 - h * in.width);
-    load8<DT>(in.X, at, cnt, v);
+  for (int u = 0; u < U; ++u) {
+    const uint32_t j = skip + kGroups * u;
+    const uint32_t r = quotient(j, nb, nb_inv);
+    const int64_t row = row0 + r;
+    blk[u] = (int)(j - r * nb);
+    to[u] = row < n ? row : -1;
+    if constexpr (SLOTS != 0) {
+      if (row < n) {
+        to[u] = SLOTS == 8 ? static_cast<const int64_t*>(slots)[row]
+                           : (int64_t) static_cast<const int32_t*>(slots)[row];
+        if (to[u] >= cap) to[u] = -1;
+      }
+    }
+    c0[u] = blk[u] * block + 8 * sub;  // first column of the lane
+    cnt[u] = 8 * sub < block ? min(8, min(d, (blk[u] + 1) * block) - c0[u]) : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+    if (cnt[u] > 0 && row < n) {
+      int64_t at = row * in.rs + c0[u];
+      if (in.width != d) {
+        const int h = c0[u] / in.width;
+        at += h * (in.hs - in.width);
+      }
+      load8<DT>(in.X, at, cnt[u], v[u]);
+    }
   }
-  uint32_t m = group_max<G>(amax8(v));
-  const bool odd = m >= kInfBits;
-  if (odd) m = group_max<G>(amax8_finite(v));
-  const uint32_t byte = scale_byte<I8>(m);
-  if (cnt > 0) store_codes(codes + to * ldc + c0, codes8<I8>(v, inv_scale(byte), odd), cnt);
-  if (sub == 0) scales[to * lds + b] = (uint8_t)byte;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t m = group_max<G>(amax8(v[u]));
+    const bool odd = m >= kInfBits;
+    if (odd) m = group_max<G>(amax8_finite(v[u]));
+    const uint32_t byte = scale_byte<I8>(m);
+    if (to[u] < 0) continue;
+    if (cnt[u] > 0)
+      store_codes(codes + to[u] * ldc + c0[u], codes8<I8>(v[u], inv_scale(byte), odd), cnt[u]);
+    if (sub == 0) scales[to[u] * lds + blk[u]] = (uint8_t)byte;
+  }
 }
 
 // ---------------------------------------------------------------------------
 // One 128 x 128 tile per workgroup, read once for both orders: codes of the
-// rows and the codes of the columns, transposed. Thread t holds rows
-// 8 (t / 16) .. + 8 and columns 8 (t % 16) .. + 8, so a row's maximum is a
-// reduction over 16 lanes, a column's one over the thread's rows, four lane
-// groups and four waves, and a column's eight codes of a thread are eight
-// consecutive bytes of the transposed output. TILES: one scale for the tile,
+// rows and the codes of the columns, transposed. Thread t holds PR rows from
+// PR (t / 16) on (PR = 8, or 4 for fp32) and columns 8 (t % 16) .. + 8, so a
+// row's maximum is a reduction over 16 lanes, a column's one over the thread's
+// rows, four lane groups and the waves, and a column's codes of a thread are
+// PR consecutive bytes of the transposed output. TILES: one scale for the tile,
 // and both orders hold the same codes.
 // ---------------------------------------------------------------------------
 // Magnitudes are compared as the bits of the number type (16-bit types two at
@@ -109,14 +139,18 @@ struct MaxU16x2 {
   }
 };
 
-// An 8 x 8 patch of a thread. Keys are magnitude bits: one per word for fp32,
-// two per word for the 16-bit types.
+// A thread's patch of PR x 8 values: 8 rows, or 4 for fp32 (its values would
+// take 64 registers, and the rest did not fit beside them). Keys are magnitude
+// bits: one per word for fp32, two per word for the 16-bit types.
 template <int DT>
 struct Patch {
+  static constexpr int PR = DT == 0 ? 4 : 8;
+  static constexpr int kThreads = 16 * kT / PR;
+  static constexpr int kWaves = kThreads / 64;
   static constexpr int W = DT == 0 ? 8 : 4;  // words of a row
   static constexpr uint32_t kAbs = DT == 0 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
   static constexpr uint32_t kInf = DT == 0 ? kInfBits : DT == 1 ? 0x7F80u : 0x7C00u;
-  uint32_t w[8][W];
+  uint32_t w[PR][W];
 
   __device__ __forceinline__ static uint32_t kmax(uint32_t a, uint32_t b) {
     if constexpr (DT == 0)
@@ -174,7 +208,7 @@ struct Patch {
   // registers more, which would spill.
   __device__ __forceinline__ void forget() {
 #pragma unroll
-    for (int p = 0; p < 8; ++p)
+    for (int p = 0; p < PR; ++p)
 #pragma unroll
       for (int q = 0; q < W; ++q) asm volatile("" : "+v"(w[p][q]));
   }
@@ -189,7 +223,7 @@ struct Patch {
   __device__ __forceinline__ uint32_t col_key(int q) const {  // of word q's column(s)
     uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) m = kmax(m, FINITE ? finite(w[p][q] & kAbs) : w[p][q] & kAbs);
+    for (int p = 0; p < PR; ++p) m = kmax(m, FINITE ? finite(w[p][q] & kAbs) : w[p][q] & kAbs);
     return m;
   }
   __device__ __forceinline__ u32x2 row_codes(int p, float inv, bool odd) const {
@@ -198,23 +232,28 @@ struct Patch {
     for (int i = 0; i < 8; ++i) y[i] = at(p, i);
     return codes8<false>(y, inv, odd);
   }
-  __device__ __forceinline__ u32x2 col_codes(int i, float inv, bool odd) const {
-    float y[8];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) y[p] = at(p, i);
-    return codes8<false>(y, inv, odd);
+  // codes of column i to p[0 .. PR)
+  __device__ __forceinline__ void col_codes(int i, float inv, bool odd, uint8_t* p) const {
+    const uint32_t lo = codes4<false>(at(0, i), at(1, i), at(2, i), at(3, i), inv, odd);
+    if constexpr (PR == 8)
+      *reinterpret_cast<u32x2*>(p) =
+          u32x2{lo, codes4<false>(at(4, i), at(5, i), at(6, i), at(7, i), inv, odd)};
+    else
+      *reinterpret_cast<uint32_t*>(p) = lo;
   }
 };
 
 template <int DT, bool TILES>
-__global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
+__global__ __launch_bounds__(Patch<DT>::kThreads) void encode_tile_kernel(
     const void* __restrict__ X, int64_t ldx, int64_t n, int d, uint8_t* __restrict__ codes,
     int64_t ldc, uint8_t* __restrict__ scales, int64_t lds, uint8_t* __restrict__ codes_t,
     int64_t ldct, uint8_t* __restrict__ scales_t, int64_t ldst) {
   using P = Patch<DT>;
+  constexpr int PR = P::PR;
   constexpr int CW = P::W * 16;  // key words of a tile's columns
   __shared__ __attribute__((aligned(16))) uint8_t tr[kT * kTPitch];
-  __shared__ uint32_t kmax[4][CW];
+  __shared__ uint32_t kmax[P::kWaves][CW];
+  __shared__ uint32_t tmax[2][P::kWaves];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int rg = t >> 4, cg = t & 15;
   const int64_t r0 = (int64_t)blockIdx.y * kT;
@@ -224,28 +263,30 @@ __global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
 
   P x;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int r = 8 * rg + p;
+  for (int p = 0; p < PR; ++p) {
+    const int r = PR * rg + p;
     x.load(p, X, (r0 + min(r, rows - 1)) * ldx + c0 + 8 * cg, r < rows ? ccnt : 0);
   }
 
   if constexpr (TILES) {
     uint32_t m = 0;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) m = max(m, x.template row_key<false>(p));
+    for (int p = 0; p < PR; ++p) m = max(m, x.template row_key<false>(p));
     m = group_max<64>(m);
-    if (lane == 0) kmax[0][wave] = m;
+    if (lane == 0) tmax[0][wave] = m;
     __syncthreads();
-    m = max(max(kmax[0][0], kmax[0][1]), max(kmax[0][2], kmax[0][3]));
+#pragma unroll
+    for (int v = 0; v < P::kWaves; ++v) m = max(m, tmax[0][v]);
     const bool odd = m >= P::kInf;
     if (odd) {  // the same answer in every thread of the workgroup
       m = 0;
 #pragma unroll
-      for (int p = 0; p < 8; ++p) m = max(m, x.template row_key<true>(p));
+      for (int p = 0; p < PR; ++p) m = max(m, x.template row_key<true>(p));
       m = group_max<64>(m);
-      if (lane == 0) kmax[1][wave] = m;
+      if (lane == 0) tmax[1][wave] = m;
       __syncthreads();
-      m = max(max(kmax[1][0], kmax[1][1]), max(kmax[1][2], kmax[1][3]));
+#pragma unroll
+      for (int v = 0; v < P::kWaves; ++v) m = max(m, tmax[1][v]);
     }
     const uint32_t byte = scale_byte<false>(P::bits(m));
     const float inv = inv_scale(byte);
@@ -255,14 +296,14 @@ __global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
     }
     if (codes) {
 #pragma unroll
-      for (int p = 0; p < 8; ++p)
-        if (8 * rg + p < rows && ccnt > 0)
-          store_codes(codes + (r0 + 8 * rg + p) * ldc + c0 + 8 * cg, x.row_codes(p, inv, odd), ccnt);
+      for (int p = 0; p < PR; ++p)
+        if (PR * rg + p < rows && ccnt > 0)
+          store_codes(codes + (r0 + PR * rg + p) * ldc + c0 + 8 * cg, x.row_codes(p, inv, odd), ccnt);
     }
     if (!codes_t) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<u32x2*>(&tr[(8 * cg + i) * kTPitch + 8 * rg]) = x.col_codes(i, inv, odd);
+      x.col_codes(i, inv, odd, &tr[(8 * cg + i) * kTPitch + PR * rg]);
   } else {
     // columns: the thread's rows, the four row groups of the wave, the waves.
     // A column that holds a non-finite value takes its finite maximum in a
@@ -280,7 +321,10 @@ __global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
 #pragma unroll
       for (int q = 0; q < P::W; ++q) {
         const int c = P::W * cg + q;
-        ck[q] = P::kmax(P::kmax(kmax[0][c], kmax[1][c]), P::kmax(kmax[2][c], kmax[3][c]));
+        uint32_t m = kmax[0][c];
+#pragma unroll
+        for (int v = 1; v < P::kWaves; ++v) m = P::kmax(m, kmax[v][c]);
+        ck[q] = m;
       }
     };
     columns(std::false_type());
@@ -293,20 +337,19 @@ __global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
     for (int i = 0; i < 8; ++i) {
       const uint32_t byte = scale_byte<false>(
           P::bits(DT == 0 ? ck[i] : P::key(ck[DT == 0 ? i : i >> 1], i & 1)));
-      *reinterpret_cast<u32x2*>(&tr[(8 * cg + i) * kTPitch + 8 * rg]) =
-          x.col_codes(i, inv_scale(byte), odd);
+      x.col_codes(i, inv_scale(byte), odd, &tr[(8 * cg + i) * kTPitch + PR * rg]);
       if (rg == 0 && i < ccnt)
         scales_t[(int64_t)(c0 + 8 * cg + i) * ldst + blockIdx.y] = (uint8_t)byte;
     }
     x.forget();
     if (codes) {
 #pragma unroll
-      for (int p = 0; p < 8; ++p) {
+      for (int p = 0; p < PR; ++p) {
         uint32_t m = group_max<16>(x.template row_key<false>(p));
         const bool bad = m >= P::kInf;
         if (bad) m = group_max<16>(x.template row_key<true>(p));
         const uint32_t byte = scale_byte<false>(P::bits(m));
-        const int r = 8 * rg + p;
+        const int r = PR * rg + p;
         if (r < rows) {
           if (ccnt > 0)
             store_codes(codes + (r0 + r) * ldc + c0 + 8 * cg, x.row_codes(p, inv_scale(byte), bad),
@@ -319,8 +362,8 @@ __global__ __launch_bounds__(256, DT == 0 ? 3 : 5) void encode_tile_kernel(
   __syncthreads();
   // transposed rows: 8 lanes write the 128 bytes of one column
 #pragma unroll
-  for (int q = 0; q < kT * 8 / 256; ++q) {
-    const int f = q * 256 + t;
+  for (int q = 0; q < kT * 8 / P::kThreads; ++q) {
+    const int f = q * P::kThreads + t;
     const int c = f >> 3, ch = f & 7;
     if (c >= cols) break;
     const u32x2 lo = *reinterpret_cast<const u32x2*>(&tr[c * kTPitch + 16 * ch]);
@@ -402,10 +445,6 @@ __device__ __forceinline__ int64_t source_row(const RowsFrom& f, int64_t row, in
 // the pieces per row and by the block are products by `inv` = 2^32 / divisor,
 // rounded up (exact while dividend x divisor < 2^32, which the host checks).
 constexpr int kReadRows = 64;  // R at most
-
-__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t div, uint32_t inv) {
-  return inv ? __umulhi(a, inv) : a / div;
-}
 
 // The first cnt values of a piece of output: read once by whoever comes next,
 // so they are not kept in the caches on their way.
@@ -506,17 +545,19 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restr
   }
 }
 
-template <int DT, bool I8, int G>
-hipError_t encode_rows_g(const EncodeRows& a, hipStream_t st) {
-  const int nb = (a.d + a.block - 1) / a.block;
-  const int64_t groups = a.n * nb;
-  const int64_t blocks = (groups * G + 255) / 256;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), wg(256);
+template <int DT, bool I8, int G, int U>
+hipError_t encode_rows_u(const EncodeRows& a, hipStream_t st) {
+  const int64_t nb = (a.d + a.block - 1) / a.block;
+  constexpr int64_t per = 256 / G * U;
+  const int64_t wgs = (a.n * nb + per - 1) / per;
+  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)wgs), wg(256);
   const RowsIn in{a.X, a.rs, a.hs, a.width};
-#define EMK_GO(S)                                                                          \
-  encode_rows_kernel<DT, I8, G, S><<<grid, wg, 0, st>>>(in, a.n, a.d, a.block, nb, a.slots, \
-                                                        a.cap, a.codes, a.ldc, a.scales, a.lds)
+  const uint32_t inv = inverse(nb, nb + per);
+#define EMK_GO(S)                                                                               \
+  encode_rows_kernel<DT, I8, G, S, U><<<grid, wg, 0, st>>>(in, a.n, a.d, a.block, (uint32_t)nb,  \
+                                                           inv, a.slots, a.cap, a.codes, a.ldc, \
+                                                           a.scales, a.lds)
   if (!a.slots)
     EMK_GO(0);
   else if (a.slot_bytes == 8)
@@ -525,6 +566,13 @@ hipError_t encode_rows_g(const EncodeRows& a, hipStream_t st) {
     EMK_GO(4);
 #undef EMK_GO
   return hipGetLastError();
+}
+
+template <int DT, bool I8, int G>
+hipError_t encode_rows_g(const EncodeRows& a, hipStream_t st) {
+  const int64_t groups = a.n * ((a.d + a.block - 1) / a.block);
+  if (groups * G >= 4 * 256 * 1024) return encode_rows_u<DT, I8, G, 4>(a, st);
+  return encode_rows_u<DT, I8, G, 1>(a, st);
 }
 
 template <int DT, bool I8>
@@ -542,7 +590,7 @@ hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
   // rows in launches of at most 65535 tiles (the grid's y limit)
   for (int64_t y0 = 0; y0 < gy; y0 += 65535) {
     const int64_t ny = gy - y0 < 65535 ? gy - y0 : 65535;
-    const dim3 grid((unsigned)gx, (unsigned)ny), wg(256);
+    const dim3 grid((unsigned)gx, (unsigned)ny), wg(Patch<DT>::kThreads);
     const int64_t r = y0 * kT, size = DT == 0 ? 4 : 2;
     const void* X = static_cast<const char*>(a.X) + r * a.ldx * size;
     uint8_t* codes = a.codes ? a.codes + r * a.ldc : nullptr;
@@ -559,10 +607,6 @@ hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
-}
-
-uint32_t inverse(uint64_t div, uint64_t most) {  // 0: divide
-  return div > 1 && most * div < (1ull << 32) ? (uint32_t)((1ull << 32) / div + 1) : 0;
 }
 
 template <int OT, bool I8>
