@@ -67,8 +67,8 @@ template <>
 struct Operand<true> {
   i32x8 v;
   uint32_t scale;
-  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi, uint32_t byte) {
-    v = join(lo, hi);
+  __device__ __forceinline__ void set(i32x8 codes, uint32_t byte) {
+    v = codes;
     scale = byte;
   }
 };
@@ -77,15 +77,14 @@ template <>
 struct Operand<false> {
   bf16x8 v[4];
   int rest;
-  __device__ __forceinline__ void set(u32x4 lo, u32x4 hi, uint32_t byte) {
+  __device__ __forceinline__ void set(i32x8 codes, uint32_t byte) {
     const int e = (int)byte - 127;
     const int f = max(-kFold, min(kFold, e));
     rest = byte == 255u ? kRestNaN : e - f;
     const float s = __uint_as_float((uint32_t)(f + 127) << 23);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t w0 = q < 2 ? lo[2 * q] : hi[2 * q - 4];
-      const uint32_t w1 = q < 2 ? lo[2 * q + 1] : hi[2 * q - 3];
+      const uint32_t w0 = (uint32_t)codes[2 * q], w1 = (uint32_t)codes[2 * q + 1];
       const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
       const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
       const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
@@ -174,13 +173,14 @@ __device__ __forceinline__ void store4(void* out, int64_t at, f32x4 y, int cnt) 
 // ---------------------------------------------------------------------------
 constexpr int kAT = 64;
 
-template <int OT>
-__global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsigned tiles_n) {
-  __shared__ __attribute__((aligned(16))) uint8_t la[kAT * kStep], lb[kAT * kStep];
+// Columns m0 .. + 64 and n0 .. + 64 of the product over k-steps [s0, s1), given
+// to put(m, n, four sums for n .. n + 3) for every m < p.m; 256 threads, la and
+// lb 8 KB of LDS each.
+template <bool F8, typename PUT>
+__device__ __forceinline__ void any_tile(const BlockProduct& p, int64_t m0, int64_t n0, int s0,
+                                         int s1, uint8_t* la, uint8_t* lb, PUT put) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kAT;
-  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * kAT;
   const int r = t >> 2, q = 2 * (t & 3);  // this thread's row and first of two chunks
   const int64_t am = min(m0 + r, p.m - 1), bn = min(n0 + r, p.n - 1);
   const uint8_t* ap = p.A + am * p.lda + 16 * q;
@@ -199,8 +199,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int steps = (p.k + kStep - 1) / kStep;
-  for (int s = 0; s < steps; ++s) {
+  for (int s = s0; s < s1; ++s) {
     const int left = p.k - s * kStep - 16 * q;
     const u32x4 a0 = load16(ap + (int64_t)s * kStep, left);
     const u32x4 a1 = load16(ap + (int64_t)s * kStep + 16, left - 16);
@@ -212,14 +211,16 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
     *reinterpret_cast<u32x4*>(&lb[r * kStep + 16 * (q ^ (r & 7))]) = b0;
     *reinterpret_cast<u32x4*>(&lb[r * kStep + 16 * ((q + 1) ^ (r & 7))]) = b1;
     __syncthreads();
-    Operand<OT != 0> fa[2], fb[2];
+    Operand<F8> fa[2], fb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int ra = wm + 16 * i + col, rb = wn + 16 * i + col, x = col & 7;
-      fa[i].set(*reinterpret_cast<const u32x4*>(&la[ra * kStep + 16 * (grp ^ x)]),
-                *reinterpret_cast<const u32x4*>(&la[ra * kStep + 16 * ((grp + 4) ^ x)]), sa[i][s]);
-      fb[i].set(*reinterpret_cast<const u32x4*>(&lb[rb * kStep + 16 * (grp ^ x)]),
-                *reinterpret_cast<const u32x4*>(&lb[rb * kStep + 16 * ((grp + 4) ^ x)]), sb[i][s]);
+      fa[i].set(join(*reinterpret_cast<const u32x4*>(&la[ra * kStep + 16 * (grp ^ x)]),
+                     *reinterpret_cast<const u32x4*>(&la[ra * kStep + 16 * ((grp + 4) ^ x)])),
+                sa[i][s]);
+      fb[i].set(join(*reinterpret_cast<const u32x4*>(&lb[rb * kStep + 16 * (grp ^ x)]),
+                     *reinterpret_cast<const u32x4*>(&lb[rb * kStep + 16 * ((grp + 4) ^ x)])),
+                sb[i][s]);
     }
     const bool extreme = any_rest(fa) || any_rest(fb);
 #pragma unroll
@@ -232,11 +233,19 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
     const int64_t m = m0 + wm + 16 * i + col;
     if (m >= p.m) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t n = n0 + wn + 16 * j + 4 * grp;
-      store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
-    }
+    for (int j = 0; j < 2; ++j) put(m, n0 + wn + 16 * j + 4 * grp, acc[i][j]);
   }
+}
+
+template <int OT>
+__global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsigned tiles_n) {
+  __shared__ __attribute__((aligned(16))) uint8_t la[kAT * kStep], lb[kAT * kStep];
+  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kAT;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * kAT;
+  any_tile<OT != 0>(p, m0, n0, 0, (p.k + kStep - 1) / kStep, la, lb,
+                    [&](int64_t m, int64_t n, f32x4 y) {
+                      store4<OT>(p.out, m * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
+                    });
 }
 
 // ---------------------------------------------------------------------------
@@ -317,31 +326,46 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
       sp[q] = p.Bs + (p.b_tiles ? n / kStep : n) * p.ldbs;
     }
   }
-  auto issue = [&](int s, int buf) {
+  // The last stage of a k that is no multiple of 128: chunks past k are not
+  // read (chunk 0 stands in), and what is not a code is cleared in LDS.
+  const int last = p.k % kStep ? steps - 1 : -1;
+  const uint32_t skip = lx >= p.k % kStep ? -(uint32_t)lx : 0u;
+  // Direct load l of stage s: l < MI + NI a window, the others scales.
+  constexpr int kLoads = MI + NI + Q;
+  const uint32_t lc0 = (uint32_t)(uintptr_t)(lds_ptr_t)lc, ls0 = (uint32_t)(uintptr_t)(lds_ptr_t)ls;
+  auto load = [&](int on, int s, int buf, int l, uint32_t shift) {
+    on = __builtin_amdgcn_readfirstlane(on);
     const int64_t k0 = (int64_t)s * kStep;
-    uint8_t* da = lc[buf] + wave * MI * 1024;
-    uint8_t* db = lc[buf] + BM * kStep + wave * NI * 1024;
-    if (k0 + kStep <= p.k) {
+    const uint32_t to = lc0 + buf * R * kStep;
+    if (l < MI)
+      lds_load16_if(on, a0 + k0, off[l] + shift, to + (wave * MI + l) * 1024);
+    else if (l < MI + NI)
+      lds_load16_if(on, b0 + k0, off[l] + shift, to + BM * kStep + (wave * NI + l - MI) * 1024);
+    else
+      lds_load1_if(__builtin_amdgcn_readfirstlane(wave + 4 * (l - MI - NI) < R / 64 ? on : 0),
+                   sp[l - MI - NI] + s, ls0 + buf * R * 4 + 256 * (wave + 4 * (l - MI - NI)));
+  };
+  auto issue = [&](int s, int buf) {
+    const uint32_t shift = s == last ? skip : 0u;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) lds_load16_at(a0 + k0, off[i], da + i * 1024);
+    for (int l = 0; l < kLoads; ++l) load(s < s1, s, buf, l, shift);
+  };
+  auto clear = [&](int buf) {
+    const int left = p.k % kStep;
+    for (int f = threadIdx.x; f < R * 8; f += 256) {
+      const int r = f >> 3, c = f & 7;  // chunk c of row r
+      const int cnt = left - 16 * c;
+      if (cnt >= 16) continue;
+      u32x4* q = reinterpret_cast<u32x4*>(lc[buf] + r * kStep + 16 * (c ^ (r & 7)));
+      u32x4 w = *q;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) lds_load16_at(b0 + k0, off[MI + i], db + i * 1024);
-    } else {
-      const int left = p.k - (int)k0 - lx;
-#pragma unroll 1
-      for (int i = 0; i < MI; ++i) {
-        const uint32_t o = (uint32_t)min(8 * (wave * MI + i) + lr, mrows - 1) * (uint32_t)p.lda + lx;
-        *reinterpret_cast<u32x4*>(da + i * 1024 + 16 * lane) = load16(a0 + k0 + o, left);
+      for (int d = 0; d < 4; ++d) {
+        const int n = cnt - 4 * d;
+        w[d] = n <= 0 ? 0u : n >= 4 ? w[d] : w[d] & ((1u << (8 * n)) - 1u);
       }
-#pragma unroll 1
-      for (int i = 0; i < NI; ++i) {
-        const uint32_t o = (uint32_t)min(8 * (wave * NI + i) + lr, nrows - 1) * (uint32_t)p.ldb + lx;
-        *reinterpret_cast<u32x4*>(db + i * 1024 + 16 * lane) = load16(b0 + k0 + o, left);
-      }
+      *q = w;
     }
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (wave + 4 * q < R / 64) lds_load1(sp[q] + s, &ls[buf][64 * (wave + 4 * q)]);
+    lds_barrier();
   };
 
   f32x4 acc[MI][NI];
@@ -350,31 +374,143 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // A k-step is four quarters of HA x HB output tiles: (A0, B0), (A0, B1),
+  // (A1, B1), (A1, B0). Each quarter's MFMAs run while the fragments of the
+  // next one are read from LDS; the last runs after the barrier that says the
+  // next stage is there and this one has been read by all, so it also covers
+  // the next stage's first fragments and the loads of the stage after it.
+  // The B half that the last quarter does not use takes the next stage's B0.
+  constexpr int HA = MI / 2, HB = NI / 2;
   const int ra = (wave & 1) * 16 * MI + col, rb = BM + (wave >> 1) * 16 * NI + col;
   const int fx = 16 * (grp ^ (col & 7));
-  if (s0 < s1) issue(s0, 0);
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
+  struct Raw {
+    i32x8 v;
+    uint32_t scale;
+  };
+  // LDS addresses of this lane's fragments (A, B; either 16-byte piece; either
+  // buffer) and scales. Opaque to the compiler, so that the rows are offsets in
+  // the instructions: it would keep a register for the address of every row.
+  uint32_t fa[2][2], fb[2][2], sa = ls0 + 4 * ra, sb = ls0 + 4 * rb;
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fa[b][h] = lc0 + (b * R + ra) * kStep + (fx ^ (64 * h));
+      fb[b][h] = lc0 + (b * R + rb) * kStep + (fx ^ (64 * h));
+      asm volatile("" : "+v"(fa[b][h]), "+v"(fb[b][h]));
+    }
+  asm volatile("" : "+v"(sa), "+v"(sb));
+  auto lds16 = [](uint32_t at) {
+    return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)at;
+  };
+  auto lds4 = [](uint32_t at) {
+    return *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t)at;
+  };
+  auto read_a = [&](Raw& o, int buf, int i) {
+    o.v = join(lds16(fa[buf][0] + i * 16 * kStep), lds16(fa[buf][1] + i * 16 * kStep));
+    o.scale = lds4(sa + 4 * (buf * R + 16 * i));
+  };
+  auto read_b = [&](Raw& o, int buf, int j) {
+    o.v = join(lds16(fb[buf][0] + j * 16 * kStep), lds16(fb[buf][1] + j * 16 * kStep));
+    o.scale = lds4(sb + 4 * (buf * R + 16 * j));
+  };
+  Raw A0[HA], A1[HA], X[HB], Y[HB];
+  int rest = 0;  // bf16 unit: some scale is beyond what is folded into the operands
+  // Keeps an MFMA where it stands among the reads and loads: the compiler would
+  // gather the MFMAs of several quarters behind them, and hold every fragment.
+  auto pin = [](f32x4& c) {
+    if constexpr (MI * NI >= 64)
+      asm volatile("" : "+a"(c)::"memory");
+    else
+      asm volatile("" : "+v"(c)::"memory");
+  };
+  // the MFMAs of one quarter; after each, one piece of other work (beside(q))
+  auto quarter = [&](const Raw(&fa)[HA], const Raw(&fb)[HB], int i0, int j0, auto beside) {
+    Operand<F8> a[HA], b[HB];
+#pragma unroll
+    for (int i = 0; i < HA; ++i) a[i].set(fa[i].v, fa[i].scale);
+#pragma unroll
+    for (int j = 0; j < HB; ++j) b[j].set(fb[j].v, fb[j].scale);
+    if constexpr (!F8) {
+#pragma unroll
+      for (int i = 0; i < HA; ++i) rest |= a[i].rest;
+#pragma unroll
+      for (int j = 0; j < HB; ++j) rest |= b[j].rest;
+    }
+#pragma unroll
+    for (int i = 0; i < HA; ++i)
+#pragma unroll
+      for (int j = 0; j < HB; ++j) {
+        acc[i0 + i][j0 + j] = step(b[j], a[i], acc[i0 + i][j0 + j]);
+        pin(acc[i0 + i][j0 + j]);
+        beside(i * HB + j);
+      }
+  };
+  constexpr int kQ = HA * HB;
+  constexpr int kPer = (kLoads + kQ - 1) / kQ;  // loads beside each MFMA of the last quarter
+  auto head = [&](int buf, Raw(&first)[HB], Raw(&second)[HB]) {
+    quarter(A0, first, 0, 0, [&](int q) {
+      if (q < HB) read_b(second[q], buf, HB + q);
+    });
+    quarter(A0, second, 0, HB, [&](int q) {
+      if (q < HA) read_a(A1[q], buf, HA + q);
+    });
+    quarter(A1, second, HA, HB, [](int) {});
+  };
+  auto next = [&](int q, int buf, Raw(&second)[HB]) {  // the next stage's first fragments
+    if (q < HA) read_a(A0[q], buf ^ 1, q);
+    if (q < HB) read_b(second[q], buf ^ 1, q);
+  };
+  auto kstep = [&](int s, int buf, Raw(&first)[HB], Raw(&second)[HB]) {
+    head(buf, first, second);
     EMK_WAIT_VMCNT(0);
     lds_barrier();
-    if (s + 1 < s1) issue(s + 1, buf ^ 1);
-    const uint8_t* L = lc[buf];
-    auto frag = [&](Operand<F8>& o, int row) {
-      const uint8_t* r = L + row * kStep;
-      o.set(*reinterpret_cast<const u32x4*>(r + fx), *reinterpret_cast<const u32x4*>(r + (fx ^ 64)),
-            ls[buf][row]);
-    };
-    Operand<F8> b[NI];
+    if (s + 1 == last) clear(buf ^ 1);
+    const int on = s + 2 < s1;
+    const uint32_t shift = s + 2 == last ? skip : 0u;
+    quarter(A1, first, HA, 0, [&](int q) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) frag(b[j], rb + 16 * j);
-    const bool eb = any_rest(b);
+      for (int l = 0; l < kPer; ++l)
+        if (q * kPer + l < kLoads) load(on, s + 2, buf, q * kPer + l, shift);
+      next(q, buf, second);  // after the last step: stale stages, not used
+    });
+  };
+  auto begin = [&](int buf, Raw(&first)[HB]) {
+    issue(s0, buf);
+    issue(s0 + 1, buf ^ 1);
+    EMK_WAIT_VMCNT(0);
+    lds_barrier();
+    if (s0 == last) clear(buf);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      Operand<F8> a[1];
-      frag(a[0], ra + 16 * i);
-      const bool ea = eb || any_rest(a);
+    for (int i = 0; i < HA; ++i) read_a(A0[i], buf, i);
 #pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = add_step(b[j], a[0], acc[i][j], ea);
+    for (int j = 0; j < HB; ++j) read_b(first[j], buf, j);
+  };
+  // steps in pairs, so that the halves of B keep their registers; an odd one first
+  int s = s0;
+  if ((s1 - s0) & 1) {
+    begin(1, Y);
+    kstep(s++, 1, Y, X);
+  } else {
+    begin(0, X);
+  }
+  for (; s < s1; s += 2) {
+    kstep(s, 0, X, Y);
+    kstep(s + 1, 1, Y, X);
+  }
+  auto put = [&](int64_t m, int64_t n, f32x4 y) {
+    if constexpr (SPLIT) {
+      if (n < p.n) store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, y, 4);
+    } else {
+      store4<OT>(p.out, m * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
+    }
+  };
+  if constexpr (!F8) {
+    if (__syncthreads_or(rest)) {  // scales beyond 2^+-kFold: the tile again, with care
+      for (int q = 0; q < MI * NI / 4; ++q)
+        any_tile<F8>(p, m0 + kAT * (q / (NI / 2)), n0 + kAT * (q % (NI / 2)), s0, s1, lc[0], lc[1],
+                     put);
+      return;
     }
   }
 #pragma unroll
@@ -382,15 +518,7 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     const int64_t m = m0 + ra + 16 * i;
     if (m >= p.m) continue;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) {
-      const int64_t n = n0 + (rb - BM) - col + 16 * j + 4 * grp;
-      if constexpr (SPLIT) {
-        if (n < p.n)
-          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4);
-      } else {
-        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
-      }
-    }
+    for (int j = 0; j < NI; ++j) put(m, n0 + (rb - BM) - col + 16 * j + 4 * grp, acc[i][j]);
   }
 }
 
@@ -498,14 +626,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
       if constexpr (kEncode) {
         const uint8_t* q = room + (am * steps + t) * kStep;
         const int x = 16 * (grp ^ (am & 7));
-        a[0].set(*reinterpret_cast<const u32x4*>(q + x), *reinterpret_cast<const u32x4*>(q + (x ^ 64)),
+        a[0].set(join(*reinterpret_cast<const u32x4*>(q + x),
+                      *reinterpret_cast<const u32x4*>(q + (x ^ 64))),
                  scales[am * steps + t]);
       } else {
         const int64_t k0 = (int64_t)t * kStep;
         const int left = p.k - (int)k0 - 16 * grp;
-        a[0].set(load16(ap + k0, left), load16(ap + k0 + 64, left - 64), as[t]);
+        a[0].set(join(load16(ap + k0, left), load16(ap + k0 + 64, left - 64)), as[t]);
       }
-      b[0].set(lo[u], hi[u], sc[u]);
+      b[0].set(join(lo[u], hi[u]), sc[u]);
       acc = add_step(b[0], a[0], acc, any_rest(a) || any_rest(b));
     }
   }

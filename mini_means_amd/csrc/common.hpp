@@ -276,17 +276,21 @@ __device__ __forceinline__ void lds_load4(const void* src, void* lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
-// The same with a wave-uniform base and a 32-bit byte offset per lane.
-__device__ __forceinline__ void lds_load16_at(const void* base, uint32_t off, void* lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(off), "s"(base)
-               : "memory", "m0");
+// The same with a wave-uniform base, a 32-bit byte offset per lane and the LDS
+// byte address as a number, done only where `on` (wave-uniform) is not 0. The
+// branch is inside the asm: as one of the program's it would part the
+// instructions around it into blocks, and the compiler then copies the
+// accumulators of a matrix product from block to block.
+__device__ __forceinline__ void lds_load16_if(int on, const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %1\n\t"
+               "global_load_lds_dwordx4 %2, %3\n.Lskip%=:" ::"s"(on), "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0", "scc");
 }
 // One byte per lane, zero-extended to LDS bytes [lds + 4 i, lds + 4 i + 4).
-__device__ __forceinline__ void lds_load1(const void* src, void* lds) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(m0), "v"(src)
-               : "memory", "m0");
+__device__ __forceinline__ void lds_load1_if(int on, const void* src, uint32_t lds) {
+  asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %1\n\t"
+               "global_load_lds_ubyte %2, off\n.Lskip%=:" ::"s"(on), "s"(lds), "v"(src)
+               : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
 
