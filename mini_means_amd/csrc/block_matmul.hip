@@ -23,6 +23,8 @@
 // The first operand is B's rows (n), the second A's (m): the result then has
 // n = 4 (l / 16) + v, v < 4, and m = l % 16 in lane l, four consecutive
 // values of an output row.
+#include <type_traits>
+
 #include "block.hpp"
 #include "kernels.hpp"
 
@@ -333,22 +335,22 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   // Direct load l of stage s: l < MI + NI a window, the others scales.
   constexpr int kLoads = MI + NI + Q;
   const uint32_t lc0 = (uint32_t)(uintptr_t)(lds_ptr_t)lc, ls0 = (uint32_t)(uintptr_t)(lds_ptr_t)ls;
-  auto load = [&](int on, int s, int buf, int l, uint32_t shift) {
-    on = __builtin_amdgcn_readfirstlane(on);
+  auto load = [&](int s, int buf, int l, uint32_t shift) {
     const int64_t k0 = (int64_t)s * kStep;
     const uint32_t to = lc0 + buf * R * kStep;
-    if (l < MI)
-      lds_load16_if(on, a0 + k0, off[l] + shift, to + (wave * MI + l) * 1024);
-    else if (l < MI + NI)
-      lds_load16_if(on, b0 + k0, off[l] + shift, to + BM * kStep + (wave * NI + l - MI) * 1024);
-    else
-      lds_load1_if(__builtin_amdgcn_readfirstlane(wave + 4 * (l - MI - NI) < R / 64 ? on : 0),
-                   sp[l - MI - NI] + s, ls0 + buf * R * 4 + 256 * (wave + 4 * (l - MI - NI)));
+    if (l < MI) {
+      lds_load16_at(a0 + k0, off[l] + shift, to + (wave * MI + l) * 1024);
+    } else if (l < MI + NI) {
+      lds_load16_at(b0 + k0, off[l] + shift, to + BM * kStep + (wave * NI + l - MI) * 1024);
+    } else {
+      const int q = wave + 4 * (l - MI - NI);
+      if (R / 64 % 4 == 0 || q < R / 64) lds_load1_at(sp[l - MI - NI] + s, ls0 + buf * R * 4 + 256 * q);
+    }
   };
   auto issue = [&](int s, int buf) {
     const uint32_t shift = s == last ? skip : 0u;
 #pragma unroll
-    for (int l = 0; l < kLoads; ++l) load(s < s1, s, buf, l, shift);
+    for (int l = 0; l < kLoads; ++l) load(s, buf, l, shift);
   };
   auto clear = [&](int buf) {
     const int left = p.k % kStep;
@@ -447,37 +449,47 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
       }
   };
   constexpr int kQ = HA * HB;
-  constexpr int kPer = (kLoads + kQ - 1) / kQ;  // loads beside each MFMA of the last quarter
-  auto head = [&](int buf, Raw(&first)[HB], Raw(&second)[HB]) {
+  // The reads of n fragments, spread over the MFMAs of a quarter.
+  auto spread = [](int q, int n, auto one) {
+#pragma unroll
+    for (int x = 0; x < n; ++x)
+      if (q == x * kQ / n) one(x);
+  };
+  // Step s in buffer buf, B0 in `first`; NEXT: there is a stage s + 1; LOAD: stage
+  // `later` is loaded into buf once this one has been read.
+  auto kstep = [&](auto next, auto load_later, int s, int later, int buf, Raw(&first)[HB],
+                   Raw(&second)[HB]) {
+    constexpr bool NEXT = decltype(next)::value, LOAD = decltype(load_later)::value;
     quarter(A0, first, 0, 0, [&](int q) {
-      if (q < HB) read_b(second[q], buf, HB + q);
+      spread(q, HB, [&](int x) { read_b(second[x], buf, HB + x); });
     });
     quarter(A0, second, 0, HB, [&](int q) {
-      if (q < HA) read_a(A1[q], buf, HA + q);
+      spread(q, HA, [&](int x) { read_a(A1[x], buf, HA + x); });
     });
     quarter(A1, second, HA, HB, [](int) {});
-  };
-  auto next = [&](int q, int buf, Raw(&second)[HB]) {  // the next stage's first fragments
-    if (q < HA) read_a(A0[q], buf ^ 1, q);
-    if (q < HB) read_b(second[q], buf ^ 1, q);
-  };
-  auto kstep = [&](int s, int buf, Raw(&first)[HB], Raw(&second)[HB]) {
-    head(buf, first, second);
-    EMK_WAIT_VMCNT(0);
-    lds_barrier();
-    if (s + 1 == last) clear(buf ^ 1);
-    const int on = s + 2 < s1;
-    const uint32_t shift = s + 2 == last ? skip : 0u;
+    if constexpr (NEXT) {
+      EMK_WAIT_VMCNT(0);
+      lds_barrier();
+      if (s + 1 == last) clear(buf ^ 1);
+    }
+    const uint32_t shift = later == last ? skip : 0u;
     quarter(A1, first, HA, 0, [&](int q) {
-#pragma unroll
-      for (int l = 0; l < kPer; ++l)
-        if (q * kPer + l < kLoads) load(on, s + 2, buf, q * kPer + l, shift);
-      next(q, buf, second);  // after the last step: stale stages, not used
+      if constexpr (LOAD)
+        spread(q, kLoads, [&](int x) { load(later, buf, x, shift); });
+      if constexpr (NEXT)
+        spread(q, HA + HB, [&](int x) {  // A0[0], B0, the rest of A0
+          if (x == 0)
+            read_a(A0[0], buf ^ 1, 0);
+          else if (x <= HB)
+            read_b(second[x - 1], buf ^ 1, x - 1);
+          else
+            read_a(A0[x - HB], buf ^ 1, x - HB);
+        });
     });
   };
   auto begin = [&](int buf, Raw(&first)[HB]) {
     issue(s0, buf);
-    issue(s0 + 1, buf ^ 1);
+    issue(min(s0 + 1, s1 - 1), buf ^ 1);
     EMK_WAIT_VMCNT(0);
     lds_barrier();
     if (s0 == last) clear(buf);
@@ -487,17 +499,26 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     for (int j = 0; j < HB; ++j) read_b(first[j], buf, j);
   };
   // steps in pairs, so that the halves of B keep their registers; an odd one first
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
   int s = s0;
   if ((s1 - s0) & 1) {
     begin(1, Y);
-    kstep(s++, 1, Y, X);
+    kstep(yes, yes, s, min(s + 2, s1 - 1), 1, Y, X);
+    ++s;
   } else {
     begin(0, X);
   }
-  for (; s < s1; s += 2) {
-    kstep(s, 0, X, Y);
-    kstep(s + 1, 1, Y, X);
+  for (; s + 2 < s1; s += 2) {
+    kstep(yes, yes, s, s + 2, 0, X, Y);
+    kstep(yes, yes, s + 1, s + 3, 1, Y, X);
   }
+  if (s < s1) {
+    kstep(yes, no, s, s, 0, X, Y);
+    kstep(no, no, s + 1, s, 1, Y, X);
+  }
+  EMK_WAIT_VMCNT(0);  // the load that a single step makes for nobody
+
   auto put = [&](int64_t m, int64_t n, f32x4 y) {
     if constexpr (SPLIT) {
       if (n < p.n) store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, y, 4);

@@ -277,20 +277,15 @@ __device__ __forceinline__ void lds_load4(const void* src, void* lds) {
                : "memory", "m0");
 }
 // The same with a wave-uniform base, a 32-bit byte offset per lane and the LDS
-// byte address as a number, done only where `on` (wave-uniform) is not 0. The
-// branch is inside the asm: as one of the program's it would part the
-// instructions around it into blocks, and the compiler then copies the
-// accumulators of a matrix product from block to block.
-__device__ __forceinline__ void lds_load16_if(int on, const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %1\n\t"
-               "global_load_lds_dwordx4 %2, %3\n.Lskip%=:" ::"s"(on), "s"(lds), "v"(off), "s"(base)
-               : "memory", "m0", "scc");
+// byte address as a (wave-uniform) number.
+__device__ __forceinline__ void lds_load16_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 // One byte per lane, zero-extended to LDS bytes [lds + 4 i, lds + 4 i + 4).
-__device__ __forceinline__ void lds_load1_if(int on, const void* src, uint32_t lds) {
-  asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_mov_b32 m0, %1\n\t"
-               "global_load_lds_ubyte %2, off\n.Lskip%=:" ::"s"(on), "s"(lds), "v"(src)
-               : "memory", "m0", "scc");
+__device__ __forceinline__ void lds_load1_at(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src)
+               : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
