@@ -285,12 +285,13 @@ __device__ __forceinline__ void tile_of(unsigned id, const TileMap& t, unsigned&
   tm = group * kGroup + (in - tn * rows);
 }
 
-template <int MI, int NI, int OT, bool SPLIT>
+template <int MI, int NI, int OT, bool SPLIT, bool RAGGED>
 __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kernel(BlockProduct p,
                                                                                  TileMap t) {
   constexpr bool F8 = OT != 0;
   constexpr int BM = 32 * MI, BN = 32 * NI, R = BM + BN;
-  constexpr int Q = (R / 64 + 3) / 4;  // scale loads per wave and stage, at most
+  constexpr int Q = R / 256;  // scale loads per wave and stage
+  static_assert(R % 256 == 0, "every wave issues as many loads");
   __shared__ __attribute__((aligned(1024))) uint8_t lc[2][R * kStep];
   __shared__ __attribute__((aligned(256))) uint32_t ls[2][R];
 
@@ -330,12 +331,13 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   }
   // The last stage of a k that is no multiple of 128: chunks past k are not
   // read (chunk 0 stands in), and what is not a code is cleared in LDS.
-  const int last = p.k % kStep ? steps - 1 : -1;
-  const uint32_t skip = lx >= p.k % kStep ? -(uint32_t)lx : 0u;
+  const int last = RAGGED ? steps - 1 : -1;
+  const uint32_t skip = RAGGED && lx >= p.k % kStep ? -(uint32_t)lx : 0u;
   // Direct load l of stage s: l < MI + NI a window, the others scales.
   constexpr int kLoads = MI + NI + Q;
   const uint32_t lc0 = (uint32_t)(uintptr_t)(lds_ptr_t)lc, ls0 = (uint32_t)(uintptr_t)(lds_ptr_t)ls;
   auto load = [&](int s, int buf, int l, uint32_t shift) {
+    if constexpr (!RAGGED) shift = 0;
     const int64_t k0 = (int64_t)s * kStep;
     const uint32_t to = lc0 + buf * R * kStep;
     if (l < MI) {
@@ -343,8 +345,7 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     } else if (l < MI + NI) {
       lds_load16_at(b0 + k0, off[l] + shift, to + BM * kStep + (wave * NI + l - MI) * 1024);
     } else {
-      const int q = wave + 4 * (l - MI - NI);
-      if (R / 64 % 4 == 0 || q < R / 64) lds_load1_at(sp[l - MI - NI] + s, ls0 + buf * R * 4 + 256 * q);
+      lds_load1_at(sp[l - MI - NI] + s, ls0 + buf * R * 4 + 256 * (wave + 4 * (l - MI - NI)));
     }
   };
   auto issue = [&](int s, int buf) {
@@ -377,11 +378,15 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   // A k-step is four quarters of HA x HB output tiles: (A0, B0), (A0, B1),
-  // (A1, B1), (A1, B0). Each quarter's MFMAs run while the fragments of the
-  // next one are read from LDS; the last runs after the barrier that says the
-  // next stage is there and this one has been read by all, so it also covers
-  // the next stage's first fragments and the loads of the stage after it.
-  // The B half that the last quarter does not use takes the next stage's B0.
+  // (A1, B1), (A1, B0). All of the stage's fragments have been read when the
+  // first quarter ends; behind a barrier the stage after the next is loaded into
+  // its place, spread over the other three: a CU takes a 1 KB load in 16 clocks,
+  // so four waves that issue theirs back to back wait for each other, with their
+  // MFMAs behind them (all loads beside one quarter: 1.47 us a step; spread:
+  // see the figures above). Before the last quarter the next stage's loads are
+  // waited for, three to six quarters after they were issued, and a second
+  // barrier makes them everyone's; its first fragments are read beside the last
+  // quarter's MFMAs. The B half that quarter does not use takes the next B0.
   constexpr int HA = MI / 2, HB = NI / 2;
   const int ra = (wave & 1) * 16 * MI + col, rb = BM + (wave >> 1) * 16 * NI + col;
   const int fx = 16 * (grp ^ (col & 7));
@@ -443,6 +448,7 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     for (int i = 0; i < HA; ++i)
 #pragma unroll
       for (int j = 0; j < HB; ++j) {
+        pin(acc[i0 + i][j0 + j]);
         acc[i0 + i][j0 + j] = step(b[j], a[i], acc[i0 + i][j0 + j]);
         pin(acc[i0 + i][j0 + j]);
         beside(i * HB + j);
@@ -460,22 +466,34 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   auto kstep = [&](auto next, auto load_later, int s, int later, int buf, Raw(&first)[HB],
                    Raw(&second)[HB]) {
     constexpr bool NEXT = decltype(next)::value, LOAD = decltype(load_later)::value;
-    quarter(A0, first, 0, 0, [&](int q) {
-      spread(q, HB, [&](int x) { read_b(second[x], buf, HB + x); });
-    });
-    quarter(A0, second, 0, HB, [&](int q) {
-      spread(q, HA, [&](int x) { read_a(A1[x], buf, HA + x); });
-    });
-    quarter(A1, second, HA, HB, [](int) {});
-    if constexpr (NEXT) {
-      EMK_WAIT_VMCNT(0);
-      lds_barrier();
-      if (s + 1 == last) clear(buf ^ 1);
-    }
     const uint32_t shift = later == last ? skip : 0u;
+    // load x stands beside MFMA 3 kQ x / kLoads of the last three quarters
+    auto loads = [&](int slot) {
+      if constexpr (LOAD) {
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x)
+          if (slot == x * 3 * kQ / kLoads) load(later, buf, x, shift);
+      }
+    };
+    constexpr int kEarly = (2 * kLoads + 2) / 3;  // in the second and third quarter
+    quarter(A0, first, 0, 0, [&](int q) {
+      spread(q, HB + HA, [&](int x) {
+        if (x < HB)
+          read_b(second[x], buf, HB + x);
+        else
+          read_a(A1[x - HB], buf, HA + x - HB);
+      });
+    });
+    if constexpr (LOAD) lds_barrier();  // every wave has read this stage
+    quarter(A0, second, 0, HB, [&](int q) { loads(q); });
+    quarter(A1, second, HA, HB, [&](int q) { loads(kQ + q); });
+    if constexpr (NEXT) {
+      EMK_WAIT_VMCNT(LOAD ? kEarly : 0);  // the next stage: all but the loads just issued
+      lds_barrier();
+      if (RAGGED && s + 1 == last) clear(buf ^ 1);
+    }
     quarter(A1, first, HA, 0, [&](int q) {
-      if constexpr (LOAD)
-        spread(q, kLoads, [&](int x) { load(later, buf, x, shift); });
+      loads(2 * kQ + q);
       if constexpr (NEXT)
         spread(q, HA + HB, [&](int x) {  // A0[0], B0, the rest of A0
           if (x == 0)
@@ -492,7 +510,7 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     issue(min(s0 + 1, s1 - 1), buf ^ 1);
     EMK_WAIT_VMCNT(0);
     lds_barrier();
-    if (s0 == last) clear(buf);
+    if (RAGGED && s0 == last) clear(buf);
 #pragma unroll
     for (int i = 0; i < HA; ++i) read_a(A0[i], buf, i);
 #pragma unroll
@@ -723,11 +741,18 @@ hipError_t product_tiles(const BlockProduct& p, const Plan& plan, hipStream_t st
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   TileMap t{(unsigned)tm, (unsigned)tn, plan.per, static_cast<float*>(p.work), part_pitch(p.n)};
   const dim3 grid((unsigned)(tm * tn), (unsigned)plan.splits);
+  const bool ragged = p.k % kStep != 0;
   if (plan.splits == 1) {
-    product_tile_kernel<MI, NI, OT, false><<<grid, 256, 0, st>>>(p, t);
+    if (ragged)
+      product_tile_kernel<MI, NI, OT, false, true><<<grid, 256, 0, st>>>(p, t);
+    else
+      product_tile_kernel<MI, NI, OT, false, false><<<grid, 256, 0, st>>>(p, t);
     return hipGetLastError();
   }
-  product_tile_kernel<MI, NI, OT, true><<<grid, 256, 0, st>>>(p, t);
+  if (ragged)
+    product_tile_kernel<MI, NI, OT, true, true><<<grid, 256, 0, st>>>(p, t);
+  else
+    product_tile_kernel<MI, NI, OT, true, false><<<grid, 256, 0, st>>>(p, t);
   const int64_t threads = p.m * (t.part_ld / 4);
   join_kernel<OT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
       t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo);
