@@ -552,12 +552,32 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
       return;
     }
   }
+  const int64_t mw = m0 + ra, nw = n0 + (rb - BM) - col;  // the wave's first column, this lane's row
+  if constexpr (F8 && !SPLIT) {
+    if (mrows == BM && nrows == BN) {
+      // 16 bytes per lane: lanes of odd groups trade their values of tile j for the
+      // even groups' values of tile j + 1
+      uint16_t* out = static_cast<uint16_t*>(p.out) + mw * p.ldo + nw + 16 * (grp & 1) + 8 * (grp >> 1);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; j += 2) {
+          const f32x4 x = acc[i][j], y = acc[i][j + 1];
+          const auto lo = __builtin_amdgcn_permlane16_swap(pack2<OT>(x[0], x[1]),
+                                                           pack2<OT>(y[0], y[1]), false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(pack2<OT>(x[2], x[3]),
+                                                           pack2<OT>(y[2], y[3]), false, false);
+          store_any(out + 16 * i * p.ldo + 16 * j, u32x4{lo[0], hi[0], lo[1], hi[1]});
+        }
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t m = m0 + ra + 16 * i;
+    const int64_t m = mw + 16 * i;
     if (m >= p.m) continue;
 #pragma unroll
-    for (int j = 0; j < NI; ++j) put(m, n0 + (rb - BM) - col + 16 * j + 4 * grp, acc[i][j]);
+    for (int j = 0; j < NI; ++j) put(m, nw + 16 * j + 4 * grp, acc[i][j]);
   }
 }
 
