@@ -481,6 +481,31 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
                         int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
                         void* stream);
 
+/* The forward pass of y = x w^T for training, and its gradients: all numbers are
+ * encoded in the calls, and the rounding passes gradients straight through.
+ *   forward   out = Q(X) Q(W)^T, Q(X) with blocks along rows, Q(W) in tiles
+ *   gradient  dX = Q(dY) Q(W),   dW = Qt(dY) Qt(X)^T, Qt the transpose with
+ *             blocks along its rows (the rows of X)
+ * The forward pass leaves what the gradients need in
+ *   saved  device, emeans_block_train_saved(m, n, k) bytes: transposed codes of
+ *          X and W (1 byte a value) and their scales
+ * need: what the gradient pass will be asked for, 1 dX, 2 dW, 3 both (only that
+ * is made). dX, dW: device, m x k and n x k, or NULL (not computed).
+ *   work   device, emeans_block_train_work(m, n, k, 0 forward / 1 gradient)
+ *          bytes, 16-byte aligned, or NULL (allocated stream-ordered)
+ * saved must be 16-byte aligned. With m = 0 dW is zeros.
+ * Errors: as emeans_block_matmul; EINVAL for n or k < 1 and need outside 0..3. */
+int64_t emeans_block_train_saved(int64_t m, int64_t n, int32_t k);
+int64_t emeans_block_train_work(int64_t m, int64_t n, int32_t k, int32_t gradient);
+int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, const void* W,
+                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int32_t k,
+                               int32_t need, void* out, int32_t out_dtype, int64_t ldo,
+                               void* saved, void* work, void* stream);
+int emeans_block_train_gradient(const void* dY, int32_t dtype, int64_t lddy, const void* saved,
+                                int64_t m, int64_t n, int32_t k, void* dX, int32_t dx_dtype,
+                                int64_t lddx, void* dW, int32_t dw_dtype, int64_t lddw,
+                                void* work, void* stream);
+
 /* A store ("cache") of `rows` rows of d codes (contiguous, EMEANS_F8 or
  * EMEANS_I8) with one scale for each block of `block` values along the row (a
  * multiple of 16, at most 256; the last block of a row may be short).

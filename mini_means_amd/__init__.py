@@ -104,6 +104,16 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = c_i64
         L.emeans_block_linear.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
                                           c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_vp]
+        L.emeans_block_train_saved.argtypes = [c_i64, c_i64, c_i32]
+        L.emeans_block_train_saved.restype = c_i64
+        L.emeans_block_train_work.argtypes = [c_i64, c_i64, c_i32, c_i32]
+        L.emeans_block_train_work.restype = c_i64
+        L.emeans_block_train_forward.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_i64,
+                                                 c_i64, c_i32, c_i32, c_vp, c_i32, c_i64, c_vp,
+                                                 c_vp, c_vp]
+        L.emeans_block_train_gradient.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_i64, c_i32,
+                                                  c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_vp,
+                                                  c_vp]
         L.emeans_cache_write.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i32, c_i64, c_i64, c_vp,
                                          c_i32, c_vp, c_vp, c_i64, c_i32, c_i32, c_vp]
         L.emeans_cache_read.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32,
@@ -112,6 +122,7 @@ def lib() -> ctypes.CDLL:
                                               c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_i32,
                                               c_i64, c_vp]
         for f in ("emeans_block_encode", "emeans_block_matmul", "emeans_block_linear",
+                  "emeans_block_train_forward", "emeans_block_train_gradient",
                   "emeans_cache_write", "emeans_cache_read", "emeans_cache_read_pages"):
             getattr(L, f).restype = ctypes.c_int
         L.emeans_last_error.restype = ctypes.c_char_p
@@ -431,88 +442,85 @@ def fp8_decode(C, shift, scale: float, stream=None):
 
 
 # ---- block codes: 8-bit codes with one power-of-two scale per block ----------
+# These calls are short (a token's layer takes microseconds), so the checks read
+# each attribute once.
 
 BLOCK = 128  # values per scale of the matrix codes
 
 
-def _types():
-    """(number types, code formats) by torch dtype, made on first use."""
-    global _NUMBERS, _FORMATS
-    import torch
-    _NUMBERS = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    _FORMATS = {torch.float8_e4m3fn: F8, torch.int8: I8}
-    return _NUMBERS, _FORMATS
+class _Types:
+    """torch and its types, looked up on first use."""
+    torch = None
 
 
-_NUMBERS = _FORMATS = None
+def _T():
+    t = _Types
+    if t.torch is None:
+        import torch
+        t.numbers = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+        t.formats = {torch.float8_e4m3fn: F8, torch.int8: I8}
+        t.codes = (torch.float8_e4m3fn,)
+        t.bytes = (torch.float8_e8m0fnu, torch.uint8)
+        t.stream = torch._C._cuda_getCurrentRawStream
+        t.current = torch.cuda.current_device
+        t.torch = torch
+    return t
 
 
 def _number(dtype, what: str) -> int:
-    code = (_NUMBERS or _types()[0]).get(dtype)
+    code = _T().numbers.get(dtype)
     if code is None:
         raise EmeansError(f"EDTYPE: {what} {dtype} not supported (float32, bfloat16 or float16)")
     return code
 
 
-class _queue:
-    """Where a call runs: the tensor's device made current, new tensors
-    allocated on the stream that the library works on (.ptr)."""
-
-    def __init__(self, X, stream, what="X"):
-        import torch
-        if not getattr(X, "is_cuda", False):
-            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU")
-        i = X.device.index
-        self._on = None
-        if stream is not None:
-            self._on = torch.cuda.stream(stream)
-            self.ptr = stream.cuda_stream
-        else:
-            if i != torch.cuda.current_device():
-                self._on = torch.cuda.device(i)
-            self.ptr = torch._C._cuda_getCurrentRawStream(i)
-        self.index = i
-
-    def __enter__(self):
-        if self._on is not None:
-            self._on.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._on is not None:
-            self._on.__exit__(*exc)
-
-    def matrix(self, A, what, dtypes, names):
-        """A 2-D tensor on this device whose rows are runs of values; its row
-        distance."""
-        if not getattr(A, "is_cuda", False) or A.device.index != self.index:
-            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
-        if A.dtype not in dtypes:
-            raise EmeansError(f"EDTYPE: {what} must be {names} (got {A.dtype})")
-        if A.dim() != 2 or (A.stride(1) != 1 and A.shape[1] > 1 and A.numel()):
-            raise EmeansError(f"EINVAL: {what} must be 2-D with adjacent values in a row")
-        return A.stride(0)
+def _device_of(X, what="X") -> int:
+    if not getattr(X, "is_cuda", False):
+        raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU")
+    return X.get_device()
 
 
-def _byte_types():
-    import torch
-    return (torch.float8_e8m0fnu, torch.uint8)
+def _elsewhere(device: int, stream):
+    """The context a call has to enter: the given stream, so that new tensors
+    are allocated where the library works, or the tensors' device; None where
+    it is the current one already."""
+    t = _T()
+    if stream is not None:
+        return t.torch.cuda.stream(stream)
+    return t.torch.cuda.device(device) if device != t.current() else None
 
 
-def _codes_room(n: int, d: int, device):
-    """Codes n x d with rows a multiple of 16 bytes apart, and the scales
-    n_s x ceil(d/128) made by _scales_room: what the product reads fastest."""
-    import torch
-    pitch = (d + 15) // 16 * 16
-    room = torch.empty((n, pitch), dtype=torch.float8_e4m3fn, device=device)
+def _run(device: int, stream, call):
+    """call(stream pointer) where the tensors live."""
+    ctx = _elsewhere(device, stream)
+    if ctx is None:
+        return call(_T().stream(device))
+    with ctx:
+        return call(stream.cuda_stream if stream is not None else _T().stream(device))
+
+
+def _matrix(A, device: int, what, dtypes, names):
+    """A 2-D tensor on that device whose rows are runs of values: its rows,
+    columns and row distance."""
+    if not getattr(A, "is_cuda", False) or A.get_device() != device:
+        raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
+    if A.dtype not in dtypes:
+        raise EmeansError(f"EDTYPE: {what} must be {names} (got {A.dtype})")
+    shape = A.shape
+    if len(shape) != 2:
+        raise EmeansError(f"EINVAL: {what} must be 2-D with adjacent values in a row")
+    n, d = shape
+    ld, one = A.stride()
+    if one != 1 and d > 1 and n:
+        raise EmeansError(f"EINVAL: {what} must be 2-D with adjacent values in a row")
+    return n, d, ld
+
+
+def _room(n: int, d: int, unit: int, dtype, device):
+    """n x d one-byte values with rows a multiple of `unit` bytes apart."""
+    pitch = -(-d // unit) * unit
+    room = _T().torch.empty((n, pitch), dtype=dtype, device=device)
     return room if pitch == d else room[:, :d]
-
-
-def _scales_room(n: int, nb: int, device):
-    import torch
-    pitch = (nb + 3) // 4 * 4
-    room = torch.empty((n, pitch), dtype=torch.float8_e8m0fnu, device=device)
-    return room if pitch == nb else room[:, :nb]
 
 
 def block_encode(X, *, tiles: bool = False, rows: bool = True, cols: bool = False, stream=None):
@@ -528,49 +536,48 @@ def block_encode(X, *, tiles: bool = False, rows: bool = True, cols: bool = Fals
     a block is a 128 x 128 tile, scales ceil(n/128) x ceil(d/128), and both
     orders hold the same codes (the form for weights). Rows of codes start at
     multiples of 16 bytes: for other d the tensors are views of wider ones."""
-    with _queue(X, stream) as q:
-        dt = _number(X.dtype, "X")
-        ldx = q.matrix(X, "X", (X.dtype,), "")
-        if not rows and not cols:
-            raise EmeansError("EINVAL: block_encode makes rows, cols or both")
-        n, d = X.shape
-        if X.stride(0) < d and n > 1:
-            raise EmeansError("EINVAL: the rows of X overlap")
-        nb, db = -(-n // BLOCK), -(-d // BLOCK)
+    dev = _device_of(X)
+    dt = _number(X.dtype, "X")
+    n, d, ldx = _matrix(X, dev, "X", (X.dtype,), "")
+    if not rows and not cols:
+        raise EmeansError("EINVAL: block_encode makes rows, cols or both")
+    if ldx < d and n > 1:
+        raise EmeansError("EINVAL: the rows of X overlap")
+    nb, db = -(-n // BLOCK), -(-d // BLOCK)
+
+    def call(st):
+        f8, e8 = _T().codes[0], _T().bytes[0]
         out = [None] * 4
-        args = [None, 0, None, 0, None, 0, None, 0]
         if rows:
-            out[0], out[1] = _codes_room(n, d, X.device), \
-                _scales_room(nb if tiles else n, db, X.device)
+            out[0] = _room(n, d, 16, f8, X.device)
+            out[1] = _room(nb if tiles else n, db, 4, e8, X.device)
         if cols:
-            out[2], out[3] = _codes_room(d, n, X.device), \
-                _scales_room(db if tiles else d, nb, X.device)
+            out[2] = _room(d, n, 16, f8, X.device)
+            out[3] = _room(db if tiles else d, nb, 4, e8, X.device)
         if n and d:
-            for i, t in enumerate(out):
-                if t is not None:
-                    args[2 * i], args[2 * i + 1] = t.data_ptr(), t.stride(0)
-            _check(lib().emeans_block_encode(X.data_ptr(), dt, n, d, ldx, 1 if tiles else 0,
-                                             *args, q.ptr))
-    return tuple(out) if cols else (out[0], out[1])
+            args = [v for t in out for v in ((None, 0) if t is None else (t.data_ptr(), t.stride(0)))]
+            _check(lib().emeans_block_encode(X.data_ptr(), dt, n, d, ldx, 1 if tiles else 0, *args,
+                                             st))
+        return tuple(out) if cols else (out[0], out[1])
+
+    return _run(dev, stream, call)
 
 
-def _product_side(q, codes, scales, what):
-    """Arguments of one side of the product; True if its scales stand per tile."""
-    import torch
-    ld = q.matrix(codes, what, (torch.float8_e4m3fn,), "float8_e4m3fn codes")
-    lds = q.matrix(scales, f"{what}_scales", _byte_types(), "float8_e8m0fnu or uint8 scales")
-    n, k = codes.shape
-    kb = -(-k // BLOCK)
-    if scales.shape[1] != kb or scales.shape[0] not in (n, -(-n // BLOCK)):
-        raise EmeansError(f"EINVAL: {what}_scales must be {n} x {kb} (rows) or {-(-n // BLOCK)} x "
-                          f"{kb} (tiles), got {tuple(scales.shape)}")
-    return ld, lds, scales.shape[0] != n
+def _product_side(dev, codes, scales, what):
+    """Rows, columns and row distances of one side of the product, and whether
+    its scales stand per tile."""
+    t = _T()
+    n, k, ld = _matrix(codes, dev, what, t.codes, "float8_e4m3fn codes")
+    sn, sk, lds = _matrix(scales, dev, "its scales", t.bytes, "float8_e8m0fnu or uint8 scales")
+    if sk != -(-k // BLOCK) or (sn != n and sn != -(-n // BLOCK)):
+        raise EmeansError(f"EINVAL: scales of {what} must be {n} x {-(-k // BLOCK)} (rows) or "
+                          f"{-(-n // BLOCK)} x {-(-k // BLOCK)} (tiles), got {sn} x {sk}")
+    return n, k, ld, lds, sn != n
 
 
 def _product_out(m, n, out, out_dtype, device):
-    import torch
     if out is None:
-        return torch.empty((m, n), dtype=out_dtype, device=device)
+        return _T().torch.empty((m, n), dtype=out_dtype, device=device)
     if not (getattr(out, "is_cuda", False) and out.device == device and out.dtype == out_dtype
             and out.shape == (m, n) and (out.stride(1) == 1 or n <= 1)):
         raise EmeansError(f"EINVAL: out must be an {m} x {n} {out_dtype} GPU tensor with adjacent "
@@ -578,17 +585,9 @@ def _product_out(m, n, out, out_dtype, device):
     return out
 
 
-class _Work:
-    """Working memory of one call, allocated where the call runs."""
-
-    def __init__(self, need, device):
-        import torch
-        self.room = torch.empty((need,), dtype=torch.uint8, device=device)
-        self.data_ptr = self.room.data_ptr
-
-
 def _work(need: int, device):
-    return _Work(need, device) if need else None
+    """Working memory of one call, allocated where the call runs; None for none."""
+    return _T().torch.empty((need,), dtype=_T().torch.uint8, device=device) if need else None
 
 
 def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=None):
@@ -598,57 +597,61 @@ def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=N
     (sums in fp32), bfloat16 (the default) or float16 (sums of the FP8 matrix
     unit, off by about 1.5e-5 of the result's norm). out: a tensor to write
     into."""
-    import torch
-    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    out_dtype = out_dtype or (out.dtype if out is not None else _T().torch.bfloat16)
     ot = _number(out_dtype, "out_dtype")
-    with _queue(a, stream, "a") as q:
-        lda, ldas, a_tiles = _product_side(q, a, a_scales, "a")
-        ldb, ldbs, b_tiles = _product_side(q, b, b_scales, "b")
-        m, k = a.shape
-        n = b.shape[0]
-        if b.shape[1] != k:
-            raise EmeansError(f"EINVAL: a has {k} columns, b has {b.shape[1]}")
-        if a_tiles:
-            raise EmeansError("EINVAL: a_scales must stand per row (tiles are for b)")
-        out = _product_out(m, n, out, out_dtype, a.device)
+    dev = _device_of(a, "a")
+    m, k, lda, ldas, a_tiles = _product_side(dev, a, a_scales, "a")
+    n, kb, ldb, ldbs, b_tiles = _product_side(dev, b, b_scales, "b")
+    if kb != k:
+        raise EmeansError(f"EINVAL: a has {k} columns, b has {kb}")
+    if a_tiles:
+        raise EmeansError("EINVAL: a_scales must stand per row (tiles are for b)")
+
+    def call(st):
+        y = _product_out(m, n, out, out_dtype, a.device)
         if m and n:
             L = lib()
             work = _work(L.emeans_block_matmul_work(m, n, k), a.device)
             _check(L.emeans_block_matmul(a.data_ptr(), lda, a_scales.data_ptr(), ldas,
                                          b.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
-                                         1 if b_tiles else 0, m, n, k, out.data_ptr(), ot,
-                                         out.stride(0), work and work.data_ptr(), q.ptr))
-    return out
+                                         1 if b_tiles else 0, m, n, k, y.data_ptr(), ot,
+                                         y.stride(0), None if work is None else work.data_ptr(),
+                                         st))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def _linear_codes(x, w, w_scales, out_dtype, stream):
     """x (m x k numbers) times the transpose of codes: one library call."""
-    import torch
-    with _queue(x, stream) as q:
-        dt = _number(x.dtype, "X")
-        ldx = q.matrix(x, "X", (x.dtype,), "")
-        ldb, ldbs, tiles = _product_side(q, w, w_scales, "w")
-        m, k = x.shape
-        n = w.shape[0]
-        if w.shape[1] != k:
-            raise EmeansError(f"EINVAL: X has {k} columns, w has {w.shape[1]}")
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
+    dev = x.get_device()
+    dt = _number(x.dtype, "X")
+    ot = _number(out_dtype, "out_dtype")
+    m, k, ldx = _matrix(x, dev, "X", (x.dtype,), "")
+    n, kw, ldb, ldbs, tiles = _product_side(dev, w, w_scales, "w")
+    if kw != k:
+        raise EmeansError(f"EINVAL: X has {k} columns, w has {kw}")
+
+    def call(st):
+        y = _T().torch.empty((m, n), dtype=out_dtype, device=x.device)
         if m and n:
             L = lib()
             work = _work(L.emeans_block_linear_work(m, n, k), x.device)
             _check(L.emeans_block_linear(x.data_ptr(), dt, ldx, w.data_ptr(), ldb,
                                          w_scales.data_ptr(), ldbs, 1 if tiles else 0, m, n, k,
-                                         out.data_ptr(), _number(out_dtype, "out_dtype"),
-                                         out.stride(0), work and work.data_ptr(), q.ptr))
-    return out
+                                         y.data_ptr(), ot, n,
+                                         None if work is None else work.data_ptr(), st))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def _rows(t):
     """t as a matrix whose rows are runs that do not overlap (a copy if it is
     not one: an expanded gradient, say)."""
-    if (t.stride(1) == 1 or t.shape[1] <= 1) and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1):
-        return t
-    return t.contiguous()
+    n, d = t.shape
+    ld, one = t.stride()
+    return t if (one == 1 or d <= 1) and (ld >= d or n <= 1) else t.contiguous()
 
 
 _linear_function = None
@@ -657,43 +660,80 @@ _linear_function = None
 def _linear_fn():
     global _linear_function
     if _linear_function is None:
-        import torch
+        torch = _T().torch
 
         class BlockLinear(torch.autograd.Function):
             """y = Q(x) Q(w)^T; the rounding passes gradients straight through."""
 
             @staticmethod
-            def forward(ctx, x, w, frozen, out_dtype, stream):
-                need_x, need_w = ctx.needs_input_grad[:2]
-                xr, xs, xc, xcs = block_encode(x, cols=True, stream=stream) if need_w else \
-                    (*block_encode(x, stream=stream), None, None)
-                if frozen is not None:
-                    wr, ws, wc, wcs = frozen
-                elif need_x:
-                    wr, ws, wc, wcs = block_encode(w, tiles=True, cols=True, stream=stream)
-                else:
-                    wr, ws, wc, wcs = *block_encode(w, tiles=True, stream=stream), None, None
-                ctx.save_for_backward(xc, xcs, wc if need_x else None, wcs if need_x else None)
-                ctx.types = x.dtype, None if w is None else w.dtype, stream
-                return block_matmul(xr, xs, wr, ws, out_dtype=out_dtype, stream=stream)
+            def forward(ctx, x, w, out_dtype, stream):
+                dev = x.get_device()
+                dt, wt = _number(x.dtype, "X"), _number(w.dtype, "w")
+                ot = _number(out_dtype, "out_dtype")
+                m, k, ldx = _matrix(x, dev, "X", (x.dtype,), "")
+                n, _, ldw = _matrix(w, dev, "w", (w.dtype,), "")
+                if n < 1 or k < 1:
+                    raise EmeansError("EINVAL: w must have rows and columns")
+                need = sum(b for b, g in zip((1, 2), ctx.needs_input_grad) if g)
+                L = lib()
+
+                def call(st):
+                    y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+                    saved = _work(L.emeans_block_train_saved(m, n, k), x.device)
+                    work = _work(L.emeans_block_train_work(m, n, k, 0), x.device)
+                    if m:
+                        _check(L.emeans_block_train_forward(
+                            x.data_ptr(), dt, ldx, w.data_ptr(), wt, ldw, m, n, k, need,
+                            y.data_ptr(), ot, n, saved.data_ptr(), work.data_ptr(), st))
+                    return y, saved
+
+                y, saved = _run(dev, stream, call)
+                ctx.save_for_backward(saved)
+                ctx.args = m, n, k, x.dtype, dt, w.dtype, wt, stream
+                return y
 
             @staticmethod
             @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
-                xc, xcs, wc, wcs = ctx.saved_tensors
-                x_type, w_type, stream = ctx.types
-                dy = _rows(dy)
+                saved, = ctx.saved_tensors
+                m, n, k, x_type, dt, w_type, wt, stream = ctx.args
                 need_x, need_w = ctx.needs_input_grad[:2]
-                dx = dw = None
-                gr, gs, gc, gcs = block_encode(dy, rows=need_x, cols=True, stream=stream) \
-                    if need_w else (*block_encode(dy, stream=stream), None, None)
-                if need_x:
-                    dx = block_matmul(gr, gs, wc, wcs, out_dtype=x_type, stream=stream)
-                if need_w:
-                    dw = block_matmul(gc, gcs, xc, xcs, out_dtype=w_type, stream=stream)
-                return dx, dw, None, None, None
+                L = lib()
 
-        _linear_function = BlockLinear
+                def call(st):
+                    g = _rows(dy)
+                    dx = torch.empty((m, k), dtype=x_type, device=g.device) if need_x else None
+                    dw = torch.empty((n, k), dtype=w_type, device=g.device) if need_w else None
+                    work = _work(L.emeans_block_train_work(m, n, k, 1), g.device)
+                    if m or need_w:
+                        _check(L.emeans_block_train_gradient(
+                            g.data_ptr(), _number(g.dtype, "the gradient"), g.stride(0),
+                            saved.data_ptr() if m else None, m, n, k,
+                            dx.data_ptr() if need_x else None, dt, k,
+                            dw.data_ptr() if need_w else None, wt, k,
+                            work.data_ptr() if m else None, st))
+                    return dx, dw
+
+                return *_run(dy.get_device(), stream, call), None, None
+
+        class BlockLinearFrozen(torch.autograd.Function):
+            """The same with w as codes in both orders: a gradient of x alone."""
+
+            @staticmethod
+            def forward(ctx, x, frozen, out_dtype, stream):
+                w, s, wc, wcs = frozen
+                ctx.save_for_backward(wc, wcs)
+                ctx.args = x.dtype, stream
+                return _linear_codes(x, w, s, out_dtype, stream)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                wc, wcs = ctx.saved_tensors
+                x_type, stream = ctx.args
+                return _linear_codes(_rows(dy), wc, wcs, x_type, stream), None, None, None
+
+        _linear_function = BlockLinear, BlockLinearFrozen
     return _linear_function
 
 
@@ -712,73 +752,78 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
 
     On `stream` (the current one by default) the backward pass runs too; its
     caller orders the gradients' use, as for any work on another stream."""
-    import torch
-    if not getattr(X, "is_cuda", False):
-        raise EmeansError("ENOTDEVICE: X must be a tensor on the GPU")
+    _device_of(X)
     out_dtype = out_dtype or X.dtype
-    lead = X.shape[:-1]
-    x = X if X.dim() == 2 else X.reshape(-1, X.shape[-1])
-    frozen = w if isinstance(w, (tuple, list)) else None
-    if frozen is not None and len(frozen) not in (2, 4):
-        raise EmeansError("EINVAL: w must be a tensor, (codes, scales) or the four of "
-                          "block_encode(w, tiles=True, cols=True)")
-    grad = torch.is_grad_enabled() and (X.requires_grad or (frozen is None and w.requires_grad))
-    if grad:
-        if frozen is not None and len(frozen) != 4:
-            raise EmeansError("EINVAL: the gradient of X needs the transposed codes of w: pass "
-                              "the four of block_encode(w, tiles=True, cols=True)")
-        wt = None if frozen is not None else w
-        if wt is not None and (wt.dim() != 2 or wt.shape[1] != x.shape[1]):
-            raise EmeansError(f"EINVAL: w must be n x {x.shape[1]}")
-        y = _linear_fn().apply(_rows(x), wt if wt is None else _rows(wt), frozen, out_dtype, stream)
+    flat = X.dim() == 2
+    x = X if flat else X.reshape(-1, X.shape[-1])
+    grad = _T().torch.is_grad_enabled()
+    if isinstance(w, (tuple, list)):
+        if len(w) not in (2, 4):
+            raise EmeansError("EINVAL: w must be a tensor, (codes, scales) or the four of "
+                              "block_encode(w, tiles=True, cols=True)")
+        if grad and X.requires_grad:
+            if len(w) != 4:
+                raise EmeansError("EINVAL: the gradient of X needs the transposed codes of w: pass "
+                                  "the four of block_encode(w, tiles=True, cols=True)")
+            y = _linear_fn()[1].apply(_rows(x), tuple(w), out_dtype, stream)
+        else:
+            y = _linear_codes(_rows(x), w[0], w[1], out_dtype, stream)
     else:
-        codes, scales = frozen[:2] if frozen is not None else \
-            block_encode(w, tiles=True, stream=stream)
-        y = _linear_codes(_rows(x), codes, scales, out_dtype, stream)
-    return y if X.dim() == 2 else y.view(*lead, y.shape[1])
+        if w.dim() != 2 or w.shape[1] != x.shape[1]:
+            raise EmeansError(f"EINVAL: w must be n x {x.shape[1]}")
+        if grad and (X.requires_grad or w.requires_grad):
+            y = _linear_fn()[0].apply(_rows(x), _rows(w), out_dtype, stream)
+        else:
+            y = _linear_codes(_rows(x), *block_encode(_rows(w), tiles=True, stream=stream),
+                              out_dtype, stream)
+    return y if flat else y.view(*X.shape[:-1], y.shape[1])
 
 
 def cache_new(rows, d: int, *, block: int = BLOCK, dtype=None, device="cuda"):
     """An empty store of codes: (codes, scales) of shape rows + (d,) and rows +
     (ceil(d / block),), rows a number or a shape such as (pages, rows per
     page). dtype float8_e4m3fn (default) or int8. Its rows read as zeros."""
-    import torch
+    torch = _T().torch
     shape = (rows,) if isinstance(rows, int) else tuple(rows)
     dtype = dtype or torch.float8_e4m3fn
-    if dtype not in (_FORMATS or _types()[1]):
+    if dtype not in _T().formats:
         raise EmeansError(f"EDTYPE: {dtype} not supported (float8_e4m3fn or int8)")
     codes = torch.zeros((*shape, d), dtype=torch.uint8, device=device).view(dtype)
     scales = torch.full((*shape, -(-d // block)), 127, dtype=torch.uint8, device=device)
     return codes, scales.view(torch.float8_e8m0fnu)
 
 
-def _store(q, codes, scales, block):
-    fmt = (_FORMATS or _types()[1]).get(codes.dtype)
+def _store(dev, codes, scales, block):
+    """Format, rows and row length of a store."""
+    t = _T()
+    fmt = t.formats.get(codes.dtype)
     if fmt is None:
         raise EmeansError(f"EDTYPE: codes must be float8_e4m3fn or int8 (got {codes.dtype})")
-    if scales.dtype not in _byte_types():
+    if scales.dtype not in t.bytes:
         raise EmeansError(f"EDTYPE: scales must be float8_e8m0fnu or uint8 (got {scales.dtype})")
-    for t, what in ((codes, "codes"), (scales, "scales")):
-        if not getattr(t, "is_cuda", False) or t.device.index != q.index:
-            raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
-        if not t.is_contiguous() or t.dim() < 2:
-            raise EmeansError(f"EINVAL: {what} must be contiguous, rows last but one")
-    d = codes.shape[-1]
-    if block < 1 or codes.shape[:-1] != scales.shape[:-1] or scales.shape[-1] != -(-d // block):
-        raise EmeansError(f"EINVAL: scales must be {tuple(codes.shape[:-1])} x ceil({d} / {block}),"
-                          f" got {tuple(scales.shape)}")
+    if not codes.is_cuda or not scales.is_cuda or codes.get_device() != dev \
+            or scales.get_device() != dev:
+        raise EmeansError("ENOTDEVICE: codes and scales must be tensors on the GPU of the others")
+    shape, sshape = codes.shape, scales.shape
+    if len(shape) < 2 or not codes.is_contiguous() or not scales.is_contiguous():
+        raise EmeansError("EINVAL: codes and scales must be contiguous, rows last but one")
+    d = shape[-1]
+    if block < 1 or shape[:-1] != sshape[:-1] or sshape[-1] != -(-d // block):
+        raise EmeansError(f"EINVAL: scales must be {tuple(shape[:-1])} x ceil({d} / {block}), got "
+                          f"{tuple(sshape)}")
     return fmt, codes.numel() // d if d else 0, d
 
 
-def _slots(q, slots, n=None):
-    import torch
-    if not getattr(slots, "is_cuda", False) or slots.device.index != q.index:
+def _slots(dev, slots, n=None):
+    if not getattr(slots, "is_cuda", False) or slots.get_device() != dev:
         raise EmeansError("ENOTDEVICE: slots must be a tensor on the GPU of the others")
-    if slots.dtype not in (torch.int32, torch.int64):
-        raise EmeansError(f"EDTYPE: slots must be int32 or int64 (got {slots.dtype})")
-    if slots.dim() != 1 or not slots.is_contiguous() or (n is not None and slots.numel() != n):
+    torch = _T().torch
+    dtype = slots.dtype
+    if dtype is not torch.int64 and dtype is not torch.int32:
+        raise EmeansError(f"EDTYPE: slots must be int32 or int64 (got {dtype})")
+    if slots.dim() != 1 or not slots.is_contiguous() or (n is not None and slots.shape[0] != n):
         raise EmeansError("EINVAL: slots must be one contiguous number per row")
-    return slots.element_size()
+    return 8 if dtype is torch.int64 else 4
 
 
 def cache_write(X, slots, codes, scales, *, block: int = BLOCK, stream=None) -> None:
@@ -788,40 +833,42 @@ def cache_write(X, slots, codes, scales, *, block: int = BLOCK, stream=None) -> 
     one scale for each `block` values of a row. The store may have any shape
     rows x d, pages x page rows x d, ...: a slot counts its rows in order.
     Negative slots and slots past its end are skipped."""
-    with _queue(X, stream) as q:
-        dt = _number(X.dtype, "X")
-        fmt, rows, d = _store(q, codes, scales, block)
-        if X.dim() not in (2, 3) or (X.stride(-1) != 1 and X.shape[-1] > 1):
-            raise EmeansError("EINVAL: X must be n x d or n x heads x width with adjacent values")
-        n = X.shape[0]
-        heads, width = (1, X.shape[1]) if X.dim() == 2 else X.shape[1:]
-        if heads * width != d:
-            raise EmeansError(f"EINVAL: X has rows of {heads * width} values, the store of {d}")
-        size = _slots(q, slots, n)
-        if n and rows:
-            _check(lib().emeans_cache_write(X.data_ptr(), dt, n, heads, width, X.stride(0),
-                                            X.stride(1) if X.dim() == 3 else width,
-                                            slots.data_ptr(), size, codes.data_ptr(),
-                                            scales.data_ptr(), rows, block, fmt, q.ptr))
+    dev = _device_of(X)
+    dt = _number(X.dtype, "X")
+    fmt, rows, d = _store(dev, codes, scales, block)
+    shape, stride = X.shape, X.stride()
+    if len(shape) not in (2, 3) or (stride[-1] != 1 and shape[-1] > 1):
+        raise EmeansError("EINVAL: X must be n x d or n x heads x width with adjacent values")
+    n, heads, width = (shape[0], 1, shape[1]) if len(shape) == 2 else shape
+    if heads * width != d:
+        raise EmeansError(f"EINVAL: X has rows of {heads * width} values, the store of {d}")
+    size = _slots(dev, slots, n)
+    if n and rows:
+        _run(dev, stream, lambda st: _check(lib().emeans_cache_write(
+            X.data_ptr(), dt, n, heads, width, stride[0], stride[1] if len(shape) == 3 else width,
+            slots.data_ptr(), size, codes.data_ptr(), scales.data_ptr(), rows, block, fmt, st)))
 
 
 def cache_read(codes, scales, slots, *, block: int = BLOCK, out_dtype=None, out=None, stream=None):
     """Rows slots (int32 or int64) of a store as numbers (len(slots) x d,
     out_dtype: bfloat16 by default, float32 or float16). A slot outside the
     store reads as zeros. out: a tensor to write into."""
-    import torch
-    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    out_dtype = out_dtype or (out.dtype if out is not None else _T().torch.bfloat16)
     ot = _number(out_dtype, "out_dtype")
-    with _queue(codes, stream, "codes") as q:
-        fmt, rows, d = _store(q, codes, scales, block)
-        size = _slots(q, slots)
-        n = slots.numel()
-        out = _product_out(n, d, out, out_dtype, codes.device)
+    dev = _device_of(codes, "codes")
+    fmt, rows, d = _store(dev, codes, scales, block)
+    size = _slots(dev, slots)
+    n = slots.shape[0]
+
+    def call(st):
+        y = _product_out(n, d, out, out_dtype, codes.device)
         if n:
             _check(lib().emeans_cache_read(codes.data_ptr(), scales.data_ptr(), rows, d, block,
-                                           fmt, slots.data_ptr(), size, n, out.data_ptr(), ot,
-                                           out.stride(0), q.ptr))
-    return out
+                                           fmt, slots.data_ptr(), size, n, y.data_ptr(), ot,
+                                           y.stride(0), st))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def cache_read_pages(codes, scales, table, starts, total: int, *, block: int = BLOCK,
@@ -832,27 +879,30 @@ def cache_read_pages(codes, scales, table, starts, total: int, *, block: int = B
     (table: seqs x pages of the longest, int32). Rows of the result outside
     every sequence, and rows whose page is negative or past the end, are zeros.
     total is the host's number: nothing is read back."""
-    import torch
+    torch = _T().torch
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
     ot = _number(out_dtype, "out_dtype")
-    with _queue(codes, stream, "codes") as q:
-        fmt, _, d = _store(q, codes, scales, block)
-        if codes.dim() != 3:
-            raise EmeansError("EINVAL: codes must be pages x page rows x d")
-        ldt = q.matrix(table, "table", (torch.int32,), "int32")
-        if not getattr(starts, "is_cuda", False) or starts.device.index != q.index:
-            raise EmeansError("ENOTDEVICE: starts must be a tensor on the GPU of the others")
-        if starts.dtype != torch.int32 or not starts.is_contiguous() \
-                or starts.shape != (table.shape[0] + 1,):
-            raise EmeansError(f"EINVAL: starts must be {table.shape[0] + 1} contiguous int32")
-        total = int(total)
-        out = _product_out(total, d, out, out_dtype, codes.device)
+    dev = _device_of(codes, "codes")
+    fmt, _, d = _store(dev, codes, scales, block)
+    if codes.dim() != 3:
+        raise EmeansError("EINVAL: codes must be pages x page rows x d")
+    seqs, table_pages, ldt = _matrix(table, dev, "table", (torch.int32,), "int32")
+    if not getattr(starts, "is_cuda", False) or starts.get_device() != dev:
+        raise EmeansError("ENOTDEVICE: starts must be a tensor on the GPU of the others")
+    if starts.dtype is not torch.int32 or not starts.is_contiguous() or starts.shape != (seqs + 1,):
+        raise EmeansError(f"EINVAL: starts must be {seqs + 1} contiguous int32")
+    total = int(total)
+
+    def call(st):
+        y = _product_out(total, d, out, out_dtype, codes.device)
         if total:
             _check(lib().emeans_cache_read_pages(
                 codes.data_ptr(), scales.data_ptr(), codes.shape[0], codes.shape[1], d, block,
-                fmt, table.data_ptr(), ldt, table.shape[1], starts.data_ptr(), table.shape[0],
-                total, out.data_ptr(), ot, out.stride(0), q.ptr))
-    return out
+                fmt, table.data_ptr(), ldt, table_pages, starts.data_ptr(), seqs, total,
+                y.data_ptr(), ot, y.stride(0), st))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def batch_rows(n: int, seed: int, pass_: int, start: int, count: int, device="cuda", stream=None):

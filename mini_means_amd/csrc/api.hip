@@ -1392,6 +1392,167 @@ done:
   return release(own, st, rc);
 }
 
+namespace {
+
+// Where the codes and scales of a rows x d matrix (tiles: one scale per tile)
+// stand in working memory, from `at` on: rows a multiple of 16 bytes apart, then
+// scales with rows a multiple of 4 bytes apart, both starts 16-byte aligned.
+struct CodesAt {
+  int64_t codes, ld, scales, lds, end;
+  CodesAt(int64_t at, int64_t rows, int64_t d, bool tiles) {
+    codes = at;
+    ld = blocks_of(d, 16) * 16;
+    scales = codes + rows * ld;
+    lds = blocks_of(blocks_of(d, 128), 4) * 4;
+    end = blocks_of(scales + (tiles ? blocks_of(rows, 128) : rows) * lds, 16) * 16;
+  }
+  uint8_t* c(void* base) const { return static_cast<uint8_t*>(base) + codes; }
+  uint8_t* s(void* base) const { return static_cast<uint8_t*>(base) + scales; }
+};
+
+struct TrainSaved {  // X^T by rows, W^T by tiles
+  CodesAt x, w;
+  TrainSaved(int64_t m, int64_t n, int64_t k) : x(0, k, m, false), w(x.end, k, n, true) {}
+};
+
+struct TrainForward {
+  CodesAt x, w;
+  int64_t own, end;
+  TrainForward(int64_t m, int64_t n, int64_t k) : x(0, m, k, false), w(x.end, n, k, true) {
+    own = w.end;
+    end = own + emeans_block_matmul_work(m, n, (int32_t)k);
+  }
+};
+
+struct TrainGradient {
+  CodesAt y, yt;
+  int64_t own, end;
+  TrainGradient(int64_t m, int64_t n, int64_t k) : y(0, m, n, false), yt(y.end, n, m, false) {
+    own = yt.end;
+    const int64_t a = emeans_block_matmul_work(m, k, (int32_t)n);
+    const int64_t b = emeans_block_matmul_work(n, k, (int32_t)m);
+    end = own + (a > b ? a : b);
+  }
+};
+
+int check_train(int64_t m, int64_t n, int32_t k, const void* saved, const void* work) {
+  int rc;
+  if ((rc = check_count(m, "m"))) return rc;
+  if (n < 1 || n >= kMaxRows) return fail(EMEANS_EINVAL, "n out of range (%lld)", (long long)n);
+  if (k < 1) return fail(EMEANS_EINVAL, "k out of range (%d)", k);
+  if ((uintptr_t)saved % 16 || (uintptr_t)work % 16)
+    return fail(EMEANS_EINVAL, "saved and work must be 16-byte aligned");
+  return EMEANS_OK;
+}
+
+bool train_sizes(int64_t m, int64_t n, int32_t k) {
+  return m >= 1 && m < kMaxRows && n >= 1 && n < kMaxRows && k >= 1;
+}
+
+}  // namespace
+
+int64_t emeans_block_train_saved(int64_t m, int64_t n, int32_t k) {
+  return train_sizes(m, n, k) ? TrainSaved(m, n, k).w.end : 0;
+}
+
+int64_t emeans_block_train_work(int64_t m, int64_t n, int32_t k, int32_t gradient) {
+  if (!train_sizes(m, n, k)) return 0;
+  return gradient ? TrainGradient(m, n, k).end : TrainForward(m, n, k).end;
+}
+
+int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, const void* W,
+                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int32_t k,
+                               int32_t need, void* out, int32_t out_dtype, int64_t ldo,
+                               void* saved, void* work, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_train(m, n, k, saved, work)) || (rc = check_number_type(x_dtype, "x_dtype")) ||
+      (rc = check_number_type(w_dtype, "w_dtype")) ||
+      (rc = check_number_type(out_dtype, "out_dtype")) || (rc = check_ld(ldx, k, m, "ldx")) ||
+      (rc = check_ld(ldw, k, n, "ldw")) || (rc = check_ld(ldo, n, m, "ldo")))
+    return rc;
+  if (need < 0 || need > 3) return fail(EMEANS_EINVAL, "need must be 0..3 (got %d)", need);
+  if (m == 0) return EMEANS_OK;
+  if (!X || !W || !out || (need && !saved))
+    return fail(EMEANS_EINVAL, "X, W, out and saved must not be NULL");
+  if ((rc = check_device(X, "X")) || (rc = check_device(W, "W")) ||
+      (rc = check_device(out, "out")) || (need && (rc = check_device(saved, "saved"))) ||
+      (work && (rc = check_device(work, "work"))))
+    return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const TrainSaved sv(m, n, k);
+  const TrainForward f(m, n, k);
+  const bool dx = need & 1, dw = need & 2;
+  void* own = nullptr;
+  rc = EMEANS_OK;
+  if (!work) HIP_TRY(hipMallocAsync(&own, f.end, st));
+  if (own) work = own;
+  if (dw)
+    HIP_TRY(launch_encode_tiles({x_dtype, X, ldx, m, k, false, f.x.c(work), f.x.ld, f.x.s(work),
+                                 f.x.lds, sv.x.c(saved), sv.x.ld, sv.x.s(saved), sv.x.lds}, st));
+  else
+    HIP_TRY(launch_encode_rows({x_dtype, X, m, k, k, ldx, 0, 128, false, nullptr, 0, m,
+                                f.x.c(work), f.x.ld, f.x.s(work), f.x.lds}, st));
+  HIP_TRY(launch_encode_tiles({w_dtype, W, ldw, n, k, true, f.w.c(work), f.w.ld, f.w.s(work),
+                               f.w.lds, dx ? sv.w.c(saved) : nullptr, sv.w.ld,
+                               dx ? sv.w.s(saved) : nullptr, sv.w.lds}, st));
+  HIP_TRY(launch_block_product({f.x.c(work), f.x.ld, f.x.s(work), f.x.lds, f.w.c(work), f.w.ld,
+                                f.w.s(work), f.w.lds, true, m, n, k, out_dtype, out, ldo,
+                                static_cast<uint8_t*>(work) + f.own}, st));
+done:
+  return release(own, st, rc);
+}
+
+int emeans_block_train_gradient(const void* dY, int32_t dtype, int64_t lddy, const void* saved,
+                                int64_t m, int64_t n, int32_t k, void* dX, int32_t dx_dtype,
+                                int64_t lddx, void* dW, int32_t dw_dtype, int64_t lddw,
+                                void* work, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_train(m, n, k, saved, work)) || (rc = check_number_type(dtype, "dtype")) ||
+      (rc = check_ld(lddy, n, m, "lddy")))
+    return rc;
+  if (dX && ((rc = check_number_type(dx_dtype, "dx_dtype")) || (rc = check_ld(lddx, k, m, "lddx"))))
+    return rc;
+  if (dW && ((rc = check_number_type(dw_dtype, "dw_dtype")) || (rc = check_ld(lddw, k, n, "lddw"))))
+    return rc;
+  if (!dX && !dW) return fail(EMEANS_EINVAL, "dX and dW are both NULL");
+  if (m == 0 && !dW) return EMEANS_OK;
+  if (m > 0 && (!dY || !saved)) return fail(EMEANS_EINVAL, "dY and saved must not be NULL");
+  if (m > 0 && ((rc = check_device(dY, "dY")) || (rc = check_device(saved, "saved")))) return rc;
+  if ((m > 0 && dX && (rc = check_device(dX, "dX"))) || (dW && (rc = check_device(dW, "dW"))) ||
+      (work && (rc = check_device(work, "work"))))
+    return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (m == 0)
+    return launched(launch_block_product({nullptr, 0, nullptr, 0, nullptr, 0, nullptr, 0, false, n,
+                                          k, 0, dw_dtype, dW, lddw, nullptr}, st), "block gradient");
+  const TrainSaved sv(m, n, k);
+  const TrainGradient g(m, n, k);
+  void* kept = const_cast<void*>(saved);
+  void* own = nullptr;
+  rc = EMEANS_OK;
+  if (!work) HIP_TRY(hipMallocAsync(&own, g.end, st));
+  if (own) work = own;
+  if (dW)
+    HIP_TRY(launch_encode_tiles({dtype, dY, lddy, m, (int)n, false, dX ? g.y.c(work) : nullptr,
+                                 g.y.ld, dX ? g.y.s(work) : nullptr, g.y.lds, g.yt.c(work),
+                                 g.yt.ld, g.yt.s(work), g.yt.lds}, st));
+  else
+    HIP_TRY(launch_encode_rows({dtype, dY, m, (int)n, (int)n, lddy, 0, 128, false, nullptr, 0, m,
+                                g.y.c(work), g.y.ld, g.y.s(work), g.y.lds}, st));
+  if (dX)
+    HIP_TRY(launch_block_product({g.y.c(work), g.y.ld, g.y.s(work), g.y.lds, sv.w.c(kept), sv.w.ld,
+                                  sv.w.s(kept), sv.w.lds, true, m, k, (int)n, dx_dtype, dX, lddx,
+                                  static_cast<uint8_t*>(work) + g.own}, st));
+  if (dW)
+    HIP_TRY(launch_block_product({g.yt.c(work), g.yt.ld, g.yt.s(work), g.yt.lds, sv.x.c(kept),
+                                  sv.x.ld, sv.x.s(kept), sv.x.lds, false, n, k, (int)m, dw_dtype, dW,
+                                  lddw, static_cast<uint8_t*>(work) + g.own}, st));
+done:
+  return release(own, st, rc);
+}
+
 int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,
                        int64_t row_stride, int64_t head_stride, const void* slots,
                        int32_t slot_bytes, void* codes, uint8_t* scales, int64_t rows,

@@ -113,6 +113,35 @@ def test_work_sizes(L):
     assert L.emeans_block_linear_work(0, 5, 200) == 0 and L.emeans_block_matmul_work(3, 5, 0) == 0
 
 
+def test_train_refuses(L):
+    def forward(X=FAKE, xt=0, ldx=200, W=FAKE, wt=1, ldw=200, m=4, n=5, k=200, need=3, out=FAKE,
+                ot=0, ldo=5, saved=FAKE, work=None):
+        return L.emeans_block_train_forward(X, xt, ldx, W, wt, ldw, m, n, k, need, out, ot, ldo,
+                                            saved, work, None)
+
+    def gradient(dY=FAKE, t=0, ld=5, saved=FAKE, m=4, n=5, k=200, dX=FAKE, xt=0, ldx=200, dW=FAKE,
+                 wt=0, ldw=200, work=None):
+        return L.emeans_block_train_gradient(dY, t, ld, saved, m, n, k, dX, xt, ldx, dW, wt, ldw,
+                                             work, None)
+
+    for call, cases in (
+        (forward, [(dict(m=-1), -1), (dict(n=0), -1), (dict(k=0), -1), (dict(xt=2), -2),
+                   (dict(wt=3), -2), (dict(ot=9), -2), (dict(ldx=9), -1), (dict(ldw=9), -1),
+                   (dict(ldo=4), -1), (dict(need=4), -1), (dict(saved=None), -1),
+                   (dict(saved=8), -1), (dict(work=4), -1), (dict(X=None), -1), (dict(W=None), -1),
+                   (dict(out=None), -1)]),
+        (gradient, [(dict(t=2), -2), (dict(xt=2), -2), (dict(wt=5), -2), (dict(ld=4), -1),
+                    (dict(ldx=9), -1), (dict(ldw=9), -1), (dict(dX=None, dW=None), -1),
+                    (dict(dY=None), -1), (dict(saved=None), -1), (dict(work=8), -1),
+                    (dict(n=0), -1), (dict(m=1 << 31), -1)])):
+        for change, code in cases:
+            assert call(**change) == code, (call, change)
+            assert L.emeans_last_error() and b"device" not in L.emeans_last_error()
+    assert forward(m=0) == 0 and gradient(m=0, dW=None) == 0
+    assert L.emeans_block_train_saved(300, 200, 130) > 2 * 130 * 200
+    assert L.emeans_block_train_saved(0, 5, 5) == L.emeans_block_train_work(5, 5, 0, 1) == 0
+
+
 def _write(L, **kw):
     a = dict(X=FAKE, dtype=0, n=3, heads=2, width=96, rs=192, hs=96, slots=FAKE, sb=4, c=FAKE,
              s=FAKE, rows=10, block=96, fmt=3)
