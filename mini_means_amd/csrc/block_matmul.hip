@@ -262,11 +262,9 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
 // Workgroups go round the eight XCDs in launch order, so XCD x takes the x-th
 // run of tiles, and a run walks kGroup tile rows at a time: the tiles that
 // share an L2 at one time form a compact patch of the output.
-//
-// SPLIT: blockIdx.y takes `per` k-steps and writes fp32 sums to part[y], which
-// join_kernel adds in order.
 // ---------------------------------------------------------------------------
 constexpr int kGroup = 4;
+constexpr int kCUs = 256;
 
 struct TileMap {
   unsigned tiles_m, tiles_n;
@@ -285,7 +283,21 @@ __device__ __forceinline__ void tile_of(unsigned id, const TileMap& t, unsigned&
   tm = group * kGroup + (in - tn * rows);
 }
 
-template <int MI, int NI, int OT, bool SPLIT, bool RAGGED>
+// Zeros past the `left` codes that chunk c of an LDS row's stage has in all.
+__device__ __forceinline__ void clear_chunk(uint8_t* row, int r, int c, int left) {
+  const int cnt = left - 16 * c;
+  if (cnt >= 16) return;
+  u32x4* q = reinterpret_cast<u32x4*>(row + 16 * (c ^ (r & 7)));
+  u32x4 w = *q;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int n = cnt - 4 * d;
+    w[d] = n <= 0 ? 0u : n >= 4 ? w[d] : w[d] & ((1u << (8 * n)) - 1u);
+  }
+  *q = w;
+}
+
+template <int MI, int NI, int OT, bool RAGGED>
 __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kernel(BlockProduct p,
                                                                                  TileMap t) {
   constexpr bool F8 = OT != 0;
@@ -303,8 +315,6 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int mrows = (int)min((int64_t)BM, p.m - m0), nrows = (int)min((int64_t)BN, p.n - n0);
   const int steps = (p.k + kStep - 1) / kStep;
-  const int s0 = SPLIT ? (int)blockIdx.y * t.per : 0;
-  const int s1 = SPLIT ? min(steps, s0 + t.per) : steps;
 
   // Window w of the stage is rows 8 w .. 8 w + 7 (A's rows, then B's): lane l
   // loads position l % 8 of row l / 8, which holds chunk (l % 8) ^ (l / 8).
@@ -354,20 +364,8 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     for (int l = 0; l < kLoads; ++l) load(s, buf, l, shift);
   };
   auto clear = [&](int buf) {
-    const int left = p.k % kStep;
-    for (int f = threadIdx.x; f < R * 8; f += 256) {
-      const int r = f >> 3, c = f & 7;  // chunk c of row r
-      const int cnt = left - 16 * c;
-      if (cnt >= 16) continue;
-      u32x4* q = reinterpret_cast<u32x4*>(lc[buf] + r * kStep + 16 * (c ^ (r & 7)));
-      u32x4 w = *q;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const int n = cnt - 4 * d;
-        w[d] = n <= 0 ? 0u : n >= 4 ? w[d] : w[d] & ((1u << (8 * n)) - 1u);
-      }
-      *q = w;
-    }
+    for (int f = threadIdx.x; f < R * 8; f += 256)
+      clear_chunk(lc[buf] + (f >> 3) * kStep, f >> 3, f & 7, p.k % kStep);
     lds_barrier();
   };
 
@@ -506,11 +504,11 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
     });
   };
   auto begin = [&](int buf, Raw(&first)[HB]) {
-    issue(s0, buf);
-    issue(min(s0 + 1, s1 - 1), buf ^ 1);
+    issue(0, buf);
+    issue(min(1, steps - 1), buf ^ 1);
     EMK_WAIT_VMCNT(0);
     lds_barrier();
-    if (RAGGED && s0 == last) clear(buf);
+    if (RAGGED && steps == 1) clear(buf);
 #pragma unroll
     for (int i = 0; i < HA; ++i) read_a(A0[i], buf, i);
 #pragma unroll
@@ -519,41 +517,37 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   // steps in pairs, so that the halves of B keep their registers; an odd one first
   constexpr std::true_type yes;
   constexpr std::false_type no;
-  int s = s0;
-  if ((s1 - s0) & 1) {
+  int s = 0;
+  if (steps & 1) {
     begin(1, Y);
-    kstep(yes, yes, s, min(s + 2, s1 - 1), 1, Y, X);
+    kstep(yes, yes, s, min(s + 2, steps - 1), 1, Y, X);
     ++s;
   } else {
     begin(0, X);
   }
-  for (; s + 2 < s1; s += 2) {
+  for (; s + 2 < steps; s += 2) {
     kstep(yes, yes, s, s + 2, 0, X, Y);
     kstep(yes, yes, s + 1, s + 3, 1, Y, X);
   }
-  if (s < s1) {
+  if (s < steps) {
     kstep(yes, no, s, s, 0, X, Y);
     kstep(no, no, s + 1, s, 1, Y, X);
   }
   EMK_WAIT_VMCNT(0);  // the load that a single step makes for nobody
 
   auto put = [&](int64_t m, int64_t n, f32x4 y) {
-    if constexpr (SPLIT) {
-      if (n < p.n) store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, y, 4);
-    } else {
-      store4<OT>(p.out, m * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
-    }
+    store4<OT>(p.out, m * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
   };
   if constexpr (!F8) {
     if (__syncthreads_or(rest)) {  // scales beyond 2^+-kFold: the tile again, with care
       for (int q = 0; q < MI * NI / 4; ++q)
-        any_tile<F8>(p, m0 + kAT * (q / (NI / 2)), n0 + kAT * (q % (NI / 2)), s0, s1, lc[0], lc[1],
+        any_tile<F8>(p, m0 + kAT * (q / (NI / 2)), n0 + kAT * (q % (NI / 2)), 0, steps, lc[0], lc[1],
                      put);
       return;
     }
   }
   const int64_t mw = m0 + ra, nw = n0 + (rb - BM) - col;  // the wave's first column, this lane's row
-  if constexpr (F8 && !SPLIT) {
+  if constexpr (F8) {
     if (mrows == BM && nrows == BN) {
       // 16 bytes per lane: lanes of odd groups trade their values of tile j for the
       // even groups' values of tile j + 1
@@ -581,6 +575,123 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few outputs: 64 x 64 tiles, 32 x 32 per wave, so that more CUs have one, and
+// a ring of four stages, three of them on their way: with little to compute
+// per step it is the loads' latency that counts.
+//
+// SPLIT: blockIdx.y takes `per` k-steps and writes fp32 sums to part[y], which
+// join_kernel adds in order.
+// ---------------------------------------------------------------------------
+constexpr int kST = 64;
+constexpr int kRing = 4;
+
+template <int OT, bool SPLIT>
+__global__ __launch_bounds__(256) void product_small_kernel(BlockProduct p, TileMap t) {
+  constexpr bool F8 = OT != 0;
+  constexpr int R = 2 * kST;
+  constexpr int kLoads = 5;  // per wave and stage: two windows of A, two of B, 64 scales
+  __shared__ __attribute__((aligned(1024))) uint8_t lc[kRing][R * kStep];
+  __shared__ __attribute__((aligned(256))) uint32_t ls[kRing][R];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  unsigned tm, tn;
+  tile_of(blockIdx.x, t, tm, tn);
+  const int64_t m0 = (int64_t)tm * kST, n0 = (int64_t)tn * kST;
+  const int mrows = (int)min((int64_t)kST, p.m - m0), nrows = (int)min((int64_t)kST, p.n - n0);
+  const int steps = (p.k + kStep - 1) / kStep;
+  const int s0 = SPLIT ? (int)blockIdx.y * t.per : 0;
+  const int s1 = SPLIT ? min(steps, s0 + t.per) : steps;
+
+  const uint8_t* a0 = p.A + m0 * p.lda;
+  const uint8_t* b0 = p.B + n0 * p.ldb;
+  const int lr = lane >> 3, lx = 16 * ((lane & 7) ^ lr);
+  uint32_t off[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    off[i] = (uint32_t)min(8 * (wave * 2 + i) + lr, mrows - 1) * (uint32_t)p.lda + lx;
+    off[2 + i] = (uint32_t)min(8 * (wave * 2 + i) + lr, nrows - 1) * (uint32_t)p.ldb + lx;
+  }
+  // scales: A's rows by the even waves, B's by the odd ones
+  const int64_t sr = wave & 1 ? n0 + min(lane, nrows - 1) : m0 + min(lane, mrows - 1);
+  const uint8_t* sp = wave & 1 ? p.Bs + (p.b_tiles ? sr / kStep : sr) * p.ldbs : p.As + sr * p.ldas;
+  // the last stage of a k that is no multiple of 128, as in the larger tiles
+  const int rem = p.k % kStep;
+  const int last = rem ? steps - 1 : -1;
+  const uint32_t skip = rem && lx >= rem ? -(uint32_t)lx : 0u;
+  const uint32_t lc0 = (uint32_t)(uintptr_t)(lds_ptr_t)lc, ls0 = (uint32_t)(uintptr_t)(lds_ptr_t)ls;
+  auto issue = [&](int s) {
+    const int buf = (s - s0) % kRing;
+    const int64_t k0 = (int64_t)s * kStep;
+    const uint32_t shift = s == last ? skip : 0u;
+    const uint32_t to = lc0 + buf * R * kStep + wave * 2048;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lds_load16_at(a0 + k0, off[i] + shift, to + i * 1024);
+      lds_load16_at(b0 + k0, off[2 + i] + shift, to + kST * kStep + i * 1024);
+    }
+    lds_load1_at(sp + s, ls0 + buf * R * 4 + 256 * (wave & 1));
+  };
+
+  const int ra = 32 * (wave & 1) + col, rb = kST + 32 * (wave >> 1) + col;
+  const int fx = 16 * (grp ^ (col & 7));
+  f32x4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int x = 0; x < kRing - 1; ++x)
+    if (s0 + x < s1) issue(s0 + x);
+  for (int s = s0; s < s1; ++s) {
+    const int buf = (s - s0) % kRing;
+    if (s + 2 < s1)
+      EMK_WAIT_VMCNT(2 * kLoads);  // this stage: all but the next two
+    else if (s + 1 < s1)
+      EMK_WAIT_VMCNT(kLoads);
+    else
+      EMK_WAIT_VMCNT(0);
+    lds_barrier();  // everyone's part of it; and the stage before has been read
+    if (s + kRing - 1 < s1) issue(s + kRing - 1);
+    if (s == last) {
+      for (int f = threadIdx.x; f < R * 8; f += 256)
+        clear_chunk(lc[buf] + (f >> 3) * kStep, f >> 3, f & 7, rem);
+      lds_barrier();
+    }
+    Operand<F8> a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* qa = lc[buf] + (ra + 16 * i) * kStep;
+      const uint8_t* qb = lc[buf] + (rb + 16 * i) * kStep;
+      a[i].set(join(*reinterpret_cast<const u32x4*>(qa + fx),
+                    *reinterpret_cast<const u32x4*>(qa + (fx ^ 64))), ls[buf][ra + 16 * i]);
+      b[i].set(join(*reinterpret_cast<const u32x4*>(qb + fx),
+                    *reinterpret_cast<const u32x4*>(qb + (fx ^ 64))), ls[buf][rb + 16 * i]);
+    }
+    const bool extreme = any_rest(a) || any_rest(b);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = add_step(b[j], a[i], acc[i][j], extreme);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t m = m0 + ra + 16 * i;
+    if (m >= p.m) continue;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = n0 + (rb - kST) - col + 16 * j + 4 * grp;
+      if constexpr (SPLIT) {
+        if (n < p.n)
+          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4);
+      } else {
+        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
+      }
+    }
+  }
+}
+
 // out = the sum of the splits' parts, in order, rounded once.
 template <int OT>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int splits,
@@ -597,24 +708,25 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 rows of A (a few tokens): bound by reading B once. A workgroup of
-// eight waves takes 16 * 8 / wk rows of B; wk waves share their k-steps and
+// Up to 64 rows of A (tokens being served): bound by reading B once. A workgroup
+// of eight waves takes 16 * 8 / wk rows of B; wk waves share their k-steps and
 // add their sums through LDS in order. Fragments of B go straight from memory
-// to registers, kAhead k-steps at a time.
+// to registers, kAhead k-steps at a time; those of A, MT blocks of 16 rows, come
+// from the caches.
 //
-// XT >= 0: A is given as numbers (that dt) and encoded by every workgroup into
-// LDS while its first codes of B are on their way; block rows of m * k bytes
-// are small beside B, and it saves a launch.
+// XT >= 0 (MT = 1): A is given as numbers (that dt) and encoded by every
+// workgroup into LDS while its first codes of B are on their way; block rows of
+// m * k bytes are small beside B, and it saves a launch.
 // ---------------------------------------------------------------------------
-constexpr int kFew = 16;
 constexpr int kFewWaves = 8;
-constexpr int kAhead = 4;
 
-template <int OT, int XT>
+template <int OT, int XT, int MT>
 __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduct p, int wk_log) {
   constexpr bool F8 = OT != 0;
   constexpr bool kEncode = XT >= 0;
-  __shared__ f32x4 part[kFewWaves][64];
+  constexpr int kAhead = 4;
+  static_assert(!kEncode || MT == 1, "one block of rows is encoded in LDS");
+  __shared__ f32x4 part[kFewWaves][MT][64];
   extern __shared__ __attribute__((aligned(16))) uint8_t room[];  // m x kb * 128 codes, m x kb scales
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -626,9 +738,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
   const int64_t bn = min(nb + col, p.n - 1);
   const uint8_t* bp = p.B + bn * p.ldb + 16 * grp;
   const uint8_t* bs = p.Bs + (p.b_tiles ? bn / kStep : bn) * p.ldbs;
-  const int am = min(col, m - 1);
-  const uint8_t* ap = p.A + am * p.lda + 16 * grp;
-  const uint8_t* as = p.As + am * p.ldas;
 
   u32x4 lo[kAhead], hi[kAhead];
   uint32_t sc[kAhead];
@@ -674,47 +783,72 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
     }
     __syncthreads();
   }
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = kw; s < steps; s += kAhead << wk_log) {
     if (s != kw) load_b(s);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int t = s + (u << wk_log);
       if (t >= steps) break;
-      Operand<F8> a[1], b[1];
-      if constexpr (kEncode) {
-        const uint8_t* q = room + (am * steps + t) * kStep;
-        const int x = 16 * (grp ^ (am & 7));
-        a[0].set(join(*reinterpret_cast<const u32x4*>(q + x),
-                      *reinterpret_cast<const u32x4*>(q + (x ^ 64))),
-                 scales[am * steps + t]);
-      } else {
-        const int64_t k0 = (int64_t)t * kStep;
-        const int left = p.k - (int)k0 - 16 * grp;
-        a[0].set(join(load16(ap + k0, left), load16(ap + k0 + 64, left - 64)), as[t]);
+      Operand<F8> a[MT], b[1];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int am = min(16 * i + col, m - 1);
+        if constexpr (kEncode) {
+          const uint8_t* q = room + (am * steps + t) * kStep;
+          const int x = 16 * (grp ^ (am & 7));
+          a[i].set(join(*reinterpret_cast<const u32x4*>(q + x),
+                        *reinterpret_cast<const u32x4*>(q + (x ^ 64))),
+                   scales[am * steps + t]);
+        } else {
+          const int64_t k0 = (int64_t)t * kStep;
+          const uint8_t* ap = p.A + am * p.lda + 16 * grp + k0;
+          if (k0 + kStep <= p.k) {
+            a[i].set(join(load_any<u32x4>(ap), load_any<u32x4>(ap + 64)), p.As[am * p.ldas + t]);
+          } else {
+            const int left = p.k - (int)k0 - 16 * grp;
+            a[i].set(join(load16(ap, left), load16(ap + 64, left - 64)), p.As[am * p.ldas + t]);
+          }
+        }
       }
       b[0].set(join(lo[u], hi[u]), sc[u]);
-      acc = add_step(b[0], a[0], acc, any_rest(a) || any_rest(b));
+      const bool extreme = any_rest(a) || any_rest(b);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = add_step(b[0], a[i], acc[i], extreme);
     }
   }
   const int64_t n = nb + 4 * grp;
-  if (wk > 1) {
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (kw) return;
-    for (int w = 1; w < wk; ++w) acc += part[wave + w][lane];
+  auto put = [&](int i, f32x4 y) {
+    if (16 * i + col < m)
+      store4<OT>(p.out, (16 * i + col) * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
+  };
+  if (wk == 1) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) put(i, acc[i]);
+    return;
   }
-  if (col < m) store4<OT>(p.out, col * p.ldo + n, acc, (int)min((int64_t)4, p.n - n));
+#pragma unroll
+  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int i = kw; i < MT; i += wk) {  // the wk waves take the blocks of rows in turn
+    f32x4 y = part[wave - kw][i][lane];
+    for (int w = 1; w < wk; ++w) y += part[wave - kw + w][i][lane];
+    put(i, y);
+  }
 }
 
-constexpr size_t kFewRoom = 48 << 10;  // LDS for the codes made in product_few_kernel
+constexpr int kFewRows = 64;
+constexpr int kFewEncoded = 16;         // rows that product_few_kernel encodes
+constexpr size_t kFewRoom = 48 << 10;  // LDS for their codes
 
 size_t few_room(int64_t m, int32_t k) {
   const int64_t steps = (k + kStep - 1) / kStep;
   return (size_t)(m * steps * (kStep + 1));
 }
 
-template <int OT, int XT>
+template <int OT, int XT, int MT>
 hipError_t product_few(const BlockProduct& p, hipStream_t st) {
   const int steps = (p.k + kStep - 1) / kStep;
   int wk_log = 0;
@@ -722,61 +856,72 @@ hipError_t product_few(const BlockProduct& p, hipStream_t st) {
   const int64_t per = 16 * (kFewWaves >> wk_log);
   const int64_t wgs = (p.n + per - 1) / per;
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
-  product_few_kernel<OT, XT><<<(unsigned)wgs, 64 * kFewWaves, XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(
-      p, wk_log);
+  product_few_kernel<OT, XT, MT><<<(unsigned)wgs, 64 * kFewWaves,
+                                   XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(p, wk_log);
   return hipGetLastError();
 }
 
-constexpr int kCUs = 256;
+enum Kind { kAny, kFew, kSmall, kTile4, kTile8 };
 
 struct Plan {
-  int tile;       // 0: any alignment, 1: few rows, 4: 128 x 128, 8: 256 x 256
+  Kind kind;
   int splits, per;
 };
 
-// Which kernel and how many splits of k. vec: rows of codes start at multiples
+// Which kernel, and how many splits of k. vec: rows of codes start at multiples
 // of 16 bytes, offsets inside a tile fit 31 bits.
 Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec) {
   const int steps = (k + kStep - 1) / kStep;
-  if (steps == 0) return {0, 1, steps};
-  if (m <= kFew) return {1, 1, steps};
-  if (!vec) return {0, 1, steps};
+  if (steps == 0) return {kAny, 1, steps};
+  if (m <= kFewRows) return {kFew, 1, steps};
+  if (!vec) return {kAny, 1, steps};
   auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
-  if (tiles(256) >= kCUs) return {8, 1, steps};
-  const int64_t t = tiles(128);
-  int64_t s = t > 0 ? kCUs / t : 1;
-  s = s < 1 ? 1 : s > 16 ? 16 : s;
-  const int64_t most = steps / 4 < 1 ? 1 : steps / 4;  // at least four k-steps each
-  if (s > most) s = most;
+  if (tiles(256) >= kCUs) return {kTile8, 1, steps};
+  if (tiles(128) >= kCUs / 2) return {kTile4, 1, steps};
+  const int64_t t = tiles(kST);
+  int64_t s = t > 0 ? 2 * kCUs / t : 1;
+  const int64_t most = steps / 8 < 1 ? 1 : steps / 8;  // at least eight k-steps each
+  s = s < 1 ? 1 : s > most ? most : s;
   const int per = (int)((steps + s - 1) / s);
-  return {4, (int)((steps + per - 1) / (per < 1 ? 1 : per)), per};
+  return {kSmall, (int)((steps + per - 1) / per), per};
 }
 
 int64_t part_pitch(int64_t n) { return (n + 3) / 4 * 4; }
+
+template <int OT>
+hipError_t join(const BlockProduct& p, const TileMap& t, const Plan& plan, hipStream_t st) {
+  const int64_t threads = p.m * (t.part_ld / 4);
+  join_kernel<OT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
+      t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo);
+  return hipGetLastError();
+}
 
 template <int MI, int NI, int OT>
 hipError_t product_tiles(const BlockProduct& p, const Plan& plan, hipStream_t st) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+  const TileMap t{(unsigned)tm, (unsigned)tn, plan.per, nullptr, 0};
+  const unsigned grid = (unsigned)(tm * tn);
+  if (p.k % kStep)
+    product_tile_kernel<MI, NI, OT, true><<<grid, 256, 0, st>>>(p, t);
+  else
+    product_tile_kernel<MI, NI, OT, false><<<grid, 256, 0, st>>>(p, t);
+  return hipGetLastError();
+}
+
+template <int OT>
+hipError_t product_small(const BlockProduct& p, const Plan& plan, hipStream_t st) {
+  const int64_t tm = (p.m + kST - 1) / kST, tn = (p.n + kST - 1) / kST;
+  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   TileMap t{(unsigned)tm, (unsigned)tn, plan.per, static_cast<float*>(p.work), part_pitch(p.n)};
   const dim3 grid((unsigned)(tm * tn), (unsigned)plan.splits);
-  const bool ragged = p.k % kStep != 0;
   if (plan.splits == 1) {
-    if (ragged)
-      product_tile_kernel<MI, NI, OT, false, true><<<grid, 256, 0, st>>>(p, t);
-    else
-      product_tile_kernel<MI, NI, OT, false, false><<<grid, 256, 0, st>>>(p, t);
+    product_small_kernel<OT, false><<<grid, 256, 0, st>>>(p, t);
     return hipGetLastError();
   }
-  if (ragged)
-    product_tile_kernel<MI, NI, OT, true, true><<<grid, 256, 0, st>>>(p, t);
-  else
-    product_tile_kernel<MI, NI, OT, true, false><<<grid, 256, 0, st>>>(p, t);
-  const int64_t threads = p.m * (t.part_ld / 4);
-  join_kernel<OT><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
-      t.part, plan.splits, p.m, p.n, t.part_ld, p.out, p.ldo);
-  return hipGetLastError();
+  product_small_kernel<OT, true><<<grid, 256, 0, st>>>(p, t);
+  return join<OT>(p, t, plan, st);
 }
 
 template <int OT>
@@ -784,10 +929,19 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
   const bool vec = (uintptr_t)p.A % 16 == 0 && p.lda % 16 == 0 && p.lda < (1 << 22) &&
                    (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0 && p.ldb < (1 << 22);
   const Plan plan = plan_of(p.m, p.n, p.k, vec);
-  if (plan.tile == 1) return product_few<OT, -1>(p, st);
-  if constexpr (OT != 0)  // decoded operands do not fit beside 256 accumulators
-    if (plan.tile == 8) return product_tiles<8, 8, OT>(p, plan, st);
-  if (plan.tile >= 4) return product_tiles<4, 4, OT>(p, plan, st);
+  switch (plan.kind) {
+    case kFew:
+      if (p.m <= 16) return product_few<OT, -1, 1>(p, st);
+      if (p.m <= 32) return product_few<OT, -1, 2>(p, st);
+      return product_few<OT, -1, 4>(p, st);
+    case kSmall: return product_small<OT>(p, plan, st);
+    case kTile8:
+      if constexpr (OT != 0) return product_tiles<8, 8, OT>(p, plan, st);
+      // decoded operands do not fit beside 256 accumulators
+      return product_tiles<4, 4, OT>(p, plan, st);
+    case kTile4: return product_tiles<4, 4, OT>(p, plan, st);
+    case kAny: break;
+  }
   const int64_t tm = (p.m + kAT - 1) / kAT, tn = (p.n + kAT - 1) / kAT;
   if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, (unsigned)tn);
@@ -797,16 +951,16 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
 }  // namespace
 
 bool block_product_encodes(int64_t m, int32_t k) {
-  return m <= kFew && k > 0 && few_room(m, k) <= kFewRoom;
+  return m <= kFewEncoded && k > 0 && few_room(m, k) <= kFewRoom;
 }
 
 hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) {
   if (p.m <= 0 || p.n <= 0) return hipSuccess;
 #define EMK_XT(OT)                                \
   switch (dt) {                                   \
-    case 0: return product_few<OT, 0>(p, st);       \
-    case 1: return product_few<OT, 1>(p, st);       \
-    case 4: return product_few<OT, 4>(p, st);       \
+    case 0: return product_few<OT, 0, 1>(p, st);       \
+    case 1: return product_few<OT, 1, 1>(p, st);       \
+    case 4: return product_few<OT, 4, 1>(p, st);       \
   }                                               \
   break
   switch (p.ot) {
