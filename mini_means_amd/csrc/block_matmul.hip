@@ -708,25 +708,24 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 }
 
 // ---------------------------------------------------------------------------
-// Up to 64 rows of A (tokens being served): bound by reading B once. A workgroup
-// of eight waves takes 16 * 8 / wk rows of B; wk waves share their k-steps and
+// Up to 16 rows of A (tokens being served): bound by reading B once. A workgroup
+// of eight waves takes 16 NT * 8 / wk rows of B; wk waves share their k-steps and
 // add their sums through LDS in order. Fragments of B go straight from memory
-// to registers, kAhead k-steps at a time; those of A, MT blocks of 16 rows, come
-// from the caches.
+// to registers, AH k-steps at a time, and with them those of A from the caches.
+// NT > 1: k of one step and many rows of B, of which a wave has NT blocks in
+// flight instead.
 //
-// XT >= 0 (MT = 1): A is given as numbers (that dt) and encoded by every
-// workgroup into LDS while its first codes of B are on their way; block rows of
-// m * k bytes are small beside B, and it saves a launch.
+// XT >= 0: A is given as numbers (that dt) and encoded by every workgroup into
+// LDS while its first codes of B are on their way; block rows of m * k bytes
+// are small beside B, and it saves a launch.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
-template <int OT, int XT, int MT>
+template <int OT, int XT, int AH, int NT>
 __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduct p, int wk_log) {
   constexpr bool F8 = OT != 0;
   constexpr bool kEncode = XT >= 0;
-  constexpr int kAhead = 4;
-  static_assert(!kEncode || MT == 1, "one block of rows is encoded in LDS");
-  __shared__ f32x4 part[kFewWaves][MT][64];
+  __shared__ f32x4 part[kFewWaves][NT][64];
   extern __shared__ __attribute__((aligned(16))) uint8_t room[];  // m x kb * 128 codes, m x kb scales
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -734,131 +733,147 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few_kernel(BlockProduc
   const int col = lane & 15, grp = lane >> 4;
   const int m = (int)p.m;
   const int steps = (p.k + kStep - 1) / kStep;
-  const int64_t nb = ((int64_t)blockIdx.x * (kFewWaves >> wk_log) + (wave >> wk_log)) * 16;
-  const int64_t bn = min(nb + col, p.n - 1);
-  const uint8_t* bp = p.B + bn * p.ldb + 16 * grp;
-  const uint8_t* bs = p.Bs + (p.b_tiles ? bn / kStep : bn) * p.ldbs;
-
-  u32x4 lo[kAhead], hi[kAhead];
-  uint32_t sc[kAhead];
-  auto load_b = [&](int s) {
+  const int64_t nb = ((int64_t)blockIdx.x * (kFewWaves >> wk_log) + (wave >> wk_log)) * (16 * NT);
+  const int am = min(col, m - 1);
+  const uint8_t *bp[NT], *bs[NT];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+  for (int j = 0; j < NT; ++j) {
+    const int64_t bn = min(nb + 16 * j + col, p.n - 1);
+    bp[j] = p.B + bn * p.ldb + 16 * grp;
+    bs[j] = p.Bs + (p.b_tiles ? bn / kStep : bn) * p.ldbs;
+  }
+  // one lane's codes of k-step t of a row, from q = its row + 16 grp on
+  auto codes_at = [&](const uint8_t* q, int t) {
+    const int64_t k0 = (int64_t)t * kStep;
+    if (k0 + kStep <= p.k) return join(load_any<u32x4>(q + k0), load_any<u32x4>(q + k0 + 64));
+    const int left = p.k - (int)k0 - 16 * grp;
+    return join(load16(q + k0, left), load16(q + k0 + 64, left - 64));
+  };
+  i32x8 fb[AH][NT], fa[AH];
+  uint32_t eb[AH][NT], ea[AH];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int u = 0; u < AH; ++u) {
       const int t = s + (u << wk_log);
       if (t < steps) {
-        const int64_t k0 = (int64_t)t * kStep;
-        if (k0 + kStep <= p.k) {
-          lo[u] = load_any<u32x4>(bp + k0);
-          hi[u] = load_any<u32x4>(bp + k0 + 64);
-        } else {
-          const int left = p.k - (int)k0 - 16 * grp;
-          lo[u] = load16(bp + k0, left);
-          hi[u] = load16(bp + k0 + 64, left - 64);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          fb[u][j] = codes_at(bp[j], t);
+          eb[u][j] = bs[j][t];
         }
-        sc[u] = bs[t];
+        if constexpr (!kEncode) {
+          fa[u] = codes_at(p.A + am * p.lda + 16 * grp, t);
+          ea[u] = p.As[am * p.ldas + t];
+        }
       }
     }
   };
-  load_b(kw);
+  load(kw);
   uint8_t* scales = room + m * steps * kStep;
   if constexpr (kEncode) {
     const int sub = threadIdx.x & 15;
     const int items = m * steps;
-    for (int i = threadIdx.x >> 4; i < items; i += 64 * kFewWaves / 16) {
-      const int r = i / steps, b = i - r * steps;
-      const int c = b * kStep + 8 * sub;
-      const int cnt = min(8, p.k - c);
-      float v[8];
+    constexpr int kStride = 64 * kFewWaves / 16;
+    constexpr int kFlight = 4;  // blocks whose values a group of lanes has in flight
+    for (int i0 = threadIdx.x >> 4; i0 < items; i0 += kFlight * kStride) {
+      float v[kFlight][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      if (cnt > 0) load8<XT < 0 ? 0 : XT>(p.A, r * p.lda + c, cnt, v);
-      uint32_t a = group_max<16>(amax8(v));
-      const bool odd = a >= kInfBits;
-      if (odd) a = group_max<16>(amax8_finite(v));
-      const uint32_t byte = scale_byte<false>(a);
-      *reinterpret_cast<u32x2*>(room + r * steps * kStep + b * kStep +
-                                16 * ((sub >> 1) ^ (r & 7)) + 8 * (sub & 1)) =
-          codes8<false>(v, inv_scale(byte), odd);
-      if (sub == 0) scales[r * steps + b] = (uint8_t)byte;
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * kStride;
+        const int r = i / steps, c = (i - r * steps) * kStep + 8 * sub;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
+        if (i < items && c < p.k)
+          load8<XT < 0 ? 0 : XT>(p.A, r * p.lda + c, min(8, p.k - c), v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * kStride;
+        if (i >= items) break;  // a group of lanes at a time
+        const int r = i / steps;
+        uint32_t a = group_max<16>(amax8(v[u]));
+        const bool odd = a >= kInfBits;
+        if (odd) a = group_max<16>(amax8_finite(v[u]));
+        const uint32_t byte = scale_byte<false>(a);
+        *reinterpret_cast<u32x2*>(room + i * kStep + 16 * ((sub >> 1) ^ (r & 7)) + 8 * (sub & 1)) =
+            codes8<false>(v[u], inv_scale(byte), odd);
+        if (sub == 0) scales[i] = (uint8_t)byte;
+      }
     }
     __syncthreads();
   }
-  f32x4 acc[MT];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = kw; s < steps; s += kAhead << wk_log) {
-    if (s != kw) load_b(s);
+  for (int j = 0; j < NT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = kw; s < steps; s += AH << wk_log) {
+    if (s != kw) load(s);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < AH; ++u) {
       const int t = s + (u << wk_log);
       if (t >= steps) break;
-      Operand<F8> a[MT], b[1];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int am = min(16 * i + col, m - 1);
-        if constexpr (kEncode) {
-          const uint8_t* q = room + (am * steps + t) * kStep;
-          const int x = 16 * (grp ^ (am & 7));
-          a[i].set(join(*reinterpret_cast<const u32x4*>(q + x),
-                        *reinterpret_cast<const u32x4*>(q + (x ^ 64))),
-                   scales[am * steps + t]);
-        } else {
-          const int64_t k0 = (int64_t)t * kStep;
-          const uint8_t* ap = p.A + am * p.lda + 16 * grp + k0;
-          if (k0 + kStep <= p.k) {
-            a[i].set(join(load_any<u32x4>(ap), load_any<u32x4>(ap + 64)), p.As[am * p.ldas + t]);
-          } else {
-            const int left = p.k - (int)k0 - 16 * grp;
-            a[i].set(join(load16(ap, left), load16(ap + 64, left - 64)), p.As[am * p.ldas + t]);
-          }
-        }
+      Operand<F8> a[1], b[NT];
+      if constexpr (kEncode) {
+        const uint8_t* q = room + (am * steps + t) * kStep;
+        const int x = 16 * (grp ^ (am & 7));
+        a[0].set(join(*reinterpret_cast<const u32x4*>(q + x),
+                      *reinterpret_cast<const u32x4*>(q + (x ^ 64))),
+                 scales[am * steps + t]);
+      } else {
+        a[0].set(fa[u], ea[u]);
       }
-      b[0].set(join(lo[u], hi[u]), sc[u]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[j].set(fb[u][j], eb[u][j]);
       const bool extreme = any_rest(a) || any_rest(b);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = add_step(b[0], a[i], acc[i], extreme);
+      for (int j = 0; j < NT; ++j) acc[j] = add_step(b[j], a[0], acc[j], extreme);
     }
   }
-  const int64_t n = nb + 4 * grp;
-  auto put = [&](int i, f32x4 y) {
-    if (16 * i + col < m)
-      store4<OT>(p.out, (16 * i + col) * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
-  };
-  if (wk == 1) {
+  if (wk > 1) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) put(i, acc[i]);
-    return;
+    for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+    __syncthreads();
+    if (kw) return;
+    for (int w = 1; w < wk; ++w)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] += part[wave + w][j][lane];
   }
+  if (col >= m) return;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
-  __syncthreads();
-  for (int i = kw; i < MT; i += wk) {  // the wk waves take the blocks of rows in turn
-    f32x4 y = part[wave - kw][i][lane];
-    for (int w = 1; w < wk; ++w) y += part[wave - kw + w][i][lane];
-    put(i, y);
+  for (int j = 0; j < NT; ++j) {
+    const int64_t n = nb + 16 * j + 4 * grp;
+    store4<OT>(p.out, col * p.ldo + n, acc[j], (int)min((int64_t)4, p.n - n));
   }
 }
 
-constexpr int kFewRows = 64;
-constexpr int kFewEncoded = 16;         // rows that product_few_kernel encodes
-constexpr size_t kFewRoom = 48 << 10;  // LDS for their codes
+constexpr int kFewRows = 16;
+constexpr size_t kFewRoom = 48 << 10;  // LDS for rows encoded in product_few_kernel
 
 size_t few_room(int64_t m, int32_t k) {
   const int64_t steps = (k + kStep - 1) / kStep;
   return (size_t)(m * steps * (kStep + 1));
 }
 
-template <int OT, int XT, int MT>
+template <int OT, int XT, int AH, int NT>
+hipError_t product_few_t(const BlockProduct& p, int wk_log, hipStream_t st) {
+  const int64_t per = 16 * NT * (kFewWaves >> wk_log);
+  const int64_t wgs = (p.n + per - 1) / per;
+  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  product_few_kernel<OT, XT, AH, NT><<<(unsigned)wgs, 64 * kFewWaves,
+                                       XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(p, wk_log);
+  return hipGetLastError();
+}
+
+template <int OT, int XT>
 hipError_t product_few(const BlockProduct& p, hipStream_t st) {
   const int steps = (p.k + kStep - 1) / kStep;
   int wk_log = 0;
   while (wk_log < 3 && (2 << wk_log) <= steps) ++wk_log;
-  const int64_t per = 16 * (kFewWaves >> wk_log);
-  const int64_t wgs = (p.n + per - 1) / per;
-  if (wgs > INT32_MAX) return hipErrorInvalidValue;
-  product_few_kernel<OT, XT, MT><<<(unsigned)wgs, 64 * kFewWaves,
-                                   XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(p, wk_log);
-  return hipGetLastError();
+  if constexpr (XT < 0) {
+    if (steps == 1 && p.n >= 16 * 4 * kFewWaves * kCUs)
+      return product_few_t<OT, XT, 1, 4>(p, wk_log, st);
+    if (steps <= 2 << wk_log) return product_few_t<OT, XT, 2, 1>(p, wk_log, st);
+  }
+  return product_few_t<OT, XT, 4, 1>(p, wk_log, st);
 }
 
 enum Kind { kAny, kFew, kSmall, kTile4, kTile8 };
@@ -930,10 +945,7 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
                    (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0 && p.ldb < (1 << 22);
   const Plan plan = plan_of(p.m, p.n, p.k, vec);
   switch (plan.kind) {
-    case kFew:
-      if (p.m <= 16) return product_few<OT, -1, 1>(p, st);
-      if (p.m <= 32) return product_few<OT, -1, 2>(p, st);
-      return product_few<OT, -1, 4>(p, st);
+    case kFew: return product_few<OT, -1>(p, st);
     case kSmall: return product_small<OT>(p, plan, st);
     case kTile8:
       if constexpr (OT != 0) return product_tiles<8, 8, OT>(p, plan, st);
@@ -951,16 +963,16 @@ hipError_t product_t(const BlockProduct& p, hipStream_t st) {
 }  // namespace
 
 bool block_product_encodes(int64_t m, int32_t k) {
-  return m <= kFewEncoded && k > 0 && few_room(m, k) <= kFewRoom;
+  return m <= kFewRows && k > 0 && few_room(m, k) <= kFewRoom;
 }
 
 hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) {
   if (p.m <= 0 || p.n <= 0) return hipSuccess;
 #define EMK_XT(OT)                                \
   switch (dt) {                                   \
-    case 0: return product_few<OT, 0, 1>(p, st);       \
-    case 1: return product_few<OT, 1, 1>(p, st);       \
-    case 4: return product_few<OT, 4, 1>(p, st);       \
+    case 0: return product_few<OT, 0>(p, st);       \
+    case 1: return product_few<OT, 1>(p, st);       \
+    case 4: return product_few<OT, 4>(p, st);       \
   }                                               \
   break
   switch (p.ot) {
