@@ -577,8 +577,8 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
 
 // ---------------------------------------------------------------------------
 // Few outputs: 64 x 64 tiles, 32 x 32 per wave, so that more CUs have one, and
-// a ring of four stages, three of them on their way: with little to compute
-// per step it is the loads' latency that counts.
+// a ring of four stages. A step's MFMAs run while the next stage's fragments
+// are read; the three stages after that are on their way.
 //
 // SPLIT: blockIdx.y takes `per` k-steps and writes fp32 sums to part[y], which
 // join_kernel adds in order.
@@ -587,7 +587,7 @@ constexpr int kST = 64;
 constexpr int kRing = 4;
 
 template <int OT, bool SPLIT>
-__global__ __launch_bounds__(256) void product_small_kernel(BlockProduct p, TileMap t) {
+__global__ __launch_bounds__(256, 2) void product_small_kernel(BlockProduct p, TileMap t) {
   constexpr bool F8 = OT != 0;
   constexpr int R = 2 * kST;
   constexpr int kLoads = 5;  // per wave and stage: two windows of A, two of B, 64 scales
@@ -621,10 +621,8 @@ __global__ __launch_bounds__(256) void product_small_kernel(BlockProduct p, Tile
   const int last = rem ? steps - 1 : -1;
   const uint32_t skip = rem && lx >= rem ? -(uint32_t)lx : 0u;
   const uint32_t lc0 = (uint32_t)(uintptr_t)(lds_ptr_t)lc, ls0 = (uint32_t)(uintptr_t)(lds_ptr_t)ls;
-  auto issue = [&](int s) {
-    const int buf = (s - s0) % kRing;
+  auto issue = [&](int s, int buf, uint32_t shift) {
     const int64_t k0 = (int64_t)s * kStep;
-    const uint32_t shift = s == last ? skip : 0u;
     const uint32_t to = lc0 + buf * R * kStep + wave * 2048;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -641,54 +639,126 @@ __global__ __launch_bounds__(256) void product_small_kernel(BlockProduct p, Tile
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  struct Frags {
+    i32x8 a[2], b[2];
+    uint32_t ea[2], eb[2];
+  };
+  // this lane's places in a stage's LDS: opaque, so that buffers and rows are
+  // offsets in the instructions
+  uint32_t fa[2], fb[2], la = ls0 + 4 * ra, lb = ls0 + 4 * rb;
 #pragma unroll
-  for (int x = 0; x < kRing - 1; ++x)
-    if (s0 + x < s1) issue(s0 + x);
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) % kRing;
+  for (int h = 0; h < 2; ++h) {
+    fa[h] = lc0 + ra * kStep + (fx ^ (64 * h));
+    fb[h] = lc0 + rb * kStep + (fx ^ (64 * h));
+    asm volatile("" : "+v"(fa[h]), "+v"(fb[h]));
+  }
+  asm volatile("" : "+v"(la), "+v"(lb));
+  auto lds16 = [](uint32_t at) {
+    return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)at;
+  };
+  auto lds4 = [](uint32_t at) {
+    return *(const __attribute__((address_space(3))) uint32_t*)(uintptr_t)at;
+  };
+  auto read = [&](Frags& f, int buf) {
+    const uint32_t at = buf * R * kStep, es = buf * R * 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f.a[i] = join(lds16(fa[0] + at + i * 16 * kStep), lds16(fa[1] + at + i * 16 * kStep));
+      f.b[i] = join(lds16(fb[0] + at + i * 16 * kStep), lds16(fb[1] + at + i * 16 * kStep));
+      f.ea[i] = lds4(la + es + 64 * i);
+      f.eb[i] = lds4(lb + es + 64 * i);
+    }
+  };
+  int rest = 0;
+  auto product = [&](const Frags& f) {
+    Operand<F8> a[2], b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a[i].set(f.a[i], f.ea[i]);
+      b[i].set(f.b[i], f.eb[i]);
+      if constexpr (!F8) rest |= a[i].rest | b[i].rest;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = step(b[j], a[i], acc[i][j]);
+  };
+  // stage s is everyone's, and the one before it has been read
+  auto arrive = [&](int s) {
     if (s + 2 < s1)
-      EMK_WAIT_VMCNT(2 * kLoads);  // this stage: all but the next two
+      EMK_WAIT_VMCNT(2 * kLoads);  // all but the two after it
     else if (s + 1 < s1)
       EMK_WAIT_VMCNT(kLoads);
     else
       EMK_WAIT_VMCNT(0);
-    lds_barrier();  // everyone's part of it; and the stage before has been read
-    if (s + kRing - 1 < s1) issue(s + kRing - 1);
+    lds_barrier();
     if (s == last) {
-      for (int f = threadIdx.x; f < R * 8; f += 256)
-        clear_chunk(lc[buf] + (f >> 3) * kStep, f >> 3, f & 7, rem);
+      uint8_t* stage = lc[(s - s0) % kRing];
+      for (int c = threadIdx.x; c < R * 8; c += 256)
+        clear_chunk(stage + (c >> 3) * kStep, c >> 3, c & 7, rem);
       lds_barrier();
     }
-    Operand<F8> a[2], b[2];
+  };
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint8_t* qa = lc[buf] + (ra + 16 * i) * kStep;
-      const uint8_t* qb = lc[buf] + (rb + 16 * i) * kStep;
-      a[i].set(join(*reinterpret_cast<const u32x4*>(qa + fx),
-                    *reinterpret_cast<const u32x4*>(qa + (fx ^ 64))), ls[buf][ra + 16 * i]);
-      b[i].set(join(*reinterpret_cast<const u32x4*>(qb + fx),
-                    *reinterpret_cast<const u32x4*>(qb + (fx ^ 64))), ls[buf][rb + 16 * i]);
+  for (int x = 0; x < kRing; ++x)
+    if (s0 + x < s1) issue(s0 + x, x, s0 + x == last ? skip : 0u);
+  Frags f0, f1;
+  if (s0 + 3 < s1) {
+    EMK_WAIT_VMCNT(3 * kLoads);
+    lds_barrier();
+  } else {
+    arrive(s0);
+  }
+  read(f0, 0);
+  // whole rings without a condition inside, for as long as full stages follow
+  int s = s0;
+  const int whole = rem && s1 == steps ? s1 - 1 : s1;
+  auto steady = [&](int x, const Frags& f, Frags& next) {
+    EMK_WAIT_VMCNT(2 * kLoads);
+    lds_barrier();
+    issue(s + x + kRing, x, 0u);
+    read(next, (x + 1) % kRing);
+    product(f);
+  };
+  for (; s + 2 * kRing <= whole; s += kRing) {
+    steady(0, f0, f1);
+    steady(1, f1, f0);
+    steady(2, f0, f1);
+    steady(3, f1, f0);
+  }
+  auto ending = [&](const Frags& f, Frags& next) {
+    if (s + 1 < s1) {
+      arrive(s + 1);
+      if (s + kRing < s1) issue(s + kRing, (s - s0) % kRing, s + kRing == last ? skip : 0u);
+      read(next, (s + 1 - s0) % kRing);
     }
-    const bool extreme = any_rest(a) || any_rest(b);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = add_step(b[j], a[i], acc[i][j], extreme);
+    product(f);
+  };
+  for (;;) {
+    ending(f0, f1);
+    if (++s >= s1) break;
+    ending(f1, f0);
+    if (++s >= s1) break;
+  }
+  auto put = [&](int64_t m, int64_t n, f32x4 y) {
+    if constexpr (SPLIT) {
+      if (n < p.n) store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, y, 4);
+    } else {
+      store4<OT>(p.out, m * p.ldo + n, y, (int)min((int64_t)4, p.n - n));
+    }
+  };
+  if constexpr (!F8) {
+    if (__syncthreads_or(rest)) {  // scales beyond 2^+-kFold: the tile again, with care
+      any_tile<F8>(p, m0, n0, s0, s1, lc[0], lc[1], put);
+      return;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t m = m0 + ra + 16 * i;
     if (m >= p.m) continue;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t n = n0 + (rb - kST) - col + 16 * j + 4 * grp;
-      if constexpr (SPLIT) {
-        if (n < p.n)
-          store4<0>(t.part, ((int64_t)blockIdx.y * p.m + m) * t.part_ld + n, acc[i][j], 4);
-      } else {
-        store4<OT>(p.out, m * p.ldo + n, acc[i][j], (int)min((int64_t)4, p.n - n));
-      }
-    }
+    for (int j = 0; j < 2; ++j) put(m, n0 + (rb - kST) - col + 16 * j + 4 * grp, acc[i][j]);
   }
 }
 
