@@ -954,19 +954,34 @@ struct Plan {
 };
 
 // Which kernel, and how many splits of k. vec: rows of codes start at multiples
-// of 16 bytes, offsets inside a tile fit 31 bits.
-Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec) {
+// of 16 bytes, offsets inside a tile fit 31 bits. f32: the bf16 unit's tiles.
+//
+// Measured (us, this card, bf16 results if not said otherwise):
+//   64 x 64 up to two per CU (512), else 128 x 128:
+//     256 x 4096 x 4096 (256 tiles) 11.0 against 18.6, 512 x 4096 x 4096 (512)
+//     18.3 against 19.0, 700 x 4096 x 4096 (704) 25.0 against 19.7; fp32 17.7
+//     against 31.2, 25.8 against 32.4, 35.3 against 32.9
+//   256 x 256 where they fill the CUs, or half of them over a long k:
+//     4096 x 4096 x 768 (256 tiles) 18.9 against 19.5 with 128 x 128, 3000^3 (144)
+//     40.9 against 43.7, 6000 x 5000 x 2000 73 against 97, but 3000 x 3000 x 768
+//     19.7 against 15.6
+//   k split (at least eight steps each) where fewer than 128 tiles have a long k:
+//     200 x 200 x 8192 9.3 against 15.0, 64 x 1024 x 8192 10.3 against 15.9,
+//     but 128 x 768 x 2048 7.6 against 6.5; fp32 128 x 768 x 2048 9.6 against 10.1
+Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec, bool f32) {
   const int steps = (k + kStep - 1) / kStep;
   if (steps == 0) return {kAny, 1, steps};
   if (m <= kFewRows) return {kFew, 1, steps};
   if (!vec) return {kAny, 1, steps};
   auto tiles = [&](int64_t b) { return ((m + b - 1) / b) * ((n + b - 1) / b); };
-  if (tiles(256) >= kCUs) return {kTile8, 1, steps};
-  if (tiles(128) >= kCUs / 2) return {kTile4, 1, steps};
   const int64_t t = tiles(kST);
-  int64_t s = t > 0 ? 2 * kCUs / t : 1;
-  const int64_t most = steps / 8 < 1 ? 1 : steps / 8;  // at least eight k-steps each
-  s = s < 1 ? 1 : s > most ? most : s;
+  if (t > 2 * kCUs) {
+    const int64_t t8 = tiles(256);
+    const bool large = t8 >= kCUs || (t8 > kCUs / 2 && steps >= 16);
+    return {large && !f32 ? kTile8 : kTile4, 1, steps};
+  }
+  int64_t s = 1;
+  if (t < kCUs / 2 && steps >= (f32 ? 16 : 32)) s = kCUs / t < steps / 8 ? kCUs / t : steps / 8;
   const int per = (int)((steps + s - 1) / s);
   return {kSmall, (int)((steps + per - 1) / per), per};
 }
@@ -1013,14 +1028,13 @@ template <int OT>
 hipError_t product_t(const BlockProduct& p, hipStream_t st) {
   const bool vec = (uintptr_t)p.A % 16 == 0 && p.lda % 16 == 0 && p.lda < (1 << 22) &&
                    (uintptr_t)p.B % 16 == 0 && p.ldb % 16 == 0 && p.ldb < (1 << 22);
-  const Plan plan = plan_of(p.m, p.n, p.k, vec);
+  const Plan plan = plan_of(p.m, p.n, p.k, vec, OT == 0);
   switch (plan.kind) {
     case kFew: return product_few<OT, -1>(p, st);
     case kSmall: return product_small<OT>(p, plan, st);
-    case kTile8:
+    case kTile8:  // not for fp32: decoded operands do not fit beside 256 accumulators
       if constexpr (OT != 0) return product_tiles<8, 8, OT>(p, plan, st);
-      // decoded operands do not fit beside 256 accumulators
-      return product_tiles<4, 4, OT>(p, plan, st);
+      break;
     case kTile4: return product_tiles<4, 4, OT>(p, plan, st);
     case kAny: break;
   }
@@ -1055,8 +1069,10 @@ hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) 
 }
 
 size_t block_product_work(int64_t m, int64_t n, int32_t k) {
-  const Plan plan = plan_of(m, n, k, true);
-  return plan.splits > 1 ? (size_t)plan.splits * m * part_pitch(n) * sizeof(float) : 0;
+  // the result's type is not known here: what either kind needs
+  const int a = plan_of(m, n, k, true, false).splits, b = plan_of(m, n, k, true, true).splits;
+  const int splits = a > b ? a : b;
+  return splits > 1 ? (size_t)splits * m * part_pitch(n) * sizeof(float) : 0;
 }
 
 hipError_t launch_block_product(const BlockProduct& p, hipStream_t st) {
