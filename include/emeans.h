@@ -461,7 +461,8 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
  *        16-byte aligned, or NULL: the library then allocates it stream-ordered
  * A NaN code or a scale byte of 255 makes the outputs it enters NaN. k = 0
  * gives zeros. Any alignment and any leading dimension is right; codes whose
- * rows start at multiples of 16 bytes are read fastest.
+ * rows start at multiples of 16 bytes are read fastest (in whole 16-byte words,
+ * so up to 15 bytes past a row's last code are read too, of the same word).
  * Errors: EINVAL (m, n or k < 0, m or n >= 2^31, a leading dimension below
  * the row length, work not aligned, NULL), EDTYPE, ENOTDEVICE, ENOMEM, EHIP. */
 int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k);

@@ -10,7 +10,8 @@
 // to even; infinities saturate, NaN becomes the E4M3 NaN or int8 0.
 //
 // All kernels here move bytes: a few VALU operations per value, bound by HBM
-// at large sizes and by the launch at small ones.
+// at large sizes (a 1 GiB copy reaches 5.2 TB/s on this card) and by the launch
+// at small ones (3.5-4 us in a graph, of which the kernel is a third).
 #include <type_traits>
 
 #include "block.hpp"
@@ -41,6 +42,9 @@ __device__ __forceinline__ void store_codes(uint8_t* p, u32x2 w, int cnt) {
 // The value (h, c) of row r sits at r * rs + h * hs + c, c < width: heads of a
 // fused projection, or one head of width d for plain rows. Blocks never
 // straddle heads (the host checks it).
+//
+// Measured: 32768 rows of 16 heads of 128, bf16, to random slots 43.6 us (4.6
+// TB/s: each row lands in a 2 KB run of its own); 33 rows 4 us.
 // ---------------------------------------------------------------------------
 struct RowsIn {
   const void* X;
@@ -128,6 +132,10 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, 
 // ---------------------------------------------------------------------------
 // Magnitudes are compared as the bits of the number type (16-bit types two at
 // a time, in packed registers that also hold the values until they are used).
+//
+// Measured: 16384 x 4096 bf16 both orders 56 us (4.8 TB/s), tiles 47 us (5.7);
+// fp32 both 80 us (5.1); 777 x 768 fp32 7.3 us, where 42 tiles do not fill the
+// card: a column's block is 128 rows, so the tile cannot be smaller.
 constexpr int kT = 128;
 constexpr int kTPitch = kT + 8;  // bytes per transposed row in LDS: 8-byte aligned
 
@@ -442,9 +450,13 @@ __device__ __forceinline__ int64_t source_row(const RowsFrom& f, int64_t row, in
 // (a page table costs a chain of dependent reads, paid once per R rows), then
 // the threads go over the rows' pieces of E values, E = 4 (fp32 out) or 8
 // (16-bit out; block borders are at multiples of 16). Only a row's last piece
-// may be short. Rows outside the store are zeros. The quotients by
-// the pieces per row and by the block are products by `inv` = 2^32 / divisor,
-// rounded up (exact while dividend x divisor < 2^32, which the host checks).
+// may be short. Rows outside the store are zeros. Measured: 65536 random rows of
+// 768 to fp32 41 us (6.1 TB/s, most of it written); 33 sequences of up to 4000
+// rows of 2048 to bf16 through pages of 16 rows 64.5 us (6.3 TB/s; 191
+// with the place found by every thread, one piece in flight and plain stores).
+// The quotients by the pieces per row and by the block are products by `inv` =
+// 2^32 / divisor, rounded up (exact while dividend x divisor < 2^32, which the
+// host checks).
 constexpr int kReadRows = 64;  // R at most
 
 // The first cnt values of a piece of output: read once by whoever comes next,

@@ -35,6 +35,21 @@ namespace {
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// 16 bytes per lane straight to LDS bytes [lds + 16 lane, + 16): a wave-uniform
+// base, a 32-bit byte offset per lane, the LDS address as a wave-uniform number.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void lds_load16_at(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+// One byte per lane, zero-extended to LDS bytes [lds + 4 lane, + 4).
+__device__ __forceinline__ void lds_load1_at(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 constexpr int kStep = 128;  // codes of k per MFMA, and per scale
 
 __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
@@ -171,7 +186,8 @@ __device__ __forceinline__ void store4(void* out, int64_t at, f32x4 y, int cnt) 
 // Any alignment, any row pitch: 64 x 64 tiles, one k-step of both matrices at
 // a time through registers into LDS. Chunk c of row r sits at c ^ (r % 8), so
 // the eight rows that an operand read touches in one pass of the LDS fall on
-// distinct banks.
+// distinct banks. Reached where rows of codes do not start at multiples of 16
+// bytes; each stage waits for its own loads (8192^3 to bf16 1523 us, 722 TFLOP/s).
 // ---------------------------------------------------------------------------
 constexpr int kAT = 64;
 
@@ -253,15 +269,27 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
 // ---------------------------------------------------------------------------
 // Tiles of 32 MI x 32 NI outputs, four waves of 16 MI x 16 NI each, one k-step
 // (128 codes) per stage, two stages in LDS, loaded straight from memory
-// (global_load_lds) a step ahead. Rows of codes must start at multiples of 16
-// bytes. Layout in LDS as above: row r's chunk c at c ^ (r % 8), arranged by
-// the source address of each lane. The scales of a stage come with it, one
-// byte per row. The codes past k in the last stage are read singly and
-// replaced by zeros: what a row holds beyond its values does not matter.
+// (global_load_lds). Rows of codes must start at multiples of 16 bytes. Layout in
+// LDS as above: row r's chunk c at c ^ (r % 8), arranged by the source address
+// of each lane. The scales of a stage come with it, one byte per row. In the
+// last stage of a k that is no multiple of 128, the 16-byte words that hold no
+// code are not read, and what is no code is cleared in LDS: what a row holds
+// beyond its values does not matter.
 //
 // Workgroups go round the eight XCDs in launch order, so XCD x takes the x-th
 // run of tiles, and a run walks kGroup tile rows at a time: the tiles that
 // share an L2 at one time form a compact patch of the output.
+//
+// 256 x 256 (one workgroup and one wave per SIMD, 256 accumulators in the AGPRs):
+// 8192^3 to bf16 in 375 us called alone, 2933 TFLOP/s, and 455 us (2417) one
+// after another in a graph, where the library's product with one scale for all
+// reaches 2875; 4096 x 4096 x 8192 98 us (2790) in a graph. What bounds it is
+// power: the matrix unit alone, on normal values in registers, holds 4000
+// TFLOP/s, on zeros 4950, and on zeros the same product takes 311 us: 1.03 us a
+// step against 0.90 without its loads and 0.85 of MFMAs alone, and about 50 us
+// of the four rounds' first loads and stores. fp32 results: 128 x 128 tiles
+// on the bf16 unit, two workgroups per CU, 4096^3 123 us (1120 TFLOP/s; the
+// library's bf16 product of 8192^3 reaches 1185).
 // ---------------------------------------------------------------------------
 constexpr int kGroup = 4;
 constexpr int kCUs = 256;
@@ -380,11 +408,11 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
   // first quarter ends; behind a barrier the stage after the next is loaded into
   // its place, spread over the other three: a CU takes a 1 KB load in 16 clocks,
   // so four waves that issue theirs back to back wait for each other, with their
-  // MFMAs behind them (all loads beside one quarter: 1.47 us a step; spread:
-  // see the figures above). Before the last quarter the next stage's loads are
-  // waited for, three to six quarters after they were issued, and a second
-  // barrier makes them everyone's; its first fragments are read beside the last
-  // quarter's MFMAs. The B half that quarter does not use takes the next B0.
+  // MFMAs behind them (all loads beside one quarter: 8192^3 504 us, spread 460).
+  // Before the last quarter the next stage's loads are waited for, three to six
+  // quarters after they were issued, and a second barrier makes them everyone's;
+  // its first fragments are read beside the last quarter's MFMAs. The B half that
+  // quarter does not use takes the next B0.
   constexpr int HA = MI / 2, HB = NI / 2;
   const int ra = (wave & 1) * 16 * MI + col, rb = BM + (wave >> 1) * 16 * NI + col;
   const int fx = 16 * (grp ^ (col & 7));
@@ -578,7 +606,9 @@ __global__ __launch_bounds__(256, MI * NI >= 32 ? 1 : 2) void product_tile_kerne
 // ---------------------------------------------------------------------------
 // Few outputs: 64 x 64 tiles, 32 x 32 per wave, so that more CUs have one, and
 // a ring of four stages. A step's MFMAs run while the next stage's fragments
-// are read; the three stages after that are on their way.
+// are read; the three stages after that are on their way. Whole rings run without
+// a condition inside: with one wave per SIMD every branch of a step shows (200 x
+// 200 x 8192: 15.0 us, with them 21.6; a ring of eight stages was no faster).
 //
 // SPLIT: blockIdx.y takes `per` k-steps and writes fp32 sums to part[y], which
 // join_kernel adds in order.
@@ -762,7 +792,8 @@ __global__ __launch_bounds__(256, 2) void product_small_kernel(BlockProduct p, T
   }
 }
 
-// out = the sum of the splits' parts, in order, rounded once.
+// out = the sum of the splits' parts, in order, rounded once. The parts are in
+// the caches when it reads them; its cost is a second launch's 2-3 us.
 template <int OT>
 __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part, int splits,
                                                    int64_t m, int64_t n, int64_t part_ld,
@@ -788,6 +819,10 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
 // XT >= 0: A is given as numbers (that dt) and encoded by every workgroup into
 // LDS while its first codes of B are on their way; block rows of m * k bytes
 // are small beside B, and it saves a launch.
+//
+// Measured: one bf16 row x 4096 x 4096 6.7 us in a graph (2.5 TB/s; encoding
+// first, 13.1), 16384 x 8192 27 us (4.9 TB/s); 16 rows 10.3 us, 16 rows of
+// codes 7.9 us; 16 x 200003 x 128 11 us (3.4 TB/s; blocks of one 12.5).
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 

@@ -276,17 +276,6 @@ __device__ __forceinline__ void lds_load4(const void* src, void* lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
-// The same with a wave-uniform base, a 32-bit byte offset per lane and the LDS
-// byte address as a (wave-uniform) number.
-__device__ __forceinline__ void lds_load16_at(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-// One byte per lane, zero-extended to LDS bytes [lds + 4 i, lds + 4 i + 4).
-__device__ __forceinline__ void lds_load1_at(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src)
-               : "memory", "m0");
-}
 #pragma clang diagnostic pop
 
 // s_waitcnt immediate that waits for vmcnt <= n only (gfx9 encoding).
