@@ -193,6 +193,26 @@ def test_matmul_alignment_and_tails(mm, m, n, k, pitch, offset):
     assert torch.all(out[:, 0] == 7) and torch.all(out[:, n + 1:] == 7)
 
 
+@pytest.mark.parametrize("m,n,k,out", [(4099, 4096, 160, "bf16"), (4196, 4096, 100, "f16"),
+                                       (4096, 4103, 256, "bf16"), (4100, 4296, 130, "f16"),
+                                       (4098, 4096, 2048, "f32"), (4096, 4196, 2000, "f32"),
+                                       (4120, 4100, 2048, "f32"), (4100, 4112, 4096, "bf16")])
+@pytest.mark.parametrize("tiles", [False, True])
+def test_matmul_a_little_over_whole_rounds(mm, m, n, k, out, tiles):
+    """The rows and columns past the large tiles are products of their own: their
+    scales, their places in a wider result, and nothing beside it written."""
+    import torch
+    a, sa, va = code_matrix(m, k, m + k)
+    b, sb, vb = code_matrix(n, k, n, tiles)
+    y, tol = ref.product(va, vb, out)
+    wide = torch.full((m, n + 5), 7.0, device="cuda", dtype=T(out))
+    got = mm.block_matmul(a, sa, b, sb, out=wide[:, 2:n + 2])
+    err = np.abs(f64(got) - y)
+    fits = np.abs(y) + tol < 65504 if out == "f16" else np.ones_like(y, bool)
+    assert np.all(err[fits] <= tol[fits]), float(np.max(err[fits] / tol[fits]))
+    assert torch.all(wide[:, :2] == 7) and torch.all(wide[:, n + 2:] == 7)
+
+
 @pytest.mark.parametrize("m", [1, 16, 40, 200, 300])
 @pytest.mark.parametrize("out", NUMBERS)
 def test_matmul_of_small_integers_is_exact(mm, m, out):
