@@ -1060,7 +1060,8 @@ Plan plan_of(int64_t m, int64_t n, int32_t k, bool vec, bool f32) {
 // against 23.1, x 128 20.3 against 16.5; 4316 rows 85.5 against 62.0; 4096 x 4103 x
 // 4096 96.5 against 67.4; 8200 x 8192 x 8192 438 against 412; 16392 x 8192 x 768 149
 // against 148. fp32: 4099 x 4096 x 4096 137 against 121, 4196 x 4096 x 4096 133
-// against 129, but 4196 x 4096 x 768 37.3 against 38.6.
+// against 129, but 4196 x 4096 x 768 37.3 against 38.6; 4099 x 4096 x 768 (three rows
+// for kFew) 42.0 against 37.5; bf16 2051 x 4096 x 768 in 128 x 128 tiles 15.3 against 16.0.
 struct Cut {
   int64_t m, n;
 };
@@ -1068,7 +1069,8 @@ struct Cut {
 Cut cut_of(int64_t m, int64_t n, int32_t k, bool vec, bool f32) {
   const Plan plan = plan_of(m, n, k, vec, f32);
   Cut best{m, n};
-  if (plan.kind != kTile8 && (plan.kind != kTile4 || plan.per < 16)) return best;
+  if (plan.kind != kTile8 && plan.kind != kTile4) return best;
+  const bool any = plan.kind == kTile8 || plan.per >= 16;  // else rows of A for kFew only
   const int64_t edge = plan.kind == kTile8 ? 256 : 128;
   const int64_t slots = plan.kind == kTile8 ? kCUs : 2 * kCUs;
   auto rounds = [&](const Cut& c) {
@@ -1082,7 +1084,8 @@ Cut cut_of(int64_t m, int64_t n, int32_t k, bool vec, bool f32) {
   const int64_t m0 = m / edge * edge, n0 = n / edge * edge;
   const Cut cuts[] = {{m0, n}, {m, n0}, {m0, n0}};
   for (const Cut& c : cuts)
-    if (c.m > 0 && c.n > 0 && rounds(c) < rounds(best) && small(c.m, n - c.n) && small(m - c.m, n))
+    if (c.m > 0 && c.n > 0 && rounds(c) < rounds(best) && small(c.m, n - c.n) &&
+        small(m - c.m, n) && (any || (f32 && c.n == n && m - c.m <= kFewRows)))
       best = c;
   return best;
 }
