@@ -281,14 +281,14 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
 // share an L2 at one time form a compact patch of the output.
 //
 // 256 x 256 (one workgroup and one wave per SIMD, 256 accumulators in the AGPRs):
-// 8192^3 to bf16 in 375 us called alone, 2933 TFLOP/s, and 455 us (2417) one
-// after another in a graph, where the library's product with one scale for all
+// 8192^3 to bf16 in 375-392 us called alone, 2800-2930 TFLOP/s, and 455 us (2417)
+// one after another in a graph; the library's product with one scale for all
 // reaches 2875; 4096 x 4096 x 8192 98 us (2790) in a graph. What bounds it is
 // power: the matrix unit alone, on normal values in registers, holds 4000
-// TFLOP/s, on zeros 4950, and on zeros the same product takes 311 us: 1.03 us a
+// TFLOP/s, on zeros 4950, and on zeros the same product takes 304-311 us: 1.03 us a
 // step against 0.90 without its loads and 0.85 of MFMAs alone, and about 50 us
 // of the four rounds' first loads and stores. fp32 results: 128 x 128 tiles
-// on the bf16 unit, two workgroups per CU, 4096^3 123 us (1120 TFLOP/s; the
+// on the bf16 unit, two workgroups per CU, 4096^3 121 us (1134 TFLOP/s; the
 // library's bf16 product of 8192^3 reaches 1185).
 // ---------------------------------------------------------------------------
 constexpr int kGroup = 4;
