@@ -622,7 +622,7 @@ def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=N
     return _run(dev, stream, call)
 
 
-def _linear_codes(x, w, w_scales, out_dtype, stream):
+def _linear_codes(x, w, w_scales, out_dtype):
     """x (m x k numbers) times the transpose of codes: one library call."""
     dev = x.get_device()
     dt = _number(x.dtype, "X")
@@ -643,7 +643,7 @@ def _linear_codes(x, w, w_scales, out_dtype, stream):
                                          None if work is None else work.data_ptr(), st))
         return y
 
-    return _run(dev, stream, call)
+    return _run(dev, None, call)
 
 
 def _rows(t):
@@ -666,7 +666,7 @@ def _linear_fn():
             """y = Q(x) Q(w)^T; the rounding passes gradients straight through."""
 
             @staticmethod
-            def forward(ctx, x, w, out_dtype, stream):
+            def forward(ctx, x, w, out_dtype):
                 dev = x.get_device()
                 dt, wt = _number(x.dtype, "X"), _number(w.dtype, "w")
                 ot = _number(out_dtype, "out_dtype")
@@ -687,16 +687,16 @@ def _linear_fn():
                             y.data_ptr(), ot, n, saved.data_ptr(), work.data_ptr(), st))
                     return y, saved
 
-                y, saved = _run(dev, stream, call)
+                y, saved = _run(dev, None, call)
                 ctx.save_for_backward(saved)
-                ctx.args = m, n, k, x.dtype, dt, w.dtype, wt, stream
+                ctx.args = m, n, k, x.dtype, dt, w.dtype, wt
                 return y
 
             @staticmethod
             @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
                 saved, = ctx.saved_tensors
-                m, n, k, x_type, dt, w_type, wt, stream = ctx.args
+                m, n, k, x_type, dt, w_type, wt = ctx.args
                 need_x, need_w = ctx.needs_input_grad[:2]
                 L = lib()
 
@@ -714,24 +714,23 @@ def _linear_fn():
                             work.data_ptr() if m else None, st))
                     return dx, dw
 
-                return *_run(dy.get_device(), stream, call), None, None
+                return *_run(dy.get_device(), None, call), None
 
         class BlockLinearFrozen(torch.autograd.Function):
             """The same with w as codes in both orders: a gradient of x alone."""
 
             @staticmethod
-            def forward(ctx, x, frozen, out_dtype, stream):
+            def forward(ctx, x, frozen, out_dtype):
                 w, s, wc, wcs = frozen
                 ctx.save_for_backward(wc, wcs)
-                ctx.args = x.dtype, stream
-                return _linear_codes(x, w, s, out_dtype, stream)
+                ctx.x_type = x.dtype
+                return _linear_codes(x, w, s, out_dtype)
 
             @staticmethod
             @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
                 wc, wcs = ctx.saved_tensors
-                x_type, stream = ctx.args
-                return _linear_codes(_rows(dy), wc, wcs, x_type, stream), None, None, None
+                return _linear_codes(_rows(dy), wc, wcs, ctx.x_type), None, None
 
         _linear_function = BlockLinear, BlockLinearFrozen
     return _linear_function
@@ -750,9 +749,13 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     tuple of four of block_encode(w, tiles=True, cols=True), X has a gradient
     and the frozen w none.
 
-    On `stream` (the current one by default) the backward pass runs too; its
-    caller orders the gradients' use, as for any work on another stream."""
+    On `stream` (the current one by default) everything runs, copies of inputs
+    whose values are not adjacent too; the backward pass as well, ordered behind
+    its gradient by autograd."""
     _device_of(X)
+    if stream is not None:
+        with _T().torch.cuda.stream(stream):
+            return block_linear(X, w, out_dtype=out_dtype)
     out_dtype = out_dtype or X.dtype
     flat = X.dim() == 2
     x = X if flat else X.reshape(-1, X.shape[-1])
@@ -765,17 +768,16 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
             if len(w) != 4:
                 raise EmeansError("EINVAL: the gradient of X needs the transposed codes of w: pass "
                                   "the four of block_encode(w, tiles=True, cols=True)")
-            y = _linear_fn()[1].apply(_rows(x), tuple(w), out_dtype, stream)
+            y = _linear_fn()[1].apply(_rows(x), tuple(w), out_dtype)
         else:
-            y = _linear_codes(_rows(x), w[0], w[1], out_dtype, stream)
+            y = _linear_codes(_rows(x), w[0], w[1], out_dtype)
     else:
         if w.dim() != 2 or w.shape[1] != x.shape[1]:
             raise EmeansError(f"EINVAL: w must be n x {x.shape[1]}")
         if grad and (X.requires_grad or w.requires_grad):
-            y = _linear_fn()[0].apply(_rows(x), _rows(w), out_dtype, stream)
+            y = _linear_fn()[0].apply(_rows(x), _rows(w), out_dtype)
         else:
-            y = _linear_codes(_rows(x), *block_encode(_rows(w), tiles=True, stream=stream),
-                              out_dtype, stream)
+            y = _linear_codes(_rows(x), *block_encode(_rows(w), tiles=True), out_dtype)
     return y if flat else y.view(*X.shape[:-1], y.shape[1])
 
 

@@ -533,6 +533,35 @@ def test_on_another_stream(mm):
     assert torch.equal(y, z) and torch.equal(y, mm.block_linear(x, w))
 
 
+def test_another_stream_waits_for_nothing_else_and_its_gradient(mm):
+    """Inputs that have to be copied are copied on the given stream, while the
+    current one is busy; a gradient made late on the current stream is waited
+    for."""
+    import torch
+    s = torch.cuda.Stream()
+    x, w = numbers(300, 40, "f32", 1, 0.1), numbers(50, 300, "f32", 2, 0.1)
+    g = numbers(40, 50, "f32", 3)
+    want_x, want_w = x.t().clone().requires_grad_(), w.clone().requires_grad_()
+    want = mm.block_linear(want_x, want_w)
+    want.backward(g)
+    codes = mm.block_encode(w, tiles=True)
+    xs, ws = x.clone().requires_grad_(), w.clone().requires_grad_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)            # the current stream, about 0.1 s
+    y = mm.block_linear(xs.t(), ws, stream=s)
+    z = mm.block_linear(x.t(), codes, stream=s)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(y, want) and torch.equal(z, want)
+    torch.cuda._sleep(200_000_000)
+    late = torch.zeros_like(g)
+    late.add_(g)
+    y.backward(late)
+    torch.cuda.synchronize()
+    assert torch.equal(ws.grad, want_w.grad) and torch.equal(xs.grad, want_x.grad.t())
+
+
 @pytest.mark.parametrize("m", [1, 20, 150])
 def test_graph_replays(mm, m):
     """Captured calls, replayed with other inputs between eager work."""
