@@ -429,7 +429,8 @@ int emeans_fp8_decode(const float* C, int64_t k, int32_t d, const float* shift, 
  * code is the nearest representable value of x / s, ties to even; infinities
  * saturate, NaN becomes the E4M3 NaN, or int8 0. Number types are EMEANS_F32,
  * EMEANS_BF16 and EMEANS_F16. Leading dimensions (ld...) are the distance of
- * consecutive rows, in elements. All calls are asynchronous on `stream` and
+ * consecutive rows, in elements. A row has at most 2^31 - 1024 values (nor has
+ * any side of a training pass more). All calls are asynchronous on `stream` and
  * may be captured into a graph.
  * ------------------------------------------------------------------------- */
 

@@ -1186,6 +1186,7 @@ int emeans_fp8_decode(const float* C, int64_t k, int32_t d, const float* shift, 
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int64_t kMaxLength = kMaxRows - 1024;  // of a row: its last block's end is an int32
 
 bool number_type(int32_t dt) { return dt == EMEANS_F32 || dt == EMEANS_BF16 || dt == EMEANS_F16; }
 
@@ -1208,12 +1209,18 @@ int check_count(int64_t n, const char* name) {
                                 : EMEANS_OK;
 }
 
+int check_length(int64_t d, int64_t least, const char* name) {
+  return d < least || d > kMaxLength ? fail(EMEANS_EINVAL, "%s out of range (%lld)", name,
+                                            (long long)d)
+                                     : EMEANS_OK;
+}
+
 // Checks shared by the two products.
 int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs, bool b_tiles,
                   int64_t m, int64_t n, int32_t k, const void* out, int32_t out_dtype,
                   int64_t ldo, const void* work) {
   int rc;
-  if ((rc = check_count(m, "m")) || (rc = check_count(n, "n")) || (rc = check_count(k, "k")) ||
+  if ((rc = check_count(m, "m")) || (rc = check_count(n, "n")) || (rc = check_length(k, 0, "k")) ||
       (rc = check_number_type(out_dtype, "out_dtype")))
     return rc;
   const int64_t kb = blocks_of(k, 128), sr = b_tiles ? blocks_of(n, 128) : n;
@@ -1231,7 +1238,7 @@ int check_store(const void* codes, const uint8_t* scales, int64_t rows, int64_t 
                 int32_t fmt) {
   if (rows < 0 || rows > ((int64_t)1 << 40))
     return fail(EMEANS_EINVAL, "rows out of range (%lld)", (long long)rows);
-  if (d < 1 || d >= kMaxRows) return fail(EMEANS_EINVAL, "d out of range (%lld)", (long long)d);
+  if (const int rc = check_length(d, 1, "d")) return rc;
   if (block < 16 || block > 256 || block % 16)
     return fail(EMEANS_EINVAL, "block must be a multiple of 16 in [16, 256] (got %d)", block);
   if (fmt != EMEANS_F8 && fmt != EMEANS_I8)
@@ -1278,6 +1285,7 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
   int rc;
   if ((rc = check_count(n, "n")) || (rc = check_number_type(dtype, "dtype"))) return rc;
   if (d < 1) return fail(EMEANS_EINVAL, "d must be >= 1");
+  if ((rc = check_length(d, 1, "d"))) return rc;
   if (!codes && !codes_t) return fail(EMEANS_EINVAL, "codes and codes_t are both NULL");
   if (!codes != !scales || !codes_t != !scales_t)
     return fail(EMEANS_EINVAL, "codes and scales (codes_t and scales_t) come together");
@@ -1306,14 +1314,14 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
 }
 
 int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k) {
-  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1) return 0;
+  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1 || k > kMaxLength) return 0;
   return (int64_t)block_product_work(m, n, k);
 }
 
 // The product's own working memory, then codes of X with rows a multiple of 16
 // bytes apart, then their scales with rows a multiple of 4 bytes apart.
 int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k) {
-  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1) return 0;
+  if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1 || k > kMaxLength) return 0;
   if (block_product_encodes(m, k)) return 0;
   return emeans_block_matmul_work(m, n, k) +
          m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
@@ -1437,16 +1445,16 @@ struct TrainGradient {
 
 int check_train(int64_t m, int64_t n, int32_t k, const void* saved, const void* work) {
   int rc;
-  if ((rc = check_count(m, "m"))) return rc;
-  if (n < 1 || n >= kMaxRows) return fail(EMEANS_EINVAL, "n out of range (%lld)", (long long)n);
-  if (k < 1) return fail(EMEANS_EINVAL, "k out of range (%d)", k);
+  if ((rc = check_length(m, 0, "m")) || (rc = check_length(n, 1, "n")) ||
+      (rc = check_length(k, 1, "k")))
+    return rc;
   if ((uintptr_t)saved % 16 || (uintptr_t)work % 16)
     return fail(EMEANS_EINVAL, "saved and work must be 16-byte aligned");
   return EMEANS_OK;
 }
 
 bool train_sizes(int64_t m, int64_t n, int32_t k) {
-  return m >= 1 && m < kMaxRows && n >= 1 && n < kMaxRows && k >= 1;
+  return m >= 1 && m <= kMaxLength && n >= 1 && n <= kMaxLength && k >= 1 && k <= kMaxLength;
 }
 
 }  // namespace

@@ -217,3 +217,15 @@ def test_binding_refuses_cpu_tensors():
                  lambda: mm.cache_read_pages(c[None], s[None], i[None], i, 3)):
         with pytest.raises(mm.EmeansError, match="ENOTDEVICE"):
             call()
+
+
+@pytest.mark.parametrize("d", [2 ** 31 - 1023, 2 ** 31 - 1])
+def test_rows_too_long_for_their_last_block(L, d):
+    """The end of a row's last block has to fit 31 bits; nothing is computed from
+    a longer length."""
+    assert _encode(L, d=d, ldx=d, ldc=d, lds=d) == -1 and b"d out" in L.emeans_last_error()
+    assert _matmul(L, k=d, lda=d, ldb=d, ldas=d, ldbs=d) == -1 and b"k out" in L.emeans_last_error()
+    assert L.emeans_block_matmul_work(4, 5, d) == 0 and L.emeans_block_linear_work(40, 5, d) == 0
+    for m, n, k in ((d, 5, 5), (5, d, 5), (5, 5, d)):
+        assert L.emeans_block_train_saved(m, n, k) == 0
+        assert L.emeans_block_train_work(m, n, k, 0) == L.emeans_block_train_work(m, n, k, 1) == 0
