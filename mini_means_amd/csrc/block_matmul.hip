@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256) void product_any_kernel(BlockProduct p, unsign
 // share an L2 at one time form a compact patch of the output.
 //
 // 256 x 256 (one workgroup and one wave per SIMD, 256 accumulators in the AGPRs):
-// 8192^3 to bf16 in 375-392 us called alone, 2800-2930 TFLOP/s, and 455 us (2417)
+// 8192^3 to bf16 in 369-392 us called alone, 2800-2980 TFLOP/s, and 455 us (2417)
 // one after another in a graph; the library's product with one scale for all
 // reaches 2875; 4096 x 4096 x 8192 98 us (2790) in a graph. What bounds it is
 // power: the matrix unit alone, on normal values in registers, holds 4000
