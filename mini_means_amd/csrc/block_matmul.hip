@@ -37,15 +37,16 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // 16 bytes per lane straight to LDS bytes [lds + 16 lane, + 16): a wave-uniform
 // base, a 32-bit byte offset per lane, the LDS address as a wave-uniform number.
+// s_nop: the wait state between the write of M0 and a direct load (common.hpp).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load16_at(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
                : "memory", "m0");
 }
 // One byte per lane, zero-extended to LDS bytes [lds + 4 lane, + 4).
 __device__ __forceinline__ void lds_load1_at(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(lds), "v"(src)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop

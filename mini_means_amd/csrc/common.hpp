@@ -260,7 +260,9 @@ __device__ __forceinline__ double readlane_f64(double v, int lane) {
 // the asm has no register outputs, and completion is waited for with
 // EMK_WAIT_VMCNT. M0 is clobbered: the backend reserves it and sets it right
 // before any instruction that reads it, so no value of its own is live
-// across the asm.
+// across the asm. A direct load needs one wait state after the scalar write of
+// M0 (the backend puts in the same s_nop around its own direct loads, but does
+// not look into asm); without it the load may go where the M0 before it pointed.
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
@@ -268,12 +270,12 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load16(const void* src, void* lds) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
 __device__ __forceinline__ void lds_load4(const void* src, void* lds) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
