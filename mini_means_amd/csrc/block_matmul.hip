@@ -76,7 +76,9 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p, int cnt) {
 // product one of fp32's range; what is left of a scale beyond (`rest`, 0 in
 // all ordinary data) is applied to the step's sums.
 constexpr int kFold = 50;
-constexpr int kRestNaN = 1 << 20;  // the scale byte 255
+// The rest of the scale byte 255. A sum of two rests holds one if it is above half
+// of it: the other rest, +-77 at most, may have taken away from it.
+constexpr int kRestNaN = 1 << 20;
 
 template <bool F8>
 struct Operand;
@@ -140,7 +142,7 @@ __device__ __forceinline__ f32x4 add_step(const Operand<false>& bn, const Operan
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int r = am.rest + __shfl(bn.rest, 4 * (lane >> 4) + v, 64);  // row n = 4 (l / 16) + v
-    c[v] += r >= kRestNaN ? __builtin_nanf("") : __builtin_ldexpf(t[v], r);
+    c[v] += r > kRestNaN / 2 ? __builtin_nanf("") : __builtin_ldexpf(t[v], r);
   }
   return c;
 }
