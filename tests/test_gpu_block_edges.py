@@ -1,10 +1,11 @@
 """Block codes on the GPU at the edges of their number formats, for every kernel
-of the product: scale bytes of NaN beside any other scale."""
+of the product: scale bytes of NaN beside any other scale, scales at both ends
+of their range, and exact integers at sizes of each kernel."""
 import numpy as np
 import pytest
 
 import block_ref as ref
-from test_gpu_block import NUMBERS, T, f64, mm  # noqa: F401
+from test_gpu_block import NUMBERS, T, code_matrix, f64, mm, numbers  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,85 @@ def test_nan_scale_beside_any_other(mm, m, n, k, pitch, other):
         assert np.array_equal(np.isnan(got), bad), (out, int((np.isnan(got) != bad).sum()))
         ok = ~bad & ((np.abs(y) + tol < 65504) if out == "f16" else True)
         assert np.all(np.abs(got - y)[ok] <= tol[ok]), out
+
+
+@pytest.mark.parametrize("m,n,k,pitch", KERNELS)
+def test_nan_codes(mm, m, n, k, pitch):
+    """NaN codes of either sign, in the first and the last place of a row."""
+    rng = np.random.default_rng(m)
+    ba, bb = finite_codes(rng, m, k), finite_codes(rng, n, k)
+    ba[m - 1, k - 1] = 0xFF
+    bb[3, 0], bb[5, k - 1] = 0x7F, 0xFF
+    bad = np.zeros((m, n), bool)
+    bad[m - 1] = bad[:, 3] = bad[:, 5] = True
+    kb = -(-k // 128)
+    a, sa = on_gpu(ba, np.full((m, kb), 120), pitch)
+    b, sb = on_gpu(bb, np.full((n, kb), 125), pitch)
+    for out in NUMBERS:
+        got = f64(mm.block_matmul(a, sa, b, sb, out_dtype=T(out)))
+        assert np.array_equal(np.isnan(got), bad), out
+
+
+def exact(mm, rng, m, n, k, pitch, ea, eb):
+    """Integer codes of -8 .. 8: with scales that leave sums below 2^24, exact in
+    either matrix unit, so the result is the rounded sum. This pins each value
+    and each scale to its place."""
+    import torch
+    va, vb = (rng.integers(-8, 9, (rows, k)).astype(float) for rows in (m, n))
+    code = lambda v: torch.from_numpy(v).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()  # noqa: E731
+    a, sa = on_gpu(code(va), ea + 127, pitch)
+    b, sb = on_gpu(code(vb), eb + 127, pitch)
+    y = torch.from_numpy(ref.values(va, ea) @ ref.values(vb, eb).T)
+    for out in NUMBERS:
+        got = mm.block_matmul(a, sa, b, sb, out_dtype=T(out)).cpu()
+        assert torch.equal(got, y.to(T(out))), (out, int((got != y.to(T(out))).sum()))
+
+
+@pytest.mark.parametrize("m,n,k,pitch", KERNELS + [(4100, 4100, 520, 0), (4096, 4099, 768, 0)])
+@pytest.mark.parametrize("tiles", [False, True])
+def test_matmul_of_small_integers_is_exact_in_every_kernel(mm, m, n, k, pitch, tiles):
+    rng = np.random.default_rng(m + n + k)
+    kb = -(-k // 128)
+    exact(mm, rng, m, n, k, pitch, rng.integers(0, 2, (m, kb)),
+          rng.integers(0, 2, (-(-n // 128) if tiles else n, kb)))
+
+
+@pytest.mark.parametrize("m,n,k,pitch", KERNELS)
+def test_scales_at_both_ends_cancel(mm, m, n, k, pitch):
+    """Scales from 2^-127 to 2^127 whose products are 1 and 2: beyond what the
+    bf16 unit's operands hold (2^+-50), in splits of k and in redone tiles too."""
+    rng = np.random.default_rng(m + n + k)
+    kb = -(-k // 128)
+    e = rng.choice([-127, -90, -51, -50, 0, 50, 51, 90, 126], kb)
+    exact(mm, rng, m, n, k, pitch, e + rng.integers(0, 2, (m, kb)), np.tile(-e, (n, 1)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 9, 16, 40, 300])
+def test_linear_special_rows_in_the_default_type(mm, dtype, m):
+    """Zero rows, infinities and NaN of x, and rows that start at odd places:
+    results of x's own 16-bit type."""
+    import torch
+    n, k = 200, 300
+    wide = numbers(m, k + 40, dtype, 3, spread=0.1)
+    x = wide[:, 7:7 + k]
+    x[0, :] = 0
+    if m > 3:
+        x[1, 5], x[2, 150], x[3, 299] = float("inf"), float("nan"), -float("inf")
+    w, sw, vw = code_matrix(n, k, 4)
+    y, tol = ref.product(ref.values(*ref.encode(f64(x))), vw, dtype)
+    got = f64(mm.block_linear(x, (w, sw)))
+    assert np.array_equal(np.isnan(got), np.isnan(y)) and np.all(got[0] == 0)
+    ok = ~np.isnan(y) & ((np.abs(y) + tol < 65504) if dtype == "f16" else True)
+    assert np.all(np.abs(got - y)[ok] <= tol[ok])
+
+
+@pytest.mark.parametrize("dtype", NUMBERS)
+@pytest.mark.parametrize("m", [1, 9, 16, 40])
+def test_linear_rows_at_odd_starts(mm, dtype, m):
+    n, k = 200, 300
+    x = numbers(m, k + 40, dtype, 3, spread=0.1)[:, 7:7 + k]
+    w, sw, vw = code_matrix(n, k, 4)
+    y, tol = ref.product(ref.values(*ref.encode(f64(x))), vw, "f32")
+    got = f64(mm.block_linear(x, (w, sw), out_dtype=T("f32")))
+    assert np.all(np.abs(got - y) <= tol)
