@@ -444,7 +444,7 @@ int emeans_fp8_decode(const float* C, int64_t k, int32_t d, const float* shift, 
  *   X  device, n x d, dtype
  * Errors: EINVAL (n < 0, n >= 2^31, d < 1, a leading dimension below the row
  * length, no output, codes without scales), EDTYPE, ENOTDEVICE, EHIP. */
-int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int64_t ldx,
+int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int64_t d, int64_t ldx,
                         int32_t tiles, uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
                         uint8_t* codes_t, int64_t ldct, uint8_t* scales_t, int64_t ldst,
                         void* stream);
@@ -466,10 +466,10 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
  * so up to 15 bytes past a row's last code are read too, of the same word).
  * Errors: EINVAL (m, n or k < 0, m or n >= 2^31, a leading dimension below
  * the row length, work not aligned, NULL), EDTYPE, ENOTDEVICE, ENOMEM, EHIP. */
-int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k);
+int64_t emeans_block_matmul_work(int64_t m, int64_t n, int64_t k);
 int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
                         const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
-                        int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
+                        int32_t b_tiles, int64_t m, int64_t n, int64_t k, void* out,
                         int32_t out_dtype, int64_t ldo, void* work, void* stream);
 
 /* The same product with A given as numbers: X (m x k, dtype) is encoded as
@@ -477,10 +477,10 @@ int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_
  * are encoded inside the product's own launch; more are encoded first, into
  * work (emeans_block_linear_work(m, n, k) bytes, 16-byte aligned, or NULL).
  * Errors: as emeans_block_matmul. */
-int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k);
+int64_t emeans_block_linear_work(int64_t m, int64_t n, int64_t k);
 int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
                         const uint8_t* Bs, int64_t ldbs, int32_t b_tiles, int64_t m, int64_t n,
-                        int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
+                        int64_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
                         void* stream);
 
 /* The forward pass of y = x w^T for training, and its gradients: all numbers are
@@ -497,14 +497,14 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
  *          bytes, 16-byte aligned, or NULL (allocated stream-ordered)
  * saved must be 16-byte aligned. With m = 0 dW is zeros.
  * Errors: as emeans_block_matmul; EINVAL for n or k < 1 and need outside 0..3. */
-int64_t emeans_block_train_saved(int64_t m, int64_t n, int32_t k);
-int64_t emeans_block_train_work(int64_t m, int64_t n, int32_t k, int32_t gradient);
+int64_t emeans_block_train_saved(int64_t m, int64_t n, int64_t k);
+int64_t emeans_block_train_work(int64_t m, int64_t n, int64_t k, int32_t gradient);
 int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, const void* W,
-                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int32_t k,
+                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int64_t k,
                                int32_t need, void* out, int32_t out_dtype, int64_t ldo,
                                void* saved, void* work, void* stream);
 int emeans_block_train_gradient(const void* dY, int32_t dtype, int64_t lddy, const void* saved,
-                                int64_t m, int64_t n, int32_t k, void* dX, int32_t dx_dtype,
+                                int64_t m, int64_t n, int64_t k, void* dX, int32_t dx_dtype,
                                 int64_t lddx, void* dW, int32_t dw_dtype, int64_t lddw,
                                 void* work, void* stream);
 
@@ -521,18 +521,18 @@ int emeans_block_train_gradient(const void* dY, int32_t dtype, int64_t lddy, con
  *   slots   device, n integers of slot_bytes (4 or 8)
  *   codes   device, rows x d      scales  device, rows x ceil(d/block)
  * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
-int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,
+int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int64_t heads, int64_t width,
                        int64_t row_stride, int64_t head_stride, const void* slots,
                        int32_t slot_bytes, void* codes, uint8_t* scales, int64_t rows,
-                       int32_t block, int32_t fmt, void* stream);
+                       int64_t block, int32_t fmt, void* stream);
 
 /* out[i] = row slots[i] of the store as numbers (code * scale, one rounding to
  * out_dtype); a slot outside [0, rows) reads as zeros.
  *   slots  device, n integers of slot_bytes (4 or 8)
  *   out    device, n x d, out_dtype, rows ldo elements apart
  * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
-int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d,
-                      int32_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
+int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int64_t d,
+                      int64_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
                       int64_t n, void* out, int32_t out_dtype, int64_t ldo, void* stream);
 
 /* Ragged sequences read through a page table into packed rows: the store is
@@ -544,9 +544,9 @@ int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, in
  *   starts  device, seqs + 1 int32, not decreasing
  * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
 int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pages,
-                            int32_t page_rows, int32_t d, int32_t block, int32_t fmt,
-                            const int32_t* table, int64_t table_ld, int32_t table_pages,
-                            const int32_t* starts, int32_t seqs, int64_t n, void* out,
+                            int64_t page_rows, int64_t d, int64_t block, int32_t fmt,
+                            const int32_t* table, int64_t table_ld, int64_t table_pages,
+                            const int32_t* starts, int64_t seqs, int64_t n, void* out,
                             int32_t out_dtype, int64_t ldo, void* stream);
 
 /* Message for the last non-zero return on this thread ("" if none). */

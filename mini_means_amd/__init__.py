@@ -94,32 +94,32 @@ def lib() -> ctypes.CDLL:
         for f in ("emeans_fp8_calibrate", "emeans_fp8_encode", "emeans_fp8_decode"):
             getattr(L, f).argtypes = getattr(L, f.replace("fp8", "int8")).argtypes
             getattr(L, f).restype = ctypes.c_int
-        L.emeans_block_encode.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i64, c_i32, c_vp, c_i64,
+        # lengths are 64 bits wide, as ctypes cuts what does not fit without a word
+        L.emeans_block_encode.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_i32, c_vp, c_i64,
                                           c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]
         L.emeans_block_matmul.argtypes = [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64,
-                                          c_i32, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp,
+                                          c_i32, c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp,
                                           c_vp]
-        for f in ("emeans_block_matmul_work", "emeans_block_linear_work"):
-            getattr(L, f).argtypes = [c_i64, c_i64, c_i32]
+        for f in ("emeans_block_matmul_work", "emeans_block_linear_work",
+                  "emeans_block_train_saved"):
+            getattr(L, f).argtypes = [c_i64, c_i64, c_i64]
             getattr(L, f).restype = c_i64
         L.emeans_block_linear.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
-                                          c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_vp]
-        L.emeans_block_train_saved.argtypes = [c_i64, c_i64, c_i32]
-        L.emeans_block_train_saved.restype = c_i64
-        L.emeans_block_train_work.argtypes = [c_i64, c_i64, c_i32, c_i32]
+                                          c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, c_vp]
+        L.emeans_block_train_work.argtypes = [c_i64, c_i64, c_i64, c_i32]
         L.emeans_block_train_work.restype = c_i64
         L.emeans_block_train_forward.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_i64,
-                                                 c_i64, c_i32, c_i32, c_vp, c_i32, c_i64, c_vp,
+                                                 c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp,
                                                  c_vp, c_vp]
-        L.emeans_block_train_gradient.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_i64, c_i32,
+        L.emeans_block_train_gradient.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_i64, c_i64,
                                                   c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_vp,
                                                   c_vp]
-        L.emeans_cache_write.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i32, c_i64, c_i64, c_vp,
-                                         c_i32, c_vp, c_vp, c_i64, c_i32, c_i32, c_vp]
-        L.emeans_cache_read.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, c_i32,
+        L.emeans_cache_write.argtypes = [c_vp, c_i32, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                         c_i32, c_vp, c_vp, c_i64, c_i64, c_i32, c_vp]
+        L.emeans_cache_read.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_i32,
                                         c_i64, c_vp, c_i32, c_i64, c_vp]
-        L.emeans_cache_read_pages.argtypes = [c_vp, c_vp, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp,
-                                              c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_i32,
+        L.emeans_cache_read_pages.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp,
+                                              c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i32,
                                               c_i64, c_vp]
         for f in ("emeans_block_encode", "emeans_block_matmul", "emeans_block_linear",
                   "emeans_block_train_forward", "emeans_block_train_gradient",
@@ -585,6 +585,11 @@ def _product_out(m, n, out, out_dtype, device):
     return out
 
 
+def _ptr(t):
+    """Address of a tensor; None for none."""
+    return None if t is None else t.data_ptr()
+
+
 def _work(need: int, device):
     """Working memory of one call, allocated where the call runs; None for none."""
     return _T().torch.empty((need,), dtype=_T().torch.uint8, device=device) if need else None
@@ -615,8 +620,7 @@ def block_matmul(a, a_scales, b, b_scales, *, out_dtype=None, out=None, stream=N
             _check(L.emeans_block_matmul(a.data_ptr(), lda, a_scales.data_ptr(), ldas,
                                          b.data_ptr(), ldb, b_scales.data_ptr(), ldbs,
                                          1 if b_tiles else 0, m, n, k, y.data_ptr(), ot,
-                                         y.stride(0), None if work is None else work.data_ptr(),
-                                         st))
+                                         y.stride(0), _ptr(work), st))
         return y
 
     return _run(dev, stream, call)
@@ -639,8 +643,7 @@ def _linear_codes(x, w, w_scales, out_dtype):
             work = _work(L.emeans_block_linear_work(m, n, k), x.device)
             _check(L.emeans_block_linear(x.data_ptr(), dt, ldx, w.data_ptr(), ldb,
                                          w_scales.data_ptr(), ldbs, 1 if tiles else 0, m, n, k,
-                                         y.data_ptr(), ot, n,
-                                         None if work is None else work.data_ptr(), st))
+                                         y.data_ptr(), ot, n, _ptr(work), st))
         return y
 
     return _run(dev, None, call)
@@ -684,7 +687,7 @@ def _linear_fn():
                     if m:
                         _check(L.emeans_block_train_forward(
                             x.data_ptr(), dt, ldx, w.data_ptr(), wt, ldw, m, n, k, need,
-                            y.data_ptr(), ot, n, saved.data_ptr(), work.data_ptr(), st))
+                            y.data_ptr(), ot, n, _ptr(saved), _ptr(work), st))
                     return y, saved
 
                 y, saved = _run(dev, None, call)
@@ -810,7 +813,9 @@ def _store(dev, codes, scales, block):
     if len(shape) < 2 or not codes.is_contiguous() or not scales.is_contiguous():
         raise EmeansError("EINVAL: codes and scales must be contiguous, rows last but one")
     d = shape[-1]
-    if block < 1 or shape[:-1] != sshape[:-1] or sshape[-1] != -(-d // block):
+    if not 16 <= block <= 256 or block % 16:
+        raise EmeansError(f"EINVAL: block must be a multiple of 16 in [16, 256] (got {block})")
+    if shape[:-1] != sshape[:-1] or sshape[-1] != -(-d // block):
         raise EmeansError(f"EINVAL: scales must be {tuple(shape[:-1])} x ceil({d} / {block}), got "
                           f"{tuple(sshape)}")
     return fmt, codes.numel() // d if d else 0, d

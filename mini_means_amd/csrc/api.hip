@@ -1217,7 +1217,7 @@ int check_length(int64_t d, int64_t least, const char* name) {
 
 // Checks shared by the two products.
 int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs, bool b_tiles,
-                  int64_t m, int64_t n, int32_t k, const void* out, int32_t out_dtype,
+                  int64_t m, int64_t n, int64_t k, const void* out, int32_t out_dtype,
                   int64_t ldo, const void* work) {
   int rc;
   if ((rc = check_count(m, "m")) || (rc = check_count(n, "n")) || (rc = check_length(k, 0, "k")) ||
@@ -1234,13 +1234,14 @@ int check_product(const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs
   return EMEANS_OK;
 }
 
-int check_store(const void* codes, const uint8_t* scales, int64_t rows, int64_t d, int32_t block,
+int check_store(const void* codes, const uint8_t* scales, int64_t rows, int64_t d, int64_t block,
                 int32_t fmt) {
   if (rows < 0 || rows > ((int64_t)1 << 40))
     return fail(EMEANS_EINVAL, "rows out of range (%lld)", (long long)rows);
   if (const int rc = check_length(d, 1, "d")) return rc;
   if (block < 16 || block > 256 || block % 16)
-    return fail(EMEANS_EINVAL, "block must be a multiple of 16 in [16, 256] (got %d)", block);
+    return fail(EMEANS_EINVAL, "block must be a multiple of 16 in [16, 256] (got %lld)",
+                (long long)block);
   if (fmt != EMEANS_F8 && fmt != EMEANS_I8)
     return fail(EMEANS_EDTYPE, "fmt %d not supported (int8 = 2, fp8 = 3)", fmt);
   if (rows > 0 && (!codes || !scales))
@@ -1248,7 +1249,7 @@ int check_store(const void* codes, const uint8_t* scales, int64_t rows, int64_t 
   return EMEANS_OK;
 }
 
-int check_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d, int64_t n,
+int check_read(const void* codes, const uint8_t* scales, int64_t rows, int64_t d, int64_t n,
                const void* out, int32_t out_dtype, int64_t ldo) {
   int rc;
   if ((rc = check_count(n, "n")) || (rc = check_number_type(out_dtype, "out_dtype")) ||
@@ -1277,7 +1278,7 @@ int launched(hipError_t e, const char* what) {
 
 }  // namespace
 
-int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int64_t ldx,
+int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int64_t d, int64_t ldx,
                         int32_t tiles, uint8_t* codes, int64_t ldc, uint8_t* scales, int64_t lds,
                         uint8_t* codes_t, int64_t ldct, uint8_t* scales_t, int64_t ldst,
                         void* stream) {
@@ -1307,29 +1308,29 @@ int emeans_block_encode(const void* X, int32_t dtype, int64_t n, int32_t d, int6
     return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (!tiles && !codes_t)
-    return launched(launch_encode_rows({dtype, X, n, d, d, ldx, 0, 128, false, nullptr, 0, n,
-                                        codes, ldc, scales, lds}, st), "block encode");
-  return launched(launch_encode_tiles({dtype, X, ldx, n, d, tiles != 0, codes, ldc, scales, lds,
-                                       codes_t, ldct, scales_t, ldst}, st), "block encode");
+    return launched(launch_encode_rows({dtype, X, n, (int)d, (int)d, ldx, 0, 128, false, nullptr, 0,
+                                        n, codes, ldc, scales, lds}, st), "block encode");
+  return launched(launch_encode_tiles({dtype, X, ldx, n, (int)d, tiles != 0, codes, ldc, scales,
+                                       lds, codes_t, ldct, scales_t, ldst}, st), "block encode");
 }
 
-int64_t emeans_block_matmul_work(int64_t m, int64_t n, int32_t k) {
+int64_t emeans_block_matmul_work(int64_t m, int64_t n, int64_t k) {
   if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1 || k > kMaxLength) return 0;
-  return (int64_t)block_product_work(m, n, k);
+  return (int64_t)block_product_work(m, n, (int)k);
 }
 
 // The product's own working memory, then codes of X with rows a multiple of 16
 // bytes apart, then their scales with rows a multiple of 4 bytes apart.
-int64_t emeans_block_linear_work(int64_t m, int64_t n, int32_t k) {
+int64_t emeans_block_linear_work(int64_t m, int64_t n, int64_t k) {
   if (m < 1 || m >= kMaxRows || n < 1 || n >= kMaxRows || k < 1 || k > kMaxLength) return 0;
-  if (block_product_encodes(m, k)) return 0;
+  if (block_product_encodes(m, (int)k)) return 0;
   return emeans_block_matmul_work(m, n, k) +
          m * (blocks_of(k, 16) * 16 + blocks_of(blocks_of(k, 128), 4) * 4);
 }
 
 int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_t ldas,
                         const uint8_t* B, int64_t ldb, const uint8_t* Bs, int64_t ldbs,
-                        int32_t b_tiles, int64_t m, int64_t n, int32_t k, void* out,
+                        int32_t b_tiles, int64_t m, int64_t n, int64_t k, void* out,
                         int32_t out_dtype, int64_t ldo, void* work, void* stream) {
   g_err.clear();
   int rc;
@@ -1343,8 +1344,8 @@ int emeans_block_matmul(const uint8_t* A, int64_t lda, const uint8_t* As, int64_
     return rc;
   if ((rc = check_device(out, "out")) || (work && (rc = check_device(work, "work")))) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  BlockProduct p{A, lda, As, ldas, B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo,
-                 work};
+  BlockProduct p{A, lda, As, ldas, B, ldb, Bs, ldbs, b_tiles != 0, m, n, (int)k, out_dtype, out,
+                 ldo, work};
   const int64_t need = emeans_block_matmul_work(m, n, k);
   void* own = nullptr;
   rc = EMEANS_OK;
@@ -1359,7 +1360,7 @@ done:
 
 int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t* B, int64_t ldb,
                         const uint8_t* Bs, int64_t ldbs, int32_t b_tiles, int64_t m, int64_t n,
-                        int32_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
+                        int64_t k, void* out, int32_t out_dtype, int64_t ldo, void* work,
                         void* stream) {
   g_err.clear();
   int rc;
@@ -1375,8 +1376,8 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
   if ((rc = check_device(out, "out")) || (work && (rc = check_device(work, "work")))) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   BlockProduct p{nullptr, blocks_of(k, 16) * 16, nullptr, blocks_of(blocks_of(k, 128), 4) * 4,
-                 B, ldb, Bs, ldbs, b_tiles != 0, m, n, k, out_dtype, out, ldo, work};
-  if (block_product_encodes(m, k)) {
+                 B, ldb, Bs, ldbs, b_tiles != 0, m, n, (int)k, out_dtype, out, ldo, work};
+  if (block_product_encodes(m, (int)k)) {
     p.A = static_cast<const uint8_t*>(X);
     p.lda = ldx;
     return launched(launch_encode_product(dtype, p, st), "block linear");
@@ -1392,8 +1393,8 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
     uint8_t* scales = codes + m * p.lda;
     p.A = codes;
     p.As = scales;
-    HIP_TRY(launch_encode_rows({dtype, X, m, k, k, ldx, 0, 128, false, nullptr, 0, m, codes,
-                                p.lda, scales, p.ldas}, st));
+    HIP_TRY(launch_encode_rows({dtype, X, m, (int)k, (int)k, ldx, 0, 128, false, nullptr, 0, m,
+                                codes, p.lda, scales, p.ldas}, st));
   }
   HIP_TRY(launch_block_product(p, st));
 done:
@@ -1428,7 +1429,7 @@ struct TrainForward {
   int64_t own, end;
   TrainForward(int64_t m, int64_t n, int64_t k) : x(0, m, k, false), w(x.end, n, k, true) {
     own = w.end;
-    end = own + emeans_block_matmul_work(m, n, (int32_t)k);
+    end = own + emeans_block_matmul_work(m, n, k);
   }
 };
 
@@ -1437,13 +1438,13 @@ struct TrainGradient {
   int64_t own, end;
   TrainGradient(int64_t m, int64_t n, int64_t k) : y(0, m, n, false), yt(y.end, n, m, false) {
     own = yt.end;
-    const int64_t a = emeans_block_matmul_work(m, k, (int32_t)n);
-    const int64_t b = emeans_block_matmul_work(n, k, (int32_t)m);
+    const int64_t a = emeans_block_matmul_work(m, k, n);
+    const int64_t b = emeans_block_matmul_work(n, k, m);
     end = own + (a > b ? a : b);
   }
 };
 
-int check_train(int64_t m, int64_t n, int32_t k, const void* saved, const void* work) {
+int check_train(int64_t m, int64_t n, int64_t k, const void* saved, const void* work) {
   int rc;
   if ((rc = check_length(m, 0, "m")) || (rc = check_length(n, 1, "n")) ||
       (rc = check_length(k, 1, "k")))
@@ -1453,23 +1454,23 @@ int check_train(int64_t m, int64_t n, int32_t k, const void* saved, const void* 
   return EMEANS_OK;
 }
 
-bool train_sizes(int64_t m, int64_t n, int32_t k) {
+bool train_sizes(int64_t m, int64_t n, int64_t k) {
   return m >= 1 && m <= kMaxLength && n >= 1 && n <= kMaxLength && k >= 1 && k <= kMaxLength;
 }
 
 }  // namespace
 
-int64_t emeans_block_train_saved(int64_t m, int64_t n, int32_t k) {
+int64_t emeans_block_train_saved(int64_t m, int64_t n, int64_t k) {
   return train_sizes(m, n, k) ? TrainSaved(m, n, k).w.end : 0;
 }
 
-int64_t emeans_block_train_work(int64_t m, int64_t n, int32_t k, int32_t gradient) {
+int64_t emeans_block_train_work(int64_t m, int64_t n, int64_t k, int32_t gradient) {
   if (!train_sizes(m, n, k)) return 0;
   return gradient ? TrainGradient(m, n, k).end : TrainForward(m, n, k).end;
 }
 
 int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, const void* W,
-                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int32_t k,
+                               int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int64_t k,
                                int32_t need, void* out, int32_t out_dtype, int64_t ldo,
                                void* saved, void* work, void* stream) {
   g_err.clear();
@@ -1496,23 +1497,23 @@ int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, cons
   if (!work) HIP_TRY(hipMallocAsync(&own, f.end, st));
   if (own) work = own;
   if (dw)
-    HIP_TRY(launch_encode_tiles({x_dtype, X, ldx, m, k, false, f.x.c(work), f.x.ld, f.x.s(work),
+    HIP_TRY(launch_encode_tiles({x_dtype, X, ldx, m, (int)k, false, f.x.c(work), f.x.ld, f.x.s(work),
                                  f.x.lds, sv.x.c(saved), sv.x.ld, sv.x.s(saved), sv.x.lds}, st));
   else
-    HIP_TRY(launch_encode_rows({x_dtype, X, m, k, k, ldx, 0, 128, false, nullptr, 0, m,
+    HIP_TRY(launch_encode_rows({x_dtype, X, m, (int)k, (int)k, ldx, 0, 128, false, nullptr, 0, m,
                                 f.x.c(work), f.x.ld, f.x.s(work), f.x.lds}, st));
-  HIP_TRY(launch_encode_tiles({w_dtype, W, ldw, n, k, true, f.w.c(work), f.w.ld, f.w.s(work),
+  HIP_TRY(launch_encode_tiles({w_dtype, W, ldw, n, (int)k, true, f.w.c(work), f.w.ld, f.w.s(work),
                                f.w.lds, dx ? sv.w.c(saved) : nullptr, sv.w.ld,
                                dx ? sv.w.s(saved) : nullptr, sv.w.lds}, st));
   HIP_TRY(launch_block_product({f.x.c(work), f.x.ld, f.x.s(work), f.x.lds, f.w.c(work), f.w.ld,
-                                f.w.s(work), f.w.lds, true, m, n, k, out_dtype, out, ldo,
+                                f.w.s(work), f.w.lds, true, m, n, (int)k, out_dtype, out, ldo,
                                 static_cast<uint8_t*>(work) + f.own}, st));
 done:
   return release(own, st, rc);
 }
 
 int emeans_block_train_gradient(const void* dY, int32_t dtype, int64_t lddy, const void* saved,
-                                int64_t m, int64_t n, int32_t k, void* dX, int32_t dx_dtype,
+                                int64_t m, int64_t n, int64_t k, void* dX, int32_t dx_dtype,
                                 int64_t lddx, void* dW, int32_t dw_dtype, int64_t lddw,
                                 void* work, void* stream) {
   g_err.clear();
@@ -1561,40 +1562,42 @@ done:
   return release(own, st, rc);
 }
 
-int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int32_t heads, int32_t width,
+int emeans_cache_write(const void* X, int32_t dtype, int64_t n, int64_t heads, int64_t width,
                        int64_t row_stride, int64_t head_stride, const void* slots,
                        int32_t slot_bytes, void* codes, uint8_t* scales, int64_t rows,
-                       int32_t block, int32_t fmt, void* stream) {
+                       int64_t block, int32_t fmt, void* stream) {
   g_err.clear();
   int rc;
   if ((rc = check_count(n, "n")) || (rc = check_number_type(dtype, "dtype"))) return rc;
   if (heads < 1 || width < 1)
-    return fail(EMEANS_EINVAL, "heads and width must be >= 1 (got %d and %d)", heads, width);
-  int64_t d = (int64_t)heads * width;
+    return fail(EMEANS_EINVAL, "heads and width must be >= 1 (got %lld and %lld)",
+                (long long)heads, (long long)width);
+  if ((rc = check_length(heads, 1, "heads")) || (rc = check_length(width, 1, "width"))) return rc;
+  const int64_t d = heads * width;
   if ((rc = check_store(codes, scales, rows, d, block, fmt))) return rc;
   if (row_stride < 0 || head_stride < 0)
     return fail(EMEANS_EINVAL, "strides must not be negative");
   if (slot_bytes != 4 && slot_bytes != 8)
     return fail(EMEANS_EINVAL, "slot_bytes must be 4 or 8 (got %d)", slot_bytes);
   if (heads == 1 || head_stride == width)
-    width = (int32_t)d;  // one run of values
+    width = d;  // one run of values
   else if (width % block)
-    return fail(EMEANS_EINVAL, "heads apart from each other need a width (%d) that is a multiple "
-                "of block (%d)", width, block);
+    return fail(EMEANS_EINVAL, "heads apart from each other need a width (%lld) that is a "
+                "multiple of block (%lld)", (long long)width, (long long)block);
   if (n == 0 || rows == 0) return EMEANS_OK;
   if (!X || !slots) return fail(EMEANS_EINVAL, "X and slots must not be NULL");
   if ((rc = check_device(X, "X")) || (rc = check_device(slots, "slots")) ||
       (rc = check_device(codes, "codes")) || (rc = check_device(scales, "scales")))
     return rc;
-  return launched(launch_encode_rows({dtype, X, n, (int)d, width, row_stride, head_stride, block,
-                                      fmt == EMEANS_I8, slots, slot_bytes, rows,
+  return launched(launch_encode_rows({dtype, X, n, (int)d, (int)width, row_stride, head_stride,
+                                      (int)block, fmt == EMEANS_I8, slots, slot_bytes, rows,
                                       static_cast<uint8_t*>(codes), d, scales,
                                       blocks_of(d, block)}, static_cast<hipStream_t>(stream)),
                   "cache write");
 }
 
-int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int32_t d,
-                      int32_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
+int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, int64_t d,
+                      int64_t block, int32_t fmt, const void* slots, int32_t slot_bytes,
                       int64_t n, void* out, int32_t out_dtype, int64_t ldo, void* stream) {
   g_err.clear();
   int rc;
@@ -1605,25 +1608,26 @@ int emeans_cache_read(const void* codes, const uint8_t* scales, int64_t rows, in
   if ((rc = check_read(codes, scales, rows, d, n, out, out_dtype, ldo))) return rc;
   if (n == 0) return EMEANS_OK;
   if ((rc = check_device(slots, "slots"))) return rc;
-  return launched(launch_decode_rows({static_cast<const uint8_t*>(codes), scales, rows, d, block,
-                                      fmt == EMEANS_I8, slots, slot_bytes, nullptr, 0, 0, nullptr,
+  return launched(launch_decode_rows({static_cast<const uint8_t*>(codes), scales, rows, (int)d,
+                                      (int)block, fmt == EMEANS_I8, slots, slot_bytes, nullptr, 0, 0, nullptr,
                                       0, 1, n, out_dtype, out, ldo},
                                      static_cast<hipStream_t>(stream)), "cache read");
 }
 
 int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pages,
-                            int32_t page_rows, int32_t d, int32_t block, int32_t fmt,
-                            const int32_t* table, int64_t table_ld, int32_t table_pages,
-                            const int32_t* starts, int32_t seqs, int64_t n, void* out,
+                            int64_t page_rows, int64_t d, int64_t block, int32_t fmt,
+                            const int32_t* table, int64_t table_ld, int64_t table_pages,
+                            const int32_t* starts, int64_t seqs, int64_t n, void* out,
                             int32_t out_dtype, int64_t ldo, void* stream) {
   g_err.clear();
   int rc;
-  if (page_rows < 1) return fail(EMEANS_EINVAL, "page_rows must be >= 1 (got %d)", page_rows);
-  if ((rc = check_count(pages, "pages")) || (rc = check_count(seqs, "seqs"))) return rc;
+  if ((rc = check_length(page_rows, 1, "page_rows")) || (rc = check_count(pages, "pages")) ||
+      (rc = check_count(seqs, "seqs")))
+    return rc;
   if ((rc = check_store(codes, scales, pages * page_rows, d, block, fmt))) return rc;
-  if (table_pages < 0 || (rc = check_ld(table_ld, table_pages, seqs, "table_ld")))
-    return fail(EMEANS_EINVAL, "table_pages or table_ld out of range (%d, %lld)", table_pages,
-                (long long)table_ld);
+  if ((rc = check_count(table_pages, "table_pages")) ||
+      (rc = check_ld(table_ld, table_pages, seqs, "table_ld")))
+    return rc;
   if (n > 0 && (!starts || (seqs > 0 && table_pages > 0 && !table)))
     return fail(EMEANS_EINVAL, "table and starts must not be NULL");
   if ((rc = check_read(codes, scales, pages * page_rows, d, n, out, out_dtype, ldo))) return rc;
@@ -1632,9 +1636,9 @@ int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pa
       (seqs > 0 && table_pages > 0 && (rc = check_device(table, "table"))))
     return rc;
   return launched(launch_decode_rows({static_cast<const uint8_t*>(codes), scales,
-                                      pages * page_rows, d, block, fmt == EMEANS_I8, nullptr, 4,
-                                      table, table_ld, table_pages, starts, seqs, page_rows, n,
-                                      out_dtype, out, ldo},
+                                      pages * page_rows, (int)d, (int)block, fmt == EMEANS_I8, nullptr,
+                                      4, table, table_ld, (int)table_pages, starts, (int)seqs,
+                                      (int)page_rows, n, out_dtype, out, ldo},
                                      static_cast<hipStream_t>(stream)), "cache read");
 }
 

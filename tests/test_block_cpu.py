@@ -229,3 +229,37 @@ def test_rows_too_long_for_their_last_block(L, d):
     for m, n, k in ((d, 5, 5), (5, d, 5), (5, 5, d)):
         assert L.emeans_block_train_saved(m, n, k) == 0
         assert L.emeans_block_train_work(m, n, k, 0) == L.emeans_block_train_work(m, n, k, 1) == 0
+
+
+FAR = 2 ** 32 + 128   # 128 in its lower half
+
+
+def test_lengths_keep_their_upper_bits(L):
+    """Lengths past 32 bits are refused by every entry, not taken for what their
+    lower half says; so is a block, whose lower half would give the store's rows
+    more scales than they have room for."""
+    assert _encode(L, d=FAR, ldx=FAR, ldc=FAR, lds=FAR) == -1 and b"d out" in L.emeans_last_error()
+    big = dict(k=FAR, ldb=FAR, ldbs=FAR)
+    assert _matmul(L, lda=FAR, ldas=FAR, **big) == -1 and b"k out" in L.emeans_last_error()
+    assert _linear(L, ldx=FAR, **big) == -1 and b"k out" in L.emeans_last_error()
+    assert L.emeans_block_matmul_work(40, 5, FAR) == L.emeans_block_linear_work(40, 5, FAR) == 0
+    assert L.emeans_block_train_saved(40, 5, FAR) == 0
+    for gradient in (0, 1):
+        assert L.emeans_block_train_work(40, 5, FAR, gradient) == 0
+    assert L.emeans_block_train_forward(FAKE, 0, FAR, FAKE, 0, FAR, 4, 5, FAR, 3, FAKE, 0, 5, FAKE,
+                                        None, None) == -1
+    assert b"k out" in L.emeans_last_error()
+    assert L.emeans_block_train_gradient(FAKE, 0, 5, FAKE, 4, 5, FAR, FAKE, 0, FAR, FAKE, 0, FAR,
+                                         None, None) == -1
+    assert b"k out" in L.emeans_last_error()
+    for change, word in ((dict(heads=2 ** 32 + 2), b"heads"), (dict(width=2 ** 32 + 96), b"width"),
+                         (dict(heads=1, width=FAR, rs=FAR), b"width"),
+                         (dict(heads=2 ** 33, width=2 ** 33), b"heads"),
+                         (dict(block=2 ** 32 + 96), b"block")):
+        assert _write(L, **change) == -1 and word in L.emeans_last_error(), change
+    for change, word in ((dict(d=FAR, ldo=FAR), b"d out"), (dict(block=2 ** 32 + 32), b"block")):
+        assert _read(L, **change) == -1 and word in L.emeans_last_error(), change
+        assert _pages(L, **change) == -1 and word in L.emeans_last_error(), change
+    for change, word in ((dict(page=2 ** 32 + 16), b"page_rows"), (dict(seqs=2 ** 32 + 2), b"seqs"),
+                         (dict(tp=2 ** 32 + 4, ldt=2 ** 33), b"table_pages")):
+        assert _pages(L, **change) == -1 and word in L.emeans_last_error(), change

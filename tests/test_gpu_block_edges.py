@@ -146,3 +146,20 @@ def test_linear_rows_at_odd_starts(mm, dtype, m):
     y, tol = ref.product(ref.values(*ref.encode(f64(x))), vw, "f32")
     got = f64(mm.block_linear(x, (w, sw), out_dtype=T("f32")))
     assert np.all(np.abs(got - y) <= tol)
+
+
+def test_blocks_whose_lower_half_is_another(mm):
+    """A block is its whole number, not its lower 32 or 64 bits: scales of one
+    per row would be too few for it."""
+    import torch
+    codes, scales = mm.cache_new(6, 200)
+    x, slots = numbers(4, 200, "f32", 1), torch.arange(4, device="cuda")
+    pages = codes.view(2, 3, 200), scales[:, :1].contiguous().view(2, 3, 1)
+    for block in (2 ** 32 + 128, 2 ** 64 + 128, 0, -128, 8, 24, 272):
+        one = scales[:, :1].contiguous()
+        for call in (lambda: mm.cache_write(x, slots, codes, one, block=block),
+                     lambda: mm.cache_read(codes, one, slots, block=block),
+                     lambda: mm.cache_read_pages(*pages, slots.int()[None, :2], slots.int()[:2], 1,
+                                                 block=block)):
+            with pytest.raises(mm.EmeansError, match="EINVAL.*block"):
+                call()
