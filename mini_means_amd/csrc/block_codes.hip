@@ -65,8 +65,8 @@ uint32_t inverse(uint64_t div, uint64_t most) {  // exact for dividends up to mo
 }
 
 template <int DT, bool I8, int G, int SLOTS, int U>
-__global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, int d, int block,
-                                                          uint32_t nb, uint32_t nb_inv,
+__global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t wg0, int64_t n, int d,
+                                                          int block, uint32_t nb, uint32_t nb_inv,
                                                           const void* __restrict__ slots,
                                                           int64_t cap,
                                                           uint8_t* __restrict__ codes,
@@ -74,7 +74,7 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(RowsIn in, int64_t n, 
                                                           uint8_t* __restrict__ scales,
                                                           int64_t lds) {
   constexpr int kGroups = 256 / G;
-  const int64_t first = (int64_t)blockIdx.x * (kGroups * U);
+  const int64_t first = (wg0 + blockIdx.x) * (kGroups * U);
   const int64_t row0 = first / nb;
   const uint32_t skip = (uint32_t)(first - row0 * nb) + threadIdx.x / G;
   const int sub = threadIdx.x & (G - 1);
@@ -491,13 +491,13 @@ template <int OT, bool I8, bool PAGES>
 __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
                                                           int64_t cap, int d, int nb,
-                                                          RowsFrom from, int64_t n, int R,
-                                                          Divisors dv, void* __restrict__ out,
-                                                          int64_t ldo) {
+                                                          RowsFrom from, int64_t wg0, int64_t n,
+                                                          int R, Divisors dv,
+                                                          void* __restrict__ out, int64_t ldo) {
   constexpr int E = OT == 0 ? 4 : 8;
   constexpr int U = 4;  // pieces in flight per thread
   __shared__ int64_t place[kReadRows];
-  const int64_t row0 = (int64_t)blockIdx.x * R;
+  const int64_t row0 = (wg0 + blockIdx.x) * R;
   const int rows = (int)min((int64_t)R, n - row0);
   if ((int)threadIdx.x < rows)
     place[threadIdx.x] = source_row<PAGES>(from, row0 + threadIdx.x, cap);
@@ -558,27 +558,37 @@ __global__ __launch_bounds__(256) void decode_rows_kernel(const uint8_t* __restr
   }
 }
 
+// go(first workgroup, workgroups) for each launch that `wgs` workgroups take.
+template <typename GO>
+hipError_t in_launches(int64_t wgs, GO go) {
+  for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
+    go(wg0, (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int DT, bool I8, int G, int U>
 hipError_t encode_rows_u(const EncodeRows& a, hipStream_t st) {
   const int64_t nb = (a.d + a.block - 1) / a.block;
   constexpr int64_t per = 256 / G * U;
   const int64_t wgs = (a.n * nb + per - 1) / per;
-  if (wgs > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)wgs), wg(256);
   const RowsIn in{a.X, a.rs, a.hs, a.width};
   const uint32_t inv = inverse(nb, nb + per);
-#define EMK_GO(S)                                                                               \
-  encode_rows_kernel<DT, I8, G, S, U><<<grid, wg, 0, st>>>(in, a.n, a.d, a.block, (uint32_t)nb,  \
-                                                           inv, a.slots, a.cap, a.codes, a.ldc, \
-                                                           a.scales, a.lds)
-  if (!a.slots)
-    EMK_GO(0);
-  else if (a.slot_bytes == 8)
-    EMK_GO(8);
-  else
-    EMK_GO(4);
+  return in_launches(wgs, [&](int64_t wg0, unsigned grid) {
+#define EMK_GO(S)                                                                                 \
+  encode_rows_kernel<DT, I8, G, S, U><<<grid, 256, 0, st>>>(in, wg0, a.n, a.d, a.block,           \
+                                                            (uint32_t)nb, inv, a.slots, a.cap,    \
+                                                            a.codes, a.ldc, a.scales, a.lds)
+    if (!a.slots)
+      EMK_GO(0);
+    else if (a.slot_bytes == 8)
+      EMK_GO(8);
+    else
+      EMK_GO(4);
 #undef EMK_GO
-  return hipGetLastError();
+  });
 }
 
 template <int DT, bool I8, int G>
@@ -602,21 +612,23 @@ hipError_t encode_tile_t(const EncodeTiles& a, hipStream_t st) {
   const int64_t gx = (a.d + kT - 1) / kT, gy = (a.n + kT - 1) / kT;
   // rows in launches of at most 65535 tiles (the grid's y limit)
   for (int64_t y0 = 0; y0 < gy; y0 += 65535) {
-    const int64_t ny = gy - y0 < 65535 ? gy - y0 : 65535;
-    const dim3 grid((unsigned)gx, (unsigned)ny), wg(Patch<DT>::kThreads);
-    const int64_t r = y0 * kT, size = DT == 0 ? 4 : 2;
-    const void* X = static_cast<const char*>(a.X) + r * a.ldx * size;
-    uint8_t* codes = a.codes ? a.codes + r * a.ldc : nullptr;
-    uint8_t* scales = a.scales ? a.scales + (a.tiles ? y0 : r) * a.lds : nullptr;
-    uint8_t* ct = a.codes_t ? a.codes_t + r : nullptr;
-    uint8_t* stt = a.scales_t ? a.scales_t + y0 : nullptr;
-    if (a.tiles)
-      encode_tile_kernel<DT, true><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, a.d, codes, a.ldc, scales,
-                                                        a.lds, ct, a.ldct, stt, a.ldst);
-    else
-      encode_tile_kernel<DT, false><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, a.d, codes, a.ldc,
-                                                         scales, a.lds, ct, a.ldct, stt, a.ldst);
-    const hipError_t e = hipGetLastError();
+    const unsigned ny = (unsigned)(gy - y0 < 65535 ? gy - y0 : 65535);
+    const hipError_t e = in_launches(gx, [&](int64_t x0, unsigned nx) {
+      const dim3 grid(nx, ny), wg(Patch<DT>::kThreads);
+      const int64_t r = y0 * kT, c = x0 * kT, size = DT == 0 ? 4 : 2;
+      const void* X = static_cast<const char*>(a.X) + (r * a.ldx + c) * size;
+      uint8_t* codes = a.codes ? a.codes + r * a.ldc + c : nullptr;
+      uint8_t* scales = a.scales ? a.scales + (a.tiles ? y0 : r) * a.lds + x0 : nullptr;
+      uint8_t* ct = a.codes_t ? a.codes_t + c * a.ldct + r : nullptr;
+      uint8_t* stt = a.scales_t ? a.scales_t + (a.tiles ? x0 : c) * a.ldst + y0 : nullptr;
+      const int d = a.d - (int)c;
+      if (a.tiles)
+        encode_tile_kernel<DT, true><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, d, codes, a.ldc, scales,
+                                                          a.lds, ct, a.ldct, stt, a.ldst);
+      else
+        encode_tile_kernel<DT, false><<<grid, wg, 0, st>>>(X, a.ldx, a.n - r, d, codes, a.ldc,
+                                                           scales, a.lds, ct, a.ldct, stt, a.ldst);
+    });
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -631,20 +643,18 @@ hipError_t decode_rows_t(const DecodeRows& a, hipStream_t st) {
   int64_t R = 4096 / per;
   if (R > a.n / 2048) R = a.n / 2048;
   R = R < 1 ? 1 : R > kReadRows ? kReadRows : R;
-  const int64_t blocks = (a.n + R - 1) / R;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const Divisors dv{per, inverse(per, (uint64_t)R * per), (uint32_t)a.block,
                     inverse(a.block, a.d)};
-  const dim3 grid((unsigned)blocks), wg(256);
   const RowsFrom f{a.slots, a.slot_bytes, a.table, a.table_ld, a.table_pages, a.starts, a.seqs,
                    a.page};
-  if (a.slots)
-    decode_rows_kernel<OT, I8, false><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, a.n,
-                                                           (int)R, dv, a.out, a.ldo);
-  else
-    decode_rows_kernel<OT, I8, true><<<grid, wg, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f, a.n,
-                                                          (int)R, dv, a.out, a.ldo);
-  return hipGetLastError();
+  return in_launches((a.n + R - 1) / R, [&](int64_t wg0, unsigned grid) {
+    if (a.slots)
+      decode_rows_kernel<OT, I8, false><<<grid, 256, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f,
+                                                              wg0, a.n, (int)R, dv, a.out, a.ldo);
+    else
+      decode_rows_kernel<OT, I8, true><<<grid, 256, 0, st>>>(a.codes, a.scales, a.cap, a.d, nb, f,
+                                                             wg0, a.n, (int)R, dv, a.out, a.ldo);
+  });
 }
 
 }  // namespace

@@ -23,6 +23,7 @@
 // The first operand is B's rows (n), the second A's (m): the result then has
 // n = 4 (l / 16) + v, v < 4, and m = l % 16 in lane l, four consecutive
 // values of an output row.
+#include <algorithm>
 #include <type_traits>
 
 #include "block.hpp"
@@ -995,7 +996,6 @@ template <int OT, int XT, int AH, int NT>
 hipError_t product_few_t(const BlockProduct& p, int wk_log, hipStream_t st) {
   const int64_t per = 16 * NT * (kFewWaves >> wk_log);
   const int64_t wgs = (p.n + per - 1) / per;
-  if (wgs > INT32_MAX) return hipErrorInvalidValue;
   product_few_kernel<OT, XT, AH, NT><<<(unsigned)wgs, 64 * kFewWaves,
                                        XT >= 0 ? few_room(p.m, p.k) : 0, st>>>(p, wk_log);
   return hipGetLastError();
@@ -1107,7 +1107,6 @@ template <int MI, int NI, int OT>
 hipError_t product_tiles(const BlockProduct& p, const Plan& plan, hipStream_t st) {
   constexpr int BM = 32 * MI, BN = 32 * NI;
   const int64_t tm = (p.m + BM - 1) / BM, tn = (p.n + BN - 1) / BN;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   const TileMap t{(unsigned)tm, (unsigned)tn, plan.per, nullptr, 0};
   const unsigned grid = (unsigned)(tm * tn);
   if (p.k % kStep)
@@ -1120,7 +1119,6 @@ hipError_t product_tiles(const BlockProduct& p, const Plan& plan, hipStream_t st
 template <int OT>
 hipError_t product_small(const BlockProduct& p, const Plan& plan, hipStream_t st) {
   const int64_t tm = (p.m + kST - 1) / kST, tn = (p.n + kST - 1) / kST;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   TileMap t{(unsigned)tm, (unsigned)tn, plan.per, static_cast<float*>(p.work), part_pitch(p.n)};
   const dim3 grid((unsigned)(tm * tn), (unsigned)plan.splits);
   if (plan.splits == 1) {
@@ -1150,36 +1148,66 @@ hipError_t product_one(const BlockProduct& p, hipStream_t st) {
     case kAny: break;
   }
   const int64_t tm = (p.m + kAT - 1) / kAT, tn = (p.n + kAT - 1) / kAT;
-  if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
   product_any_kernel<OT><<<(unsigned)(tm * tn), 256, 0, st>>>(p, (unsigned)tn);
   return hipGetLastError();
 }
 
-// Whole product: the tiles' rectangle, and what cut_of leaves beside it.
+// Outputs m0 .. + m and n0 .. + n of a product; n0 is a multiple of 128, a border of
+// B's tiles.
+BlockProduct part_of(const BlockProduct& p, int64_t m0, int64_t n0, int64_t m, int64_t n) {
+  BlockProduct q = p;
+  q.m = m, q.n = n;
+  if (m0) q.A += m0 * p.lda, q.As += m0 * p.ldas;
+  if (n0) q.B += n0 * p.ldb, q.Bs += (p.b_tiles ? n0 / kStep : n0) * p.ldbs;
+  q.out = static_cast<uint8_t*>(p.out) + (m0 * p.ldo + n0) * (p.ot == 0 ? 4 : 2);
+  return q;
+}
+
+// The tiles' rectangle, and what cut_of leaves beside it.
+template <int OT>
+hipError_t product_cut(const BlockProduct& p, hipStream_t st) {
+  const Cut c = cut_of(p.m, p.n, p.k, words(p), OT == 0);
+  hipError_t e = product_one<OT>(part_of(p, 0, 0, c.m, c.n), st);
+  if (e == hipSuccess && c.n < p.n)
+    e = product_one<OT>(part_of(p, 0, c.n, c.m, p.n - c.n), st);
+  if (e == hipSuccess && c.m < p.m)
+    e = product_one<OT>(part_of(p, c.m, 0, p.m - c.m, p.n), st);
+  return e;
+}
+
+// A product of more workgroups than a launch takes goes in pieces of m x n outputs:
+// at most kMaxGroups tiles of 64 x 64, the smallest there are, and of the row
+// kernel's 16 rows of B. Multiples of 256, so that pieces are whole tiles.
+struct Piece {
+  int64_t m, n;
+};
+
+Piece piece_of(int64_t m, int64_t n) {
+  Piece c{m, std::min(n, 8 * kMaxGroups)};
+  const int64_t tiles = (c.n + kST - 1) / kST;
+  c.m = std::min(m, kMaxGroups / tiles / 4 * 256);
+  return c;
+}
+
+template <typename GO>
+hipError_t in_pieces(const BlockProduct& p, GO go) {
+  const Piece c = piece_of(p.m, p.n);
+  for (int64_t n0 = 0; n0 < p.n; n0 += c.n)
+    for (int64_t m0 = 0; m0 < p.m; m0 += c.m) {
+      const hipError_t e = go(part_of(p, m0, n0, std::min(c.m, p.m - m0), std::min(c.n, p.n - n0)));
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
+}
+
 template <int OT>
 hipError_t product_t(const BlockProduct& p, hipStream_t st) {
-  const Cut c = cut_of(p.m, p.n, p.k, words(p), OT == 0);
-  const int64_t size = OT == 0 ? 4 : 2;
-  BlockProduct q = p;
-  q.m = c.m, q.n = c.n;
-  hipError_t e = product_one<OT>(q, st);
-  if (e == hipSuccess && c.n < p.n) {  // c.n is a multiple of 128: a border of B's tiles
-    q = p;
-    q.m = c.m, q.n = p.n - c.n;
-    q.B += c.n * p.ldb;
-    q.Bs += (p.b_tiles ? c.n / kStep : c.n) * p.ldbs;
-    q.out = static_cast<uint8_t*>(p.out) + c.n * size;
-    e = product_one<OT>(q, st);
-  }
-  if (e == hipSuccess && c.m < p.m) {
-    q = p;
-    q.m = p.m - c.m;
-    q.A += c.m * p.lda;
-    q.As += c.m * p.ldas;
-    q.out = static_cast<uint8_t*>(p.out) + c.m * p.ldo * size;
-    e = product_one<OT>(q, st);
-  }
-  return e;
+  return in_pieces(p, [&](const BlockProduct& q) { return product_cut<OT>(q, st); });
+}
+
+template <int OT, int XT>
+hipError_t encode_product_t(const BlockProduct& p, hipStream_t st) {  // few rows: one piece of A
+  return in_pieces(p, [&](const BlockProduct& q) { return product_few<OT, XT>(q, st); });
 }
 
 }  // namespace
@@ -1192,9 +1220,9 @@ hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st) 
   if (p.m <= 0 || p.n <= 0) return hipSuccess;
 #define EMK_XT(OT)                                \
   switch (dt) {                                   \
-    case 0: return product_few<OT, 0>(p, st);       \
-    case 1: return product_few<OT, 1>(p, st);       \
-    case 4: return product_few<OT, 4>(p, st);       \
+    case 0: return encode_product_t<OT, 0>(p, st);  \
+    case 1: return encode_product_t<OT, 1>(p, st);  \
+    case 4: return encode_product_t<OT, 4>(p, st);  \
   }                                               \
   break
   switch (p.ot) {
@@ -1213,12 +1241,16 @@ size_t block_product_work(int64_t m, int64_t n, int32_t k) {
     const size_t bytes = splits > 1 ? (size_t)splits * a * part_pitch(b) * sizeof(float) : 0;
     if (bytes > most) most = bytes;
   };
-  for (const bool f32 : {false, true}) {  // the result's type is not known here
-    const Cut c = cut_of(m, n, k, true, f32);
-    need(c.m, c.n, f32);
-    need(c.m, n - c.n, f32);
-    need(m - c.m, n, f32);
-  }
+  const Piece piece = piece_of(m, n);
+  for (const int64_t a : {piece.m, m % piece.m})  // whole pieces and the last of either side
+    for (const int64_t b : {piece.n, n % piece.n})
+      for (const bool f32 : {false, true}) {  // the result's type is not known here
+        if (a == 0 || b == 0) continue;
+        const Cut c = cut_of(a, b, k, true, f32);
+        need(c.m, c.n, f32);
+        need(c.m, b - c.n, f32);
+        need(a - c.m, b, f32);
+      }
   return most;
 }
 

@@ -223,6 +223,10 @@ hipError_t launch_decode(const float* C, int64_t k, int d, const float* shift, d
 // block of values; number types dt / ot: 0 fp32, 1 bf16, 4 fp16.
 // ---------------------------------------------------------------------------
 
+// Workgroups of one launch along a grid dimension: HIP takes fewer than 2^32 work
+// items, and workgroups here have up to 512. Larger calls are several launches.
+constexpr int64_t kMaxGroups = (int64_t)1 << 22;
+
 // Codes and scales of n rows, blocks of `block` values along the row (a
 // multiple of 16, at most 256; the last of a row may be short). Value (h, c)
 // of row r sits at X[r rs + h hs + c], c < width, and d = heads * width; with
