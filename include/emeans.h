@@ -492,12 +492,17 @@ int emeans_block_linear(const void* X, int32_t dtype, int64_t ldx, const uint8_t
  *   saved  device, emeans_block_train_saved(m, n, k) bytes: transposed codes of
  *          X and W (1 byte a value) and their scales
  * need: what the gradient pass will be asked for, 1 dX, 2 dW, 3 both (only that
- * is made). dX, dW: device, m x k and n x k, or NULL (not computed).
+ * is made). The codes of X come first: with need = 2 saved holds them alone, in
+ * emeans_block_train_saved_for(m, n, k, 2) bytes; with the others it is whole. (For
+ * dX alone, W as codes in both orders, n k bytes each, and emeans_block_linear of X
+ * and of dY give the same without the room for X.)
+ * dX, dW: device, m x k and n x k, or NULL (not computed).
  *   work   device, emeans_block_train_work(m, n, k, 0 forward / 1 gradient)
  *          bytes, 16-byte aligned, or NULL (allocated stream-ordered)
  * saved must be 16-byte aligned. With m = 0 dW is zeros.
  * Errors: as emeans_block_matmul; EINVAL for n or k < 1 and need outside 0..3. */
 int64_t emeans_block_train_saved(int64_t m, int64_t n, int64_t k);
+int64_t emeans_block_train_saved_for(int64_t m, int64_t n, int64_t k, int32_t need);
 int64_t emeans_block_train_work(int64_t m, int64_t n, int64_t k, int32_t gradient);
 int emeans_block_train_forward(const void* X, int32_t x_dtype, int64_t ldx, const void* W,
                                int32_t w_dtype, int64_t ldw, int64_t m, int64_t n, int64_t k,

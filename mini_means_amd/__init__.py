@@ -106,6 +106,8 @@ def lib() -> ctypes.CDLL:
             getattr(L, f).restype = c_i64
         L.emeans_block_linear.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i64, c_vp, c_i64, c_i32,
                                           c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, c_vp]
+        L.emeans_block_train_saved_for.argtypes = [c_i64, c_i64, c_i64, c_i32]
+        L.emeans_block_train_saved_for.restype = c_i64
         L.emeans_block_train_work.argtypes = [c_i64, c_i64, c_i64, c_i32]
         L.emeans_block_train_work.restype = c_i64
         L.emeans_block_train_forward.argtypes = [c_vp, c_i32, c_i64, c_vp, c_i32, c_i64, c_i64,
@@ -649,6 +651,13 @@ def _linear_codes(x, w, w_scales, out_dtype):
     return _run(dev, None, call)
 
 
+def _tiles_room(n: int, d: int):
+    """One room for the codes of an n x d matrix with a scale per tile: the codes'
+    row distance, where the scales start, their row distance, bytes in all."""
+    ld, lds = -(-d // 16) * 16, -(-d // (4 * BLOCK)) * 4
+    return ld, n * ld, lds, -(-(n * ld + -(-n // BLOCK) * lds) // 16) * 16
+
+
 def _rows(t):
     """t as a matrix whose rows are runs that do not overlap (a copy if it is
     not one: an expanded gradient, say)."""
@@ -682,7 +691,7 @@ def _linear_fn():
 
                 def call(st):
                     y = torch.empty((m, n), dtype=out_dtype, device=x.device)
-                    saved = _work(L.emeans_block_train_saved(m, n, k), x.device)
+                    saved = _work(L.emeans_block_train_saved_for(m, n, k, need), x.device)
                     work = _work(L.emeans_block_train_work(m, n, k, 0), x.device)
                     if m:
                         _check(L.emeans_block_train_forward(
@@ -735,7 +744,63 @@ def _linear_fn():
                 wc, wcs = ctx.saved_tensors
                 return _linear_codes(_rows(dy), wc, wcs, ctx.x_type), None, None
 
-        _linear_function = BlockLinear, BlockLinearFrozen
+        class BlockLinearX(torch.autograd.Function):
+            """The same with a gradient of x alone: w's transposed codes are kept."""
+
+            @staticmethod
+            def forward(ctx, x, w, out_dtype):
+                dev = x.get_device()
+                dt, wt = _number(x.dtype, "X"), _number(w.dtype, "w")
+                ot = _number(out_dtype, "out_dtype")
+                m, k, ldx = _matrix(x, dev, "X", (x.dtype,), "")
+                n, _, ldw = _matrix(w, dev, "w", (w.dtype,), "")
+                if n < 1 or k < 1:
+                    raise EmeansError("EINVAL: w must have rows and columns")
+                L = lib()
+                ld, scales, lds, size = _tiles_room(n, k)
+                ldt, scales_t, ldst, size_t = _tiles_room(k, n)
+
+                def call(st):
+                    y = torch.empty((m, n), dtype=out_dtype, device=x.device)
+                    kept = _work(size_t, x.device)
+                    if m:
+                        work = _work(size + L.emeans_block_linear_work(m, n, k), x.device)
+                        at, at_t = work.data_ptr(), kept.data_ptr()
+                        _check(L.emeans_block_encode(w.data_ptr(), wt, n, k, ldw, 1, at, ld,
+                                                     at + scales, lds, at_t, ldt, at_t + scales_t,
+                                                     ldst, st))
+                        _check(L.emeans_block_linear(x.data_ptr(), dt, ldx, at, ld, at + scales,
+                                                     lds, 1, m, n, k, y.data_ptr(), ot, n,
+                                                     at + size, st))
+                    return y, kept
+
+                y, kept = _run(dev, None, call)
+                ctx.save_for_backward(kept)
+                ctx.args = m, n, k, x.dtype, dt
+                return y
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                kept, = ctx.saved_tensors
+                m, n, k, x_type, dt = ctx.args
+                ldt, scales_t, ldst, _ = _tiles_room(k, n)
+                L = lib()
+
+                def call(st):
+                    g = _rows(dy)
+                    dx = torch.empty((m, k), dtype=x_type, device=g.device)
+                    if m:
+                        work = _work(L.emeans_block_linear_work(m, k, n), g.device)
+                        at = kept.data_ptr()
+                        _check(L.emeans_block_linear(g.data_ptr(), _number(g.dtype, "the gradient"),
+                                                     g.stride(0), at, ldt, at + scales_t, ldst, 1,
+                                                     m, k, n, dx.data_ptr(), dt, k, _ptr(work), st))
+                    return dx
+
+                return _run(dy.get_device(), None, call), None, None
+
+        _linear_function = BlockLinear, BlockLinearFrozen, BlockLinearX
     return _linear_function
 
 
@@ -746,7 +811,8 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     w a float32, bfloat16 or float16 tensor: encoded in the call; gradients of
     X and w pass straight through the rounding, dX = Q(dY) Q(w) and dw =
     Qt(dY) Qt(X)^T (Qt: the transpose, blocks along the rows of X), with the codes
-    of X and w kept for the backward pass instead of the numbers.
+    of X (if w has a gradient) and of w (if X has one) kept for the backward pass
+    instead of the numbers.
     w a tuple (codes, scales), as block_encode(w, tiles=True) gives: serving,
     where a few rows of X are encoded inside the product's launch. With the
     tuple of four of block_encode(w, tiles=True, cols=True), X has a gradient
@@ -777,8 +843,10 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     else:
         if w.dim() != 2 or w.shape[1] != x.shape[1]:
             raise EmeansError(f"EINVAL: w must be n x {x.shape[1]}")
-        if grad and (X.requires_grad or w.requires_grad):
+        if grad and w.requires_grad:
             y = _linear_fn()[0].apply(_rows(x), _rows(w), out_dtype)
+        elif grad and X.requires_grad:
+            y = _linear_fn()[2].apply(_rows(x), _rows(w), out_dtype)
         else:
             y = _linear_codes(_rows(x), *block_encode(_rows(w), tiles=True), out_dtype)
     return y if flat else y.view(*X.shape[:-1], y.shape[1])

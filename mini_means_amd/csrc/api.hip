@@ -1419,7 +1419,7 @@ struct CodesAt {
   uint8_t* s(void* base) const { return static_cast<uint8_t*>(base) + scales; }
 };
 
-struct TrainSaved {  // X^T by rows, W^T by tiles
+struct TrainSaved {  // X^T by rows, then W^T by tiles
   CodesAt x, w;
   TrainSaved(int64_t m, int64_t n, int64_t k) : x(0, k, m, false), w(x.end, k, n, true) {}
 };
@@ -1462,6 +1462,12 @@ bool train_sizes(int64_t m, int64_t n, int64_t k) {
 
 int64_t emeans_block_train_saved(int64_t m, int64_t n, int64_t k) {
   return train_sizes(m, n, k) ? TrainSaved(m, n, k).w.end : 0;
+}
+
+int64_t emeans_block_train_saved_for(int64_t m, int64_t n, int64_t k, int32_t need) {
+  if (!train_sizes(m, n, k) || need < 1 || need > 3) return 0;
+  const TrainSaved s(m, n, k);
+  return need == 2 ? s.x.end : s.w.end;
 }
 
 int64_t emeans_block_train_work(int64_t m, int64_t n, int64_t k, int32_t gradient) {

@@ -263,3 +263,14 @@ def test_lengths_keep_their_upper_bits(L):
     for change, word in ((dict(page=2 ** 32 + 16), b"page_rows"), (dict(seqs=2 ** 32 + 2), b"seqs"),
                          (dict(tp=2 ** 32 + 4, ldt=2 ** 33), b"table_pages")):
         assert _pages(L, **change) == -1 and word in L.emeans_last_error(), change
+
+
+def test_saved_size_by_need(L):
+    """X^T comes first, so a forward pass whose x needs no gradient saves that
+    alone; the gradient pass with dX = NULL reads no more."""
+    m, n, k = 300, 200, 130
+    whole, x = L.emeans_block_train_saved(m, n, k), 130 * 304 + 130 * 4
+    assert [L.emeans_block_train_saved_for(m, n, k, need) for need in range(4)] \
+        == [0, whole, -(-x // 16) * 16, whole]
+    assert L.emeans_block_train_saved_for(0, n, k, 2) == L.emeans_block_train_saved_for(m, n, k, 4) == 0
+    assert L.emeans_block_train_saved_for(m, n, FAR, 2) == 0

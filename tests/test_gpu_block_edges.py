@@ -163,3 +163,25 @@ def test_blocks_whose_lower_half_is_another(mm):
                                                  block=block)):
             with pytest.raises(mm.EmeansError, match="EINVAL.*block"):
                 call()
+
+
+@pytest.mark.parametrize("need", ["x", "w", "both"])
+def test_linear_keeps_what_its_gradients_need(mm, need):
+    """Between the passes: 1 byte for each value of w if x has a gradient, of x
+    if w has one, and their scales; the gradients are those of both together."""
+    import torch
+    m, n, k = 4096, 640, 1152
+    x, w = numbers(m, k, "bf16", 1, 0.1), numbers(n, k, "bf16", 2, 0.1)
+    g = numbers(m, n, "bf16", 3, 0.1)
+    want = x.clone().requires_grad_(), w.clone().requires_grad_()
+    mm.block_linear(*want).backward(g)
+    xs = x.clone().requires_grad_(need != "w")
+    ws = w.clone().requires_grad_(need != "x")
+    y = mm.block_linear(xs, ws)
+    kept = sum(t.untyped_storage().nbytes() for t in y.grad_fn.saved_tensors)
+    parts = {"x": n * k, "w": m * k, "both": (m + n) * k}
+    assert kept <= parts[need] * (1 + 2 / 128) + 4096, (kept, parts[need])
+    y.backward(g)
+    assert xs.grad is None or torch.equal(xs.grad, want[0].grad)
+    assert ws.grad is None or torch.equal(ws.grad, want[1].grad)
+    assert (xs.grad is None, ws.grad is None) == (need == "w", need == "x")
