@@ -459,12 +459,14 @@ def _T():
     t = _Types
     if t.torch is None:
         import torch
+        import torch.autograd.forward_ad as forward_ad
         t.numbers = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         t.formats = {torch.float8_e4m3fn: F8, torch.int8: I8}
         t.codes = (torch.float8_e4m3fn,)
         t.bytes = (torch.float8_e8m0fnu, torch.uint8)
         t.stream = torch._C._cuda_getCurrentRawStream
         t.current = torch.cuda.current_device
+        t.dual = forward_ad.unpack_dual
         t.torch = torch
     return t
 
@@ -816,7 +818,8 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     w a tuple (codes, scales), as block_encode(w, tiles=True) gives: serving,
     where a few rows of X are encoded inside the product's launch. With the
     tuple of four of block_encode(w, tiles=True, cols=True), X has a gradient
-    and the frozen w none.
+    and the frozen w none. Gradients are those of the backward pass, once: tangents
+    of the forward mode are refused.
 
     On `stream` (the current one by default) everything runs, copies of inputs
     whose values are not adjacent too; the backward pass as well, ordered behind
@@ -825,11 +828,14 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     if stream is not None:
         with _T().torch.cuda.stream(stream):
             return block_linear(X, w, out_dtype=out_dtype)
+    dual, coded = _T().dual, isinstance(w, (tuple, list))
+    if dual(X).tangent is not None or not coded and dual(w).tangent is not None:
+        raise EmeansError("EINVAL: block_linear has no forward-mode derivative (X or w has a tangent)")
     out_dtype = out_dtype or X.dtype
     flat = X.dim() == 2
     x = X if flat else X.reshape(-1, X.shape[-1])
     grad = _T().torch.is_grad_enabled()
-    if isinstance(w, (tuple, list)):
+    if coded:
         if len(w) not in (2, 4):
             raise EmeansError("EINVAL: w must be a tensor, (codes, scales) or the four of "
                               "block_encode(w, tiles=True, cols=True)")

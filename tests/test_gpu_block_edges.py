@@ -185,3 +185,21 @@ def test_linear_keeps_what_its_gradients_need(mm, need):
     assert xs.grad is None or torch.equal(xs.grad, want[0].grad)
     assert ws.grad is None or torch.equal(ws.grad, want[1].grad)
     assert (xs.grad is None, ws.grad is None) == (need == "w", need == "x")
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_linear_refuses_forward_mode(mm, grad):
+    """There is no forward-mode derivative: a tangent is refused, not dropped."""
+    import torch
+    import torch.autograd.forward_ad as fw
+    x, w = numbers(4, 200, "f32", 1), numbers(30, 200, "f32", 2)
+    codes = mm.block_encode(w, tiles=True, cols=True)
+    with fw.dual_level():
+        dx, dw = (fw.make_dual(t.clone().requires_grad_(grad), torch.ones_like(t)) for t in (x, w))
+        for call in (lambda: mm.block_linear(dx, codes), lambda: mm.block_linear(dx, w),
+                     lambda: mm.block_linear(x, dw), lambda: mm.block_linear(dx, dw)):
+            with pytest.raises(mm.EmeansError, match="EINVAL.*forward-mode"):
+                call()
+        assert mm.block_linear(x, codes[:2]).shape == (4, 30)   # no tangent: fine
+    with pytest.raises(mm.EmeansError, match="EINVAL.*forward-mode"):
+        torch.func.jvp(lambda t: mm.block_linear(t, codes), (x,), (x,))
