@@ -467,6 +467,7 @@ def _T():
         t.stream = torch._C._cuda_getCurrentRawStream
         t.current = torch.cuda.current_device
         t.dual = forward_ad.unpack_dual
+        t.tracing = torch.jit.is_tracing
         t.torch = torch
     return t
 
@@ -495,7 +496,10 @@ def _elsewhere(device: int, stream):
 
 
 def _run(device: int, stream, call):
-    """call(stream pointer) where the tensors live."""
+    """call(stream pointer) where the tensors live. A trace records torch's
+    operations alone, so the library's would be missing from it."""
+    if _T().tracing():
+        raise EmeansError("EINVAL: calls of block codes cannot be traced (torch.jit.trace)")
     ctx = _elsewhere(device, stream)
     if ctx is None:
         return call(_T().stream(device))

@@ -203,3 +203,18 @@ def test_linear_refuses_forward_mode(mm, grad):
         assert mm.block_linear(x, codes[:2]).shape == (4, 30)   # no tangent: fine
     with pytest.raises(mm.EmeansError, match="EINVAL.*forward-mode"):
         torch.func.jvp(lambda t: mm.block_linear(t, codes), (x,), (x,))
+
+
+def test_tracing_is_refused(mm):
+    """A trace records torch operations alone: calls of the library would be lost."""
+    import torch
+    x, w = numbers(4, 200, "f32", 1), numbers(30, 200, "f32", 2)
+    c, s = mm.block_encode(w)
+    store, factors = mm.cache_new(8, 200)
+    slots = torch.arange(4, device="cuda")
+    for call in (lambda t: mm.block_linear(t, w), lambda t: mm.block_linear(t, (c, s)),
+                 lambda t: mm.block_encode(t)[0], lambda t: mm.block_matmul(*mm.block_encode(t), c, s),
+                 lambda t: mm.cache_write(t, slots, store, factors),
+                 lambda t: t + mm.cache_read(store, factors, slots)):
+        with pytest.raises(mm.EmeansError, match="EINVAL.*trace"):
+            torch.jit.trace(call, (x,), check_trace=False)
