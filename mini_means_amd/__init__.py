@@ -977,6 +977,8 @@ def cache_read_pages(codes, scales, table, starts, total: int, *, block: int = B
     if starts.dtype is not torch.int32 or not starts.is_contiguous() or starts.shape != (seqs + 1,):
         raise EmeansError(f"EINVAL: starts must be {seqs + 1} contiguous int32")
     total = int(total)
+    if total < 0:
+        raise EmeansError(f"EINVAL: total out of range ({total})")
 
     def call(st):
         y = _product_out(total, d, out, out_dtype, codes.device)

@@ -218,3 +218,11 @@ def test_tracing_is_refused(mm):
                  lambda t: t + mm.cache_read(store, factors, slots)):
         with pytest.raises(mm.EmeansError, match="EINVAL.*trace"):
             torch.jit.trace(call, (x,), check_trace=False)
+
+
+def test_negative_total_is_refused(mm):
+    import torch
+    codes, scales = mm.cache_new((2, 3), 64)
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(mm.EmeansError, match="EINVAL.*total"):
+        mm.cache_read_pages(codes, scales, at[None], at, -1)
