@@ -867,7 +867,7 @@ def cache_new(rows, d: int, *, block: int = BLOCK, dtype=None, device="cuda"):
     (ceil(d / block),), rows a number or a shape such as (pages, rows per
     page). dtype float8_e4m3fn (default) or int8. Its rows read as zeros."""
     torch = _T().torch
-    shape = (rows,) if isinstance(rows, int) else tuple(rows)
+    shape = tuple(rows) if hasattr(rows, "__iter__") else (rows,)
     dtype = dtype or torch.float8_e4m3fn
     if dtype not in _T().formats:
         raise EmeansError(f"EDTYPE: {dtype} not supported (float8_e4m3fn or int8)")

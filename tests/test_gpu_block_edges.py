@@ -226,3 +226,10 @@ def test_negative_total_is_refused(mm):
     at = torch.zeros(2, dtype=torch.int32, device="cuda")
     with pytest.raises(mm.EmeansError, match="EINVAL.*total"):
         mm.cache_read_pages(codes, scales, at[None], at, -1)
+
+
+def test_store_of_numpy_sizes(mm):
+    codes, scales = mm.cache_new(np.int64(6), np.int32(200))
+    assert codes.shape == (6, 200) and scales.shape == (6, 2)
+    codes, scales = mm.cache_new((np.int64(2), 3), 64)
+    assert codes.shape == (2, 3, 64) and scales.shape == (2, 3, 1)
