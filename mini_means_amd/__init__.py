@@ -13,6 +13,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 from dataclasses import dataclass
@@ -837,7 +838,9 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
         raise EmeansError("EINVAL: block_linear has no forward-mode derivative (X or w has a tangent)")
     out_dtype = out_dtype or X.dtype
     flat = X.dim() == 2
-    x = X if flat else X.reshape(-1, X.shape[-1])
+    if X.dim() == 0:
+        raise EmeansError("EINVAL: X must have rows of k values")
+    x = X if flat else X.reshape(math.prod(X.shape[:-1]), X.shape[-1])
     grad = _T().torch.is_grad_enabled()
     if coded:
         if len(w) not in (2, 4):

@@ -233,3 +233,15 @@ def test_store_of_numpy_sizes(mm):
     assert codes.shape == (6, 200) and scales.shape == (6, 2)
     codes, scales = mm.cache_new((np.int64(2), 3), 64)
     assert codes.shape == (2, 3, 64) and scales.shape == (2, 3, 1)
+
+
+def test_linear_without_columns_or_dimensions(mm):
+    """k = 0 in any shape gives zeros; a number is no row."""
+    import torch
+    w = (torch.empty(5, 0, dtype=torch.float8_e4m3fn, device="cuda"),
+         torch.empty(5, 0, dtype=torch.uint8, device="cuda"))
+    for shape in ((3, 0), (2, 3, 0), (0,)):
+        y = mm.block_linear(torch.empty(shape, device="cuda"), w)
+        assert y.shape == (*shape[:-1], 5) and torch.all(y == 0)
+    with pytest.raises(mm.EmeansError, match="EINVAL"):
+        mm.block_linear(torch.ones((), device="cuda"), w)
