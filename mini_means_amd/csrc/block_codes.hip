@@ -459,8 +459,9 @@ __device__ __forceinline__ int64_t source_row(const RowsFrom& f, int64_t row, in
 // host checks).
 constexpr int kReadRows = 64;  // R at most
 
-// The first cnt values of a piece of output: read once by whoever comes next,
-// so they are not kept in the caches on their way.
+// The first cnt values of a piece of output, stored past the caches: most of the
+// time of large reads is the writing (figures above, timed without a reader; what
+// the next call gains from a small result in the caches was not measured).
 __device__ __forceinline__ void store_out(float* o, f32x4 v, int cnt) {
   typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
   if (cnt >= 4) {

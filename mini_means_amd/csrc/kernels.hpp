@@ -299,8 +299,8 @@ struct DecodeRows {
 hipError_t launch_decode_rows(const DecodeRows& a, hipStream_t st);
 
 // out[m][n] = sum_k A[m][k] B[n][k] over E4M3 codes with scales per row and
-// 128 values of k (B: per 128 x 128 tile with b_tiles), fp32 sums, rounded
-// once to ot (block_matmul.hip). work: block_product_work() bytes, 16-byte
+// 128 values of k (B: per 128 x 128 tile with b_tiles), rounded once to ot; sums
+// in fp32 for fp32 results, those of the FP8 unit for others (block_matmul.hip). work: block_product_work() bytes, 16-byte
 // aligned (NULL where that is 0).
 struct BlockProduct {
   const uint8_t* A;
