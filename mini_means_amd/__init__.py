@@ -872,6 +872,11 @@ def block_linear(X, w, *, out_dtype=None, stream=None):
     return y if flat else y.view(*X.shape[:-1], y.shape[1])
 
 
+def _check_block(block) -> None:
+    if not 16 <= block <= 256 or block % 16:
+        raise EmeansError(f"EINVAL: block must be a multiple of 16 in [16, 256] (got {block})")
+
+
 def cache_new(rows, d: int, *, block: int = BLOCK, dtype=None, device="cuda"):
     """An empty store of codes: (codes, scales) of shape rows + (d,) and rows +
     (ceil(d / block),), rows a number or a shape such as (pages, rows per
@@ -881,6 +886,7 @@ def cache_new(rows, d: int, *, block: int = BLOCK, dtype=None, device="cuda"):
     dtype = dtype or torch.float8_e4m3fn
     if dtype not in _T().formats:
         raise EmeansError(f"EDTYPE: {dtype} not supported (float8_e4m3fn or int8)")
+    _check_block(block)
     codes = torch.zeros((*shape, d), dtype=torch.uint8, device=device).view(dtype)
     scales = torch.full((*shape, -(-d // block)), 127, dtype=torch.uint8, device=device)
     return codes, scales.view(torch.float8_e8m0fnu)
@@ -901,8 +907,7 @@ def _store(dev, codes, scales, block):
     if len(shape) < 2 or not codes.is_contiguous() or not scales.is_contiguous():
         raise EmeansError("EINVAL: codes and scales must be contiguous, rows last but one")
     d = shape[-1]
-    if not 16 <= block <= 256 or block % 16:
-        raise EmeansError(f"EINVAL: block must be a multiple of 16 in [16, 256] (got {block})")
+    _check_block(block)
     if shape[:-1] != sshape[:-1] or sshape[-1] != -(-d // block):
         raise EmeansError(f"EINVAL: scales must be {tuple(shape[:-1])} x ceil({d} / {block}), got "
                           f"{tuple(sshape)}")

@@ -245,3 +245,9 @@ def test_linear_without_columns_or_dimensions(mm):
         assert y.shape == (*shape[:-1], 5) and torch.all(y == 0)
     with pytest.raises(mm.EmeansError, match="EINVAL"):
         mm.block_linear(torch.ones((), device="cuda"), w)
+
+
+@pytest.mark.parametrize("block", [0, -16, 8, 100, 272])
+def test_store_of_an_impossible_block_is_refused(mm, block):
+    with pytest.raises(mm.EmeansError, match="EINVAL.*block"):
+        mm.cache_new(4, 64, block=block)
