@@ -109,3 +109,23 @@ def test_products_with_many_rows_of_b(mm, m, k, how):  # noqa: F811
         got = mm.block_matmul(ca.view(torch.float8_e4m3fn), sa, b, bs)
     assert got.shape == (m, ROWS)
     assert all_equal(got, want.to(got.dtype).cuda(), 1)
+
+
+@pytest.mark.parametrize("m", [2, 17])
+def test_products_with_many_tiles_of_b(mm, m):  # noqa: F811
+    """Scales per tile of 128 rows: every launch starts at its own."""
+    import torch
+    k = 16
+    _, cb, _ = integers(PERIOD, k, 6)
+    vb = cb.view(torch.float8_e4m3fn).double().cpu().numpy()
+    tiles = torch.randint(120, 135, (-(-ROWS // 128), 1), dtype=torch.uint8,
+                          generator=torch.Generator().manual_seed(7)).cuda()
+    va, ca, sa = integers(m, k, 8)
+    want = torch.from_numpy(va @ vb.T).float().cuda()
+    got = mm.block_matmul(ca.view(torch.float8_e4m3fn), sa,
+                          repeated(cb).view(torch.float8_e4m3fn), tiles, out_dtype=torch.float32)
+    for i in range(0, ROWS, PERIOD * 400):
+        cols = torch.arange(i, min(i + PERIOD * 400, ROWS), device="cuda")
+        factor = torch.exp2(tiles[:, 0].float() - 127)[cols // 128]
+        part = (got[:, i:i + PERIOD * 400] / factor).unflatten(1, (-1, PERIOD))
+        assert torch.all(part == want[:, None])
