@@ -562,6 +562,104 @@ int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pa
                             const int32_t* starts, int64_t seqs, int64_t n, void* out,
                             int32_t out_dtype, int64_t ldo, void* stream);
 
+/* Attention around the store: what stands between a projection and
+ * emeans_cache_write, and what reads and thins the store afterwards. Numbers are
+ * EMEANS_F32, EMEANS_BF16 or EMEANS_F16, heads adjacent runs of `width` values at
+ * any row and head stride (in elements). */
+
+/* Queries (n x hq x width) and keys (n x hk x width) normed per head and turned by
+ * their positions: with r = 1 / sqrt(mean x^2 + eps) and y = x r weight, the pairs
+ * (y[c], y[c + half]), c < half, become
+ *   (y[c] cos a - y[c + half] sin a, y[c + half] cos a + y[c] sin a),
+ * a = positions[t] freqs[c]; values from 2 half on are only normed. Norms and turns
+ * are fp32 (the angles fp64, then reduced), the result is rounded once to dtype.
+ *   width      a multiple of 8, at most 256
+ *   half       a multiple of 4, 0 <= 2 half <= width
+ *   *_weight   device, width values of weight_dtype
+ *   positions  device, n integers of position_bytes (4 or 8)
+ *   freqs      device, half doubles: radians per position
+ *   q_out      device, n x hq x width (contiguous); k_out likewise; not the inputs
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_norm_rotate(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                       int64_t k_head, int32_t dtype, int64_t n, int64_t hq, int64_t hk,
+                       int64_t width, const void* q_weight, const void* k_weight,
+                       int32_t weight_dtype, const void* positions, int32_t position_bytes,
+                       const double* freqs, int64_t half, double eps, void* q_out, void* k_out,
+                       void* stream);
+
+/* Its gradients, from the inputs and the results' gradients (dtype, any strides):
+ * dq, dk (contiguous, as the results) and dq_weight, dk_weight (width values of
+ * weight_dtype, sums over all tokens and heads in one order).
+ *   work  device, emeans_norm_rotate_work(n, width) bytes, 16-byte aligned, or NULL
+ *         (allocated stream-ordered)
+ * With n = 0 the weights' gradients are zeros. Errors: as above; ENOMEM. */
+int64_t emeans_norm_rotate_work(int64_t n, int64_t width);
+int emeans_norm_rotate_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                int64_t k_row, int64_t k_head, int32_t dtype, int64_t n,
+                                int64_t hq, int64_t hk, int64_t width, const void* q_weight,
+                                const void* k_weight, int32_t weight_dtype, const void* positions,
+                                int32_t position_bytes, const double* freqs, int64_t half,
+                                double eps, const void* dq_out, int64_t dq_row, int64_t dq_head,
+                                const void* dk_out, int64_t dk_row, int64_t dk_head, void* dq,
+                                void* dk, void* dq_weight, void* dk_weight, void* work,
+                                void* stream);
+
+/* Attention of one new token per sequence over two paged stores (keys and values,
+ * each `pages` pages of page_rows rows of hk * width codes, scales as for
+ * emeans_cache_write): out[s][h] = sum_p softmax_p(scale q[s][h] . key_p) value_p
+ * over the places p < lengths[s], place p in page table[s][p / page_rows] at
+ * p % page_rows, query head h with key-value head h / (hq / hk). Places in pages
+ * outside [0, pages) are left out; a length is cut to 0 below and to what a table
+ * row holds above; a sequence without places gives zeros. Scores, softmax and sums
+ * are fp32, products exact for bf16 queries but for the softmax weights beside the
+ * values, which are rounded to bf16 for bf16 queries, to 16 bits for fp16 ones and
+ * to 24 for fp32 ones.
+ *   width    a multiple of 16, at most 128      hq  a multiple of hk
+ *   q        device, seqs x hq x width, dtype   out the same (contiguous)
+ *   table    device, seqs x table_pages int32, rows table_ld entries apart. A part of
+ *            the call's work goes by table_pages, so pass no wider a table than needed
+ *   lengths  device, seqs int32
+ *   weights  NULL, or device, fp32, rows weights_ld apart: weights[s][p] += the sum of
+ *            the heads' softmax weights of place p, p < lengths[s]; hq at most 1024
+ *   work     device, emeans_cache_attend_work() bytes, 16-byte aligned, or NULL
+ *            (allocated stream-ordered)
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, ENOMEM, EHIP. */
+int64_t emeans_cache_attend_work(int64_t seqs, int64_t hq, int64_t hk, int64_t width,
+                                 int64_t page_rows, int64_t table_pages, int32_t with_weights);
+int emeans_cache_attend(const void* q, int32_t dtype, int64_t q_row, int64_t q_head,
+                        const void* k_codes, const uint8_t* k_scales, const void* v_codes,
+                        const uint8_t* v_scales, int64_t pages, int64_t page_rows, int64_t block,
+                        int32_t fmt, const int32_t* table, int64_t table_ld, int64_t table_pages,
+                        const int32_t* lengths, int64_t seqs, int64_t hq, int64_t hk,
+                        int64_t width, double scale, void* out, float* weights,
+                        int64_t weights_ld, void* work, void* stream);
+
+/* Rows of small weight dropped from `stores` paged stores of one page layout, in
+ * place: of a sequence of more than keep rows stay the last `recent` and, of those
+ * before them, the keep - recent of largest weight (of equal ones the first; NaN
+ * counts as -infinity). They move to the sequence's first places in their order.
+ * No page may be in use twice; a row whose place or new place lies in a page outside
+ * [0, pages) is neither read nor written.
+ *   codes, scales  host arrays of `stores` (1 to 4) device pointers; row_codes[i]
+ *                  codes and row_scales[i] scales are a row of store i
+ *   weights        device, fp32, seqs rows weights_ld apart, at least
+ *                  table_pages * page_rows each; not changed
+ *   new_lengths    device, seqs int32       kept  device, seqs x keep int32: the old
+ *                  places in order, -1 after them
+ *   new_weights    device, fp32, seqs x (table_pages * page_rows): the weights of the
+ *                  rows that stay, zeros after them
+ *   work           device, emeans_cache_evict_work(seqs, keep) bytes, 16-byte aligned,
+ *                  or NULL (allocated stream-ordered)
+ * Errors: EINVAL, ENOTDEVICE, ENOMEM, EHIP. */
+int64_t emeans_cache_evict_work(int64_t seqs, int64_t keep);
+int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t* row_codes,
+                       const int64_t* row_scales, int32_t stores, int64_t pages,
+                       int64_t page_rows, const int32_t* table, int64_t table_ld,
+                       int64_t table_pages, const int32_t* lengths, int64_t seqs,
+                       const float* weights, int64_t weights_ld, int64_t keep, int64_t recent,
+                       int32_t* new_lengths, float* new_weights, int32_t* kept, void* work,
+                       void* stream);
+
 /* Message for the last non-zero return on this thread ("" if none). */
 const char* emeans_last_error(void);
 

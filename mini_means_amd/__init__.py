@@ -124,6 +124,26 @@ def lib() -> ctypes.CDLL:
         L.emeans_cache_read_pages.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp,
                                               c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i32,
                                               c_i64, c_vp]
+        rotate = [c_vp, c_i64, c_i64] * 2 + [c_i32, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i32,
+                                             c_vp, c_i32, c_vp, c_i64, c_dbl]
+        L.emeans_norm_rotate.argtypes = rotate + [c_vp] * 3
+        L.emeans_norm_rotate_gradient.argtypes = rotate + [c_vp, c_i64, c_i64] * 2 + [c_vp] * 6
+        L.emeans_norm_rotate_work.argtypes = [c_i64, c_i64]
+        L.emeans_cache_attend_work.argtypes = [c_i64] * 6 + [c_i32]
+        L.emeans_cache_attend.argtypes = [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64,
+                                          c_i64, c_i64, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64,
+                                          c_i64, c_i64, c_i64, c_dbl, c_vp, c_vp, c_i64, c_vp,
+                                          c_vp]
+        L.emeans_cache_evict_work.argtypes = [c_i64, c_i64]
+        L.emeans_cache_evict.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_vp, c_i64,
+                                         c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp,
+                                         c_vp, c_vp, c_vp, c_vp]
+        for f in ("emeans_norm_rotate_work", "emeans_cache_attend_work",
+                  "emeans_cache_evict_work"):
+            getattr(L, f).restype = c_i64
+        for f in ("emeans_norm_rotate", "emeans_norm_rotate_gradient", "emeans_cache_attend",
+                  "emeans_cache_evict"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("emeans_block_encode", "emeans_block_matmul", "emeans_block_linear",
                   "emeans_block_train_forward", "emeans_block_train_gradient",
                   "emeans_cache_write", "emeans_cache_read", "emeans_cache_read_pages"):
@@ -1004,6 +1024,283 @@ def cache_read_pages(codes, scales, table, starts, total: int, *, block: int = B
                 y.data_ptr(), ot, y.stride(0), st))
         return y
 
+    return _run(dev, stream, call)
+
+
+# ---- attention around the store ----------------------------------------------
+
+
+def _heads(A, device: int, what, dtype=None):
+    """A tensor n x heads x width on that device whose heads are runs of values:
+    its sizes and the distances of rows and heads."""
+    if not getattr(A, "is_cuda", False) or A.get_device() != device:
+        raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
+    if dtype is not None and A.dtype != dtype:
+        raise EmeansError(f"EDTYPE: {what} must be {dtype} (got {A.dtype})")
+    shape = A.shape
+    if len(shape) != 3 or (A.stride(2) != 1 and shape[2] > 1 and A.numel()):
+        raise EmeansError(f"EINVAL: {what} must be rows x heads x width with adjacent values")
+    return (*shape, A.stride(0), A.stride(1))
+
+
+def _vector(A, device: int, what, n, dtypes, names):
+    """A contiguous 1-D tensor of n values (any number where n is None)."""
+    if not getattr(A, "is_cuda", False) or A.get_device() != device:
+        raise EmeansError(f"ENOTDEVICE: {what} must be a tensor on the GPU of the others")
+    if A.dtype not in dtypes:
+        raise EmeansError(f"EDTYPE: {what} must be {names} (got {A.dtype})")
+    if A.dim() != 1 or not A.is_contiguous() or (n is not None and A.shape[0] != n):
+        raise EmeansError(f"EINVAL: {what} must be {'contiguous' if n is None else n} "
+                          f"{names} values in a row")
+    return A.shape[0]
+
+
+def _no_tangent(name, *tensors) -> None:
+    dual = _T().dual
+    if any(dual(t).tangent is not None for t in tensors):
+        raise EmeansError(f"EINVAL: {name} has no forward-mode derivative (an input has a tangent)")
+
+
+def _adjacent(t):
+    """t with adjacent values in a row (a copy if it has not)."""
+    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
+
+
+def rotary_freqs(turned: int, base: float = 10000.0, device="cuda"):
+    """Radians per position of the turned / 2 pairs of a head, base^(-2 i / turned)
+    (float64), as norm_rotate takes them. turned: a multiple of 8."""
+    torch = _T().torch
+    if turned < 0 or turned % 8 or not base > 0:
+        raise EmeansError(f"EINVAL: turned must be a multiple of 8 and base positive (got {turned}, "
+                          f"{base})")
+    i = torch.arange(turned // 2, dtype=torch.float64, device=device)
+    return torch.exp2(i * (-2.0 * math.log2(base) / max(turned, 1)))
+
+
+def _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps):
+    """The arguments that both passes of norm_rotate share, and the sizes."""
+    t = _T()
+    dev = _device_of(q, "q")
+    dt = _number(q.dtype, "q")
+    n, hq, w, qr, qh = _heads(q, dev, "q")
+    nk, hk, wk, kr, kh = _heads(k, dev, "k", q.dtype)
+    if nk != n or wk != w:
+        raise EmeansError(f"EINVAL: k must be {n} x heads x {w} (got {tuple(k.shape)})")
+    gt = _number(q_weight.dtype, "q_weight")
+    names = str(q_weight.dtype)
+    _vector(q_weight, dev, "q_weight", w, (q_weight.dtype,), names)
+    _vector(k_weight, dev, "k_weight", w, (q_weight.dtype,), names)
+    _vector(positions, dev, "positions", n, (t.torch.int32, t.torch.int64), "int32 or int64")
+    half = _vector(freqs, dev, "freqs", None, (t.torch.float64,), "float64")
+    return dev, (n, hq, hk, w), (
+        q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, dt, n, hq, hk, w, q_weight.data_ptr(),
+        k_weight.data_ptr(), gt, positions.data_ptr(),
+        8 if positions.dtype is t.torch.int64 else 4, freqs.data_ptr(), half, eps)
+
+
+def _norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps):
+    dev, (n, hq, hk, w), args = _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps)
+
+    def call(st):
+        empty = _T().torch.empty
+        qo = empty((n, hq, w), dtype=q.dtype, device=q.device)
+        ko = empty((n, hk, w), dtype=q.dtype, device=q.device)
+        _check(lib().emeans_norm_rotate(*args, qo.data_ptr(), ko.data_ptr(), st))
+        return qo, ko
+
+    return _run(dev, None, call)
+
+
+_rotate_function = None
+
+
+def _rotate_fn():
+    global _rotate_function
+    if _rotate_function is None:
+        torch = _T().torch
+
+        class NormRotate(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, q_weight, k_weight, positions, freqs, eps):
+                ctx.save_for_backward(q, k, q_weight, k_weight, positions, freqs)
+                ctx.eps = eps
+                return _norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dqo, dko):
+                saved = ctx.saved_tensors
+                dev, (n, hq, hk, w), args = _rotate_args(*saved, ctx.eps)
+                q, gq = saved[0], saved[2]
+                L = lib()
+
+                def call(st):
+                    a, b = _adjacent(dqo), _adjacent(dko)
+                    dq = torch.empty((n, hq, w), dtype=q.dtype, device=q.device)
+                    dk = torch.empty((n, hk, w), dtype=q.dtype, device=q.device)
+                    dgq, dgk = torch.empty((2, w), dtype=gq.dtype, device=q.device).unbind(0)
+                    work = _work(L.emeans_norm_rotate_work(n, w), q.device)
+                    _check(L.emeans_norm_rotate_gradient(
+                        *args, a.data_ptr(), a.stride(0), a.stride(1), b.data_ptr(), b.stride(0),
+                        b.stride(1), dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(),
+                        _ptr(work), st))
+                    return dq, dk, dgq, dgk
+
+                return *_run(dev, None, call), None, None, None
+
+        _rotate_function = NormRotate
+    return _rotate_function
+
+
+def norm_rotate(q, k, q_weight, k_weight, positions, freqs, *, eps: float = 1e-6, stream=None):
+    """Queries (n x hq x width) and keys (n x hk x width; float32, bfloat16 or
+    float16, rows and heads any distance apart) normed per head and turned by their
+    positions in one pass: y = x / sqrt(mean x^2 + eps) * weight, then the pairs
+    (c, c + half) turned by positions[t] * freqs[c], half = len(freqs); values from
+    2 half on are only normed. Returns the two results (contiguous, one rounding).
+
+    width is a multiple of 8 up to 256, half a multiple of 4. The weights (width
+    values) are both of one number type, positions (n) int32 or int64, freqs float64
+    (rotary_freqs): angles are exact products in 64 bits, so far positions turn as
+    exactly as near ones. q, k and the weights have gradients (once: tangents of the
+    forward mode are refused); the weights' are sums in one order."""
+    _device_of(q, "q")
+    if stream is not None:
+        with _T().torch.cuda.stream(stream):
+            return norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps=eps)
+    _no_tangent("norm_rotate", q, k, q_weight, k_weight)
+    if _T().torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
+                                         or q_weight.requires_grad or k_weight.requires_grad):
+        return _rotate_fn().apply(q, k, q_weight, k_weight, positions, freqs, eps)
+    return _norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps)
+
+
+def _paged(dev, store, block, what):
+    """(codes, scales) of a paged store: its format, row length and shape."""
+    if not isinstance(store, (tuple, list)) or len(store) != 2:
+        raise EmeansError(f"EINVAL: {what} must be (codes, scales)")
+    fmt, _, d = _store(dev, store[0], store[1], block)
+    if store[0].dim() != 3:
+        raise EmeansError(f"EINVAL: codes of {what} must be pages x page rows x d")
+    return fmt, d, store[0].shape
+
+
+def _places(dev, table, lengths, page: int):
+    """Sequences, table entries of one, the table's row distance and the places
+    that a sequence has at most."""
+    t = _T().torch
+    seqs, pages, ld = _matrix(table, dev, "table", (t.int32,), "int32")
+    _vector(lengths, dev, "lengths", seqs, (t.int32,), "int32")
+    return seqs, pages, ld, pages * page
+
+
+def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=None, weights=None,
+                 stream=None):
+    """Attention of one new token per sequence over a paged store: q (seqs x hq x
+    width; float32, bfloat16 or float16), keys and values each (codes, scales) of
+    cache_new((pages, page rows), hk * width, block=block), hk dividing hq; query head
+    h reads key-value head h // (hq // hk). Sequence s is the first lengths[s] (int32)
+    places of its row of `table` (seqs x pages int32, as cache_read_pages takes it;
+    places in pages outside the store are left out, lengths cut to what the table
+    holds). Returns seqs x hq x width of q's type, zeros for a sequence without places.
+    scale: of q.k, 1 / sqrt(width) by default. width is a multiple of 16 up to 128.
+
+    weights: a float32 tensor seqs x places (places = the table's columns x page
+    rows) to whose row s the softmax weights of each place, summed over the heads, are
+    added: what cache_evict goes by.
+
+    The time goes by the table's columns too: pass table[:, :m] where m pages hold
+    every sequence."""
+    dev = _device_of(q, "q")
+    dt = _number(q.dtype, "q")
+    seqs, hq, width, qr, qh = _heads(q, dev, "q")
+    fmt, d, shape = _paged(dev, keys, block, "keys")
+    vfmt, _, vshape = _paged(dev, values, block, "values")
+    if vfmt != fmt or vshape != shape:
+        raise EmeansError("EINVAL: keys and values must be stores of one shape and format")
+    if width < 16 or width > 128 or width % 16 or d % width or not d:
+        raise EmeansError(f"EINVAL: width must be a multiple of 16 in [16, 128] that divides the "
+                          f"store's rows of {d} (got {width})")
+    hk = d // width
+    if hq < 1 or hq % hk:
+        raise EmeansError(f"EINVAL: {hq} heads of q cannot share {hk} of the store")
+    n, pages, ld, places = _places(dev, table, lengths, shape[1])
+    if n != seqs:
+        raise EmeansError(f"EINVAL: table must have a row for each of the {seqs} rows of q")
+    wld = 0
+    if weights is not None:
+        torch = _T().torch
+        wn, wd, wld = _matrix(weights, dev, "weights", (torch.float32,), "float32")
+        if (wn, wd) != (seqs, places) or (wld < places and seqs > 1):
+            raise EmeansError(f"EINVAL: weights must be {seqs} x {places}")
+
+    def call(st):
+        out = _T().torch.empty((seqs, hq, width), dtype=q.dtype, device=q.device)
+        if seqs:
+            L = lib()
+            with_weights = 1 if weights is not None else 0
+            work = _work(L.emeans_cache_attend_work(seqs, hq, hk, width, shape[1], pages,
+                                                    with_weights), q.device)
+            _check(L.emeans_cache_attend(
+                q.data_ptr(), dt, qr, qh, keys[0].data_ptr(), keys[1].data_ptr(),
+                values[0].data_ptr(), values[1].data_ptr(), shape[0], shape[1], block, fmt,
+                table.data_ptr(), ld, pages, lengths.data_ptr(), seqs, hq, hk, width,
+                width ** -0.5 if scale is None else scale, out.data_ptr(),
+                weights.data_ptr() if with_weights and places else None, wld, _ptr(work), st))
+        return out
+
+    return _run(dev, stream, call)
+
+
+def cache_evict(stores, table, lengths, weights, keep: int, *, recent: int = 0, block: int = BLOCK,
+                stream=None):
+    """Drop rows of small weight from one to four paged stores of one page layout
+    ((codes, scales) each: keys and values, say): of a sequence of more than `keep`
+    rows stay the last `recent` and, of those before them, the keep - recent of
+    largest weight (weights: seqs x places float32, as cache_attend adds them up; of
+    equal ones the first, NaN counts as -infinity). They move to the sequence's first
+    places in their order, in place; the pages behind them are free.
+
+    table and lengths as for cache_attend, lengths and weights unchanged; no page may
+    be in use twice (its rows would be moved for each use). Returns (lengths, weights,
+    kept): the new lengths (int32), the weights of the rows that stayed at their new
+    places and zeros behind them, and the places they came from (seqs x keep int32, -1
+    behind the last)."""
+    if not isinstance(stores, (tuple, list)) or not 1 <= len(stores) <= 4:
+        raise EmeansError("EINVAL: stores must be one to four (codes, scales)")
+    keep, recent = int(keep), int(recent)
+    dev = _device_of(lengths, "lengths")
+    found = [_paged(dev, s, block, "stores") for s in stores]
+    shape = found[0][2]
+    if any(f[2][:2] != shape[:2] for f in found) or not all(f[1] for f in found):
+        raise EmeansError("EINVAL: the stores must have the same pages of rows")
+    seqs, pages, ld, places = _places(dev, table, lengths, shape[1])
+    torch = _T().torch
+    wn, wd, wld = _matrix(weights, dev, "weights", (torch.float32,), "float32")
+    if (wn, wd) != (seqs, places) or (wld < places and seqs > 1):
+        raise EmeansError(f"EINVAL: weights must be {seqs} x {places}")
+    if not 0 <= keep < 2 ** 31 - 1023 or not 0 <= recent <= keep:
+        raise EmeansError(f"EINVAL: keep or recent out of range ({keep}, {recent})")
+
+    def call(st):
+        empty, device = torch.empty, codes[0].device
+        new = empty((seqs,), dtype=torch.int32, device=device)
+        new_weights = empty((seqs, places), dtype=torch.float32, device=device)
+        kept = empty((seqs, keep), dtype=torch.int32, device=device)
+        if seqs:
+            L, m = lib(), len(stores)
+            work = _work(L.emeans_cache_evict_work(seqs, keep), device)
+            _check(L.emeans_cache_evict(
+                (c_vp * m)(*(t.data_ptr() for t in codes)),
+                (c_vp * m)(*(t.data_ptr() for t in scales)),
+                (c_i64 * m)(*(t.shape[2] for t in codes)),
+                (c_i64 * m)(*(t.shape[2] for t in scales)), m, shape[0], shape[1],
+                table.data_ptr(), ld, pages, lengths.data_ptr(), seqs, weights.data_ptr(), wld,
+                keep, recent, new.data_ptr(), new_weights.data_ptr(), kept.data_ptr(), _ptr(work),
+                st))
+        return new, new_weights, kept
+
+    codes, scales = [s[0] for s in stores], [s[1] for s in stores]
     return _run(dev, stream, call)
 
 

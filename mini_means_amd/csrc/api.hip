@@ -1648,4 +1648,277 @@ int emeans_cache_read_pages(const void* codes, const uint8_t* scales, int64_t pa
                                      static_cast<hipStream_t>(stream)), "cache read");
 }
 
+// ---- attention around the store ----------------------------------------------
+
+namespace {
+
+int check_heads(int64_t heads, const char* name) {
+  return heads < 1 || heads > 65536 ? fail(EMEANS_EINVAL, "%s out of range (%lld)", name,
+                                           (long long)heads)
+                                    : EMEANS_OK;
+}
+
+// Working memory of a call: the caller's, or the call's own (allocated in stream
+// order and released by release()).
+int take_work(void* work, int64_t need, hipStream_t st, void** at, void** own) {
+  *own = nullptr;
+  *at = work;
+  if (work || need == 0) return EMEANS_OK;
+  if (const hipError_t e = hipMallocAsync(own, need, st); e != hipSuccess) {
+    *own = nullptr;
+    (void)hipGetLastError();
+    return fail(e == hipErrorOutOfMemory ? EMEANS_ENOMEM : EMEANS_EHIP, "hipMallocAsync: %s",
+                hipGetErrorString(e));
+  }
+  *at = *own;
+  return EMEANS_OK;
+}
+
+int check_rotate(const NormRotate& a, int64_t hq, int64_t hk, int64_t width, int64_t half,
+                 double eps) {
+  int rc;
+  if ((rc = check_count(a.n, "n")) || (rc = check_number_type(a.dt, "dtype")) ||
+      (rc = check_number_type(a.gdt, "weight_dtype")) || (rc = check_heads(hq, "hq")) ||
+      (rc = check_heads(hk, "hk")))
+    return rc;
+  if (width < 8 || width > 256 || width % 8)
+    return fail(EMEANS_EINVAL, "width must be a multiple of 8 in [8, 256] (got %lld)",
+                (long long)width);
+  if (half < 0 || half % 4 || 2 * half > width)
+    return fail(EMEANS_EINVAL, "half must be a multiple of 4 with 2 half <= width (got %lld)",
+                (long long)half);
+  if (a.pos_bytes != 4 && a.pos_bytes != 8)
+    return fail(EMEANS_EINVAL, "position_bytes must be 4 or 8 (got %d)", a.pos_bytes);
+  if (!(eps >= 0.0) || eps > 1e30) return fail(EMEANS_EINVAL, "eps out of range (%g)", eps);
+  if (a.q_rs < 0 || a.q_hs < 0 || a.k_rs < 0 || a.k_hs < 0 || a.dq_rs < 0 || a.dq_hs < 0 ||
+      a.dk_rs < 0 || a.dk_hs < 0)
+    return fail(EMEANS_EINVAL, "strides must not be negative");
+  return EMEANS_OK;
+}
+
+int check_rotate_pointers(const NormRotate& a) {
+  int rc;
+  if (!a.q || !a.k || !a.gq || !a.gk || !a.positions || (a.half && !a.freqs) || !a.qo || !a.ko)
+    return fail(EMEANS_EINVAL, "q, k, weights, positions, freqs and results must not be NULL");
+  if ((rc = check_device(a.q, "q")) || (rc = check_device(a.k, "k")) ||
+      (rc = check_device(a.gq, "q_weight")) || (rc = check_device(a.gk, "k_weight")) ||
+      (rc = check_device(a.positions, "positions")) ||
+      (a.half && (rc = check_device(a.freqs, "freqs"))) ||
+      (rc = check_device(a.qo, "the result of q")) || (rc = check_device(a.ko, "the result of k")))
+    return rc;
+  return EMEANS_OK;
+}
+
+int check_pages(int64_t pages, int64_t page_rows, int64_t table_ld, int64_t table_pages,
+                int64_t seqs) {
+  int rc;
+  if ((rc = check_length(page_rows, 1, "page_rows")) || (rc = check_count(pages, "pages")) ||
+      (rc = check_count(seqs, "seqs")) || (rc = check_count(table_pages, "table_pages")) ||
+      (rc = check_ld(table_ld, table_pages, seqs, "table_ld")))
+    return rc;
+  if (pages * page_rows > ((int64_t)1 << 40))
+    return fail(EMEANS_EINVAL, "rows out of range (%lld)", (long long)(pages * page_rows));
+  if (table_pages * page_rows > kMaxLength)
+    return fail(EMEANS_EINVAL, "a table row holds too many places (%lld)",
+                (long long)(table_pages * page_rows));
+  return EMEANS_OK;
+}
+
+}  // namespace
+
+int emeans_norm_rotate(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                       int64_t k_head, int32_t dtype, int64_t n, int64_t hq, int64_t hk,
+                       int64_t width, const void* q_weight, const void* k_weight,
+                       int32_t weight_dtype, const void* positions, int32_t position_bytes,
+                       const double* freqs, int64_t half, double eps, void* q_out, void* k_out,
+                       void* stream) {
+  g_err.clear();
+  NormRotate a{dtype, weight_dtype, n, (int)hq, (int)hk, (int)width, (int)half, q, q_row, q_head,
+               k, k_row, k_head, q_weight, k_weight, positions, position_bytes, freqs, (float)eps,
+               q_out, k_out};
+  int rc;
+  if ((rc = check_rotate(a, hq, hk, width, half, eps))) return rc;
+  if (n == 0) return EMEANS_OK;
+  if ((rc = check_rotate_pointers(a))) return rc;
+  return launched(launch_norm_rotate(a, static_cast<hipStream_t>(stream)), "norm rotate");
+}
+
+int64_t emeans_norm_rotate_work(int64_t n, int64_t width) {
+  if (n < 0 || n >= kMaxRows || width < 1 || width > 256) return 0;
+  return (int64_t)norm_rotate_groups(n) * 2 * width * 4;
+}
+
+int emeans_norm_rotate_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                                int64_t k_row, int64_t k_head, int32_t dtype, int64_t n,
+                                int64_t hq, int64_t hk, int64_t width, const void* q_weight,
+                                const void* k_weight, int32_t weight_dtype, const void* positions,
+                                int32_t position_bytes, const double* freqs, int64_t half,
+                                double eps, const void* dq_out, int64_t dq_row, int64_t dq_head,
+                                const void* dk_out, int64_t dk_row, int64_t dk_head, void* dq,
+                                void* dk, void* dq_weight, void* dk_weight, void* work,
+                                void* stream) {
+  g_err.clear();
+  NormRotate a{dtype, weight_dtype, n, (int)hq, (int)hk, (int)width, (int)half, q, q_row, q_head,
+               k, k_row, k_head, q_weight, k_weight, positions, position_bytes, freqs, (float)eps,
+               dq, dk, dq_out, dq_row, dq_head, dk_out, dk_row, dk_head, nullptr, dq_weight,
+               dk_weight};
+  int rc;
+  if ((rc = check_rotate(a, hq, hk, width, half, eps))) return rc;
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
+  if (!dq_weight || !dk_weight)
+    return fail(EMEANS_EINVAL, "dq_weight and dk_weight must not be NULL");
+  if (n > 0) {
+    if (!dq_out || !dk_out) return fail(EMEANS_EINVAL, "dq_out and dk_out must not be NULL");
+    if ((rc = check_rotate_pointers(a)) || (rc = check_device(dq_out, "dq_out")) ||
+        (rc = check_device(dk_out, "dk_out")))
+      return rc;
+  } else if (!q_weight || !k_weight) {
+    return fail(EMEANS_EINVAL, "the weights must not be NULL");
+  }
+  if ((rc = check_device(q_weight, "q_weight")) || (rc = check_device(k_weight, "k_weight")) ||
+      (rc = check_device(dq_weight, "dq_weight")) || (rc = check_device(dk_weight, "dk_weight")))
+    return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  void *at, *own;
+  if ((rc = take_work(work, emeans_norm_rotate_work(n, width), st, &at, &own))) return rc;
+  a.part = static_cast<float*>(at);
+  return release(own, st, launched(launch_norm_rotate_back(a, st), "norm rotate gradient"));
+}
+
+int64_t emeans_cache_attend_work(int64_t seqs, int64_t hq, int64_t hk, int64_t width,
+                                 int64_t page_rows, int64_t table_pages, int32_t with_weights) {
+  if (seqs < 1 || seqs >= kMaxRows || hk < 1 || hq < hk || hq > 65536 || hq % hk || width < 16 ||
+      width > 128 || page_rows < 1 || page_rows > kMaxLength || table_pages < 0 ||
+      table_pages >= kMaxRows || table_pages * page_rows > kMaxLength)
+    return 0;
+  return (int64_t)cache_attend_work((int)seqs, (int)hq, (int)hk, (int)width,
+                                    table_pages * page_rows, with_weights != 0);
+}
+
+int emeans_cache_attend(const void* q, int32_t dtype, int64_t q_row, int64_t q_head,
+                        const void* k_codes, const uint8_t* k_scales, const void* v_codes,
+                        const uint8_t* v_scales, int64_t pages, int64_t page_rows, int64_t block,
+                        int32_t fmt, const int32_t* table, int64_t table_ld, int64_t table_pages,
+                        const int32_t* lengths, int64_t seqs, int64_t hq, int64_t hk,
+                        int64_t width, double scale, void* out, float* weights,
+                        int64_t weights_ld, void* work, void* stream) {
+  g_err.clear();
+  int rc;
+  if ((rc = check_number_type(dtype, "dtype")) || (rc = check_heads(hq, "hq")) ||
+      (rc = check_heads(hk, "hk")) ||
+      (rc = check_pages(pages, page_rows, table_ld, table_pages, seqs)))
+    return rc;
+  if (hq % hk) return fail(EMEANS_EINVAL, "hq (%lld) must be a multiple of hk (%lld)",
+                           (long long)hq, (long long)hk);
+  if (width < 16 || width > 128 || width % 16)
+    return fail(EMEANS_EINVAL, "width must be a multiple of 16 in [16, 128] (got %lld)",
+                (long long)width);
+  const int64_t rows = pages * page_rows, places = table_pages * page_rows;
+  if ((rc = check_store(k_codes, k_scales, rows, hk * width, block, fmt)) ||
+      (rc = check_store(v_codes, v_scales, rows, hk * width, block, fmt)))
+    return rc;
+  if (q_row < 0 || q_head < 0) return fail(EMEANS_EINVAL, "strides must not be negative");
+  if (!(scale >= -1e30 && scale <= 1e30)) return fail(EMEANS_EINVAL, "scale out of range (%g)", scale);
+  if (weights && (rc = check_ld(weights_ld, places, seqs, "weights_ld"))) return rc;
+  if (weights && hq > 1024) return fail(EMEANS_EINVAL, "weights are summed over at most 1024 heads (got %lld)", (long long)hq);
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
+  if (seqs == 0) return EMEANS_OK;
+  if (!q || !out || !lengths || (places > 0 && !table))
+    return fail(EMEANS_EINVAL, "q, table, lengths and out must not be NULL");
+  if ((rc = check_device(q, "q")) || (rc = check_device(out, "out")) ||
+      (rc = check_device(lengths, "lengths")) || (places > 0 && (rc = check_device(table, "table"))) ||
+      (weights && (rc = check_device(weights, "weights"))))
+    return rc;
+  if (rows > 0 && ((rc = check_device(k_codes, "k_codes")) || (rc = check_device(k_scales, "k_scales")) ||
+                   (rc = check_device(v_codes, "v_codes")) || (rc = check_device(v_scales, "v_scales"))))
+    return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  void *at, *own;
+  if ((rc = take_work(work, emeans_cache_attend_work(seqs, hq, hk, width, page_rows, table_pages,
+                                                     weights != nullptr), st, &at, &own)))
+    return rc;
+  const CacheAttend a{dtype, q, q_row, q_head,
+                      {static_cast<const uint8_t*>(k_codes), k_scales},
+                      {static_cast<const uint8_t*>(v_codes), v_scales},
+                      rows, (int)block, fmt == EMEANS_I8, table, table_ld,
+                      rows > 0 ? (int)table_pages : 0,  // an empty store has no places
+                      (int)page_rows, lengths, (int)seqs, (int)hq, (int)hk, (int)width,
+                      (float)scale, out, weights, weights_ld, at};
+  return release(own, st, launched(launch_cache_attend(a, st), "cache attend"));
+}
+
+int64_t emeans_cache_evict_work(int64_t seqs, int64_t keep) {
+  if (seqs < 1 || seqs >= kMaxRows || keep < 0 || keep > kMaxLength) return 0;
+  return (int64_t)cache_evict_work((int)seqs, (int)keep);
+}
+
+int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t* row_codes,
+                       const int64_t* row_scales, int32_t stores, int64_t pages,
+                       int64_t page_rows, const int32_t* table, int64_t table_ld,
+                       int64_t table_pages, const int32_t* lengths, int64_t seqs,
+                       const float* weights, int64_t weights_ld, int64_t keep, int64_t recent,
+                       int32_t* new_lengths, float* new_weights, int32_t* kept, void* work,
+                       void* stream) {
+  g_err.clear();
+  int rc;
+  if (stores < 1 || stores > CacheEvict::kPlanes / 2)
+    return fail(EMEANS_EINVAL, "stores must be 1 to %d (got %d)", CacheEvict::kPlanes / 2, stores);
+  if (!codes || !scales || !row_codes || !row_scales)
+    return fail(EMEANS_EINVAL, "codes, scales and their row lengths must not be NULL");
+  if ((rc = check_pages(pages, page_rows, table_ld, table_pages, seqs))) return rc;
+  if ((rc = check_length(keep, 0, "keep"))) return rc;
+  if (recent < 0 || recent > keep)
+    return fail(EMEANS_EINVAL, "recent must be in [0, keep] (got %lld)", (long long)recent);
+  const int64_t rows = pages * page_rows, places = table_pages * page_rows;
+  if ((rc = check_ld(weights_ld, places, seqs, "weights_ld"))) return rc;
+  CacheEvict a{};
+  int64_t slices = 0;
+  for (int i = 0; i < stores; ++i) {
+    const int64_t len[2] = {row_codes[i], row_scales[i]};
+    void* const at[2] = {codes[i], scales[i]};
+    for (int j = 0; j < 2; ++j) {
+      if ((rc = check_length(len[j], 1, j ? "row_scales" : "row_codes"))) return rc;
+      if (rows > 0 && !at[j]) return fail(EMEANS_EINVAL, "codes and scales must not be NULL");
+      a.plane[a.planes] = static_cast<uint8_t*>(at[j]);
+      a.row_bytes[a.planes++] = len[j];
+      slices += blocks_of(len[j], 128);
+    }
+  }
+  if (seqs * slices > kMaxGroups)
+    return fail(EMEANS_EINVAL, "%lld sequences of these rows are too many for one call",
+                (long long)seqs);
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
+  if (seqs == 0) return EMEANS_OK;
+  if (!lengths || !new_lengths || (places > 0 && (!table || !weights || !new_weights)) ||
+      (keep > 0 && !kept))
+    return fail(EMEANS_EINVAL, "table, lengths, weights and results must not be NULL");
+  if ((rc = check_device(lengths, "lengths")) || (rc = check_device(new_lengths, "new_lengths")) ||
+      (keep > 0 && (rc = check_device(kept, "kept"))))
+    return rc;
+  if (places > 0 && ((rc = check_device(table, "table")) || (rc = check_device(weights, "weights")) ||
+                     (rc = check_device(new_weights, "new_weights"))))
+    return rc;
+  for (int p = 0; rows > 0 && p < a.planes; ++p)
+    if ((rc = check_device(a.plane[p], p % 2 ? "scales" : "codes"))) return rc;
+  a.rows = rows;
+  a.table = table;
+  a.table_ld = table_ld;
+  a.table_pages = (int)table_pages;
+  a.page = (int)page_rows;
+  a.lengths = lengths;
+  a.seqs = (int)seqs;
+  a.keep = (int)keep;
+  a.recent = (int)recent;
+  a.weights = weights;
+  a.weights_ld = weights_ld;
+  a.new_lengths = new_lengths;
+  a.new_weights = new_weights;
+  a.kept = kept;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  void *at, *own;
+  if ((rc = take_work(work, emeans_cache_evict_work(seqs, keep), st, &at, &own))) return rc;
+  a.work = at;
+  return release(own, st, launched(launch_cache_evict(a, st), "cache evict"));
+}
+
 }  // extern "C"

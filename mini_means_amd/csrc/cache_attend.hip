@@ -1,0 +1,482 @@
+// Attention of one new token per sequence over a paged store of 8-bit codes.
+//
+// For query head h and the keys k_p, values v_p of its key-value head at the places
+// p of the sequence: s_p = scale q.k_p, out = sum exp(s_p - m) v_p / sum exp(s_p - m),
+// m the largest. One pass over the codes with a running maximum and sum; the
+// sequence is cut into parts that are joined afterwards (m = max m_i, parts weighed
+// by exp(m_i - m)), as a few sequences would leave most of the card idle.
+//
+// Bound by HBM: the codes are read once. So that decoding them and the products
+// take less than the reads, both products are on the matrix unit in bf16, where a
+// code times its scale is exact, and nothing passes through LDS on the way: a wave
+// takes 32 places; S^T = K q^T leaves lane (h, g) the scores of places 4 g + i of
+// head h, which is what the product with the values reads as its operand if its
+// places are counted in that order. fp16 and fp32 queries, and the softmax weights
+// beside them, are sums of two and three bf16 terms (16 and 24 bits), bf16 ones
+// are one term.
+#include "block.hpp"
+#include "kernels.hpp"
+
+namespace emk {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kPlaces = 32;      // of a wave at a time
+constexpr int kWaves = 4;
+constexpr int kHeads = 16;       // query heads of a workgroup (of one key-value head)
+constexpr int kMaxPart = 2048;   // places of a workgroup at most
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float xor_max(float v) {
+  uint32_t b = __float_as_uint(v);
+  auto mx = [](uint32_t x, uint32_t y) {
+    return __float_as_uint(fmaxf(__uint_as_float(x), __uint_as_float(y)));
+  };
+  b = max_xor16(b, mx);
+  return __uint_as_float(max_xor32(b, mx));
+}
+
+__device__ __forceinline__ float xor_sum(float v) {
+  uint32_t b = __float_as_uint(v);
+  auto add = [](uint32_t x, uint32_t y) {
+    return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+  };
+  b = max_xor16(b, add);
+  return __uint_as_float(max_xor32(b, add));
+}
+
+// Four codes as bf16 values.
+template <bool I8>
+__device__ __forceinline__ u32x2 values_of(uint32_t w, float s) {
+  if constexpr (I8) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = (float)(int8_t)(w >> (8 * i)) * s;
+    return u32x2{pack2<1>(y[0], y[1]), pack2<1>(y[2], y[3])};
+  } else {
+    return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))};
+  }
+}
+
+// x as NT bf16 terms whose sum is x to 8 NT bits.
+template <int NT>
+__device__ __forceinline__ void terms_of(const float (&x)[8], bf16x8 (&t)[NT]) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<1>(r[2 * i], r[2 * i + 1]);
+    t[n] = __builtin_bit_cast(bf16x8, w);
+    if (n + 1 < NT) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float hi = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+        r[i] = abs_bits(hi) < kInfBits ? r[i] - hi : 0.0f;  // no inf - inf
+      }
+    }
+  }
+}
+
+struct Split {
+  CacheAttend a;
+  int64_t wg0;
+  int group;        // query heads per key-value head
+  int tiles;        // of kHeads query heads
+  int part;         // places of a workgroup, a multiple of kWaves * kPlaces
+  int parts;        // of a sequence
+  int nb;           // scales of a row
+  float* sums;      // seqs x hq x parts x width: unnormalised results (parts > 1)
+  f32x2* tops;      // seqs x hq x parts: (largest, sum), scores in units of log 2
+  float* scores;    // seqs x hq x (parts * part) (weights asked for)
+};
+
+__device__ __forceinline__ int length_of(const CacheAttend& a, int seq) {
+  const int64_t cap = (int64_t)a.table_pages * a.page, len = a.lengths[seq];
+  return (int)(len < 0 ? 0 : len > cap ? cap : len);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_number(void* out, int64_t at, float v) {
+  if constexpr (DT == 0)
+    static_cast<float*>(out)[at] = v;
+  else
+    static_cast<uint16_t*>(out)[at] = to_half_rne(v, DT == 4);
+}
+
+// W: width rounded up to 64 or 128. Lane l = 16 g + n. Keys: lane n's place, 16
+// codes per g and load (a 64-byte run of one row per instruction and place).
+// Values: places {4 g + i, 16 + 4 g + i}, the W / 16 codes from n W / 16 on.
+template <int DT, bool I8, int W, bool SCORES>
+__global__ __launch_bounds__(256) void split_kernel(Split s) {
+  constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3;
+  constexpr int KJ = W / 64;   // 16-byte loads of a key per lane
+  constexpr int VD = W / 16;   // values of a place per lane: 8 or 4
+  const CacheAttend& a = s.a;
+  __shared__ int64_t rows[kMaxPart];
+  __shared__ float join[kWaves][kHeads][W + 4];
+  __shared__ float top[kWaves][kHeads], sum[kWaves][kHeads];
+  __shared__ int holes;
+  // eight parts beside each other, one per XCD, whose heads follow each other there:
+  // the heads of a row share its lines in that XCD's L2
+  const int hh = a.hk * s.tiles;
+  const int64_t b = s.wg0 + blockIdx.x;
+  const int64_t unit = b / (8 * hh) * 8 + b % 8;
+  if (unit >= (int64_t)a.seqs * s.parts) return;
+  const int head = (int)(b / 8 % hh), kvh = head / s.tiles, q0 = head % s.tiles * kHeads;
+  const int seq = (int)(unit % a.seqs), part = (int)(unit / a.seqs);
+  const int len = length_of(a, seq), p0 = part * s.part;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int heads = min(s.group - q0, kHeads);
+  const int hq0 = kvh * s.group + q0;
+  if (p0 >= len) {
+    if (s.parts == 1)
+      for (int i = threadIdx.x; i < heads * a.width; i += 256)
+        store_number<DT>(a.out, ((int64_t)seq * a.hq + hq0) * a.width + i, 0.0f);
+    return;
+  }
+  const int cnt = min(s.part, len - p0);
+  if (threadIdx.x == 0) holes = 0;
+  __syncthreads();
+  // the places' rows; behind the last, the first place's again (never a row that
+  // the sequence does not have)
+  const int whole = (cnt + kPlaces - 1) / kPlaces * kPlaces;
+  for (int i = threadIdx.x; i < whole; i += 256) {
+    const int p = p0 + (i < cnt ? i : 0);
+    const int64_t page = a.table[seq * a.table_ld + p / a.page];
+    const int64_t row = page * a.page + p % a.page;
+    const bool in = page >= 0 && row < a.rows;
+    rows[i] = in ? row : -1;
+    if (!in) holes = 1;
+  }
+  bf16x8 qf[2 * KJ][NT];
+#pragma unroll
+  for (int m = 0; m < 2 * KJ; ++m) {
+    const int c = (m >> 1) * 64 + g * 16 + (m & 1) * 8;
+    float x[8] = {};
+    if (n < heads && c < a.width)
+      load8<DT>(a.q, seq * a.q_rs + (hq0 + n) * a.q_hs + c, 8, x);
+    terms_of<NT>(x, qf[m]);
+  }
+  __syncthreads();
+  const bool gaps = holes != 0;
+  const int64_t d = (int64_t)a.hk * a.width;
+  const int col = kvh * a.width;
+  int kb[KJ];
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) kb[j] = (col + min(j * 64 + g * 16, a.width - 16)) / a.block;
+  const bool von = n * VD < a.width;
+  const int vcol = von ? n * VD : 0;
+  const int vb = (col + vcol) / a.block;
+  const uint8_t* kp = a.k.codes + col + g * 16;
+  const uint8_t* vp = a.v.codes + col + vcol;
+  const float c2 = a.scale * kLog2e;
+
+  f32x4 acc[VD];
+#pragma unroll
+  for (int j = 0; j < VD; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;
+  for (int t = wave * kPlaces; t < whole; t += kWaves * kPlaces) {
+    // keys and scores: st[u][i] of place t + 16 u + 4 g + i
+    f32x4 st[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t row = max(rows[t + 16 * u + n], (int64_t)0);
+      st[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        u32x4 w = {0u, 0u, 0u, 0u};
+        float f = 0.0f;
+        if (j * 64 + g * 16 < a.width) {
+          w = load_any<u32x4>(kp + row * d + j * 64);
+          f = scale_value(a.k.scales[row * s.nb + kb[j]]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x2 lo = values_of<I8>(w[2 * h], f), hi = values_of<I8>(w[2 * h + 1], f);
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
+#pragma unroll
+          for (int e = NT - 1; e >= 0; --e)
+            st[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[2 * j + h][e], st[u], 0, 0, 0);
+        }
+      }
+    }
+    // values: x[u * 4 + i] of place t + 16 u + 4 g + i
+    u32x4 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t at = rows[t + 16 * (e >> 2) + 4 * g + (e & 3)];
+      const int64_t row = max(at, (int64_t)0);
+      u32x2 w = {0u, 0u};
+      if (von) {
+        if constexpr (VD == 8)
+          w = load_any<u32x2>(vp + row * d);
+        else
+          w[0] = load_any<uint32_t>(vp + row * d);
+      }
+      const float f = gaps && at < 0 ? 0.0f : scale_value(a.v.scales[row * s.nb + vb]);
+      if (gaps && at < 0) w = u32x2{0u, 0u};
+      const u32x2 lo = values_of<I8>(w[0], f), hi = values_of<I8>(w[1], f);
+      x[e] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+    float top_now = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = t + 16 * u + 4 * g + i;
+        float v = st[u][i] * c2;
+        if (p >= cnt || (gaps && rows[p] < 0)) v = -INFINITY;
+        st[u][i] = v;
+        top_now = fmaxf(top_now, v);
+      }
+    if constexpr (SCORES) {
+      if (n < heads) {
+        const int64_t at = ((int64_t)seq * a.hq + hq0 + n) * s.parts * s.part + p0 + t + 4 * g;
+        store_any(s.scores + at, st[0]);
+        store_any(s.scores + at + 16, st[1]);
+      }
+    }
+    const float m_new = fmaxf(m, xor_max(top_now));
+    const float ref = m_new == -INFINITY ? 0.0f : m_new;
+    if (__any(m_new != m)) {
+      const float f = __builtin_amdgcn_exp2f(m - ref);
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < VD; ++j) acc[j] *= f;
+      m = m_new;
+    }
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(st[e >> 2][e & 3] - ref);
+      l += p[e];
+    }
+    bf16x8 pf[NT];
+    terms_of<NT>(p, pf);
+#pragma unroll
+    for (int j = 0; j < VD; ++j) {
+      u32x4 w;  // value j of the eight places
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = __builtin_amdgcn_perm(x[2 * e + 1][j >> 1], x[2 * e][j >> 1],
+                                     j & 1 ? 0x07060302u : 0x05040100u);
+      const bf16x8 vf = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+      for (int e = NT - 1; e >= 0; --e)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[e], acc[j], 0, 0, 0);
+    }
+  }
+  // the waves' parts joined: acc[j][i] is value VD (4 g + i) + j of head n
+  l = xor_sum(l);
+  if (g == 0) {
+    top[wave][n] = m;
+    sum[wave][n] = l;
+  }
+  __syncthreads();
+  float all = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) all = fmaxf(all, top[w][n]);
+  const float f = __builtin_amdgcn_exp2f(m - (all == -INFINITY ? 0.0f : all));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < VD; j += 4)
+      *reinterpret_cast<f32x4*>(&join[wave][n][VD * (4 * g + i) + j]) =
+          f32x4{acc[j][i] * f, acc[j + 1][i] * f, acc[j + 2][i] * f, acc[j + 3][i] * f};
+  __syncthreads();
+  const int h = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * VD;
+  if (h >= heads) return;
+  float mh = -INFINITY, lh = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) mh = fmaxf(mh, top[w][h]);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w)
+    lh += sum[w][h] * __builtin_amdgcn_exp2f(top[w][h] - (mh == -INFINITY ? 0.0f : mh));
+  const int64_t at = (int64_t)seq * a.hq + hq0 + h;
+  if ((SCORES || s.parts > 1) && c0 == 0) s.tops[at * s.parts + part] = f32x2{mh, lh};
+  if (c0 >= a.width) return;
+  const float inv = s.parts > 1 ? 1.0f : lh == 0.0f ? 0.0f : 1.0f / lh;
+#pragma unroll
+  for (int j = 0; j < VD; ++j) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += join[w][h][c0 + j];
+    v = lh == 0.0f ? 0.0f : v * inv;
+    if (s.parts > 1)
+      s.sums[(at * s.parts + part) * a.width + c0 + j] = v;
+    else
+      store_number<DT>(a.out, at * a.width + c0 + j, v);
+  }
+}
+
+__device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// Workgroups below seqs * hq: the parts of one head of one sequence joined. The
+// others (weights asked for): the attention weights of one part's places, summed
+// over the heads, from the scores that split_kernel left.
+constexpr int kJoinHeads = 1024;
+
+template <int DT>
+__global__ __launch_bounds__(256) void join_kernel(Split s, int joins) {
+  const CacheAttend& a = s.a;
+  __shared__ f32x2 ml[kJoinHeads];
+  __shared__ f32x4 acc[256];
+  __shared__ float tmp[8];
+  const int64_t b = s.wg0 + blockIdx.x;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (b < joins) {
+    const int seq = (int)(b / a.hq);
+    const int used = (length_of(a, seq) + s.part - 1) / s.part;
+    const f32x2* tops = s.tops + b * s.parts;
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < used; i += 256) m = fmaxf(m, tops[i][0]);
+    m = wave_max(m);
+    if (lane == 0) tmp[wave] = m;
+    __syncthreads();
+    m = guarded(fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3])));
+    // 32 lanes of four values each, eight parts at a time
+    const int c = (threadIdx.x & 31) * 4, i0 = threadIdx.x >> 5;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+    for (int i = i0; i < used; i += 8) {
+      const f32x2 t = tops[i];
+      if (t[1] == 0.0f) continue;  // a part of gaps
+      const float f = __builtin_amdgcn_exp2f(t[0] - m);
+      l += t[1] * f;
+      if (c < a.width) v += *reinterpret_cast<const f32x4*>(s.sums + (b * s.parts + i) * a.width + c) * f;
+    }
+    acc[threadIdx.x] = v;
+    if ((threadIdx.x & 31) == 0) tmp[i0] = l;
+    __syncthreads();
+    if (threadIdx.x >= 32 || c >= a.width) return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += tmp[i];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += acc[threadIdx.x + 32 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      store_number<DT>(a.out, b * a.width + c + i, sum == 0.0f ? 0.0f : v[i] / sum);
+    return;
+  }
+  const int64_t unit = b - joins;
+  const int seq = (int)(unit % a.seqs), part = (int)(unit / a.seqs);
+  const int len = length_of(a, seq), p0 = part * s.part;
+  if (p0 >= len) return;
+  const int used = (len + s.part - 1) / s.part;
+  for (int h = wave; h < a.hq; h += 4) {
+    const f32x2* tops = s.tops + ((int64_t)seq * a.hq + h) * s.parts;
+    float m = -INFINITY, l = 0.0f;
+    for (int i = lane; i < used; i += 64) m = fmaxf(m, tops[i][0]);
+    m = guarded(wave_max(m));
+    for (int i = lane; i < used; i += 64) {
+      const f32x2 t = tops[i];
+      if (t[1] != 0.0f) l += t[1] * __builtin_amdgcn_exp2f(t[0] - m);
+    }
+    l = wave_sum(l);
+    if (lane == 0) ml[h] = f32x2{m, l == 0.0f ? 0.0f : 1.0f / l};
+  }
+  __syncthreads();
+  const int cnt = min(s.part, len - p0);
+  const int64_t ld = (int64_t)s.parts * s.part;
+  for (int i = threadIdx.x; i < cnt; i += 256) {
+    const float* sc = s.scores + (int64_t)seq * a.hq * ld + p0 + i;
+    float v = 0.0f;
+    for (int h = 0; h < a.hq; ++h) v += __builtin_amdgcn_exp2f(sc[h * ld] - ml[h][0]) * ml[h][1];
+    a.weights[seq * a.weights_ld + p0 + i] += v;
+  }
+}
+
+// Places of a workgroup: a wave's 32 at least, so many that about 2048 workgroups
+// are left where sequences reach the table's width.
+int part_of(int seqs, int hk, int tiles, int64_t places) {
+  int part = kWaves * kPlaces;
+  while (part < kMaxPart && (int64_t)seqs * hk * tiles * ((places + part - 1) / part) > 4096) part *= 2;
+  return part;
+}
+
+struct Room {
+  size_t sums, tops, scores, all;
+};
+
+Room room_of(int64_t seqs, int64_t hq, int64_t width, int64_t parts, int64_t part, bool weights) {
+  Room r = {0, 0, 0, 0};
+  auto take = [&](size_t n) {
+    const size_t at = r.all;
+    r.all += (n + 255) / 256 * 256;
+    return at;
+  };
+  if (parts > 1) r.sums = take((size_t)(seqs * hq * parts * width) * 4);
+  if (parts > 1 || weights) r.tops = take((size_t)(seqs * hq * parts) * 8);
+  if (weights) r.scores = take((size_t)(seqs * hq * parts * part) * 4);
+  return r;
+}
+
+template <int DT, bool I8, int W>
+hipError_t split_t(Split& s, int64_t wgs, bool weights, hipStream_t st) {
+  for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
+    const unsigned grid = (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups);
+    s.wg0 = wg0;
+    if (weights)
+      split_kernel<DT, I8, W, true><<<grid, 256, 0, st>>>(s);
+    else
+      split_kernel<DT, I8, W, false><<<grid, 256, 0, st>>>(s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT>
+hipError_t cache_attend_t(const CacheAttend& a, hipStream_t st) {
+  const int group = a.hq / a.hk, tiles = (group + kHeads - 1) / kHeads;
+  const int64_t places = (int64_t)a.table_pages * a.page;
+  const int part = part_of(a.seqs, a.hk, tiles, places);
+  const int64_t parts = places < 1 ? 1 : (places + part - 1) / part;
+  const bool weights = a.weights != nullptr;
+  const Room r = room_of(a.seqs, a.hq, a.width, parts, part, weights);
+  uint8_t* work = static_cast<uint8_t*>(a.work);
+  Split s{a, 0, group, tiles, part, (int)parts, (int)(((int64_t)a.hk * a.width + a.block - 1) / a.block),
+          reinterpret_cast<float*>(work + r.sums), reinterpret_cast<f32x2*>(work + r.tops),
+          reinterpret_cast<float*>(work + r.scores)};
+  const int64_t wgs = (a.seqs * parts + 7) / 8 * 8 * a.hk * tiles;
+  hipError_t e;
+  if (a.width <= 64)
+    e = a.i8 ? split_t<DT, true, 64>(s, wgs, weights, st) : split_t<DT, false, 64>(s, wgs, weights, st);
+  else
+    e = a.i8 ? split_t<DT, true, 128>(s, wgs, weights, st) : split_t<DT, false, 128>(s, wgs, weights, st);
+  if (e != hipSuccess || (parts == 1 && !weights)) return e;
+  const int joins = parts > 1 ? a.seqs * a.hq : 0;
+  const int64_t more = joins + (weights ? a.seqs * parts : 0);
+  for (int64_t wg0 = 0; wg0 < more; wg0 += kMaxGroups) {
+    s.wg0 = wg0;
+    join_kernel<DT><<<(unsigned)(more - wg0 < kMaxGroups ? more - wg0 : kMaxGroups), 256, 0, st>>>(s, joins);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t cache_attend_work(int seqs, int hq, int hk, int width, int64_t places, bool weights) {
+  const int tiles = (hq / hk + kHeads - 1) / kHeads;
+  const int part = part_of(seqs, hk, tiles, places);
+  const int64_t parts = places < 1 ? 1 : (places + part - 1) / part;
+  return room_of(seqs, hq, width, parts, part, weights).all;
+}
+
+hipError_t launch_cache_attend(const CacheAttend& a, hipStream_t st) {
+  switch (a.dt) {
+    case 0: return cache_attend_t<0>(a, st);
+    case 1: return cache_attend_t<1>(a, st);
+    case 4: return cache_attend_t<4>(a, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace emk

@@ -1,0 +1,242 @@
+// Rows of small accumulated weight dropped from paged stores.
+//
+// Of a sequence of more than `keep` rows stay the last `recent` and, of those before
+// them, the keep - recent of largest weight (of equal ones the first). They move to
+// the sequence's first places in their order, in place.
+//
+// Bound by HBM and by latency: a workgroup per sequence finds the threshold digit by
+// digit (four passes of 8 bits over the weights, which stay in L2) and lists the
+// moves; then workgroups of a sequence and 128 bytes of a row each go along the list.
+#include <type_traits>
+
+#include "block.hpp"
+#include "kernels.hpp"
+
+namespace emk {
+namespace {
+
+constexpr int kSelect = 1024;
+
+struct Move {
+  int64_t from, to;
+};
+
+struct Moves {
+  Move* list;    // seqs x keep; from or to < 0: a page outside the store
+  int32_t* span; // seqs x 2: [first rank that moves, ranks)
+};
+
+// Order of weights as unsigned numbers; NaN as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float w) {
+  const uint32_t b = __float_as_uint(w != w ? -INFINITY : w + 0.0f);
+  return b >> 31 ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ int64_t place_of(const CacheEvict& a, int seq, int p) {
+  const int64_t page = a.table[seq * a.table_ld + p / a.page];
+  const int64_t row = page * a.page + p % a.page;
+  return page >= 0 && row < a.rows ? row : -1;
+}
+
+__global__ __launch_bounds__(kSelect) void select_kernel(CacheEvict a, Moves mv) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t tmp[kSelect / 64];
+  __shared__ uint32_t found[2];  // digit, how many of it are still wanted
+  const int seq = blockIdx.x, t = threadIdx.x;
+  const int64_t cap = (int64_t)a.table_pages * a.page;
+  const int64_t given = a.lengths[seq];
+  const int len = (int)(given < 0 ? 0 : given > cap ? cap : given);
+  const float* w = a.weights + seq * a.weights_ld;
+  float* new_w = a.new_weights + seq * cap;
+  int32_t* kept = a.kept + (int64_t)seq * a.keep;
+  const int old = max(len - a.recent, 0);  // the rows that compete
+  uint32_t want = len > a.keep ? (uint32_t)(a.keep - a.recent) : (uint32_t)old;
+  uint32_t edge = 0;  // stay: order > edge, and of those equal to it the first `want`
+  if (len > a.keep) {
+    uint32_t known = 0;
+    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
+      if (t < 256) hist[t] = 0;
+      __syncthreads();
+      for (int p = t; p < old; p += kSelect) {
+        const uint32_t o = order_of(w[p]);
+        if ((o & known) == edge) atomicAdd(&hist[o >> shift & 255u], 1u);
+      }
+      __syncthreads();
+      if (t < 64) {
+        // lane t has digits 255 - 4 t down to 252 - 4 t
+        uint32_t c[4], mine = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += c[i] = hist[255 - 4 * t - i];
+        uint32_t before = wave_incl_scan(mine) - mine;
+        if (before < want && before + mine >= want) {
+          int i = 0;
+          while (before + c[i] < want) before += c[i++];
+          found[0] = 255 - 4 * t - i;
+          found[1] = want - before;
+        }
+      }
+      __syncthreads();
+      edge |= found[0] << shift;
+      known |= 255u << shift;
+      want = found[1];
+      __syncthreads();
+    }
+    if (want == 0) edge = 0xFFFFFFFFu;  // keep == recent: no other stays
+  }
+  // ranks in order; both counts of a round in one scan (each at most 1024)
+  uint32_t above = 0, equal = 0;  // of the rounds before
+  for (int p0 = 0; p0 < old; p0 += kSelect) {
+    const int p = p0 + t;
+    const uint32_t o = p < old ? order_of(w[p]) : 0u;
+    const bool gt = p < old && o > edge, eq = p < old && o == edge;
+    const uint32_t mine = (gt ? 1u << 16 : 0u) + (eq ? 1u : 0u);
+    const uint32_t upto = block_incl_scan<uint32_t, kSelect>(mine, tmp);
+    const uint32_t g0 = above + ((upto - mine) >> 16), e0 = equal + ((upto - mine) & 0xFFFFu);
+    if (gt || (eq && e0 < want)) {
+      const uint32_t r = g0 + min(e0, want);
+      kept[r] = p;
+      new_w[r] = w[p];
+      mv.list[(int64_t)seq * a.keep + r] = Move{place_of(a, seq, p), place_of(a, seq, (int)r)};
+    }
+    if (t == kSelect - 1) {
+      found[0] = upto >> 16;
+      found[1] = upto & 0xFFFFu;
+    }
+    __syncthreads();
+    above += found[0];
+    equal += found[1];
+    __syncthreads();
+  }
+  const int stay = (int)(above + min(equal, want));
+  for (int p = old + t; p < len; p += kSelect) {
+    const int r = stay + p - old;
+    kept[r] = p;
+    new_w[r] = w[p];
+    mv.list[(int64_t)seq * a.keep + r] = Move{place_of(a, seq, p), place_of(a, seq, r)};
+  }
+  const int count = stay + len - old;
+  for (int r = count + t; r < a.keep; r += kSelect) kept[r] = -1;
+  for (int64_t r = count + t; r < cap; r += kSelect) new_w[r] = 0.0f;
+  if (t == 0) {
+    found[0] = (uint32_t)count;
+    a.new_lengths[seq] = count;
+  }
+  __syncthreads();
+  // ranks are in order: those before the first gap stay where they are
+  for (int r = t; r < count; r += kSelect)
+    if (kept[r] != r && (r == 0 || kept[r - 1] == r - 1)) found[0] = (uint32_t)r;
+  __syncthreads();
+  if (t == 0) {
+    mv.span[2 * seq] = (int32_t)found[0];
+    mv.span[2 * seq + 1] = count;
+  }
+}
+
+constexpr int kSlice = 128;  // bytes of a row that a workgroup moves
+constexpr int kDeep = 4;     // rows in flight per thread and round
+
+struct Slices {
+  uint8_t* plane[CacheEvict::kPlanes];
+  int64_t row_bytes[CacheEvict::kPlanes];
+  int unit[CacheEvict::kPlanes];   // bytes of a lane: 16, 4 or 1
+  int first[CacheEvict::kPlanes];  // first slice of the plane
+  int planes, slices;
+};
+
+template <typename V>
+__device__ __forceinline__ void move_rows(uint8_t* plane, int64_t row_bytes, int64_t off,
+                                          const Move* list, int first, int count) {
+  constexpr int LPR = kSlice / sizeof(V);  // lanes of a row
+  constexpr int RPT = 256 / LPR;           // rows of the workgroup at once
+  constexpr int ROUND = RPT * kDeep;
+  const int row = threadIdx.x / LPR;
+  const int64_t at = off + (int64_t)(threadIdx.x % LPR) * sizeof(V);
+  const bool on = at < row_bytes;
+  using Held = std::conditional_t<sizeof(V) == 1, uint32_t, V>;  // in whole registers
+  Held held[2][kDeep] = {};
+  int64_t to[2][kDeep];
+  auto fetch = [&](int r0, Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int r = r0 + u * RPT + row;
+      dst[u] = -1;
+      if (on && r < count) {
+        const Move m = list[r];
+        if (m.from >= 0 && m.to >= 0) {
+          v[u] = load_any<V>(plane + m.from * row_bytes + at);
+          dst[u] = m.to * row_bytes + at;
+        }
+      }
+    }
+  };
+  // A row's place is never before its rank, so rows that are stored in one round
+  // are sources of that round or of an earlier one only: they are stored once every
+  // lane holds its rows of the round. The next round's are fetched before that.
+  auto put = [&](Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+      if (dst[u] >= 0) store_any(plane + dst[u], (V)v[u]);
+  };
+  // the loads themselves have ended, not their issue alone
+  auto arrived = [](Held(&v)[kDeep]) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) asm volatile("" : "+v"(v[u])::"memory");
+  };
+  fetch(first, held[0], to[0]);
+  for (int r0 = first; r0 < count; r0 += 2 * ROUND) {
+    arrived(held[0]);
+    __syncthreads();
+    fetch(r0 + ROUND, held[1], to[1]);
+    put(held[0], to[0]);
+    arrived(held[1]);
+    __syncthreads();
+    fetch(r0 + 2 * ROUND, held[0], to[0]);
+    put(held[1], to[1]);
+  }
+}
+
+__global__ __launch_bounds__(256) void move_kernel(Slices s, Moves mv, int keep) {
+  const int seq = blockIdx.x / s.slices, slice = blockIdx.x % s.slices;
+  const int first = mv.span[2 * seq], count = mv.span[2 * seq + 1];
+  if (first >= count) return;
+  int p = 0;
+  while (p + 1 < s.planes && slice >= s.first[p + 1]) ++p;
+  const int64_t off = (int64_t)(slice - s.first[p]) * kSlice;
+  const Move* list = mv.list + (int64_t)seq * keep;
+  if (s.unit[p] == 16)
+    move_rows<u32x4>(s.plane[p], s.row_bytes[p], off, list, first, count);
+  else if (s.unit[p] == 4)
+    move_rows<uint32_t>(s.plane[p], s.row_bytes[p], off, list, first, count);
+  else
+    move_rows<uint8_t>(s.plane[p], s.row_bytes[p], off, list, first, count);
+}
+
+size_t list_bytes(int seqs, int keep) { return ((size_t)seqs * keep * sizeof(Move) + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t cache_evict_work(int seqs, int keep) { return list_bytes(seqs, keep) + (size_t)seqs * 8; }
+
+hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st) {
+  if (a.seqs <= 0) return hipSuccess;
+  uint8_t* work = static_cast<uint8_t*>(a.work);
+  const Moves mv{reinterpret_cast<Move*>(work),
+                 reinterpret_cast<int32_t*>(work + list_bytes(a.seqs, a.keep))};
+  select_kernel<<<a.seqs, kSelect, 0, st>>>(a, mv);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  Slices s{};
+  for (int p = 0; p < a.planes; ++p) {
+    s.plane[p] = a.plane[p];
+    s.row_bytes[p] = a.row_bytes[p];
+    const uint64_t bits = (uint64_t)a.row_bytes[p] | (uint64_t)(uintptr_t)a.plane[p];
+    s.unit[p] = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    s.first[p] = s.slices;
+    s.slices += (int)((a.row_bytes[p] + kSlice - 1) / kSlice);
+  }
+  s.planes = a.planes;
+  move_kernel<<<(unsigned)a.seqs * s.slices, 256, 0, st>>>(s, mv, a.keep);
+  return hipGetLastError();
+}
+
+}  // namespace emk

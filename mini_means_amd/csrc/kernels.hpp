@@ -328,4 +328,97 @@ hipError_t launch_block_product(const BlockProduct& p, hipStream_t st);
 bool block_product_encodes(int64_t m, int32_t k);
 hipError_t launch_encode_product(int dt, const BlockProduct& p, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Queries and keys normed per head and turned by position (norm_rotate.hip):
+// q n x hq x width and k n x hk x width of type dt with any distance between
+// rows and heads, weights of type gdt, results contiguous. width is a multiple of
+// 8, at most 256, half a multiple of 4 with 2 half <= width.
+// ---------------------------------------------------------------------------
+struct NormRotate {
+  int dt, gdt;
+  int64_t n;
+  int hq, hk, width, half;
+  const void* q;
+  int64_t q_rs, q_hs;
+  const void* k;
+  int64_t k_rs, k_hs;
+  const void* gq;
+  const void* gk;
+  const void* positions;
+  int pos_bytes;
+  const double* freqs;
+  float eps;
+  void* qo;  // results; the gradient pass: dq and dk of the inputs
+  void* ko;
+  // the gradient pass
+  const void* dq;
+  int64_t dq_rs, dq_hs;
+  const void* dk;
+  int64_t dk_rs, dk_hs;
+  float* part;  // norm_rotate_groups(n) x 2 x width
+  void* dgq;
+  void* dgk;
+
+  __device__ float weight(const void* w, int c) const {
+    return gdt == 0 ? static_cast<const float*>(w)[c]
+                    : half_to_f32(static_cast<const uint16_t*>(w)[c], gdt == 4);
+  }
+};
+int norm_rotate_groups(int64_t n);
+hipError_t launch_norm_rotate(const NormRotate& a, hipStream_t st);
+hipError_t launch_norm_rotate_back(const NormRotate& a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// One new token per sequence over a paged store of codes (cache_attend.hip):
+// store as in DecodeRows, `rows` rows of d = hk * width codes. lengths are clamped
+// to what the table holds; places in pages outside the store are left out.
+// ---------------------------------------------------------------------------
+struct CacheStore {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
+struct CacheAttend {
+  int dt;  // of q and out
+  const void* q;
+  int64_t q_rs, q_hs;
+  CacheStore k, v;
+  int64_t rows;
+  int block;
+  bool i8;
+  const int32_t* table;
+  int64_t table_ld;
+  int table_pages, page;
+  const int32_t* lengths;
+  int seqs, hq, hk, width;
+  float scale;
+  void* out;       // seqs x hq x width
+  float* weights;  // NULL, or seqs rows weights_ld apart: added to
+  int64_t weights_ld;
+  void* work;
+};
+size_t cache_attend_work(int seqs, int hq, int hk, int width, int64_t places, bool weights);
+hipError_t launch_cache_attend(const CacheAttend& a, hipStream_t st);
+
+// Rows of small weight dropped from paged stores of one shape (cache_evict.hip).
+struct CacheEvict {
+  static constexpr int kPlanes = 8;
+  uint8_t* plane[kPlanes];  // codes and scales of each store
+  int64_t row_bytes[kPlanes];
+  int planes;
+  int64_t rows;
+  const int32_t* table;
+  int64_t table_ld;
+  int table_pages, page;
+  const int32_t* lengths;
+  int seqs, keep, recent;
+  const float* weights;
+  int64_t weights_ld;
+  int32_t* new_lengths;
+  float* new_weights;  // seqs x (table_pages * page)
+  int32_t* kept;       // seqs x keep
+  void* work;          // cache_evict_work() bytes
+};
+size_t cache_evict_work(int seqs, int keep);
+hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st);
+
 }  // namespace emk
