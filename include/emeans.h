@@ -604,6 +604,47 @@ int emeans_norm_rotate_gradient(const void* q, int64_t q_row, int64_t q_head, co
                                 void* dk, void* dq_weight, void* dk_weight, void* work,
                                 void* stream);
 
+/* Attention over packed sequences: sequence s is rows starts[s] .. starts[s + 1] of q
+ * (n x hq x width) and k_starts[s] .. k_starts[s + 1] of k and v (nk x hk x width);
+ * query head h goes with key-value head h / (hq / hk). A query row sees all keys of its
+ * sequence or, with causal != 0, row i of lq those j <= i + lk - lq of lk (the last
+ * query sees them all). out = softmax(scale q k^T) v, rows that see no key and rows
+ * outside every sequence are zeros; what a row does not see does not show in it, an
+ * infinity or a NaN neither. Scores, softmax and sums are fp32; the softmax weights are
+ * rounded to dtype beside the values.
+ *   dtype     EMEANS_BF16 or EMEANS_F16 (EDTYPE for EMEANS_F32)
+ *   width     a multiple of 8, at most 128      hq  a multiple of hk
+ *   strides   rows and heads start at multiples of 16 bytes
+ *   starts, k_starts  device, seqs + 1 int32, not decreasing (the same for
+ *             self-attention; cut to the tensors)
+ *   out       device, n x hq x width (contiguous)
+ *   lse, rest NULL, or device, hq x n fp32 and n x hq x width of dtype: what the
+ *             gradients need, each row's log sum and what the rounding of out took away
+ * Errors: EINVAL, EDTYPE, ENOTDEVICE, EHIP. */
+int emeans_attend(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                  int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int32_t dtype,
+                  int64_t n, int64_t nk, int64_t hq, int64_t hk, int64_t width,
+                  const int32_t* starts, const int32_t* k_starts, int64_t seqs, int32_t causal,
+                  double scale, void* out, float* lse, void* rest, void* stream);
+
+/* Its gradients dq, dk, dv (contiguous, zeros outside every sequence) from the inputs,
+ * out, lse, rest and dout (strides as the inputs'); the heads of a group are summed in order,
+ * and equal calls give equal bits. Weights and their gradients are rounded to dtype
+ * beside the other operand. A NaN or an infinity may show anywhere in its sequence's
+ * gradients.
+ *   work  device, emeans_attend_work(n, hq) bytes, 16-byte aligned, or NULL (allocated
+ *         stream-ordered)
+ * Errors: as above; ENOMEM. */
+int64_t emeans_attend_work(int64_t n, int64_t hq);
+int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                           int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                           int64_t v_head, int32_t dtype, int64_t n, int64_t nk, int64_t hq,
+                           int64_t hk, int64_t width, const int32_t* starts,
+                           const int32_t* k_starts, int64_t seqs, int32_t causal, double scale,
+                           const void* out, const float* lse, const void* rest,
+                           const void* dout, int64_t do_row, int64_t do_head, void* dq,
+                           void* dk, void* dv, void* work, void* stream);
+
 /* Attention of one new token per sequence over two paged stores (keys and values,
  * each `pages` pages of page_rows rows of hk * width codes, scales as for
  * emeans_cache_write): out[s][h] = sum_p softmax_p(scale q[s][h] . key_p) value_p

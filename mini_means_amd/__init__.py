@@ -129,6 +129,10 @@ def lib() -> ctypes.CDLL:
         L.emeans_norm_rotate.argtypes = rotate + [c_vp] * 3
         L.emeans_norm_rotate_gradient.argtypes = rotate + [c_vp, c_i64, c_i64] * 2 + [c_vp] * 6
         L.emeans_norm_rotate_work.argtypes = [c_i64, c_i64]
+        attend = [c_vp, c_i64, c_i64] * 3 + [c_i32] + [c_i64] * 5 + [c_vp, c_vp, c_i64, c_i32, c_dbl]
+        L.emeans_attend.argtypes = attend + [c_vp] * 4
+        L.emeans_attend_gradient.argtypes = attend + [c_vp] * 4 + [c_i64, c_i64] + [c_vp] * 5
+        L.emeans_attend_work.argtypes = [c_i64, c_i64]
         L.emeans_cache_attend_work.argtypes = [c_i64] * 6 + [c_i32]
         L.emeans_cache_attend.argtypes = [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64,
                                           c_i64, c_i64, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64,
@@ -138,11 +142,11 @@ def lib() -> ctypes.CDLL:
         L.emeans_cache_evict.argtypes = [c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i64, c_vp, c_i64,
                                          c_i64, c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp,
                                          c_vp, c_vp, c_vp, c_vp]
-        for f in ("emeans_norm_rotate_work", "emeans_cache_attend_work",
+        for f in ("emeans_norm_rotate_work", "emeans_attend_work", "emeans_cache_attend_work",
                   "emeans_cache_evict_work"):
             getattr(L, f).restype = c_i64
-        for f in ("emeans_norm_rotate", "emeans_norm_rotate_gradient", "emeans_cache_attend",
-                  "emeans_cache_evict"):
+        for f in ("emeans_norm_rotate", "emeans_norm_rotate_gradient", "emeans_attend",
+                  "emeans_attend_gradient", "emeans_cache_attend", "emeans_cache_evict"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("emeans_block_encode", "emeans_block_matmul", "emeans_block_linear",
                   "emeans_block_train_forward", "emeans_block_train_gradient",
@@ -1173,6 +1177,132 @@ def norm_rotate(q, k, q_weight, k_weight, positions, freqs, *, eps: float = 1e-6
                                          or q_weight.requires_grad or k_weight.requires_grad):
         return _rotate_fn().apply(q, k, q_weight, k_weight, positions, freqs, eps)
     return _norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps)
+
+
+def _aligned(t):
+    """t with heads of adjacent values at multiples of 16 bytes (a copy if they are not)."""
+    a, b, c = t.stride()
+    if (c == 1 or t.shape[2] <= 1) and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0:
+        return t
+    return t.contiguous() if t.data_ptr() % 16 == 0 or not t.is_contiguous() else t.clone()
+
+
+def _attend_args(q, k, v, starts, k_starts, causal, scale):
+    """The arguments that both passes of attend share, and the sizes."""
+    torch = _T().torch
+    dev = _device_of(q, "q")
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise EmeansError(f"EDTYPE: q {q.dtype} not supported (bfloat16 or float16)")
+    n, hq, w, qr, qh = _heads(q, dev, "q")
+    nk, hk, wk, kr, kh = _heads(k, dev, "k", q.dtype)
+    nv, hv, wv, vr, vh = _heads(v, dev, "v", q.dtype)
+    if wk != w or (nv, hv, wv) != (nk, hk, wk):
+        raise EmeansError(f"EINVAL: k and v must be rows x heads x {w} of one shape (got "
+                          f"{tuple(k.shape)} and {tuple(v.shape)})")
+    if w < 8 or w > 128 or w % 8:
+        raise EmeansError(f"EINVAL: width must be a multiple of 8 in [8, 128] (got {w})")
+    if hq < 1 or hk < 1 or hq % hk:
+        raise EmeansError(f"EINVAL: {hq} heads of q cannot share {hk} of k and v")
+    seqs = _vector(starts, dev, "starts", None, (torch.int32,), "int32") - 1
+    if seqs < 0:
+        raise EmeansError("EINVAL: starts must be one more than the sequences")
+    if k_starts is not starts:
+        _vector(k_starts, dev, "k_starts", seqs + 1, (torch.int32,), "int32")
+    elif nk != n:
+        raise EmeansError(f"EINVAL: k and v must have the {n} rows of q, or k_starts be given")
+    return dev, (n, hq, w), (nk, hk, w), (
+        q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, v.data_ptr(), vr, vh,
+        BF16 if q.dtype is torch.bfloat16 else F16, n, nk, hq, hk, w, starts.data_ptr(),
+        k_starts.data_ptr(), seqs, 1 if causal else 0, w ** -0.5 if scale is None else scale)
+
+
+def _attend(q, k, v, starts, k_starts, causal, scale, keep):
+    dev, shape, _, args = _attend_args(q, k, v, starts, k_starts, causal, scale)
+
+    def call(st):
+        torch = _T().torch
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        lse = rest = None
+        if keep:  # what the gradients need
+            lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=q.device)
+            rest = torch.empty_like(out)
+        _check(lib().emeans_attend(*args, out.data_ptr(), _ptr(lse), _ptr(rest), st))
+        return out, lse, rest
+
+    return _run(dev, None, call)
+
+
+_attend_function = None
+
+
+def _attend_fn():
+    global _attend_function
+    if _attend_function is None:
+        torch = _T().torch
+
+        class Attend(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, q, k, v, starts, k_starts, causal, scale):
+                out, lse, rest = _attend(q, k, v, starts, k_starts, causal, scale, True)
+                ctx.one = k_starts is starts
+                ctx.save_for_backward(q, k, v, starts, k_starts, out, lse, rest)
+                ctx.args = causal, scale
+                return out
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dout):
+                q, k, v, starts, k_starts, out, lse, rest = ctx.saved_tensors
+                dev, shape, k_shape, args = _attend_args(q, k, v, starts,
+                                                         starts if ctx.one else k_starts, *ctx.args)
+                L = lib()
+
+                def call(st):
+                    g = _aligned(dout)
+                    dq = torch.empty(shape, dtype=q.dtype, device=q.device)
+                    dk, dv = (torch.empty(k_shape, dtype=q.dtype, device=q.device) for _ in range(2))
+                    work = _work(L.emeans_attend_work(shape[0], shape[1]), q.device)
+                    _check(L.emeans_attend_gradient(
+                        *args, out.data_ptr(), lse.data_ptr(), rest.data_ptr(), g.data_ptr(),
+                        g.stride(0), g.stride(1), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                        _ptr(work), st))
+                    return dq, dk, dv
+
+                return *_run(dev, None, call), None, None, None, None
+
+        _attend_function = Attend
+    return _attend_function
+
+
+def attend(q, k, v, starts, *, k_starts=None, causal: bool = True, scale=None, stream=None):
+    """Attention over packed sequences of different lengths: q (n x hq x width), k and v
+    (nk x hk x width; bfloat16 or float16), hk dividing hq; query head h reads key-value
+    head h // (hq // hk). Sequence s is rows starts[s] .. starts[s + 1] (int32, one more
+    than sequences, not decreasing) of q, and of k and v too or, where the keys are more
+    or fewer than the queries, k_starts[s] .. k_starts[s + 1] of these. Returns
+    softmax(scale q k^T) v, n x hq x width of q's type; scale is 1 / sqrt(width) by
+    default, width a multiple of 8 up to 128.
+
+    causal: of lq queries and lk keys of a sequence, query i sees keys j <= i + lk - lq
+    (the last sees them all); otherwise every query sees all. Rows that see no key, and
+    rows outside every sequence, are zeros. What a row does not see does not show in it,
+    a NaN neither. The host reads no lengths, so the call may be captured.
+
+    q, k and v have gradients (once: tangents of the forward mode are refused), sums in
+    one order; a NaN may show anywhere in its sequence's gradients. Rows or heads that
+    do not start at multiples of 16 bytes are copied first."""
+    _device_of(q, "q")
+    if stream is not None:
+        with _T().torch.cuda.stream(stream):
+            return attend(q, k, v, starts, k_starts=k_starts, causal=causal, scale=scale)
+    _no_tangent("attend", q, k, v)
+    if any(t.dim() != 3 for t in (q, k, v)):
+        raise EmeansError("EINVAL: q, k and v must be rows x heads x width")
+    k_starts = starts if k_starts is None else k_starts
+    q, k, v = _aligned(q), _aligned(k), _aligned(v)
+    if _T().torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return _attend_fn().apply(q, k, v, starts, k_starts, causal, scale)
+    return _attend(q, k, v, starts, k_starts, causal, scale, False)[0]
 
 
 def _paged(dev, store, block, what):

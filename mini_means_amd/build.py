@@ -17,7 +17,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libemeans.so")
 SOURCES = ["assign.hip", "assign_bf16.hip", "assign_i8r.hip", "assign_wide.hip", "update.hip",
            "codes.hip", "block_codes.hip", "block_matmul.hip", "norm_rotate.hip",
-           "cache_attend.hip", "cache_evict.hip", "api.hip"]
+           "attend.hip", "cache_attend.hip", "cache_evict.hip", "api.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = os.environ.get("EMEANS_ARCH", "gfx950")

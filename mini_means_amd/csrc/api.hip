@@ -1785,6 +1785,105 @@ int emeans_norm_rotate_gradient(const void* q, int64_t q_row, int64_t q_head, co
   return release(own, st, launched(launch_norm_rotate_back(a, st), "norm rotate gradient"));
 }
 
+namespace {
+
+int check_attend(const Attend& a, int64_t hq, int64_t hk, int64_t width, int64_t seqs,
+                 double scale) {
+  int rc;
+  if (a.dt != EMEANS_BF16 && a.dt != EMEANS_F16)
+    return fail(EMEANS_EDTYPE, "dtype %d not supported (bf16 = 1, fp16 = 4)", a.dt);
+  if ((rc = check_length(a.n, 0, "n")) || (rc = check_length(a.nk, 0, "nk")) ||
+      (rc = check_heads(hq, "hq")) || (rc = check_heads(hk, "hk")) ||
+      (rc = check_count(seqs, "seqs")))
+    return rc;
+  if (hq % hk) return fail(EMEANS_EINVAL, "hq (%lld) must be a multiple of hk (%lld)",
+                           (long long)hq, (long long)hk);
+  if (width < 8 || width > 128 || width % 8)
+    return fail(EMEANS_EINVAL, "width must be a multiple of 8 in [8, 128] (got %lld)",
+                (long long)width);
+  if (!(scale >= -1e30 && scale <= 1e30)) return fail(EMEANS_EINVAL, "scale out of range (%g)", scale);
+  const int64_t strides[] = {a.q_rs, a.q_hs, a.k_rs, a.k_hs, a.v_rs, a.v_hs, a.do_rs, a.do_hs};
+  for (const int64_t s : strides)
+    if (s < 0 || s % 8)
+      return fail(EMEANS_EINVAL, "strides must be multiples of 8, not negative (got %lld)", (long long)s);
+  const void* at[] = {a.q, a.k, a.v, a.dout, a.o, a.rest, a.dq, a.dk, a.dv};
+  for (const void* p : at)
+    if ((uintptr_t)p % 16) return fail(EMEANS_EINVAL, "rows must start at multiples of 16 bytes");
+  return EMEANS_OK;
+}
+
+int check_attend_pointers(const Attend& a) {
+  int rc;
+  if (!a.q || !a.starts || !a.k_starts || !a.o || (a.nk > 0 && (!a.k || !a.v)))
+    return fail(EMEANS_EINVAL, "q, k, v, starts and out must not be NULL");
+  if ((rc = check_device(a.q, "q")) || (a.nk > 0 && ((rc = check_device(a.k, "k")) ||
+                                                     (rc = check_device(a.v, "v")))) ||
+      (rc = check_device(a.starts, "starts")) || (rc = check_device(a.k_starts, "k_starts")) ||
+      (rc = check_device(a.o, "out")))
+    return rc;
+  return EMEANS_OK;
+}
+
+}  // namespace
+
+int emeans_attend(const void* q, int64_t q_row, int64_t q_head, const void* k, int64_t k_row,
+                  int64_t k_head, const void* v, int64_t v_row, int64_t v_head, int32_t dtype,
+                  int64_t n, int64_t nk, int64_t hq, int64_t hk, int64_t width,
+                  const int32_t* starts, const int32_t* k_starts, int64_t seqs, int32_t causal,
+                  double scale, void* out, float* lse, void* rest, void* stream) {
+  g_err.clear();
+  const Attend a{dtype, n, nk, (int)hq, (int)hk, (int)width, causal != 0, (float)scale,
+                 q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, starts, k_starts,
+                 (int)seqs, out, lse, rest};
+  int rc;
+  if ((rc = check_attend(a, hq, hk, width, seqs, scale))) return rc;
+  if (n == 0) return EMEANS_OK;
+  if ((rc = check_attend_pointers(a)) || (lse && (rc = check_device(lse, "lse"))) ||
+      (rest && (rc = check_device(rest, "rest"))))
+    return rc;
+  return launched(launch_attend(a, static_cast<hipStream_t>(stream)), "attend");
+}
+
+int64_t emeans_attend_work(int64_t n, int64_t hq) {
+  if (n < 0 || n > kMaxLength || hq < 1 || hq > 65536) return 0;
+  return (int64_t)attend_work(n, (int)hq);
+}
+
+int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
+                           int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                           int64_t v_head, int32_t dtype, int64_t n, int64_t nk, int64_t hq,
+                           int64_t hk, int64_t width, const int32_t* starts,
+                           const int32_t* k_starts, int64_t seqs, int32_t causal, double scale,
+                           const void* out, const float* lse, const void* rest,
+                           const void* dout, int64_t do_row, int64_t do_head, void* dq,
+                           void* dk, void* dv, void* work, void* stream) {
+  g_err.clear();
+  const Attend a{dtype, n, nk, (int)hq, (int)hk, (int)width, causal != 0, (float)scale,
+                 q, q_row, q_head, k, k_row, k_head, v, v_row, v_head, starts, k_starts,
+                 (int)seqs, const_cast<void*>(out), const_cast<float*>(lse),
+                 const_cast<void*>(rest), dout, do_row, do_head, dq, dk, dv};
+  int rc;
+  if ((rc = check_attend(a, hq, hk, width, seqs, scale))) return rc;
+  if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");
+  if (n == 0 && nk == 0) return EMEANS_OK;
+  if ((n > 0 && (!q || !out || !lse || !rest || !dout || !dq)) || (nk > 0 && (!k || !v || !dk || !dv)) ||
+      !starts || !k_starts)
+    return fail(EMEANS_EINVAL, "inputs, out, lse, rest, dout and gradients must not be NULL");
+  const void* const rows[] = {q, out, lse, rest, dout, dq};
+  const char* const row_names[] = {"q", "out", "lse", "rest", "dout", "dq"};
+  for (int i = 0; n > 0 && i < 6; ++i)
+    if ((rc = check_device(rows[i], row_names[i]))) return rc;
+  const void* const keys[] = {k, v, dk, dv};
+  const char* const key_names[] = {"k", "v", "dk", "dv"};
+  for (int i = 0; nk > 0 && i < 4; ++i)
+    if ((rc = check_device(keys[i], key_names[i]))) return rc;
+  if ((rc = check_device(starts, "starts")) || (rc = check_device(k_starts, "k_starts"))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  void *at, *own;
+  if ((rc = take_work(work, emeans_attend_work(n, hq), st, &at, &own))) return rc;
+  return release(own, st, launched(launch_attend_back(a, at, st), "attend gradient"));
+}
+
 int64_t emeans_cache_attend_work(int64_t seqs, int64_t hq, int64_t hk, int64_t width,
                                  int64_t page_rows, int64_t table_pages, int32_t with_weights) {
   if (seqs < 1 || seqs >= kMaxRows || hk < 1 || hq < hk || hq > 65536 || hq % hk || width < 16 ||

@@ -1,0 +1,779 @@
+// Attention over packed sequences, forward and backward (bf16 and fp16).
+//
+// For a query row i of a sequence (lq queries, lk keys) and the keys j it sees, all of
+// them or (causal) those with j <= i + lk - lq:
+//   s = scale q k^T, o = sum exp(s - m) v / l, m the largest s, l = sum exp(s - m)
+// in one pass over the keys with a running maximum and sum. Backward, with
+// P = exp(s - lse), lse = m + log l, D = rowsum(dO o):
+//   dV = P^T dO, dS = P (dO V^T - D), dQ = scale dS K, dK = scale dS^T Q,
+// as two kernels, one that owns query rows (dQ) and one that owns key rows (dK, dV,
+// summed over the query heads of a group in order): seven products instead of the
+// five that atomic sums of dQ would leave, but the same bits each time.
+//
+// Bound by the matrix unit, beside it by LDS reads and the exponentials. All products
+// are 32 x 32 x 16 MFMAs laid out so that nothing crosses lanes between them: with A
+// the tile's rows and B a wave's own 32 rows (kept in registers), a lane holds 16 of
+// 32 results of one own row, and these are the B operand of the next product when
+// its sum index is counted in the order in which they stand. Its A operand is the
+// tile transposed, which ds_read_b64_tr_b16 reads from the same LDS rows.
+#include <type_traits>
+
+#include "block.hpp"
+#include "kernels.hpp"
+
+namespace emk {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTile = 64;  // rows of a tile in LDS
+constexpr int kZeroGroups = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <bool F16>
+using Half8 = std::conditional_t<F16, f16x8, bf16x8>;
+
+template <bool F16>
+__device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// The place of a row's 16-byte chunks: XOR with a number of the row, so that eight
+// rows read at one chunk, and four rows read at two (transposed reads), cover all
+// banks. Rows of 96 values start half the banks apart already.
+template <int W>
+__device__ __forceinline__ int swizzle(int row) {
+  if constexpr (W == 96)
+    return ((row >> 1) & 1) << 1 | ((row >> 2) & 1);
+  else
+    return (row & 3) << 1 | ((row >> 2) & 1);
+}
+
+// Rows row0 .. row0 + 63 of a head into LDS, past `last` that row again (so that what
+// is masked is a row of this sequence, never another's). Chunks past width are not
+// written: they hold the zeros that the workgroup began with.
+template <int W, int NW>
+__device__ __forceinline__ void load_tile(const uint16_t* base, int64_t rs, int row0, int last,
+                                          int width, uint8_t* lds, int wave, int lane) {
+  constexpr int CPR = W / 8;
+#pragma unroll
+  for (int i0 = 0; i0 < CPR; i0 += NW) {
+    const int i = i0 + wave;
+    if (CPR % NW && i >= CPR) break;
+    const int at = i * 64 + lane, row = at / CPR;
+    const int chunk = (at - row * CPR) ^ swizzle<W>(row);
+    const uint16_t* src = base + min(row0 + row, last) * rs + chunk * 8;
+    if (chunk * 8 < width) lds_load16(src, lds + i * 1024);
+  }
+}
+
+template <int W>
+__device__ __forceinline__ u32x4 row_frag(const uint8_t* lds, int row, int chunk) {
+  return *reinterpret_cast<const u32x4*>(lds + row * (W * 2) + ((chunk ^ swizzle<W>(row)) << 4));
+}
+
+// A operand of the transposed tile: values d0 + lane % 32 of the 16 rows from r0 on, in the
+// order r0 + 4 h + {0..3}, r0 + 8 + 4 h + {0..3} for lane half h.
+template <int W>
+__device__ __forceinline__ u32x4 column_frag(const uint8_t* lds, int r0, int d0, int lane) {
+  const int row = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
+  const int chunk = d0 / 8 + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+  const uint8_t* p = lds + row * (W * 2) + ((chunk ^ swizzle<W>(row)) << 4) + (lane & 1) * 8;
+  typedef __attribute__((address_space(3))) s16x4* at;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(p));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(p + 8 * W * 2));
+  const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+  return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// A wave's own rows as B operands: row `row` of a head (any valid one for lanes past
+// the last), values 16 ks + 8 h + {0..7}; zeros past width.
+template <int W>
+__device__ __forceinline__ void own_frags(const uint16_t* p, int width, int half,
+                                          u32x4 (&f)[W / 16]) {
+#pragma unroll
+  for (int ks = 0; ks < W / 16; ++ks) {
+    const int c = 16 * ks + 8 * half;
+    f[ks] = c < width ? *reinterpret_cast<const u32x4*>(p + c) : u32x4{0u, 0u, 0u, 0u};
+  }
+}
+
+// Results of 8 sum indices, in order, as a B operand.
+template <bool F16>
+__device__ __forceinline__ u32x4 packed(const f32x16& s, int r) {
+  constexpr int OT = F16 ? 4 : 1;
+  return u32x4{pack2<OT>(s[r], s[r + 1]), pack2<OT>(s[r + 2], s[r + 3]),
+               pack2<OT>(s[r + 4], s[r + 5]), pack2<OT>(s[r + 6], s[r + 7])};
+}
+
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// acc (values 8 (r / 4) + 4 h + r % 4 of 32, of row lane % 32) times f to 16-bit rows:
+// the lane halves trade their runs of four, so that a lane stores 16 bytes. rest: what
+// the rounding took away, rounded to 16 bits itself, or NULL.
+template <bool F16, int W>
+__device__ __forceinline__ void store_rows(const f32x16 (&acc)[W / 32], float f, uint16_t* row,
+                                           uint16_t* rest, int width, int half, bool on) {
+  constexpr int OT = F16 ? 4 : 1;
+  auto put = [&](uint16_t* to, int c, const uint32_t(&a)[2], const uint32_t(&b)[2]) {
+    const auto x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    if (on && c < width) *reinterpret_cast<u32x4*>(to + c) = u32x4{x[0], y[0], x[1], y[1]};
+  };
+  auto left = [&](float x, float y, uint32_t w) {
+    return pack2<OT>(x - half_to_f32((uint16_t)w, F16), y - half_to_f32((uint16_t)(w >> 16), F16));
+  };
+#pragma unroll
+  for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+      uint32_t a[2], b[2];
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = acc[dt][4 * g + i] * f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = pack2<OT>(x[2 * i], x[2 * i + 1]);
+        b[i] = pack2<OT>(x[4 + 2 * i], x[5 + 2 * i]);
+      }
+      const int c = dt * 32 + (g + half) * 8;
+      put(row, c, a, b);
+      if (rest) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          a[i] = left(x[2 * i], x[2 * i + 1], a[i]);
+          b[i] = left(x[4 + 2 * i], x[5 + 2 * i], b[i]);
+        }
+        put(rest, c, a, b);
+      }
+    }
+}
+
+// Rows of a sequence in the packed order, cut to what the tensors hold whatever
+// `starts` says.
+struct Span {
+  int first, len;
+};
+
+__device__ __forceinline__ Span span_of(const int32_t* starts, int s, int64_t n) {
+  const int a = max(0, min(starts[s], (int)n)), b = max(a, min(starts[s + 1], (int)n));
+  return {a, b - a};
+}
+
+// Tiles of `rows` rows: sequence s has those from starts[s] / rows + s on, enough for
+// any alignment, so that a tile finds its sequence without the host knowing lengths.
+struct Place {
+  int seq, row0;  // first row of the tile in its sequence
+};
+
+__device__ __forceinline__ Place place_of(const int32_t* starts, int seqs, int64_t n, int rows,
+                                          int64_t tile) {
+  int lo = 0, hi = seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)(max(0, min(starts[mid], (int)n)) / rows) + mid <= tile)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int64_t j = tile - (max(0, min(starts[lo], (int)n)) / rows + lo);
+  return {lo, j < 0 || j * rows > 0x7FFFFFFF ? 0x7FFFFFFF : (int)(j * rows)};
+}
+
+// Rows of out (rows x d) that no sequence has become zeros.
+__device__ __forceinline__ void zero_outside(const int32_t* starts, int seqs, int64_t n, int64_t d,
+                                             uint16_t* out, int64_t wg, int threads) {
+  const int64_t first = max(0, min(starts[0], (int)n)), last = max(0, min(starts[seqs], (int)n));
+  const int64_t step = (int64_t)kZeroGroups * threads * 8;
+  for (int64_t i = (wg * threads + threadIdx.x) * 8; i < first * d; i += step)
+    *reinterpret_cast<u32x4*>(out + i) = u32x4{0u, 0u, 0u, 0u};
+  for (int64_t i = last * d + (wg * threads + threadIdx.x) * 8; i < n * d; i += step)
+    *reinterpret_cast<u32x4*>(out + i) = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Workgroup b as (tile, head): the heads of a tile follow each other, and where eight
+// divides them, those of one XCD (every eighth workgroup) are neighbours, which share
+// a key-value head's rows in its L2.
+__device__ __forceinline__ int head_of(int64_t b, int heads) {
+  const int i = (int)(b % heads);
+  return heads % 8 ? i : (i % 8) * (heads / 8) + i / 8;
+}
+
+template <int W>
+__device__ __forceinline__ void clear_lds(uint8_t* lds, int bytes, int width, int threads) {
+  if (width == W) return;
+  for (int i = threadIdx.x * 16; i < bytes; i += threads * 16)
+    *reinterpret_cast<u32x4*>(lds + i) = u32x4{0u, 0u, 0u, 0u};
+  __syncthreads();
+}
+
+// V rows that a query does not see must not show in it, but 0 x infinity is NaN. A
+// tile that some rows see in part is therefore, where a first pass gave no numbers,
+// done with its infinities and NaN taken out, and these are counted beside it as
+// products of their own: 1 for each +infinity that a row sees, 2^7 for each
+// -infinity, 2^14 for each NaN (64 rows at most, so the counts do not mix).
+template <bool F16>
+__device__ __forceinline__ void split_odd(u32x4 v, u32x4& numbers, u32x4& odd) {
+  constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
+  constexpr uint32_t kPlus = F16 ? 0x3C00u : 0x3F80u, kMinus = F16 ? 0x5800u : 0x4300u,
+                     kNan = F16 ? 0x7400u : 0x4680u;  // 1, 2^7, 2^14
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t n = 0, o = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t x = v[i] >> (16 * h) & 0xFFFFu;
+      const bool bad = (x & E) == E;
+      const uint32_t kind = (x & 0x7FFFu) != E ? kNan : x >> 15 ? kMinus : kPlus;
+      n |= (bad ? 0u : x) << (16 * h);
+      o |= (bad ? kind : 0u) << (16 * h);
+    }
+    numbers[i] = n;
+    odd[i] = o;
+  }
+}
+
+__device__ __forceinline__ float odd_value(float counts) {
+  if (counts == 0.0f) return 0.0f;
+  if (counts >= 16384.0f) return __uint_as_float(0x7FC00000u);
+  const bool minus = counts >= 128.0f, plus = counts - 128.0f * floorf(counts * (1.0f / 128.0f)) > 0.0f;
+  return plus && minus ? __uint_as_float(0x7FC00000u) : plus ? INFINITY : -INFINITY;
+}
+
+// A workgroup owns NW waves x NQ x 32 query rows of one head and goes over its keys
+// in tiles of 64, double buffered, the next tile's direct loads beside this tile's
+// products; one barrier per tile.
+template <bool F16, int W, int NW, int NQ>
+__global__ __launch_bounds__(NW * 64, NQ == 1 ? 2 : 1) void attend_kernel(Attend a, int64_t wg0,
+                                                                          int64_t tiles) {
+  constexpr int ROWS = NW * NQ * 32;
+  constexpr int TB = kTile * W * 2;  // bytes of a tile
+  __shared__ __align__(1024) uint8_t lds[4 * TB];
+  const int64_t b = wg0 + blockIdx.x;
+  if (b >= tiles * a.hq) {
+    zero_outside(a.starts, a.seqs, a.n, (int64_t)a.hq * a.width, static_cast<uint16_t*>(a.o),
+                 b - tiles * a.hq, NW * 64);
+    return;
+  }
+  // causal: later rows see more keys, so the longest workgroups come first
+  const Place at = place_of(a.starts, a.seqs, a.n, ROWS, tiles - 1 - b / a.hq);
+  const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
+  if (at.row0 >= sq.len) return;
+  const int head = head_of(b, a.hq), kvh = head / (a.hq / a.hk);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int shift = sk.len - sq.len;
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sk.first * a.k_rs + kvh * a.k_hs;
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
+  clear_lds<W>(lds, 4 * TB, a.width, NW * 64);
+
+  int row[NQ], sees[NQ];  // a lane's query row, the keys it sees
+  u32x4 qf[NQ][W / 16];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    row[q] = at.row0 + (wave * NQ + q) * 32 + (lane & 31);
+    const int r = min(row[q], sq.len - 1);
+    sees[q] = max(a.causal ? min(r + shift + 1, sk.len) : sk.len, 0);
+    own_frags<W>(static_cast<const uint16_t*>(a.q) + (sq.first + r) * a.q_rs + head * a.q_hs,
+                 a.width, half, qf[q]);
+    // scores times a positive number keep their order, and -infinity (masked) its value
+    if (a.scale <= 0.0f)
+#pragma unroll
+      for (int ks = 0; ks < W / 16; ++ks)
+        qf[q][ks] = a.scale == 0.0f ? u32x4{0u, 0u, 0u, 0u} : qf[q][ks] ^ 0x80008000u;
+  }
+  const float c2 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
+  const int end_row = min(at.row0 + ROWS, sq.len);  // past the last
+  const int keys = max(a.causal ? min(end_row + shift, sk.len) : sk.len, 0);
+  const int n_tiles = (keys + kTile - 1) / kTile;
+
+  f32x16 acc[NQ][W / 32];
+  float m[NQ], l[NQ];
+  for (int careful = 0;; careful = 1) {
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      m[q] = -INFINITY;
+      l[q] = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[q][dt][r] = 0.0f;
+    }
+    if (n_tiles > 0) {
+      load_tile<W, NW>(kp, a.k_rs, 0, sk.len - 1, a.width, lds, wave, lane);
+      load_tile<W, NW>(vp, a.v_rs, 0, sk.len - 1, a.width, lds + TB, wave, lane);
+    }
+    for (int j = 0; j < n_tiles; ++j) {
+      EMK_WAIT_VMCNT(0);
+      lds_barrier();  // tile j is whole, and tile j - 1 has been read
+      uint8_t* now = lds + (j & 1) * 2 * TB;
+      if (j + 1 < n_tiles) {
+        uint8_t* next = lds + ((j + 1) & 1) * 2 * TB;
+        load_tile<W, NW>(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, a.width, next, wave, lane);
+        load_tile<W, NW>(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, a.width, next + TB, wave, lane);
+      }
+      const int k0 = j * kTile;
+      // the wave's first row sees least, its last most
+      const int row0 = at.row0 + wave * NQ * 32;
+      const int most = a.causal ? min(row0 + NQ * 32 + shift, sk.len) : sk.len;
+      if (k0 >= most || row0 >= sq.len) continue;
+      const bool part = k0 + kTile > (a.causal ? min(row0 + shift + 1, sk.len) : sk.len);
+      f32x16 s[NQ][2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) s[q][kt][r] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < W / 16; ++ks) {
+          const u32x4 kf = row_frag<W>(now, kt * 32 + (lane & 31), 2 * ks + half);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) s[q][kt] = product<F16>(kf, qf[q][ks], s[q][kt]);
+        }
+      }
+      u32x4 pf[NQ][4];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (part) {
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees[q]) s[q][kt][r] = -INFINITY;
+        }
+        float top = s[q][0][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[q][0][r]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[q][1][r]);
+        top = half_max(top);
+        // a row's maximum is followed only when it grows by a factor of 2^6 of the
+        // weights: what matters is that they stay in range
+        const bool up = (top - m[q]) * c2 > 6.0f;
+        if (__any(up)) {
+          const float f = up ? __builtin_amdgcn_exp2f((m[q] - top) * c2) : 1.0f;
+          m[q] = up ? top : m[q];
+          l[q] *= f;
+#pragma unroll
+          for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[q][dt][r] *= f;
+        }
+        const float ref = (m[q] == -INFINITY ? 0.0f : m[q]) * c2;
+        float sum = 0.0f;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            s[q][kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q][kt][r], c2, -ref));
+            sum += s[q][kt][r];
+          }
+        l[q] += sum;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) pf[q][t] = packed<F16>(s[q][t >> 1], 8 * (t & 1));
+      }
+      if (!(careful && part)) {
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const u32x4 vf = column_frag<W>(now + TB, 16 * t, 32 * dt, lane);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) acc[q][dt] = product<F16>(vf, pf[q][t], acc[q][dt]);
+          }
+      } else {
+        constexpr uint32_t kOne = F16 ? 0x3C00u : 0x3F80u;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          u32x4 seen[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = k0 + 16 * t + 4 * half + (i >> 1) * 8 + (i & 1) * 2;
+              seen[t][i] = (k < sees[q] ? kOne : 0u) | (k + 1 < sees[q] ? kOne << 16 : 0u);
+            }
+#pragma unroll
+          for (int dt = 0; dt < W / 32; ++dt) {
+            f32x16 counts = {};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              u32x4 numbers, odd;
+              split_odd<F16>(column_frag<W>(now + TB, 16 * t, 32 * dt, lane), numbers, odd);
+              acc[q][dt] = product<F16>(numbers, pf[q][t], acc[q][dt]);
+              counts = product<F16>(odd, seen[t], counts);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[q][dt][r] += odd_value(counts[r]);
+          }
+        }
+      }
+    }
+    if (careful) break;
+    // no numbers though the scores were: look again, rows that see part of a tile apart
+    bool odd = false;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float z = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z += acc[q][dt][r] * 0.0f;
+      odd |= z != 0.0f && l[q] == l[q];
+    }
+    if (!__syncthreads_or(odd)) break;
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const float sum = half_sum(l[q]);
+    const bool on = row[q] < sq.len;
+    if (a.lse && half == 0 && on)
+      a.lse[(int64_t)head * a.n + sq.first + row[q]] =
+          sum == 0.0f ? INFINITY
+                      : (m[q] == -INFINITY ? 0.0f : m[q] * c2) + __builtin_amdgcn_logf(sum);
+    const int64_t to = ((int64_t)(sq.first + min(row[q], sq.len - 1)) * a.hq + head) * a.width;
+    store_rows<F16, W>(acc[q], sum == 0.0f ? 0.0f : 1.0f / sum, static_cast<uint16_t*>(a.o) + to,
+                       a.rest ? static_cast<uint16_t*>(a.rest) + to : nullptr, a.width, half, on);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+// ---------------------------------------------------------------------------
+
+// The largest |dO| and |V| of fp16 data, one pair per workgroup.
+constexpr int kTops = 256;
+
+__global__ __launch_bounds__(256) void tops_kernel(Attend a) {
+  __shared__ float tmp[4];
+  float top[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const uint16_t* p = static_cast<const uint16_t*>(s ? a.v : a.dout);
+    const int64_t rs = s ? a.v_rs : a.do_rs, hs = s ? a.v_hs : a.do_hs;
+    const int heads = s ? a.hk : a.hq, chunks = a.width / 8;
+    const int64_t rows = s ? a.nk : a.n;
+    const int per = heads * chunks;
+    for (int64_t r = blockIdx.x; r < rows; r += kTops)
+      for (int i = threadIdx.x; i < per; i += 256) {
+        const int h = i / chunks, c = i - h * chunks;
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p + r * rs + h * hs + c * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = fabsf(f16_to_f32((uint16_t)w[e])), y = fabsf(f16_to_f32((uint16_t)(w[e] >> 16)));
+          if (x < INFINITY) top[s] = fmaxf(top[s], x);
+          if (y < INFINITY) top[s] = fmaxf(top[s], y);
+        }
+      }
+    top[s] = wave_max(top[s]);
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top[s];
+    __syncthreads();
+    if (threadIdx.x == 0)
+      a.tops[s * kTops + blockIdx.x] = fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3]));
+    __syncthreads();
+  }
+}
+
+// fp16 holds 2^-24 to 65504, while dS may be anything: it is kept times a power of two
+// that leaves its bound, |dO V^T - D| <= 2 width max|dO| max|V|, at most 2^15. (The same
+// number in every workgroup: a maximum has no order.)
+__device__ __forceinline__ float grad_factor(const Attend& a) {
+  float x = 0.0f, y = 0.0f;
+  for (int i = threadIdx.x & 63; i < kTops; i += 64) {
+    x = fmaxf(x, a.tops[i]);
+    y = fmaxf(y, a.tops[kTops + i]);
+  }
+  const float bound = wave_max(x) * wave_max(y) * (2.0f * (float)a.width);
+  if (!(bound > 0.0f)) return 1.0f;
+  return __uint_as_float((uint32_t)(min(max(127 + 14 - (int)(__float_as_uint(bound) >> 23) + 127, 27), 227)) << 23);
+}
+
+// dQ: a workgroup owns 128 query rows of a head; P^T and dS^T of a tile of 64 keys have
+// a lane's query row as column. D of the rows is made here and left for the other
+// kernel.
+template <bool F16, int W>
+__global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
+  constexpr int NW = 4, ROWS = NW * 32, TB = kTile * W * 2;
+  __shared__ __align__(1024) uint8_t lds[4 * TB];
+  const int64_t b = wg0 + blockIdx.x;
+  if (b >= tiles * a.hq) {
+    zero_outside(a.starts, a.seqs, a.n, (int64_t)a.hq * a.width, static_cast<uint16_t*>(a.dq),
+                 b - tiles * a.hq, NW * 64);
+    return;
+  }
+  const Place at = place_of(a.starts, a.seqs, a.n, ROWS, tiles - 1 - b / a.hq);
+  const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
+  if (at.row0 >= sq.len) return;
+  const int head = head_of(b, a.hq), kvh = head / (a.hq / a.hk);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int shift = sk.len - sq.len;
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sk.first * a.k_rs + kvh * a.k_hs;
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
+  clear_lds<W>(lds, 4 * TB, a.width, NW * 64);
+
+  const int row = at.row0 + wave * 32 + (lane & 31), r0 = min(row, sq.len - 1);
+  const int sees = max(a.causal ? min(r0 + shift + 1, sk.len) : sk.len, 0);
+  const int64_t full = sq.first + r0;
+  u32x4 qf[W / 16], gf[W / 16];
+  own_frags<W>(static_cast<const uint16_t*>(a.q) + full * a.q_rs + head * a.q_hs, a.width, half, qf);
+  own_frags<W>(static_cast<const uint16_t*>(a.dout) + full * a.do_rs + head * a.do_hs, a.width, half, gf);
+  const float factor = F16 ? grad_factor(a) : 1.0f;
+  float d = 0.0f;
+  {
+    // o as it was before its rounding to 16 bits: the rounding would stand in D, which all
+    // of a row's dS share, and grow the error of dQ and dK by 8% (measured on causal rows)
+    u32x4 of[W / 16], rf[W / 16];
+    const int64_t o = (full * a.hq + head) * a.width;
+    own_frags<W>(static_cast<const uint16_t*>(a.o) + o, a.width, half, of);
+    own_frags<W>(static_cast<const uint16_t*>(a.rest) + o, a.width, half, rf);
+    auto number = [](const u32x4& w, int i) {
+      return half_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))), F16);
+    };
+#pragma unroll
+    for (int ks = 0; ks < W / 16; ++ks)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d += (number(of[ks], i) + number(rf[ks], i)) * number(gf[ks], i);
+  }
+  d = half_sum(d) * factor;
+  const float lse = a.lse[(int64_t)head * a.n + full];
+  if (half == 0 && row < sq.len) a.delta[(int64_t)head * a.n + full] = d;
+  const float c2 = a.scale * kLog2e;
+  const int keys = max(a.causal ? min(min(at.row0 + ROWS, sq.len) + shift, sk.len) : sk.len, 0);
+  const int n_tiles = (keys + kTile - 1) / kTile;
+  f32x16 acc[W / 32];
+#pragma unroll
+  for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[dt][r] = 0.0f;
+  if (n_tiles > 0) {
+    load_tile<W, NW>(kp, a.k_rs, 0, sk.len - 1, a.width, lds, wave, lane);
+    load_tile<W, NW>(vp, a.v_rs, 0, sk.len - 1, a.width, lds + TB, wave, lane);
+  }
+  for (int j = 0; j < n_tiles; ++j) {
+    EMK_WAIT_VMCNT(0);
+    lds_barrier();
+    uint8_t* now = lds + (j & 1) * 2 * TB;
+    if (j + 1 < n_tiles) {
+      uint8_t* next = lds + ((j + 1) & 1) * 2 * TB;
+      load_tile<W, NW>(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, a.width, next, wave, lane);
+      load_tile<W, NW>(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, a.width, next + TB, wave, lane);
+    }
+    const int k0 = j * kTile, w0 = at.row0 + wave * 32;
+    if (k0 >= (a.causal ? min(w0 + 32 + shift, sk.len) : sk.len) || w0 >= sq.len) continue;
+    const bool part = k0 + kTile > (a.causal ? min(w0 + shift + 1, sk.len) : sk.len);
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      f32x16 s = {}, dp = {};
+#pragma unroll
+      for (int ks = 0; ks < W / 16; ++ks) {
+        s = product<F16>(row_frag<W>(now, kt * 32 + (lane & 31), 2 * ks + half), qf[ks], s);
+        dp = product<F16>(row_frag<W>(now + TB, kt * 32 + (lane & 31), 2 * ks + half), gf[ks], dp);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -lse));
+        dp[r] = p * __builtin_fmaf(dp[r], factor, -d);
+        if (part && k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) dp[r] = 0.0f;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const u32x4 ds = packed<F16>(dp, 8 * t);
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt)
+          acc[dt] = product<F16>(column_frag<W>(now, kt * 32 + 16 * t, 32 * dt, lane), ds, acc[dt]);
+      }
+    }
+  }
+  store_rows<F16, W>(acc, a.scale / factor,
+                     static_cast<uint16_t*>(a.dq) + (full * a.hq + head) * a.width, nullptr, a.width,
+                     half, row < sq.len);
+}
+
+// dK and dV: a workgroup owns 128 key rows of a key-value head and goes over the
+// queries that see them, head by head of the group, in tiles of 64; P and dS of a tile
+// have a lane's key row as column.
+template <bool F16, int W>
+__global__ __launch_bounds__(256, 1) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
+  constexpr int NW = 4, ROWS = NW * 32, TB = kTile * W * 2;
+  constexpr float kLift = F16 ? 14.0f : 0.0f;  // fp16: P times 2^14, which stays in range
+  __shared__ __align__(1024) uint8_t lds[4 * TB];
+  __shared__ float lse[2][kTile], delta[2][kTile];
+  const int64_t b = wg0 + blockIdx.x;
+  if (b >= tiles * a.hk) {
+    zero_outside(a.k_starts, a.seqs, a.nk, (int64_t)a.hk * a.width, static_cast<uint16_t*>(a.dk),
+                 b - tiles * a.hk, NW * 64);
+    zero_outside(a.k_starts, a.seqs, a.nk, (int64_t)a.hk * a.width, static_cast<uint16_t*>(a.dv),
+                 b - tiles * a.hk, NW * 64);
+    return;
+  }
+  const Place at = place_of(a.k_starts, a.seqs, a.nk, ROWS, b / a.hk);
+  const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
+  if (at.row0 >= sk.len) return;
+  const int kvh = head_of(b, a.hk), group = a.hq / a.hk;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int shift = sk.len - sq.len;
+  clear_lds<W>(lds, 4 * TB, a.width, NW * 64);
+
+  const int key = at.row0 + wave * 32 + (lane & 31);
+  const int64_t full = sk.first + min(key, sk.len - 1);
+  u32x4 kf[W / 16], vf[W / 16];
+  own_frags<W>(static_cast<const uint16_t*>(a.k) + full * a.k_rs + kvh * a.k_hs, a.width, half, kf);
+  own_frags<W>(static_cast<const uint16_t*>(a.v) + full * a.v_rs + kvh * a.v_hs, a.width, half, vf);
+  const float factor = F16 ? grad_factor(a) : 1.0f;
+  const float lifted = factor * (F16 ? 0x1p-14f : 1.0f), unlift = F16 ? 0x1p-14f : 1.0f;
+  const float c2 = a.scale * kLog2e;
+  // query rows that see the workgroup's first key
+  const int first = a.causal ? max(at.row0 - shift, 0) / kTile * kTile : 0;
+  const int per = sq.len > first ? (sq.len - first + kTile - 1) / kTile : 0;
+  const int n_tiles = per * group;
+  f32x16 dk[W / 32], dv[W / 32];
+#pragma unroll
+  for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.0f;
+  auto fetch = [&](int j) {
+    const int head = kvh * group + j / per, q0 = first + j % per * kTile;
+    uint8_t* to = lds + (j & 1) * 2 * TB;
+    load_tile<W, NW>(static_cast<const uint16_t*>(a.q) + sq.first * a.q_rs + head * a.q_hs, a.q_rs,
+                     q0, sq.len - 1, a.width, to, wave, lane);
+    load_tile<W, NW>(static_cast<const uint16_t*>(a.dout) + sq.first * a.do_rs + head * a.do_hs,
+                     a.do_rs, q0, sq.len - 1, a.width, to + TB, wave, lane);
+    if (wave < 2) {
+      const float* from = (wave ? a.delta : a.lse) + (int64_t)head * a.n + sq.first;
+      lds_load4(from + min(q0 + lane, sq.len - 1), wave ? &delta[j & 1][0] : &lse[j & 1][0]);
+    }
+  };
+  if (n_tiles > 0) fetch(0);
+  for (int j = 0; j < n_tiles; ++j) {
+    EMK_WAIT_VMCNT(0);
+    lds_barrier();
+    if (j + 1 < n_tiles) fetch(j + 1);
+    const uint8_t* now = lds + (j & 1) * 2 * TB;
+    const int q0 = first + j % per * kTile, w0 = at.row0 + wave * 32;
+    if (w0 >= sk.len) continue;
+    // rows q0 + 63 - shift.. see: none of the wave's keys before its first
+    if (a.causal && q0 + kTile - 1 + shift < w0) continue;
+    const bool part = q0 + kTile > sq.len || (a.causal && q0 + shift < w0 + 31);
+#pragma unroll
+    for (int qt = 0; qt < 2; ++qt) {
+      f32x16 s = {}, dp = {};
+#pragma unroll
+      for (int ks = 0; ks < W / 16; ++ks) {
+        s = product<F16>(row_frag<W>(now, qt * 32 + (lane & 31), 2 * ks + half), kf[ks], s);
+        dp = product<F16>(row_frag<W>(now + TB, qt * 32 + (lane & 31), 2 * ks + half), vf[ks], dp);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int r0 = qt * 32 + 8 * g + 4 * half;
+        const f32x4 e = *reinterpret_cast<const f32x4*>(&lse[j & 1][r0]);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&delta[j & 1][r0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * g + i, q = q0 + r0 + i;
+          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, kLift - e[i]));
+          float ds = p * __builtin_fmaf(dp[r], lifted, -d[i] * unlift);
+          if (part && (q >= sq.len || (a.causal && q + shift < key))) p = ds = 0.0f;
+          s[r] = p;
+          dp[r] = ds;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const u32x4 p = packed<F16>(s, 8 * t), ds = packed<F16>(dp, 8 * t);
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt) {
+          dv[dt] = product<F16>(column_frag<W>(now + TB, qt * 32 + 16 * t, 32 * dt, lane), p, dv[dt]);
+          dk[dt] = product<F16>(column_frag<W>(now, qt * 32 + 16 * t, 32 * dt, lane), ds, dk[dt]);
+        }
+      }
+    }
+  }
+  const int64_t to = (full * a.hk + kvh) * a.width;
+  store_rows<F16, W>(dk, a.scale / factor, static_cast<uint16_t*>(a.dk) + to, nullptr, a.width,
+                     half, key < sk.len);
+  store_rows<F16, W>(dv, unlift, static_cast<uint16_t*>(a.dv) + to, nullptr, a.width, half,
+                     key < sk.len);
+}
+
+template <typename GO>
+hipError_t in_launches(int64_t wgs, GO go) {
+  for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
+    go(wg0, (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <bool F16, int W>
+hipError_t forward_t(const Attend& a, hipStream_t st) {
+  constexpr int NW = 4, NQ = 1;
+  const int64_t tiles = a.n / (NW * NQ * 32) + a.seqs;
+  return in_launches(tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
+    attend_kernel<F16, W, NW, NQ><<<grid, NW * 64, 0, st>>>(a, wg0, tiles);
+  });
+}
+
+template <bool F16, int W>
+hipError_t backward_t(const Attend& a, hipStream_t st) {
+  if (F16) {
+    tops_kernel<<<kTops, 256, 0, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t q_tiles = a.n / 128 + a.seqs, k_tiles = a.nk / 128 + a.seqs;
+  const hipError_t e = in_launches(q_tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
+    query_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, q_tiles);
+  });
+  if (e != hipSuccess) return e;
+  return in_launches(k_tiles * a.hk + kZeroGroups, [&](int64_t wg0, unsigned grid) {
+    key_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, k_tiles);
+  });
+}
+
+template <typename GO>
+hipError_t by_type(const Attend& a, GO go) {
+  auto width = [&](auto f16) {
+    if (a.width <= 64) return go(f16, std::integral_constant<int, 64>());
+    if (a.width <= 96) return go(f16, std::integral_constant<int, 96>());
+    return go(f16, std::integral_constant<int, 128>());
+  };
+  return a.dt == 4 ? width(std::true_type()) : width(std::false_type());
+}
+
+}  // namespace
+
+size_t attend_work(int64_t n, int hq) { return (size_t)n * hq * 4 + 2 * kTops * 4; }
+
+hipError_t launch_attend(const Attend& a, hipStream_t st) {
+  return by_type(a, [&](auto f16, auto w) {
+    return forward_t<decltype(f16)::value, decltype(w)::value>(a, st);
+  });
+}
+
+hipError_t launch_attend_back(Attend a, void* work, hipStream_t st) {
+  a.tops = static_cast<float*>(work);
+  a.delta = a.tops + 2 * kTops;
+  return by_type(a, [&](auto f16, auto w) {
+    return backward_t<decltype(f16)::value, decltype(w)::value>(a, st);
+  });
+}
+
+}  // namespace emk

@@ -421,4 +421,43 @@ struct CacheEvict {
 size_t cache_evict_work(int seqs, int keep);
 hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Attention over packed sequences (attend.hip): q n x hq x width, k and v nk x hk x
+// width of type dt (1 bf16, 4 fp16), rows and heads at multiples of 16 bytes;
+// sequence s is rows starts[s] .. starts[s + 1] of q and k_starts of k and v (cut to
+// the tensors). Results and gradients are contiguous; their rows outside every
+// sequence become zeros (not those of rest). lse (hq x n, in units of log 2, infinity for
+// rows that see no key) may be NULL in the forward pass.
+// ---------------------------------------------------------------------------
+struct Attend {
+  int dt;
+  int64_t n, nk;
+  int hq, hk, width;
+  bool causal;
+  float scale;
+  const void* q;
+  int64_t q_rs, q_hs;
+  const void* k;
+  int64_t k_rs, k_hs;
+  const void* v;
+  int64_t v_rs, v_hs;
+  const int32_t* starts;
+  const int32_t* k_starts;
+  int seqs;
+  void* o;
+  float* lse;
+  void* rest;  // as o: what its rounding took away, or NULL in the forward pass
+  // backward
+  const void* dout;
+  int64_t do_rs, do_hs;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* tops;   // set by launch_attend_back
+  float* delta;
+};
+size_t attend_work(int64_t n, int hq);
+hipError_t launch_attend(const Attend& a, hipStream_t st);
+hipError_t launch_attend_back(Attend a, void* work, hipStream_t st);
+
 }  // namespace emk

@@ -101,3 +101,55 @@ def evict(weights, length, keep, recent):
     w = np.where(np.isnan(weights), -np.inf, weights)
     old = sorted(range(length - recent), key=lambda p: (-w[p], p))[:keep - recent]
     return sorted(old) + list(range(length - recent, length))
+
+
+def seen(lq, lk, causal):
+    return np.arange(lk) <= np.arange(lq)[:, None] + lk - lq if causal else np.ones((lq, lk), bool)
+
+
+def attend(q, k, v, scale, causal, dtype):
+    """One head of one sequence (rows x w each): result, what it may be off by, and what it
+    may be off by before its rounding."""
+    w, lk = q.shape[1], len(k)
+    mask = seen(len(q), lk, causal)
+    p = softmax(np.where(mask, q @ k.T * scale, -np.inf))
+    rel = p_error(q, k, scale, mask, w)
+    out = p @ v
+    inner = (p * (rel + HALF_ULP[dtype] * 1.01)) @ np.abs(v)
+    return out, inner + HALF_ULP[dtype] * 1.01 * np.abs(out) + TINY[dtype], inner
+
+
+def p_error(q, k, scale, mask, w):
+    """Relative error of the softmax weights of each row: that of its scores (w products and
+    additions) twice, once by the sum, and that of the sum of its weights."""
+    if not mask.shape[1]:
+        return np.zeros((len(q), 1))
+    d = np.where(mask, np.abs(scale) * (np.abs(q) @ np.abs(k).T), 0.0).max(1, keepdims=True) * ((w + 8) * SUM_ULP)
+    return 2.1 * d + (mask.shape[1] + 24) * SUM_ULP
+
+
+def attend_grad(q, k, v, do, scale, causal, dtype, top=None):
+    """One head of one sequence: (dq, dk, dv) and what each may be off by. top: the largest
+    |dO| and |V| of the call, for fp16's weights' gradients: they are kept times a
+    power of two that leaves 2 w top at least 2^14 of fp16's range, in steps of 2^-24."""
+    w = q.shape[1]
+    mask = seen(len(q), len(k), causal)
+    p = softmax(np.where(mask, q @ k.T * scale, -np.inf))
+    rel = p_error(q, k, scale, mask, w)
+    out = p @ v
+    dp, d = do @ v.T, (do * out).sum(1, keepdims=True)
+    ds = p * (dp - d)
+    dq, dk, dv = scale * ds @ k, scale * ds.T @ q, p.T @ do
+    half = HALF_ULP[dtype] * 1.01
+    # O stands in D as it was before its rounding to 16 bits, with 16 bits more or less
+    o_off = (p * (rel + half)) @ np.abs(v) + half * half * np.abs(out) + TINY[dtype]
+    d_off = (np.abs(do) * o_off).sum(1, keepdims=True) + (w + 8) * SUM_ULP * (np.abs(do) * np.abs(out)).sum(1, keepdims=True)
+    dp_off = (w + 8) * SUM_ULP * (np.abs(do) @ np.abs(v).T)
+    steps = max(len(q), len(k)) + 16
+    off = p * (dp_off + d_off) + np.abs(ds) * (rel + half + steps * SUM_ULP) + 4 * SUM_ULP * p * (np.abs(dp) + np.abs(d))
+    pv_off = p * (rel + half + steps * SUM_ULP)
+    if dtype == "f16":
+        off = off + mask * 2.0 ** -24 * 2 * w * (top or 0.0) / 2.0 ** 14
+        pv_off = pv_off + mask * 2.0 ** -24 * 2.0 ** -14
+    tols = (abs(scale) * off @ np.abs(k), abs(scale) * off.T @ np.abs(q), pv_off.T @ np.abs(do))
+    return (dq, dk, dv), tols

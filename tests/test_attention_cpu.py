@@ -155,3 +155,73 @@ def test_binding_refuses_cpu_tensors():
         mm.rotary_freqs(12)
     f = mm.rotary_freqs(64, 500.0, device="cpu").numpy()
     assert np.allclose(f, 500.0 ** (-2 * np.arange(32) / 64), rtol=1e-14, atol=0)
+
+
+# ---- packed sequences ----------------------------------------------------------
+
+def test_attention_gradients_are_differences():
+    rng = np.random.default_rng(3)
+    for lq, lk, causal in ((5, 5, True), (3, 6, True), (6, 3, True), (4, 5, False)):
+        x = [rng.normal(size=(n, 8)) for n in (lq, lk, lk)]
+        do = rng.normal(size=(lq, 8))
+        grads, _ = ref.attend_grad(*x, do, 0.4, causal, "bf16")
+        for i, t in enumerate(x):
+            for j in np.ndindex(*t.shape):
+                ends = []
+                for e in (1e-5, -1e-5):
+                    y = [a.copy() for a in x]
+                    y[i][j] += e
+                    ends.append((ref.attend(*y, 0.4, causal, "bf16")[0] * do).sum())
+                assert abs((ends[0] - ends[1]) / 2e-5 - grads[i][j]) < 1e-7
+
+
+def test_attention_of_one_token_is_the_last_row_of_causal_attention():
+    rng = np.random.default_rng(4)
+    q, k, v = (rng.normal(size=(7, 16)) for _ in range(3))
+    full = ref.attend(q, k, v, 0.25, True, "bf16")[0]
+    one = ref.decode(q[6:7], k[:, None], v[:, None], 0.25, "bf16")[0]
+    assert np.allclose(full[6], one[0], atol=1e-14)
+    assert not ref.attend(q, k[:3], v[:3], 0.25, True, "bf16")[0][:4].any()      # no key seen
+
+
+def _packed(L, **kw):
+    a = dict(q=FAKE, qr=256, qh=64, k=FAKE, kr=128, kh=64, v=FAKE, vr=128, vh=64, dt=1, n=10, nk=10, hq=4, hk=2,
+             w=64, starts=FAKE, ks=FAKE, seqs=2, causal=1, scale=0.1, out=FAKE, lse=None, rest=None)
+    a.update(kw)
+    return L.emeans_attend(*a.values(), None)
+
+
+def _packed_back(L, **kw):
+    a = dict(q=FAKE, qr=256, qh=64, k=FAKE, kr=128, kh=64, v=FAKE, vr=128, vh=64, dt=1, n=10, nk=10, hq=4, hk=2,
+             w=64, starts=FAKE, ks=FAKE, seqs=2, causal=1, scale=0.1, out=FAKE, lse=FAKE, rest=FAKE, do=FAKE, dr=256,
+             dh=64, dq=FAKE, dk=FAKE, dv=FAKE, work=None)
+    a.update(kw)
+    return L.emeans_attend_gradient(*a.values(), None)
+
+
+PACKED = [
+    (dict(dt=0), -2, b"dtype"), (dict(dt=3), -2, b"dtype"), (dict(n=-1), -1, b"n out"), (dict(nk=1 << 31), -1, b"nk out"),
+    (dict(hq=0), -1, b"hq"), (dict(hk=0), -1, b"hk"), (dict(hq=3), -1, b"multiple of hk"), (dict(w=4), -1, b"width"),
+    (dict(w=136), -1, b"width"), (dict(w=65), -1, b"width"), (dict(seqs=-1), -1, b"seqs"), (dict(qr=-8), -1, b"strides"),
+    (dict(kh=4), -1, b"strides"), (dict(v=FAKE + 8), -1, b"16 bytes"), (dict(out=FAKE + 2), -1, b"16 bytes"),
+    (dict(scale=float("inf")), -1, b"scale"), (dict(q=None), -1, b"NULL"), (dict(v=None), -1, b"NULL"),
+    (dict(starts=None), -1, b"NULL"), (dict(ks=None), -1, b"NULL"), (dict(out=None), -1, b"NULL")]
+
+
+@pytest.mark.parametrize("change,code,word", PACKED)
+def test_attend_refuses(L, change, code, word):
+    assert _packed(L, **change) == code and word in L.emeans_last_error()
+    assert _packed_back(L, **change) == code and word in L.emeans_last_error()
+
+
+@pytest.mark.parametrize("change,word", [
+    (dict(lse=None), b"NULL"), (dict(rest=None), b"NULL"), (dict(do=None), b"NULL"), (dict(dq=None), b"NULL"),
+    (dict(dk=None), b"NULL"), (dict(dv=None), b"NULL"), (dict(dr=12), b"strides"), (dict(do=FAKE + 8), b"16 bytes"),
+    (dict(work=8), b"aligned")])
+def test_attend_gradient_refuses(L, change, word):
+    assert _packed_back(L, **change) == -1 and word in L.emeans_last_error()
+
+
+def test_attend_of_nothing_is_fine(L):
+    assert _packed(L, n=0, q=None, out=None) == 0 and _packed_back(L, n=0, nk=0, q=None) == 0
+    assert L.emeans_attend_work(-1, 4) == 0 and L.emeans_attend_work(10, 4) >= 160
