@@ -614,7 +614,8 @@ int emeans_norm_rotate_gradient(const void* q, int64_t q_row, int64_t q_head, co
  * rounded to dtype beside the values.
  *   dtype     EMEANS_BF16 or EMEANS_F16 (EDTYPE for EMEANS_F32)
  *   width     a multiple of 8, at most 128      hq  a multiple of hk
- *   strides   rows and heads start at multiples of 16 bytes
+ *   strides   rows and heads start at multiples of 16 bytes, rows less than 2^24 values
+ *             apart
  *   starts, k_starts  device, seqs + 1 int32, not decreasing (the same for
  *             self-attention; cut to the tensors)
  *   out       device, n x hq x width (contiguous)

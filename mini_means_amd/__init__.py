@@ -1182,7 +1182,8 @@ def norm_rotate(q, k, q_weight, k_weight, positions, freqs, *, eps: float = 1e-6
 def _aligned(t):
     """t with heads of adjacent values at multiples of 16 bytes (a copy if they are not)."""
     a, b, c = t.stride()
-    if (c == 1 or t.shape[2] <= 1) and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0:
+    if (c == 1 or t.shape[2] <= 1) and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0 \
+            and a < 1 << 24:
         return t
     return t.contiguous() if t.data_ptr() % 16 == 0 or not t.is_contiguous() else t.clone()
 

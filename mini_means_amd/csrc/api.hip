@@ -1806,6 +1806,10 @@ int check_attend(const Attend& a, int64_t hq, int64_t hk, int64_t width, int64_t
   for (const int64_t s : strides)
     if (s < 0 || s % 8)
       return fail(EMEANS_EINVAL, "strides must be multiples of 8, not negative (got %lld)", (long long)s);
+  const int64_t row_strides[] = {a.q_rs, a.k_rs, a.v_rs, a.do_rs};
+  for (const int64_t s : row_strides)
+    if (s >= (int64_t)1 << 24)  // 64 rows of a tile within 2^31 bytes
+      return fail(EMEANS_EINVAL, "rows must be less than 2^24 values apart (got %lld)", (long long)s);
   const void* at[] = {a.q, a.k, a.v, a.dout, a.o, a.rest, a.dq, a.dk, a.dv};
   for (const void* p : at)
     if ((uintptr_t)p % 16) return fail(EMEANS_EINVAL, "rows must start at multiples of 16 bytes");

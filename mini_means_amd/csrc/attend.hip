@@ -46,53 +46,103 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// The place of a row's 16-byte chunks: XOR with a number of the row, so that eight
-// rows read at one chunk, and four rows read at two (transposed reads), cover all
-// banks. Rows of 96 values start half the banks apart already.
+// The place of a row's 16-byte chunks: XOR with a number of the row. LDS has 16 times 16
+// bytes in its banks, so that is what the 16 rows (of one chunk) that a phase of a row
+// read takes, and the four rows of four chunks of a transposed read, have to differ in.
+// Rows of 64 and 96 values start at two and four different places already. (Against
+// three bits of the row in any order, row reads took 1.5 times as long.)
 template <int W>
 __device__ __forceinline__ int swizzle(int row) {
-  if constexpr (W == 96)
-    return ((row >> 1) & 1) << 1 | ((row >> 2) & 1);
+  if constexpr (W == 64)
+    return ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+  else if constexpr (W == 96)
+    return (row >> 2) & 3;
   else
-    return (row & 3) << 1 | ((row >> 2) & 1);
+    return (row & 3) << 2 | ((row >> 2) & 3);
 }
 
-// Rows row0 .. row0 + 63 of a head into LDS, past `last` that row again (so that what
+// Rows row0 .. row0 + R - 1 of a head into LDS, past `last` that row again (so that what
 // is masked is a row of this sequence, never another's). Chunks past width are not
-// written: they hold the zeros that the workgroup began with.
-template <int W, int NW>
-__device__ __forceinline__ void load_tile(const uint16_t* base, int64_t rs, int row0, int last,
-                                          int width, uint8_t* lds, int wave, int lane) {
-  constexpr int CPR = W / 8;
+// written: they hold the zeros that the workgroup began with. A lane's offsets in a
+// whole tile are the same for each tile (`at`), beside a uniform address.
+template <int W, int NW, int R = kTile>
+struct TileLoads {
+  static constexpr int CPR = W / 8, ALL = CPR * R / 64, N = (ALL + NW - 1) / NW;
+  // the rows of a lane's loads are a multiple of 16 apart, so its chunk is the same
+  static constexpr bool kEven = NW * 64 % CPR == 0;
+  static constexpr int kStep = NW * 64 / CPR, M = kEven ? 1 : N;
+  uint32_t at[M];
+  int row[M];  // -1: not this lane's
+  __device__ __forceinline__ void init(int64_t rs, int width, int wave, int lane) {
 #pragma unroll
-  for (int i0 = 0; i0 < CPR; i0 += NW) {
-    const int i = i0 + wave;
-    if (CPR % NW && i >= CPR) break;
-    const int at = i * 64 + lane, row = at / CPR;
-    const int chunk = (at - row * CPR) ^ swizzle<W>(row);
-    const uint16_t* src = base + min(row0 + row, last) * rs + chunk * 8;
-    if (chunk * 8 < width) lds_load16(src, lds + i * 1024);
+    for (int i = 0; i < M; ++i) {
+      const int c = (i * NW + wave) * 64 + lane, r = c / CPR;
+      const int chunk = (c - r * CPR) ^ swizzle<W>(r);
+      row[i] = chunk * 8 < width && (ALL % NW == 0 || i * NW + wave < ALL) ? r : -1;
+      at[i] = (uint32_t)(r * (int)rs + chunk * 8) * 2;
+    }
   }
-}
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t rs, int row0, int last,
+                                       uint8_t* lds, int wave) const {
+    const uint16_t* from = base + row0 * rs;
+    const bool whole = row0 + R - 1 <= last;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int q = kEven ? 0 : i, more = kEven ? i * kStep : 0;
+      const uint16_t* src = from + more * rs;
+      uint32_t off = at[q];
+      if (!whole) {  // from the tile's first row, so that no offset is negative
+        src = from;
+        off += (uint32_t)((more - max(row0 + more + row[q] - last, 0)) * (int)rs) * 2;
+      }
+      if (row[q] >= 0) lds_load16_from(scalar_base(src), off, lds + (i * NW + wave) * 1024);
+    }
+  }
+};
 
+// Operands read from a tile in LDS. A lane's addresses in one buffer, kept in
+// registers: everything else is an immediate offset. rows(i, r0): A operand of rows r0 +
+// lane % 32, values 16 i + 8 h + {0..7}. columns(dt, r0): of the tile transposed, values
+// 32 dt + lane % 32 of the 16 rows from r0 on, in the order r0 + 4 h + {0..3},
+// r0 + 8 + 4 h + {0..3} for lane half h. (r0 a multiple of 16.)
 template <int W>
-__device__ __forceinline__ u32x4 row_frag(const uint8_t* lds, int row, int chunk) {
-  return *reinterpret_cast<const u32x4*>(lds + row * (W * 2) + ((chunk ^ swizzle<W>(row)) << 4));
-}
-
-// A operand of the transposed tile: values d0 + lane % 32 of the 16 rows from r0 on, in the
-// order r0 + 4 h + {0..3}, r0 + 8 + 4 h + {0..3} for lane half h.
-template <int W>
-__device__ __forceinline__ u32x4 column_frag(const uint8_t* lds, int r0, int d0, int lane) {
-  const int row = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-  const int chunk = d0 / 8 + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
-  const uint8_t* p = lds + row * (W * 2) + ((chunk ^ swizzle<W>(row)) << 4) + (lane & 1) * 8;
-  typedef __attribute__((address_space(3))) s16x4* at;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(p));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(p + 8 * W * 2));
-  const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-  return u32x4{a[0], a[1], b[0], b[1]};
-}
+struct TileReads {
+  typedef __attribute__((address_space(3))) const u32x4* quad_at;
+  typedef __attribute__((address_space(3))) s16x4* tr_at;
+  uint32_t row[W / 16], col[W / 32], col8[W / 32];  // col8: eight rows on
+  __device__ __forceinline__ void init(const uint8_t* lds, int lane) {
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_ptr_t)(lds);
+    const int r = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i) row[i] = at + r * W * 2 + (((2 * i + half) ^ swizzle<W>(r)) << 4);
+    const int c = 4 * half + ((lane & 15) >> 2);
+#pragma unroll
+    for (int dt = 0; dt < W / 32; ++dt) {
+      const int chunk = 4 * dt + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1);
+      col[dt] = at + c * W * 2 + ((chunk ^ swizzle<W>(c)) << 4) + (lane & 1) * 8;
+      col8[dt] = at + (c + 8) * W * 2 + ((chunk ^ swizzle<W>(c + 8)) << 4) + (lane & 1) * 8;
+    }
+  }
+  __device__ __forceinline__ void move(uint32_t by) {
+#pragma unroll
+    for (int i = 0; i < W / 16; ++i) row[i] += by;
+#pragma unroll
+    for (int dt = 0; dt < W / 32; ++dt) {
+      col[dt] += by;
+      col8[dt] += by;
+    }
+  }
+  __device__ __forceinline__ u32x4 rows(int i, int r0, int tile = 0) const {
+    return *(quad_at)(uintptr_t)(row[i] + r0 * (W * 2) + tile);
+  }
+  __device__ __forceinline__ u32x4 columns(int dt, int r0, int tile = 0) const {
+    const uint32_t off = r0 * (W * 2) + tile;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_at)(uintptr_t)(col[dt] + off));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tr_at)(uintptr_t)(col8[dt] + off));
+    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+    return u32x4{a[0], a[1], b[0], b[1]};
+  }
+};
 
 // A wave's own rows as B operands: row `row` of a head (any valid one for lanes past
 // the last), values 16 ks + 8 h + {0..7}; zeros past width.
@@ -223,46 +273,48 @@ __device__ __forceinline__ void clear_lds(uint8_t* lds, int bytes, int width, in
   __syncthreads();
 }
 
-// V rows that a query does not see must not show in it, but 0 x infinity is NaN. A
-// tile that some rows see in part is therefore, where a first pass gave no numbers,
-// done with its infinities and NaN taken out, and these are counted beside it as
-// products of their own: 1 for each +infinity that a row sees, 2^7 for each
-// -infinity, 2^14 for each NaN (64 rows at most, so the counts do not mix).
+// V rows that a query does not see must not show in it, but 0 x infinity is NaN. Where a
+// first pass gave no numbers, the tiles that the workgroup's rows see in part are therefore
+// done with infinities and NaN taken out, and odd_values adds those that a row sees.
 template <bool F16>
-__device__ __forceinline__ void split_odd(u32x4 v, u32x4& numbers, u32x4& odd) {
+__device__ __forceinline__ u32x4 numbers_of(u32x4 v) {
   constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
-  constexpr uint32_t kPlus = F16 ? 0x3C00u : 0x3F80u, kMinus = F16 ? 0x5800u : 0x4300u,
-                     kNan = F16 ? 0x7400u : 0x4680u;  // 1, 2^7, 2^14
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t n = 0, o = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t x = v[i] >> (16 * h) & 0xFFFFu;
-      const bool bad = (x & E) == E;
-      const uint32_t kind = (x & 0x7FFFu) != E ? kNan : x >> 15 ? kMinus : kPlus;
-      n |= (bad ? 0u : x) << (16 * h);
-      o |= (bad ? kind : 0u) << (16 * h);
-    }
-    numbers[i] = n;
-    odd[i] = o;
+    if ((v[i] & E) == E) v[i] &= 0xFFFF0000u;
+    if ((v[i] >> 16 & E) == E) v[i] &= 0x0000FFFFu;
   }
+  return v;
 }
 
-__device__ __forceinline__ float odd_value(float counts) {
-  if (counts == 0.0f) return 0.0f;
-  if (counts >= 16384.0f) return __uint_as_float(0x7FC00000u);
-  const bool minus = counts >= 128.0f, plus = counts - 128.0f * floorf(counts * (1.0f / 128.0f)) > 0.0f;
-  return plus && minus ? __uint_as_float(0x7FC00000u) : plus ? INFINITY : -INFINITY;
+// Infinities and NaN of the keys [k0, k1) that the lane's row sees (keys below `sees`),
+// read once more; acc as store_rows has it.
+template <bool F16, int W>
+__device__ __forceinline__ void odd_values(const uint16_t* v, int64_t rs, int k0, int k1, int sees,
+                                           int width, int half, f32x16 (&acc)[W / 32]) {
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k)
+#pragma unroll
+    for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = dt * 32 + 8 * g + 4 * half;
+        if (c >= width || k >= sees) continue;
+        const u32x2 w = *reinterpret_cast<const u32x2*>(v + k * rs + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = half_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))), F16);
+          if (!(fabsf(x) < INFINITY)) acc[dt][4 * g + i] += x;
+        }
+      }
 }
 
-// A workgroup owns NW waves x NQ x 32 query rows of one head and goes over its keys
-// in tiles of 64, double buffered, the next tile's direct loads beside this tile's
-// products; one barrier per tile.
-template <bool F16, int W, int NW, int NQ>
-__global__ __launch_bounds__(NW * 64, NQ == 1 ? 2 : 1) void attend_kernel(Attend a, int64_t wg0,
-                                                                          int64_t tiles) {
-  constexpr int ROWS = NW * NQ * 32;
+// A workgroup owns NW waves x 32 query rows of one head and goes over its keys in tiles
+// of 64, double buffered, the next tile's direct loads beside this tile's products; one
+// barrier per tile.
+template <bool F16, int W, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void attend_kernel(Attend a, int64_t wg0, int64_t tiles) {
+  constexpr int ROWS = NW * 32;
   constexpr int TB = kTile * W * 2;  // bytes of a tile
   __shared__ __align__(1024) uint8_t lds[4 * TB];
   const int64_t b = wg0 + blockIdx.x;
@@ -276,47 +328,49 @@ __global__ __launch_bounds__(NW * 64, NQ == 1 ? 2 : 1) void attend_kernel(Attend
   const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
   if (at.row0 >= sq.len) return;
   const int head = head_of(b, a.hq), kvh = head / (a.hq / a.hk);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // uniform to the compiler too
   const int shift = sk.len - sq.len;
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sk.first * a.k_rs + kvh * a.k_hs;
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
   clear_lds<W>(lds, 4 * TB, a.width, NW * 64);
 
-  int row[NQ], sees[NQ];  // a lane's query row, the keys it sees
-  u32x4 qf[NQ][W / 16];
+  const int row0 = at.row0 + wave * 32;
+  const int row = row0 + (lane & 31), r0 = min(row, sq.len - 1);  // a lane's query row
+  const int sees = max(a.causal ? min(r0 + shift + 1, sk.len) : sk.len, 0);  // and its keys
+  u32x4 qf[W / 16];
+  own_frags<W>(static_cast<const uint16_t*>(a.q) + (sq.first + r0) * a.q_rs + head * a.q_hs,
+               a.width, half, qf);
+  // scores times a positive number keep their order, and -infinity (masked) its value
+  if (a.scale <= 0.0f)
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    row[q] = at.row0 + (wave * NQ + q) * 32 + (lane & 31);
-    const int r = min(row[q], sq.len - 1);
-    sees[q] = max(a.causal ? min(r + shift + 1, sk.len) : sk.len, 0);
-    own_frags<W>(static_cast<const uint16_t*>(a.q) + (sq.first + r) * a.q_rs + head * a.q_hs,
-                 a.width, half, qf[q]);
-    // scores times a positive number keep their order, and -infinity (masked) its value
-    if (a.scale <= 0.0f)
-#pragma unroll
-      for (int ks = 0; ks < W / 16; ++ks)
-        qf[q][ks] = a.scale == 0.0f ? u32x4{0u, 0u, 0u, 0u} : qf[q][ks] ^ 0x80008000u;
-  }
+    for (int ks = 0; ks < W / 16; ++ks)
+      qf[ks] = a.scale == 0.0f ? u32x4{0u, 0u, 0u, 0u} : qf[ks] ^ 0x80008000u;
   const float c2 = a.scale == 0.0f ? 1.0f : fabsf(a.scale) * kLog2e;
-  const int end_row = min(at.row0 + ROWS, sq.len);  // past the last
-  const int keys = max(a.causal ? min(end_row + shift, sk.len) : sk.len, 0);
+  const int keys = max(a.causal ? min(min(at.row0 + ROWS, sq.len) + shift, sk.len) : sk.len, 0);
   const int n_tiles = (keys + kTile - 1) / kTile;
+  TileLoads<W, NW> k_loads, v_loads;
+  k_loads.init(a.k_rs, a.width, wave, lane);
+  v_loads.init(a.v_rs, a.width, wave, lane);
+  // keys below: seen by every row of the workgroup; by every and by any row of the wave
+  const int by_all = max(a.causal ? min(at.row0 + shift + 1, sk.len) : sk.len, 0) / kTile * kTile;
+  const int least = a.causal ? min(row0 + shift + 1, sk.len) : sk.len;
+  const int most = row0 >= sq.len ? 0 : a.causal ? min(row0 + 32 + shift, sk.len) : sk.len;
 
-  f32x16 acc[NQ][W / 32];
-  float m[NQ], l[NQ];
+  TileReads<W> reads;
+  f32x16 acc[W / 32];
+  float m, l;
   for (int careful = 0;; careful = 1) {
+    reads.init(lds, lane);
+    m = -INFINITY;
+    l = 0.0f;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      m[q] = -INFINITY;
-      l[q] = 0.0f;
+    for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-      for (int dt = 0; dt < W / 32; ++dt)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[q][dt][r] = 0.0f;
-    }
+      for (int r = 0; r < 16; ++r) acc[dt][r] = 0.0f;
     if (n_tiles > 0) {
-      load_tile<W, NW>(kp, a.k_rs, 0, sk.len - 1, a.width, lds, wave, lane);
-      load_tile<W, NW>(vp, a.v_rs, 0, sk.len - 1, a.width, lds + TB, wave, lane);
+      k_loads.load(kp, a.k_rs, 0, sk.len - 1, lds, wave);
+      v_loads.load(vp, a.v_rs, 0, sk.len - 1, lds + TB, wave);
     }
     for (int j = 0; j < n_tiles; ++j) {
       EMK_WAIT_VMCNT(0);
@@ -324,133 +378,113 @@ __global__ __launch_bounds__(NW * 64, NQ == 1 ? 2 : 1) void attend_kernel(Attend
       uint8_t* now = lds + (j & 1) * 2 * TB;
       if (j + 1 < n_tiles) {
         uint8_t* next = lds + ((j + 1) & 1) * 2 * TB;
-        load_tile<W, NW>(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, a.width, next, wave, lane);
-        load_tile<W, NW>(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, a.width, next + TB, wave, lane);
+        k_loads.load(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, next, wave);
+        v_loads.load(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, next + TB, wave);
       }
       const int k0 = j * kTile;
-      // the wave's first row sees least, its last most
-      const int row0 = at.row0 + wave * NQ * 32;
-      const int most = a.causal ? min(row0 + NQ * 32 + shift, sk.len) : sk.len;
-      if (k0 >= most || row0 >= sq.len) continue;
-      const bool part = k0 + kTile > (a.causal ? min(row0 + shift + 1, sk.len) : sk.len);
-      f32x16 s[NQ][2];
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[q][kt][r] = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < W / 16; ++ks) {
-          const u32x4 kf = row_frag<W>(now, kt * 32 + (lane & 31), 2 * ks + half);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) s[q][kt] = product<F16>(kf, qf[q][ks], s[q][kt]);
+      if (careful && k0 >= by_all) {
+        for (int i = threadIdx.x * 16; i < TB; i += NW * 64 * 16) {
+          u32x4* v = reinterpret_cast<u32x4*>(now + TB + i);
+          *v = numbers_of<F16>(*v);
         }
+        lds_barrier();
       }
-      u32x4 pf[NQ][4];
+      if (j > 0) reads.move(j & 1 ? 2 * TB : -2 * TB);
+      if (k0 >= most) continue;
+      const bool part = k0 + kTile > least;
+      // operands are read four products ahead (the barriers keep the order: left to
+      // itself the compiler reads each right before its product)
+      constexpr int N = W / 8, kAhead = 4;
+      u32x4 f[kAhead];
+      f32x16 s[2];
+      auto key = [&](int i) { return reads.rows(i % (W / 16), i / (W / 16) * 32); };
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (part) {
+      for (int i = 0; i < kAhead; ++i) f[i] = key(i);
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
+      for (int r = 0; r < 16; ++r) s[0][r] = s[1][r] = 0.0f;
+      __builtin_amdgcn_s_setprio(1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-              if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees[q]) s[q][kt][r] = -INFINITY;
-        }
-        float top = s[q][0][0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[q][0][r]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[q][1][r]);
-        top = half_max(top);
-        // a row's maximum is followed only when it grows by a factor of 2^6 of the
-        // weights: what matters is that they stay in range
-        const bool up = (top - m[q]) * c2 > 6.0f;
-        if (__any(up)) {
-          const float f = up ? __builtin_amdgcn_exp2f((m[q] - top) * c2) : 1.0f;
-          m[q] = up ? top : m[q];
-          l[q] *= f;
-#pragma unroll
-          for (int dt = 0; dt < W / 32; ++dt)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[q][dt][r] *= f;
-        }
-        const float ref = (m[q] == -INFINITY ? 0.0f : m[q]) * c2;
-        float sum = 0.0f;
+      for (int i = 0; i < N; ++i) {
+        f32x16& to = s[i / (W / 16)];
+        to = product<F16>(f[i % kAhead], qf[i % (W / 16)], to);
+        if (i + kAhead < N) f[i % kAhead] = key(i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+      if (part) {
+        asm volatile("");  // a branch: whole tiles are most
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            s[q][kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[q][kt][r], c2, -ref));
-            sum += s[q][kt][r];
-          }
-        l[q] += sum;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) pf[q][t] = packed<F16>(s[q][t >> 1], 8 * (t & 1));
+          for (int r = 0; r < 16; ++r)
+            if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) s[kt][r] = -INFINITY;
       }
-      if (!(careful && part)) {
+      float top = s[0][0];
+#pragma unroll
+      for (int r = 1; r < 32; ++r) top = fmaxf(top, s[r >> 4][r & 15]);
+      top = half_max(top);
+      // a row's maximum is followed only when it grows by a factor of 2^6 of the weights:
+      // what matters is that they stay in range
+      const bool up = (top - m) * c2 > 6.0f;
+      if (__any(up)) {
+        const float f = up ? __builtin_amdgcn_exp2f((m - top) * c2) : 1.0f;
+        m = up ? top : m;
+        l *= f;
 #pragma unroll
         for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const u32x4 vf = column_frag<W>(now + TB, 16 * t, 32 * dt, lane);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) acc[q][dt] = product<F16>(vf, pf[q][t], acc[q][dt]);
-          }
-      } else {
-        constexpr uint32_t kOne = F16 ? 0x3C00u : 0x3F80u;
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          u32x4 seen[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = k0 + 16 * t + 4 * half + (i >> 1) * 8 + (i & 1) * 2;
-              seen[t][i] = (k < sees[q] ? kOne : 0u) | (k + 1 < sees[q] ? kOne << 16 : 0u);
-            }
-#pragma unroll
-          for (int dt = 0; dt < W / 32; ++dt) {
-            f32x16 counts = {};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              u32x4 numbers, odd;
-              split_odd<F16>(column_frag<W>(now + TB, 16 * t, 32 * dt, lane), numbers, odd);
-              acc[q][dt] = product<F16>(numbers, pf[q][t], acc[q][dt]);
-              counts = product<F16>(odd, seen[t], counts);
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[q][dt][r] += odd_value(counts[r]);
-          }
-        }
+          for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
       }
+      const float ref = (m == -INFINITY ? 0.0f : m) * c2;
+      auto value = [&](int i) { return reads.columns(i % (W / 32), 16 * (i / (W / 32)), TB); };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = value(i);
+      __builtin_amdgcn_sched_barrier(0);
+      u32x4 p[4];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          s[kt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], c2, -ref));
+          sum += s[kt][r];
+        }
+        l += sum;
+        p[2 * kt] = packed<F16>(s[kt], 0);
+        p[2 * kt + 1] = packed<F16>(s[kt], 8);
+      }
+      __builtin_amdgcn_s_setprio(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int dt = i % (W / 32);
+        acc[dt] = product<F16>(f[i % kAhead], p[i / (W / 32)], acc[dt]);
+        if (i + kAhead < N) f[i % kAhead] = value(i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
     }
-    if (careful) break;
+    if (careful) {
+      odd_values<F16, W>(vp, a.v_rs, by_all, keys, sees, a.width, half, acc);
+      break;
+    }
     // no numbers though the scores were: look again, rows that see part of a tile apart
-    bool odd = false;
+    float z = 0.0f;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      float z = 0.0f;
+    for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
-      for (int dt = 0; dt < W / 32; ++dt)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) z += acc[q][dt][r] * 0.0f;
-      odd |= z != 0.0f && l[q] == l[q];
-    }
-    if (!__syncthreads_or(odd)) break;
+      for (int r = 0; r < 16; ++r) z += acc[dt][r] * 0.0f;
+    if (!__syncthreads_or(z != 0.0f && l == l)) break;
   }
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const float sum = half_sum(l[q]);
-    const bool on = row[q] < sq.len;
-    if (a.lse && half == 0 && on)
-      a.lse[(int64_t)head * a.n + sq.first + row[q]] =
-          sum == 0.0f ? INFINITY
-                      : (m[q] == -INFINITY ? 0.0f : m[q] * c2) + __builtin_amdgcn_logf(sum);
-    const int64_t to = ((int64_t)(sq.first + min(row[q], sq.len - 1)) * a.hq + head) * a.width;
-    store_rows<F16, W>(acc[q], sum == 0.0f ? 0.0f : 1.0f / sum, static_cast<uint16_t*>(a.o) + to,
-                       a.rest ? static_cast<uint16_t*>(a.rest) + to : nullptr, a.width, half, on);
-  }
+  const float sum = half_sum(l);
+  const bool on = row < sq.len;
+  if (a.lse && half == 0 && on)
+    a.lse[(int64_t)head * a.n + sq.first + row] =
+        sum == 0.0f ? INFINITY : (m == -INFINITY ? 0.0f : m * c2) + __builtin_amdgcn_logf(sum);
+  const int64_t to = ((int64_t)(sq.first + r0) * a.hq + head) * a.width;
+  store_rows<F16, W>(acc, sum == 0.0f ? 0.0f : 1.0f / sum, static_cast<uint16_t*>(a.o) + to,
+                     a.rest ? static_cast<uint16_t*>(a.rest) + to : nullptr, a.width, half, on);
 }
 
 // ---------------------------------------------------------------------------
@@ -521,7 +555,8 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
   const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
   if (at.row0 >= sq.len) return;
   const int head = head_of(b, a.hq), kvh = head / (a.hq / a.hk);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // uniform to the compiler too
   const int shift = sk.len - sq.len;
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + sk.first * a.k_rs + kvh * a.k_hs;
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
@@ -562,20 +597,25 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
   for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[dt][r] = 0.0f;
+  TileLoads<W, NW> k_loads, v_loads;
+  k_loads.init(a.k_rs, a.width, wave, lane);
+  v_loads.init(a.v_rs, a.width, wave, lane);
+  TileReads<W> reads;
+  reads.init(lds, lane);
   if (n_tiles > 0) {
-    load_tile<W, NW>(kp, a.k_rs, 0, sk.len - 1, a.width, lds, wave, lane);
-    load_tile<W, NW>(vp, a.v_rs, 0, sk.len - 1, a.width, lds + TB, wave, lane);
+    k_loads.load(kp, a.k_rs, 0, sk.len - 1, lds, wave);
+    v_loads.load(vp, a.v_rs, 0, sk.len - 1, lds + TB, wave);
   }
   for (int j = 0; j < n_tiles; ++j) {
     EMK_WAIT_VMCNT(0);
     lds_barrier();
-    uint8_t* now = lds + (j & 1) * 2 * TB;
     if (j + 1 < n_tiles) {
       uint8_t* next = lds + ((j + 1) & 1) * 2 * TB;
-      load_tile<W, NW>(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, a.width, next, wave, lane);
-      load_tile<W, NW>(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, a.width, next + TB, wave, lane);
+      k_loads.load(kp, a.k_rs, (j + 1) * kTile, sk.len - 1, next, wave);
+      v_loads.load(vp, a.v_rs, (j + 1) * kTile, sk.len - 1, next + TB, wave);
     }
     const int k0 = j * kTile, w0 = at.row0 + wave * 32;
+    if (j > 0) reads.move(j & 1 ? 2 * TB : -2 * TB);
     if (k0 >= (a.causal ? min(w0 + 32 + shift, sk.len) : sk.len) || w0 >= sq.len) continue;
     const bool part = k0 + kTile > (a.causal ? min(w0 + shift + 1, sk.len) : sk.len);
 #pragma unroll
@@ -583,8 +623,8 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
       f32x16 s = {}, dp = {};
 #pragma unroll
       for (int ks = 0; ks < W / 16; ++ks) {
-        s = product<F16>(row_frag<W>(now, kt * 32 + (lane & 31), 2 * ks + half), qf[ks], s);
-        dp = product<F16>(row_frag<W>(now + TB, kt * 32 + (lane & 31), 2 * ks + half), gf[ks], dp);
+        s = product<F16>(reads.rows(ks, kt * 32), qf[ks], s);
+        dp = product<F16>(reads.rows(ks, kt * 32, TB), gf[ks], dp);
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -597,7 +637,7 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
         const u32x4 ds = packed<F16>(dp, 8 * t);
 #pragma unroll
         for (int dt = 0; dt < W / 32; ++dt)
-          acc[dt] = product<F16>(column_frag<W>(now, kt * 32 + 16 * t, 32 * dt, lane), ds, acc[dt]);
+          acc[dt] = product<F16>(reads.columns(dt, kt * 32 + 16 * t), ds, acc[dt]);
       }
     }
   }
@@ -607,14 +647,16 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
 }
 
 // dK and dV: a workgroup owns 128 key rows of a key-value head and goes over the
-// queries that see them, head by head of the group, in tiles of 64; P and dS of a tile
-// have a lane's key row as column.
+// queries that see them, head by head of the group, in tiles of 32; P and dS of a tile
+// have a lane's key row as column. K stays in registers and V in LDS, which leaves room
+// for two waves on a SIMD.
 template <bool F16, int W>
-__global__ __launch_bounds__(256, 1) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
-  constexpr int NW = 4, ROWS = NW * 32, TB = kTile * W * 2;
+__global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
+  constexpr int NW = 4, ROWS = NW * 32, R = 32;
+  constexpr int QB = R * W * 2, VB = ROWS * W * 2;  // bytes: of a tile of Q or dO, of V
   constexpr float kLift = F16 ? 14.0f : 0.0f;  // fp16: P times 2^14, which stays in range
-  __shared__ __align__(1024) uint8_t lds[4 * TB];
-  __shared__ float lse[2][kTile], delta[2][kTile];
+  __shared__ __align__(1024) uint8_t lds[4 * QB + VB];
+  __shared__ float lse[2][R], delta[2][R];
   const int64_t b = wg0 + blockIdx.x;
   if (b >= tiles * a.hk) {
     zero_outside(a.k_starts, a.seqs, a.nk, (int64_t)a.hk * a.width, static_cast<uint16_t*>(a.dk),
@@ -627,83 +669,141 @@ __global__ __launch_bounds__(256, 1) void key_grad_kernel(Attend a, int64_t wg0,
   const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
   if (at.row0 >= sk.len) return;
   const int kvh = head_of(b, a.hk), group = a.hq / a.hk;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // uniform to the compiler too
   const int shift = sk.len - sq.len;
-  clear_lds<W>(lds, 4 * TB, a.width, NW * 64);
+  clear_lds<W>(lds, 4 * QB + VB, a.width, NW * 64);
 
-  const int key = at.row0 + wave * 32 + (lane & 31);
+  const int w0 = at.row0 + wave * 32, key = w0 + (lane & 31);
   const int64_t full = sk.first + min(key, sk.len - 1);
-  u32x4 kf[W / 16], vf[W / 16];
+  u32x4 kf[W / 16];
   own_frags<W>(static_cast<const uint16_t*>(a.k) + full * a.k_rs + kvh * a.k_hs, a.width, half, kf);
-  own_frags<W>(static_cast<const uint16_t*>(a.v) + full * a.v_rs + kvh * a.v_hs, a.width, half, vf);
+  {
+    TileLoads<W, NW> loads;
+    loads.init(a.v_rs, a.width, wave, lane);
+    const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
+    loads.load(vp, a.v_rs, at.row0, sk.len - 1, lds + 4 * QB, wave);
+    loads.load(vp, a.v_rs, min(at.row0 + kTile, sk.len - 1), sk.len - 1, lds + 4 * QB + VB / 2, wave);
+  }
   const float factor = F16 ? grad_factor(a) : 1.0f;
   const float lifted = factor * (F16 ? 0x1p-14f : 1.0f), unlift = F16 ? 0x1p-14f : 1.0f;
   const float c2 = a.scale * kLog2e;
   // query rows that see the workgroup's first key
-  const int first = a.causal ? max(at.row0 - shift, 0) / kTile * kTile : 0;
-  const int per = sq.len > first ? (sq.len - first + kTile - 1) / kTile : 0;
-  const int n_tiles = per * group;
+  const int first = a.causal ? max(at.row0 - shift, 0) / R * R : 0;
+  const int per = sq.len > first ? (sq.len - first + R - 1) / R : 0;
   f32x16 dk[W / 32], dv[W / 32];
 #pragma unroll
   for (int dt = 0; dt < W / 32; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.0f;
+  TileLoads<W, NW, R> q_loads, g_loads;
+  q_loads.init(a.q_rs, a.width, wave, lane);
+  g_loads.init(a.do_rs, a.width, wave, lane);
+  int head = kvh * group, q0 = first;  // of the next tile to be fetched
   auto fetch = [&](int j) {
-    const int head = kvh * group + j / per, q0 = first + j % per * kTile;
-    uint8_t* to = lds + (j & 1) * 2 * TB;
-    load_tile<W, NW>(static_cast<const uint16_t*>(a.q) + sq.first * a.q_rs + head * a.q_hs, a.q_rs,
-                     q0, sq.len - 1, a.width, to, wave, lane);
-    load_tile<W, NW>(static_cast<const uint16_t*>(a.dout) + sq.first * a.do_rs + head * a.do_hs,
-                     a.do_rs, q0, sq.len - 1, a.width, to + TB, wave, lane);
-    if (wave < 2) {
+    uint8_t* to = lds + (j & 1) * 2 * QB;
+    q_loads.load(static_cast<const uint16_t*>(a.q) + sq.first * a.q_rs + head * a.q_hs, a.q_rs, q0,
+                 sq.len - 1, to, wave);
+    g_loads.load(static_cast<const uint16_t*>(a.dout) + sq.first * a.do_rs + head * a.do_hs,
+                 a.do_rs, q0, sq.len - 1, to + QB, wave);
+    if (wave < 2 && lane < R) {
       const float* from = (wave ? a.delta : a.lse) + (int64_t)head * a.n + sq.first;
       lds_load4(from + min(q0 + lane, sq.len - 1), wave ? &delta[j & 1][0] : &lse[j & 1][0]);
     }
+    q0 += R;
+    if (q0 >= sq.len) {
+      q0 = first;
+      ++head;
+    }
   };
+  TileReads<W> reads;
+  reads.init(lds, lane);
+  const uint32_t v_rows = 4 * QB + wave * 32 * W * 2;  // of the wave's V beside the tile's rows
+  const int n_tiles = per * group;
   if (n_tiles > 0) fetch(0);
-  for (int j = 0; j < n_tiles; ++j) {
+  int at_q = first;
+  for (int j = 0; j < n_tiles; ++j, at_q = at_q + R >= sq.len ? first : at_q + R) {
     EMK_WAIT_VMCNT(0);
     lds_barrier();
     if (j + 1 < n_tiles) fetch(j + 1);
-    const uint8_t* now = lds + (j & 1) * 2 * TB;
-    const int q0 = first + j % per * kTile, w0 = at.row0 + wave * 32;
+    if (j > 0) reads.move(j & 1 ? 2 * QB : -2 * QB);
     if (w0 >= sk.len) continue;
-    // rows q0 + 63 - shift.. see: none of the wave's keys before its first
-    if (a.causal && q0 + kTile - 1 + shift < w0) continue;
-    const bool part = q0 + kTile > sq.len || (a.causal && q0 + shift < w0 + 31);
+    if (a.causal && at_q + R - 1 + shift < w0) continue;  // no row sees the wave's first key
+    const bool part = at_q + R > sq.len || (a.causal && at_q + shift < w0 + 31);
+    const uint32_t v_at = v_rows - (j & 1) * 2 * QB;
+    constexpr int N = W / 16, kAhead = 4;
+    u32x4 f[kAhead];
+    f32x16 s, dp;
 #pragma unroll
-    for (int qt = 0; qt < 2; ++qt) {
-      f32x16 s = {}, dp = {};
+    for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < W / 16; ++ks) {
-        s = product<F16>(row_frag<W>(now, qt * 32 + (lane & 31), 2 * ks + half), kf[ks], s);
-        dp = product<F16>(row_frag<W>(now + TB, qt * 32 + (lane & 31), 2 * ks + half), vf[ks], dp);
+    for (int i = 0; i < kAhead; ++i) f[i] = reads.rows(i, 0);
+    __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s = product<F16>(f[i % kAhead], kf[i], s);
+      f[i % kAhead] = i + kAhead < N ? reads.rows(i + kAhead, 0) : reads.rows(i + kAhead - N, 0, QB);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (W 96 leaves the first fragments of dO in another place)
+    constexpr int kTurn = N % kAhead;
+    u32x4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) v[i] = reads.rows(i, 0, v_at);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      dp = product<F16>(f[(i + kTurn) % kAhead], v[i % kAhead], dp);
+      if (i + kAhead < N) {
+        f[(i + kTurn) % kAhead] = reads.rows(i + kAhead, 0, QB);
+        v[i % kAhead] = reads.rows(i + kAhead, 0, v_at);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    auto column = [&](int i) {  // of dO, then of Q
+      const int k = i % N;
+      return reads.columns(k % (W / 32), 16 * (k / (W / 32)), i < N ? QB : 0);
+    };
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int r0 = qt * 32 + 8 * g + 4 * half;
-        const f32x4 e = *reinterpret_cast<const f32x4*>(&lse[j & 1][r0]);
-        const f32x4 d = *reinterpret_cast<const f32x4*>(&delta[j & 1][r0]);
+    for (int i = 0; i < kAhead; ++i) f[i] = column(i);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * g + i, q = q0 + r0 + i;
-          float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, kLift - e[i]));
-          float ds = p * __builtin_fmaf(dp[r], lifted, -d[i] * unlift);
-          if (part && (q >= sq.len || (a.causal && q + shift < key))) p = ds = 0.0f;
-          s[r] = p;
-          dp[r] = ds;
-        }
-      }
+    for (int g = 0; g < 4; ++g) {
+      const int r0 = 8 * g + 4 * half;
+      const f32x4 e = *reinterpret_cast<const f32x4*>(&lse[j & 1][r0]);
+      const f32x4 d = *reinterpret_cast<const f32x4*>(&delta[j & 1][r0]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const u32x4 p = packed<F16>(s, 8 * t), ds = packed<F16>(dp, 8 * t);
-#pragma unroll
-        for (int dt = 0; dt < W / 32; ++dt) {
-          dv[dt] = product<F16>(column_frag<W>(now + TB, qt * 32 + 16 * t, 32 * dt, lane), p, dv[dt]);
-          dk[dt] = product<F16>(column_frag<W>(now, qt * 32 + 16 * t, 32 * dt, lane), ds, dk[dt]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * g + i;
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, kLift - e[i]));
+        dp[r] = s[r] * __builtin_fmaf(dp[r], lifted, -d[i] * unlift);
       }
     }
+    if (part) {
+      asm volatile("");  // a branch: whole tiles are most
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int q = at_q + 8 * (r >> 2) + 4 * half + (r & 3);
+        if (q >= sq.len || (a.causal && q + shift < key)) s[r] = dp[r] = 0.0f;
+      }
+    }
+    const u32x4 p[2] = {packed<F16>(s, 0), packed<F16>(s, 8)};
+    const u32x4 ds[2] = {packed<F16>(dp, 0), packed<F16>(dp, 8)};
+    __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+      const int k = i % N, dt = k % (W / 32), h = k / (W / 32);
+      if (i < N)
+        dv[dt] = product<F16>(f[i % kAhead], p[h], dv[dt]);
+      else
+        dk[dt] = product<F16>(f[i % kAhead], ds[h], dk[dt]);
+      if (i + kAhead < 2 * N) f[i % kAhead] = column(i + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_setprio(0);
   }
   const int64_t to = (full * a.hk + kvh) * a.width;
   store_rows<F16, W>(dk, a.scale / factor, static_cast<uint16_t*>(a.dk) + to, nullptr, a.width,
@@ -724,10 +824,10 @@ hipError_t in_launches(int64_t wgs, GO go) {
 
 template <bool F16, int W>
 hipError_t forward_t(const Attend& a, hipStream_t st) {
-  constexpr int NW = 4, NQ = 1;
-  const int64_t tiles = a.n / (NW * NQ * 32) + a.seqs;
+  constexpr int NW = 4;
+  const int64_t tiles = a.n / (NW * 32) + a.seqs;
   return in_launches(tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
-    attend_kernel<F16, W, NW, NQ><<<grid, NW * 64, 0, st>>>(a, wg0, tiles);
+    attend_kernel<F16, W, NW><<<grid, NW * 64, 0, st>>>(a, wg0, tiles);
   });
 }
 
