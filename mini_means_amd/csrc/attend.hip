@@ -618,27 +618,57 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
     if (j > 0) reads.move(j & 1 ? 2 * TB : -2 * TB);
     if (k0 >= (a.causal ? min(w0 + 32 + shift, sk.len) : sk.len) || w0 >= sq.len) continue;
     const bool part = k0 + kTile > (a.causal ? min(w0 + shift + 1, sk.len) : sk.len);
+    constexpr int N = W / 16, kAhead = 4, kTurn = N % kAhead;
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      f32x16 s = {}, dp = {};
+      u32x4 f[kAhead];
+      f32x16 s, dp;
 #pragma unroll
-      for (int ks = 0; ks < W / 16; ++ks) {
-        s = product<F16>(reads.rows(ks, kt * 32), qf[ks], s);
-        dp = product<F16>(reads.rows(ks, kt * 32, TB), gf[ks], dp);
+      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = reads.rows(i, kt * 32);
+      __builtin_amdgcn_s_setprio(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s = product<F16>(f[i % kAhead], qf[i], s);
+        f[i % kAhead] = i + kAhead < N ? reads.rows(i + kAhead, kt * 32)
+                                       : reads.rows(i + kAhead - N, kt * 32, TB);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        dp = product<F16>(f[(i + kTurn) % kAhead], gf[i], dp);
+        if (i + kAhead < N) f[(i + kTurn) % kAhead] = reads.rows(i + kAhead, kt * 32, TB);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      auto column = [&](int i) { return reads.columns(i % (W / 32), kt * 32 + 16 * (i / (W / 32))); };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) f[i] = column(i);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, -lse));
         dp[r] = p * __builtin_fmaf(dp[r], factor, -d);
-        if (part && k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) dp[r] = 0.0f;
       }
+      if (part) {
+        asm volatile("");  // a branch: whole tiles are most
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const u32x4 ds = packed<F16>(dp, 8 * t);
-#pragma unroll
-        for (int dt = 0; dt < W / 32; ++dt)
-          acc[dt] = product<F16>(reads.columns(dt, kt * 32 + 16 * t), ds, acc[dt]);
+        for (int r = 0; r < 16; ++r)
+          if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) dp[r] = 0.0f;
       }
+      const u32x4 ds[2] = {packed<F16>(dp, 0), packed<F16>(dp, 8)};
+      __builtin_amdgcn_s_setprio(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int dt = i % (W / 32);
+        acc[dt] = product<F16>(f[i % kAhead], ds[i / (W / 32)], acc[dt]);
+        if (i + kAhead < N) f[i % kAhead] = column(i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
     }
   }
   store_rows<F16, W>(acc, a.scale / factor,
