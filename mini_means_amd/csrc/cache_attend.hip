@@ -14,6 +14,8 @@
 // places are counted in that order. fp16 and fp32 queries, and the softmax weights
 // beside them, are sums of two and three bf16 terms (16 and 24 bits), bf16 ones
 // are one term.
+#include <type_traits>
+
 #include "block.hpp"
 #include "kernels.hpp"
 
@@ -108,17 +110,35 @@ __device__ __forceinline__ void store_number(void* out, int64_t at, float v) {
     static_cast<uint16_t*>(out)[at] = to_half_rne(v, DT == 4);
 }
 
-// W: width rounded up to 64 or 128. Lane l = 16 g + n. Keys: lane n's place, 16
-// codes per g and load (a 64-byte run of one row per instruction and place).
-// Values: places {4 g + i, 16 + 4 g + i}, the W / 16 codes from n W / 16 on.
-template <int DT, bool I8, int W, bool SCORES>
-__global__ __launch_bounds__(256) void split_kernel(Split s) {
+// What a wave has in flight of 32 places: their codes and, where a head has more than
+// one scale, the scales' bytes. Lane l = 16 g + n. Keys: of place 16 u + n the 16 codes
+// from 64 j + 16 g on. Values: of places 4 g + i and 16 + 4 g + i the VD codes from n VD on.
+template <int W, bool ONE>
+struct Places {
+  static constexpr int KJ = W / 64, VD = W / 16;
+  u32x4 k[2][KJ];
+  u32x2 v[8];
+  uint32_t ks[ONE ? 1 : 2][KJ], vs[ONE ? 1 : 8];
+};
+
+// W: width rounded up to 64 or 128. ONE: a head lies in one block, so that its scale is a
+// factor of the score and of the softmax weight, and the store is under 4 GiB; else every
+// 16 codes have a scale of their own and rows are found with 64 bits.
+template <int DT, bool I8, int W, bool SCORES, bool ONE>
+__global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
   constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3;
-  constexpr int KJ = W / 64;   // 16-byte loads of a key per lane
-  constexpr int VD = W / 16;   // values of a place per lane: 8 or 4
+  constexpr int KJ = W / 64, VD = W / 16;
+  typedef std::conditional_t<ONE, uint32_t, int64_t> At;
   const CacheAttend& a = s.a;
-  __shared__ int64_t rows[kMaxPart];
-  __shared__ float join[kWaves][kHeads][W + 4];
+  // per place: the row's first byte (general: its row, -1 outside the store), and for ONE
+  // both scales, the keys' times scale log2 e; the values' is 0 where there is no place.
+  // Afterwards the waves' results.
+  constexpr int kRoom = kMaxPart * (ONE ? 12 : 8), kJoin = kWaves * kHeads * (W + 4) * 4;
+  __shared__ __align__(16) uint8_t room[kRoom > kJoin ? kRoom : kJoin];
+  At* const rows = reinterpret_cast<At*>(room);
+  float* const k_scale = reinterpret_cast<float*>(room + kMaxPart * 4);
+  float* const v_scale = reinterpret_cast<float*>(room + kMaxPart * 8);
+  float(*const join)[kHeads][W + 4] = reinterpret_cast<float(*)[kHeads][W + 4]>(room);
   __shared__ float top[kWaves][kHeads], sum[kWaves][kHeads];
   __shared__ int holes;
   // eight parts beside each other, one per XCD, whose heads follow each other there:
@@ -130,7 +150,8 @@ __global__ __launch_bounds__(256) void split_kernel(Split s) {
   const int head = (int)(b / 8 % hh), kvh = head / s.tiles, q0 = head % s.tiles * kHeads;
   const int seq = (int)(unit % a.seqs), part = (int)(unit / a.seqs);
   const int len = length_of(a, seq), p0 = part * s.part;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int heads = min(s.group - q0, kHeads);
   const int hq0 = kvh * s.group + q0;
   if (p0 >= len) {
@@ -140,18 +161,29 @@ __global__ __launch_bounds__(256) void split_kernel(Split s) {
     return;
   }
   const int cnt = min(s.part, len - p0);
+  const int64_t d = (int64_t)a.hk * a.width;
+  const int col = kvh * a.width;
+  const float c2 = a.scale * kLog2e;
   if (threadIdx.x == 0) holes = 0;
   __syncthreads();
-  // the places' rows; behind the last, the first place's again (never a row that
-  // the sequence does not have)
+  // behind the last place the first one's row again (never a row that the sequence does
+  // not have)
   const int whole = (cnt + kPlaces - 1) / kPlaces * kPlaces;
   for (int i = threadIdx.x; i < whole; i += 256) {
     const int p = p0 + (i < cnt ? i : 0);
-    const int64_t page = a.table[seq * a.table_ld + p / a.page];
-    const int64_t row = page * a.page + p % a.page;
+    const int pi = p / a.page;
+    const int64_t page = a.table[seq * a.table_ld + pi];
+    const int64_t row = page * a.page + (p - pi * a.page);
     const bool in = page >= 0 && row < a.rows;
-    rows[i] = in ? row : -1;
     if (!in) holes = 1;
+    if constexpr (ONE) {
+      const int64_t at = (in ? row : 0) * s.nb + col / a.block;
+      rows[i] = (uint32_t)((in ? row : 0) * d);
+      k_scale[i] = scale_value(a.k.scales[at]) * c2;
+      v_scale[i] = in && i < cnt ? scale_value(a.v.scales[at]) : 0.0f;
+    } else {
+      rows[i] = in ? row : -1;
+    }
   }
   bf16x8 qf[2 * KJ][NT];
 #pragma unroll
@@ -164,76 +196,91 @@ __global__ __launch_bounds__(256) void split_kernel(Split s) {
   }
   __syncthreads();
   const bool gaps = holes != 0;
-  const int64_t d = (int64_t)a.hk * a.width;
-  const int col = kvh * a.width;
-  int kb[KJ];
+  // Lanes past the width read codes of the same row again: the query has zeros there, and
+  // their values go nowhere.
+  uint32_t kc[KJ], kb[KJ];
 #pragma unroll
-  for (int j = 0; j < KJ; ++j) kb[j] = (col + min(j * 64 + g * 16, a.width - 16)) / a.block;
-  const bool von = n * VD < a.width;
-  const int vcol = von ? n * VD : 0;
-  const int vb = (col + vcol) / a.block;
-  const uint8_t* kp = a.k.codes + col + g * 16;
-  const uint8_t* vp = a.v.codes + col + vcol;
-  const float c2 = a.scale * kLog2e;
+  for (int j = 0; j < KJ; ++j) {
+    kc[j] = col + min(j * 64 + g * 16, a.width - 16);
+    kb[j] = kc[j] / a.block;
+  }
+  const uint32_t vc = col + min(n * VD, a.width - VD), vb = vc / a.block;
+
+  auto fetch = [&](int t, Places<W, ONE>& x) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      At row = rows[t + 16 * u + n];
+      if (!ONE) row = max(row, (At)0);
+#pragma unroll
+      for (int j = 0; j < KJ; ++j) {
+        x.k[u][j] = load_any<u32x4>(a.k.codes + (ONE ? row + kc[j] : row * d + kc[j]));
+        if constexpr (!ONE) x.ks[u][j] = a.k.scales[row * s.nb + kb[j]];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      At row = rows[t + 16 * (e >> 2) + 4 * g + (e & 3)];
+      if (!ONE) row = max(row, (At)0);
+      const uint8_t* p = a.v.codes + (ONE ? row + vc : row * d + vc);
+      if constexpr (VD == 8)
+        x.v[e] = load_any<u32x2>(p);
+      else
+        x.v[e][0] = load_any<uint32_t>(p);
+      if constexpr (!ONE) x.vs[e] = a.v.scales[row * s.nb + vb];
+    }
+  };
 
   f32x4 acc[VD];
 #pragma unroll
   for (int j = 0; j < VD; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;
-  for (int t = wave * kPlaces; t < whole; t += kWaves * kPlaces) {
-    // keys and scores: st[u][i] of place t + 16 u + 4 g + i
-    f32x4 st[2];
+  auto take = [&](int t, Places<W, ONE>& x) {
+    // scores: st[u][i] of place t + 16 u + 4 g + i
+    f32x4 st[2], fv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t row = max(rows[t + 16 * u + n], (int64_t)0);
       st[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
-        u32x4 w = {0u, 0u, 0u, 0u};
-        float f = 0.0f;
-        if (j * 64 + g * 16 < a.width) {
-          w = load_any<u32x4>(kp + row * d + j * 64);
-          f = scale_value(a.k.scales[row * s.nb + kb[j]]);
-        }
+        const float f = ONE ? 1.0f : scale_value(x.ks[ONE ? 0 : u][j]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32x2 lo = values_of<I8>(w[2 * h], f), hi = values_of<I8>(w[2 * h + 1], f);
+          const u32x2 lo = values_of<I8>(x.k[u][j][2 * h], f), hi = values_of<I8>(x.k[u][j][2 * h + 1], f);
           const bf16x8 kf = __builtin_bit_cast(bf16x8, u32x4{lo[0], lo[1], hi[0], hi[1]});
 #pragma unroll
           for (int e = NT - 1; e >= 0; --e)
             st[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[2 * j + h][e], st[u], 0, 0, 0);
         }
       }
-    }
-    // values: x[u * 4 + i] of place t + 16 u + 4 g + i
-    u32x4 x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t at = rows[t + 16 * (e >> 2) + 4 * g + (e & 3)];
-      const int64_t row = max(at, (int64_t)0);
-      u32x2 w = {0u, 0u};
-      if (von) {
-        if constexpr (VD == 8)
-          w = load_any<u32x2>(vp + row * d);
-        else
-          w[0] = load_any<uint32_t>(vp + row * d);
+      if constexpr (ONE) {
+        st[u] *= *reinterpret_cast<const f32x4*>(&k_scale[t + 16 * u + 4 * g]);
+        fv[u] = *reinterpret_cast<const f32x4*>(&v_scale[t + 16 * u + 4 * g]);
+      } else {
+        st[u] *= c2;
       }
-      const float f = gaps && at < 0 ? 0.0f : scale_value(a.v.scales[row * s.nb + vb]);
-      if (gaps && at < 0) w = u32x2{0u, 0u};
-      const u32x2 lo = values_of<I8>(w[0], f), hi = values_of<I8>(w[1], f);
-      x[e] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+    if (gaps || t + kPlaces > cnt) {
+      asm volatile("");  // a branch: most parts are whole
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int p = t + 16 * (e >> 2) + 4 * g + (e & 3);
+        bool out;
+        if constexpr (ONE)
+          out = fv[e >> 2][e & 3] == 0.0f;
+        else
+          out = p >= cnt || rows[p] < 0;
+        if (out) {
+          st[e >> 2][e & 3] = -INFINITY;
+          if (gaps) {  // some row of the store, which may hold NaN
+            x.v[e] = u32x2{0u, 0u};
+            if constexpr (!ONE) x.vs[e] = 127;
+          }
+        }
+      }
     }
     float top_now = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p = t + 16 * u + 4 * g + i;
-        float v = st[u][i] * c2;
-        if (p >= cnt || (gaps && rows[p] < 0)) v = -INFINITY;
-        st[u][i] = v;
-        top_now = fmaxf(top_now, v);
-      }
+    for (int e = 0; e < 8; ++e) top_now = fmaxf(top_now, st[e >> 2][e & 3]);
     if constexpr (SCORES) {
       if (n < heads) {
         const int64_t at = ((int64_t)seq * a.hq + hq0 + n) * s.parts * s.part + p0 + t + 4 * g;
@@ -255,20 +302,45 @@ __global__ __launch_bounds__(256) void split_kernel(Split s) {
     for (int e = 0; e < 8; ++e) {
       p[e] = __builtin_amdgcn_exp2f(st[e >> 2][e & 3] - ref);
       l += p[e];
+      if constexpr (ONE) p[e] *= fv[e >> 2][e & 3];
     }
     bf16x8 pf[NT];
     terms_of<NT>(p, pf);
+    u32x4 y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = ONE ? 1.0f : scale_value(x.vs[ONE ? 0 : e]);
+      const u32x2 lo = values_of<I8>(x.v[e][0], f);
+      const u32x2 hi = VD == 8 ? values_of<I8>(x.v[e][1], f) : u32x2{0u, 0u};
+      y[e] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
 #pragma unroll
     for (int j = 0; j < VD; ++j) {
       u32x4 w;  // value j of the eight places
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        w[e] = __builtin_amdgcn_perm(x[2 * e + 1][j >> 1], x[2 * e][j >> 1],
+        w[e] = __builtin_amdgcn_perm(y[2 * e + 1][j >> 1], y[2 * e][j >> 1],
                                      j & 1 ? 0x07060302u : 0x05040100u);
       const bf16x8 vf = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
       for (int e = NT - 1; e >= 0; --e)
         acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[e], acc[j], 0, 0, 0);
+    }
+  };
+  // the next places' codes are on their way while these are worked on
+  {
+    constexpr int kStep = kWaves * kPlaces;
+    Places<W, ONE> x, y;
+    int t = wave * kPlaces;
+    if (t < whole) fetch(t, x);
+    while (t < whole) {
+      if (t + kStep < whole) fetch(t + kStep, y);
+      take(t, x);
+      t += kStep;
+      if (t >= whole) break;
+      if (t + kStep < whole) fetch(t + kStep, x);
+      take(t, y);
+      t += kStep;
     }
   }
   // the waves' parts joined: acc[j][i] is value VD (4 g + i) + j of head n
@@ -321,11 +393,11 @@ __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.0f
 // over the heads, from the scores that split_kernel left.
 constexpr int kJoinHeads = 1024;
 
-template <int DT>
+template <int DT, int LANES>
 __global__ __launch_bounds__(256) void join_kernel(Split s, int joins) {
   const CacheAttend& a = s.a;
   __shared__ f32x2 ml[kJoinHeads];
-  __shared__ f32x4 acc[256];
+  __shared__ f32x4 acc[4][LANES];
   __shared__ float tmp[8];
   const int64_t b = s.wg0 + blockIdx.x;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -339,31 +411,35 @@ __global__ __launch_bounds__(256) void join_kernel(Split s, int joins) {
     if (lane == 0) tmp[wave] = m;
     __syncthreads();
     m = guarded(fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3])));
-    // 32 lanes of four values each, eight parts at a time
-    const int c = (threadIdx.x & 31) * 4, i0 = threadIdx.x >> 5;
+    // LANES lanes of four values each, the others over the parts
+    const int c = blockIdx.y * (LANES * 4) + (threadIdx.x % LANES) * 4, i0 = threadIdx.x / LANES;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
-    for (int i = i0; i < used; i += 8) {
+    for (int i = i0; i < used; i += 256 / LANES) {
       const f32x2 t = tops[i];
       if (t[1] == 0.0f) continue;  // a part of gaps
       const float f = __builtin_amdgcn_exp2f(t[0] - m);
       l += t[1] * f;
       if (c < a.width) v += *reinterpret_cast<const f32x4*>(s.sums + (b * s.parts + i) * a.width + c) * f;
     }
-    acc[threadIdx.x] = v;
-    if ((threadIdx.x & 31) == 0) tmp[i0] = l;
+#pragma unroll
+    for (int off = LANES; off < 64; off <<= 1) {
+      l += __shfl_xor(l, off, kWave);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], off, kWave);
+    }
+    if (lane < LANES) acc[wave][lane] = v;
+    if (lane == 0) tmp[4 + wave] = l;
     __syncthreads();
-    if (threadIdx.x >= 32 || c >= a.width) return;
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += tmp[i];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += acc[threadIdx.x + 32 * i];
+    if (threadIdx.x >= LANES || c >= a.width) return;
+    const float sum = tmp[4] + tmp[5] + tmp[6] + tmp[7];
+    v = acc[0][lane] + acc[1][lane] + acc[2][lane] + acc[3][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       store_number<DT>(a.out, b * a.width + c + i, sum == 0.0f ? 0.0f : v[i] / sum);
     return;
   }
+  if (blockIdx.y) return;
   const int64_t unit = b - joins;
   const int seq = (int)(unit % a.seqs), part = (int)(unit / a.seqs);
   const int len = length_of(a, seq), p0 = part * s.part;
@@ -419,13 +495,19 @@ Room room_of(int64_t seqs, int64_t hq, int64_t width, int64_t parts, int64_t par
 
 template <int DT, bool I8, int W>
 hipError_t split_t(Split& s, int64_t wgs, bool weights, hipStream_t st) {
+  // a head in one block, whichever: block a multiple of width, or width itself
+  const bool one = s.a.block % s.a.width == 0 && s.a.rows * s.a.hk * s.a.width < ((int64_t)1 << 32);
   for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
     const unsigned grid = (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups);
     s.wg0 = wg0;
-    if (weights)
-      split_kernel<DT, I8, W, true><<<grid, 256, 0, st>>>(s);
+    if (weights && one)
+      split_kernel<DT, I8, W, true, true><<<grid, 256, 0, st>>>(s);
+    else if (weights)
+      split_kernel<DT, I8, W, true, false><<<grid, 256, 0, st>>>(s);
+    else if (one)
+      split_kernel<DT, I8, W, false, true><<<grid, 256, 0, st>>>(s);
     else
-      split_kernel<DT, I8, W, false><<<grid, 256, 0, st>>>(s);
+      split_kernel<DT, I8, W, false, false><<<grid, 256, 0, st>>>(s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -455,7 +537,11 @@ hipError_t cache_attend_t(const CacheAttend& a, hipStream_t st) {
   const int64_t more = joins + (weights ? a.seqs * parts : 0);
   for (int64_t wg0 = 0; wg0 < more; wg0 += kMaxGroups) {
     s.wg0 = wg0;
-    join_kernel<DT><<<(unsigned)(more - wg0 < kMaxGroups ? more - wg0 : kMaxGroups), 256, 0, st>>>(s, joins);
+    const unsigned grid = (unsigned)(more - wg0 < kMaxGroups ? more - wg0 : kMaxGroups);
+    if (parts > 16)
+      join_kernel<DT, 8><<<dim3(grid, (a.width + 31) / 32), 256, 0, st>>>(s, joins);
+    else
+      join_kernel<DT, 32><<<grid, 256, 0, st>>>(s, joins);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
