@@ -1987,7 +1987,7 @@ int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t
       slices += blocks_of(len[j], 128);
     }
   }
-  if (seqs * slices > kMaxGroups)
+  if (seqs * slices >= kMaxGroups)  // of 1024 threads
     return fail(EMEANS_EINVAL, "%lld sequences of these rows are too many for one call",
                 (long long)seqs);
   if ((uintptr_t)work % 16) return fail(EMEANS_EINVAL, "work must be 16-byte aligned");

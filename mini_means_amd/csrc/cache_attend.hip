@@ -169,20 +169,41 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
   // behind the last place the first one's row again (never a row that the sequence does
   // not have)
   const int whole = (cnt + kPlaces - 1) / kPlaces * kPlaces;
-  for (int i = threadIdx.x; i < whole; i += 256) {
-    const int p = p0 + (i < cnt ? i : 0);
-    const int pi = p / a.page;
-    const int64_t page = a.table[seq * a.table_ld + pi];
-    const int64_t row = page * a.page + (p - pi * a.page);
-    const bool in = page >= 0 && row < a.rows;
-    if (!in) holes = 1;
-    if constexpr (ONE) {
-      const int64_t at = (in ? row : 0) * s.nb + col / a.block;
-      rows[i] = (uint32_t)((in ? row : 0) * d);
-      k_scale[i] = scale_value(a.k.scales[at]) * c2;
-      v_scale[i] = in && i < cnt ? scale_value(a.v.scales[at]) : 0.0f;
-    } else {
-      rows[i] = in ? row : -1;
+  // four of a thread at a time: each is a chain of reads (table, scales)
+  constexpr int kDeep = 4;
+  for (int i0 = threadIdx.x; i0 < whole; i0 += 256 * kDeep) {
+    int64_t page[kDeep];
+    int in_page[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int i = i0 + 256 * e, p = p0 + (i < cnt ? i : 0), pi = p / a.page;
+      page[e] = a.table[seq * a.table_ld + pi];
+      in_page[e] = p - pi * a.page;
+    }
+    uint32_t ks[kDeep], vs[kDeep];
+    int64_t row[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      row[e] = page[e] * a.page + in_page[e];
+      if (page[e] < 0 || row[e] >= a.rows) row[e] = -1;
+      if constexpr (ONE) {
+        const int64_t at = max(row[e], (int64_t)0) * s.nb + col / a.block;
+        ks[e] = a.k.scales[at];
+        vs[e] = a.v.scales[at];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int i = i0 + 256 * e;
+      if (i >= whole) break;
+      if (row[e] < 0) holes = 1;
+      if constexpr (ONE) {
+        rows[i] = (uint32_t)(max(row[e], (int64_t)0) * d);
+        k_scale[i] = scale_value(ks[e]) * c2;
+        v_scale[i] = row[e] >= 0 && i < cnt ? scale_value(vs[e]) : 0.0f;
+      } else {
+        rows[i] = row[e];
+      }
     }
   }
   bf16x8 qf[2 * KJ][NT];
@@ -389,8 +410,8 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
 __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // Workgroups below seqs * hq: the parts of one head of one sequence joined. The
-// others (weights asked for): the attention weights of one part's places, summed
-// over the heads, from the scores that split_kernel left.
+// others (weights asked for): the attention weights of 256 places, summed over the heads,
+// from the scores that split_kernel left.
 constexpr int kJoinHeads = 1024;
 
 template <int DT, int LANES>
@@ -441,38 +462,48 @@ __global__ __launch_bounds__(256) void join_kernel(Split s, int joins) {
   }
   if (blockIdx.y) return;
   const int64_t unit = b - joins;
-  const int seq = (int)(unit % a.seqs), part = (int)(unit / a.seqs);
-  const int len = length_of(a, seq), p0 = part * s.part;
+  const int seq = (int)(unit % a.seqs), p0 = (int)(unit / a.seqs) * 256;
+  const int len = length_of(a, seq);
   if (p0 >= len) return;
   const int used = (len + s.part - 1) / s.part;
-  for (int h = wave; h < a.hq; h += 4) {
-    const f32x2* tops = s.tops + ((int64_t)seq * a.hq + h) * s.parts;
+  // eight lanes a head: its largest score and one over its sum
+  for (int h = threadIdx.x >> 3; h - (int)(threadIdx.x >> 3) < a.hq; h += 32) {
+    const f32x2* tops = s.tops + ((int64_t)seq * a.hq + min(h, a.hq - 1)) * s.parts;
     float m = -INFINITY, l = 0.0f;
-    for (int i = lane; i < used; i += 64) m = fmaxf(m, tops[i][0]);
-    m = guarded(wave_max(m));
-    for (int i = lane; i < used; i += 64) {
+    for (int i = lane & 7; i < used; i += 8) m = fmaxf(m, tops[i][0]);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, kWave));
+    m = guarded(m);
+    for (int i = lane & 7; i < used; i += 8) {
       const f32x2 t = tops[i];
       if (t[1] != 0.0f) l += t[1] * __builtin_amdgcn_exp2f(t[0] - m);
     }
-    l = wave_sum(l);
-    if (lane == 0) ml[h] = f32x2{m, l == 0.0f ? 0.0f : 1.0f / l};
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) l += __shfl_xor(l, off, kWave);
+    if ((lane & 7) == 0 && h < a.hq) ml[h] = f32x2{m, l == 0.0f ? 0.0f : 1.0f / l};
   }
   __syncthreads();
-  const int cnt = min(s.part, len - p0);
+  const int p = p0 + threadIdx.x;
+  if (p >= len) return;
   const int64_t ld = (int64_t)s.parts * s.part;
-  for (int i = threadIdx.x; i < cnt; i += 256) {
-    const float* sc = s.scores + (int64_t)seq * a.hq * ld + p0 + i;
-    float v = 0.0f;
-    for (int h = 0; h < a.hq; ++h) v += __builtin_amdgcn_exp2f(sc[h * ld] - ml[h][0]) * ml[h][1];
-    a.weights[seq * a.weights_ld + p0 + i] += v;
-  }
+  const float* sc = s.scores + (int64_t)seq * a.hq * ld + p;
+  float v = 0.0f;
+#pragma unroll 8
+  for (int h = 0; h < a.hq; ++h) v += __builtin_amdgcn_exp2f(sc[h * ld] - ml[h][0]) * ml[h][1];
+  a.weights[seq * a.weights_ld + p] += v;
 }
 
-// Places of a workgroup: a wave's 32 at least, so many that about 2048 workgroups
-// are left where sequences reach the table's width.
+// Places of a workgroup: at most 4096 workgroups (where sequences reach the table's
+// width), and 512 places unless that leaves fewer than 1024, as a workgroup's first reads
+// are a chain (lengths, table, scales) of about 3 us. Measured: one sequence of 131072
+// places, 8 key-value heads: 256 places 62 us, 512 50, 1024 50; 64 sequences of up to
+// 8192: 1024 places 123 us, 2048 129. Up to 512 places are one part: a join's launch
+// costs more than the other waves save.
 int part_of(int seqs, int hk, int tiles, int64_t places) {
+  if (places <= 512) return 512;
   int part = kWaves * kPlaces;
-  while (part < kMaxPart && (int64_t)seqs * hk * tiles * ((places + part - 1) / part) > 4096) part *= 2;
+  auto groups = [&] { return (int64_t)seqs * hk * tiles * ((places + part - 1) / part); };
+  while (part < kMaxPart && groups() > (part < 512 ? 1024 : 4096)) part *= 2;
   return part;
 }
 
@@ -534,7 +565,7 @@ hipError_t cache_attend_t(const CacheAttend& a, hipStream_t st) {
     e = a.i8 ? split_t<DT, true, 128>(s, wgs, weights, st) : split_t<DT, false, 128>(s, wgs, weights, st);
   if (e != hipSuccess || (parts == 1 && !weights)) return e;
   const int joins = parts > 1 ? a.seqs * a.hq : 0;
-  const int64_t more = joins + (weights ? a.seqs * parts : 0);
+  const int64_t more = joins + (weights ? a.seqs * ((places + 255) / 256) : 0);
   for (int64_t wg0 = 0; wg0 < more; wg0 += kMaxGroups) {
     s.wg0 = wg0;
     const unsigned grid = (unsigned)(more - wg0 < kMaxGroups ? more - wg0 : kMaxGroups);

@@ -133,45 +133,48 @@ __global__ __launch_bounds__(kSelect) void select_kernel(CacheEvict a, Moves mv)
 }
 
 constexpr int kSlice = 128;  // bytes of a row that a workgroup moves
+constexpr int kMovers = 1024;
 constexpr int kDeep = 4;     // rows in flight per thread and round
 
 struct Slices {
   uint8_t* plane[CacheEvict::kPlanes];
   int64_t row_bytes[CacheEvict::kPlanes];
-  int unit[CacheEvict::kPlanes];   // bytes of a lane: 16, 4 or 1
+  int unit[CacheEvict::kPlanes];   // bytes of a lane: 16, 8, 4 or 1
+  int lanes[CacheEvict::kPlanes];  // log 2 of the lanes of a row
   int first[CacheEvict::kPlanes];  // first slice of the plane
   int planes, slices;
 };
 
+// A row's place is never before its rank, so what one round overwrites are sources of that
+// round or of an earlier one: a round is stored once every lane holds its rows of it. The
+// next round's rows are fetched before that, and the list's entries another round ahead,
+// as a row's address comes from one.
 template <typename V>
 __device__ __forceinline__ void move_rows(uint8_t* plane, int64_t row_bytes, int64_t off,
-                                          const Move* list, int first, int count) {
-  constexpr int LPR = kSlice / sizeof(V);  // lanes of a row
-  constexpr int RPT = 256 / LPR;           // rows of the workgroup at once
-  constexpr int ROUND = RPT * kDeep;
-  const int row = threadIdx.x / LPR;
-  const int64_t at = off + (int64_t)(threadIdx.x % LPR) * sizeof(V);
+                                          int lanes, const Move* list, int first, int count) {
+  const int rpt = kMovers >> lanes;  // rows of the workgroup at once
+  const int round = rpt * kDeep, row = threadIdx.x >> lanes;
+  const int64_t at = off + (int64_t)(threadIdx.x & ((1 << lanes) - 1)) * sizeof(V);
   const bool on = at < row_bytes;
   using Held = std::conditional_t<sizeof(V) == 1, uint32_t, V>;  // in whole registers
   Held held[2][kDeep] = {};
   int64_t to[2][kDeep];
-  auto fetch = [&](int r0, Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
+  Move mv[kDeep];
+  auto entries = [&](int r0) {
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int r = r0 + u * RPT + row;
-      dst[u] = -1;
-      if (on && r < count) {
-        const Move m = list[r];
-        if (m.from >= 0 && m.to >= 0) {
-          v[u] = load_any<V>(plane + m.from * row_bytes + at);
-          dst[u] = m.to * row_bytes + at;
-        }
-      }
+      const int r = r0 + u * rpt + row;
+      mv[u] = r < count ? list[r] : Move{-1, -1};
     }
   };
-  // A row's place is never before its rank, so rows that are stored in one round
-  // are sources of that round or of an earlier one only: they are stored once every
-  // lane holds its rows of the round. The next round's are fetched before that.
+  auto fetch = [&](Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const bool go = on && mv[u].from >= 0 && mv[u].to >= 0;
+      dst[u] = go ? mv[u].to * row_bytes + at : -1;
+      if (go) v[u] = load_any<V>(plane + mv[u].from * row_bytes + at);
+    }
+  };
   auto put = [&](Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
 #pragma unroll
     for (int u = 0; u < kDeep; ++u)
@@ -182,20 +185,24 @@ __device__ __forceinline__ void move_rows(uint8_t* plane, int64_t row_bytes, int
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) asm volatile("" : "+v"(v[u])::"memory");
   };
-  fetch(first, held[0], to[0]);
-  for (int r0 = first; r0 < count; r0 += 2 * ROUND) {
+  entries(first);
+  fetch(held[0], to[0]);
+  entries(first + round);
+  for (int r0 = first; r0 < count; r0 += 2 * round) {
     arrived(held[0]);
     __syncthreads();
-    fetch(r0 + ROUND, held[1], to[1]);
+    fetch(held[1], to[1]);
+    entries(r0 + 2 * round);
     put(held[0], to[0]);
     arrived(held[1]);
     __syncthreads();
-    fetch(r0 + 2 * ROUND, held[0], to[0]);
+    fetch(held[0], to[0]);
+    entries(r0 + 3 * round);
     put(held[1], to[1]);
   }
 }
 
-__global__ __launch_bounds__(256) void move_kernel(Slices s, Moves mv, int keep) {
+__global__ __launch_bounds__(kMovers) void move_kernel(Slices s, Moves mv, int keep) {
   const int seq = blockIdx.x / s.slices, slice = blockIdx.x % s.slices;
   const int first = mv.span[2 * seq], count = mv.span[2 * seq + 1];
   if (first >= count) return;
@@ -203,12 +210,14 @@ __global__ __launch_bounds__(256) void move_kernel(Slices s, Moves mv, int keep)
   while (p + 1 < s.planes && slice >= s.first[p + 1]) ++p;
   const int64_t off = (int64_t)(slice - s.first[p]) * kSlice;
   const Move* list = mv.list + (int64_t)seq * keep;
-  if (s.unit[p] == 16)
-    move_rows<u32x4>(s.plane[p], s.row_bytes[p], off, list, first, count);
-  else if (s.unit[p] == 4)
-    move_rows<uint32_t>(s.plane[p], s.row_bytes[p], off, list, first, count);
-  else
-    move_rows<uint8_t>(s.plane[p], s.row_bytes[p], off, list, first, count);
+  uint8_t* plane = s.plane[p];
+  const int64_t len = s.row_bytes[p];
+  switch (s.unit[p]) {
+    case 16: return move_rows<u32x4>(plane, len, off, s.lanes[p], list, first, count);
+    case 8: return move_rows<u32x2>(plane, len, off, s.lanes[p], list, first, count);
+    case 4: return move_rows<uint32_t>(plane, len, off, s.lanes[p], list, first, count);
+    default: return move_rows<uint8_t>(plane, len, off, s.lanes[p], list, first, count);
+  }
 }
 
 size_t list_bytes(int seqs, int keep) { return ((size_t)seqs * keep * sizeof(Move) + 255) / 256 * 256; }
@@ -230,12 +239,14 @@ hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st) {
     s.plane[p] = a.plane[p];
     s.row_bytes[p] = a.row_bytes[p];
     const uint64_t bits = (uint64_t)a.row_bytes[p] | (uint64_t)(uintptr_t)a.plane[p];
-    s.unit[p] = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+    s.unit[p] = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 1;
+    const int64_t of_row = (a.row_bytes[p] < kSlice ? a.row_bytes[p] : kSlice) / s.unit[p];
+    while (((int64_t)1 << s.lanes[p]) < of_row) ++s.lanes[p];
     s.first[p] = s.slices;
     s.slices += (int)((a.row_bytes[p] + kSlice - 1) / kSlice);
   }
   s.planes = a.planes;
-  move_kernel<<<(unsigned)a.seqs * s.slices, 256, 0, st>>>(s, mv, a.keep);
+  move_kernel<<<(unsigned)a.seqs * s.slices, kMovers, 0, st>>>(s, mv, a.keep);
   return hipGetLastError();
 }
 
