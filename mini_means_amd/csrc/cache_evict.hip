@@ -5,8 +5,8 @@
 // the sequence's first places in their order, in place.
 //
 // Bound by HBM and by latency: a workgroup per sequence finds the threshold digit by
-// digit (four passes of 8 bits over the weights, which stay in L2) and lists the
-// moves; then workgroups of a sequence and 128 bytes of a row each go along the list.
+// digit (the weights stay in L2) and lists the moves; then workgroups of a sequence and
+// 128 bytes of a row each go along the list.
 #include <type_traits>
 
 #include "block.hpp"
@@ -38,11 +38,17 @@ __device__ __forceinline__ int64_t place_of(const CacheEvict& a, int seq, int p)
   return page >= 0 && row < a.rows ? row : -1;
 }
 
+// The threshold in three digits of 11, 11 and 10 bits from the top: the first has the
+// exponent and two more bits, as counts of an exponent alone would all meet in a few
+// words of LDS. Then each wave takes a run of places: counts first, ranks after.
 __global__ __launch_bounds__(kSelect) void select_kernel(CacheEvict a, Moves mv) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t tmp[kSelect / 64];
+  constexpr int kBins = 2048, kWaves = kSelect / 64, kDeep = 8;
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t tmp[kWaves];
+  __shared__ uint32_t above[kWaves], equal[kWaves];
   __shared__ uint32_t found[2];  // digit, how many of it are still wanted
-  const int seq = blockIdx.x, t = threadIdx.x;
+  const int seq = blockIdx.x, t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t cap = (int64_t)a.table_pages * a.page;
   const int64_t given = a.lengths[seq];
   const int len = (int)(given < 0 ? 0 : given > cap ? cap : given);
@@ -54,77 +60,115 @@ __global__ __launch_bounds__(kSelect) void select_kernel(CacheEvict a, Moves mv)
   uint32_t edge = 0;  // stay: order > edge, and of those equal to it the first `want`
   if (len > a.keep) {
     uint32_t known = 0;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-      if (t < 256) hist[t] = 0;
+    for (int d = 0; d < 3 && want > 0; ++d) {
+      const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+      const uint32_t mask = d == 2 ? 1023u : 2047u;
+      hist[t] = hist[kSelect + t] = 0;
       __syncthreads();
-      for (int p = t; p < old; p += kSelect) {
-        const uint32_t o = order_of(w[p]);
-        if ((o & known) == edge) atomicAdd(&hist[o >> shift & 255u], 1u);
+      for (int64_t p0 = t; p0 < old; p0 += kSelect * kDeep) {
+        uint32_t o[kDeep];
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e) {
+          const int64_t p = p0 + e * kSelect;
+          o[e] = p < old ? order_of(w[p]) : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < kDeep; ++e)
+          if (p0 + e * kSelect < old && (o[e] & known) == edge) atomicAdd(&hist[o[e] >> shift & mask], 1u);
       }
       __syncthreads();
-      if (t < 64) {
-        // lane t has digits 255 - 4 t down to 252 - 4 t
-        uint32_t c[4], mine = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine += c[i] = hist[255 - 4 * t - i];
-        uint32_t before = wave_incl_scan(mine) - mine;
-        if (before < want && before + mine >= want) {
-          int i = 0;
-          while (before + c[i] < want) before += c[i++];
-          found[0] = 255 - 4 * t - i;
-          found[1] = want - before;
-        }
+      // thread t has bins 2047 - 2 t and 2046 - 2 t
+      const uint32_t c0 = hist[kBins - 1 - 2 * t], c1 = hist[kBins - 2 - 2 * t];
+      const uint32_t before = block_incl_scan<uint32_t, kSelect>(c0 + c1, tmp) - c0 - c1;
+      if (before < want && before + c0 + c1 >= want) {
+        const int i = before + c0 < want;
+        found[0] = kBins - 1 - 2 * t - i;
+        found[1] = want - before - (i ? c0 : 0u);
       }
       __syncthreads();
       edge |= found[0] << shift;
-      known |= 255u << shift;
+      known |= mask << shift;
       want = found[1];
       __syncthreads();
     }
     if (want == 0) edge = 0xFFFFFFFFu;  // keep == recent: no other stays
   }
-  // ranks in order; both counts of a round in one scan (each at most 1024)
-  uint32_t above = 0, equal = 0;  // of the rounds before
-  for (int p0 = 0; p0 < old; p0 += kSelect) {
-    const int p = p0 + t;
-    const uint32_t o = p < old ? order_of(w[p]) : 0u;
-    const bool gt = p < old && o > edge, eq = p < old && o == edge;
-    const uint32_t mine = (gt ? 1u << 16 : 0u) + (eq ? 1u : 0u);
-    const uint32_t upto = block_incl_scan<uint32_t, kSelect>(mine, tmp);
-    const uint32_t g0 = above + ((upto - mine) >> 16), e0 = equal + ((upto - mine) & 0xFFFFu);
-    if (gt || (eq && e0 < want)) {
-      const uint32_t r = g0 + min(e0, want);
-      kept[r] = p;
-      new_w[r] = w[p];
-      mv.list[(int64_t)seq * a.keep + r] = Move{place_of(a, seq, p), place_of(a, seq, (int)r)};
+  const int run = (int)(((int64_t)old + kSelect - 1) / kSelect * 64);  // a wave's places
+  const int64_t from = (int64_t)wave * run, to = min(from + run, (int64_t)old);
+  uint32_t gts = 0, eqs = 0;
+  for (int64_t p0 = from; p0 < to; p0 += 64 * kDeep) {
+    uint32_t o[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int64_t p = p0 + e * 64 + lane;
+      o[e] = p < to ? order_of(w[p]) : 0u;
     }
-    if (t == kSelect - 1) {
-      found[0] = upto >> 16;
-      found[1] = upto & 0xFFFFu;
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const bool in = p0 + e * 64 + lane < to;
+      gts += __popcll(__ballot(in && o[e] > edge));
+      eqs += __popcll(__ballot(in && o[e] == edge));
     }
-    __syncthreads();
-    above += found[0];
-    equal += found[1];
-    __syncthreads();
   }
-  const int stay = (int)(above + min(equal, want));
+  if (lane == 0) {
+    above[wave] = gts;
+    equal[wave] = eqs;
+  }
+  __syncthreads();
+  uint32_t g0 = 0, e0 = 0, all_g = 0, all_e = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < wave) {
+      g0 += above[i];
+      e0 += equal[i];
+    }
+    all_g += above[i];
+    all_e += equal[i];
+  }
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  for (int64_t p0 = from; p0 < to; p0 += 64 * kDeep) {
+    float v[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int64_t p = p0 + e * 64 + lane;
+      v[e] = p < to ? w[p] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e) {
+      const int64_t p = p0 + e * 64 + lane;
+      const uint32_t o = order_of(v[e]);
+      const bool gt = p < to && o > edge, eq = p < to && o == edge;
+      const uint64_t bg = __ballot(gt), be = __ballot(eq);
+      const uint32_t ge = e0 + __popcll(be & below);
+      if (gt || (eq && ge < want)) {
+        const uint32_t r = g0 + __popcll(bg & below) + min(ge, want);
+        kept[r] = (int)p;
+        new_w[r] = v[e];
+      }
+      g0 += __popcll(bg);
+      e0 += __popcll(be);
+    }
+  }
+  const int stay = (int)(all_g + min(all_e, want)), count = stay + len - old;
   for (int p = old + t; p < len; p += kSelect) {
-    const int r = stay + p - old;
-    kept[r] = p;
-    new_w[r] = w[p];
-    mv.list[(int64_t)seq * a.keep + r] = Move{place_of(a, seq, p), place_of(a, seq, r)};
+    kept[stay + p - old] = p;
+    new_w[stay + p - old] = w[p];
   }
-  const int count = stay + len - old;
-  for (int r = count + t; r < a.keep; r += kSelect) kept[r] = -1;
-  for (int64_t r = count + t; r < cap; r += kSelect) new_w[r] = 0.0f;
+  for (int64_t r = (int64_t)count + t; r < a.keep; r += kSelect) kept[r] = -1;
+  for (int64_t r = (int64_t)count + t; r < cap; r += kSelect) new_w[r] = 0.0f;
   if (t == 0) {
     found[0] = (uint32_t)count;
     a.new_lengths[seq] = count;
   }
+  __threadfence_block();
   __syncthreads();
-  // ranks are in order: those before the first gap stay where they are
-  for (int r = t; r < count; r += kSelect)
-    if (kept[r] != r && (r == 0 || kept[r - 1] == r - 1)) found[0] = (uint32_t)r;
+  // the moves; ranks are in order, so those before the first gap stay where they are
+  for (int64_t r = t; r < count; r += kSelect) {
+    const int p = kept[r];
+    if (p != r) {
+      if (r == 0 || kept[r - 1] == r - 1) found[0] = (uint32_t)r;
+      mv.list[(int64_t)seq * a.keep + r] = Move{place_of(a, seq, p), place_of(a, seq, (int)r)};
+    }
+  }
   __syncthreads();
   if (t == 0) {
     mv.span[2 * seq] = (int32_t)found[0];
@@ -160,11 +204,11 @@ __device__ __forceinline__ void move_rows(uint8_t* plane, int64_t row_bytes, int
   Held held[2][kDeep] = {};
   int64_t to[2][kDeep];
   Move mv[kDeep];
-  auto entries = [&](int r0) {
+  auto entries = [&](uint32_t r0) {
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
-      const int r = r0 + u * rpt + row;
-      mv[u] = r < count ? list[r] : Move{-1, -1};
+      const uint32_t r = r0 + u * rpt + row;  // up to three rounds past count
+      mv[u] = r < (uint32_t)count ? list[r] : Move{-1, -1};
     }
   };
   auto fetch = [&](Held(&v)[kDeep], int64_t(&dst)[kDeep]) {
@@ -188,7 +232,7 @@ __device__ __forceinline__ void move_rows(uint8_t* plane, int64_t row_bytes, int
   entries(first);
   fetch(held[0], to[0]);
   entries(first + round);
-  for (int r0 = first; r0 < count; r0 += 2 * round) {
+  for (uint32_t r0 = first; r0 < (uint32_t)count; r0 += 2 * round) {
     arrived(held[0]);
     __syncthreads();
     fetch(held[1], to[1]);
