@@ -491,6 +491,7 @@ def _T():
         t.bytes = (torch.float8_e8m0fnu, torch.uint8)
         t.stream = torch._C._cuda_getCurrentRawStream
         t.current = torch.cuda.current_device
+        t.forward_ad = forward_ad
         t.dual = forward_ad.unpack_dual
         t.tracing = torch.jit.is_tracing
         t.torch = torch
@@ -1060,8 +1061,10 @@ def _vector(A, device: int, what, n, dtypes, names):
 
 
 def _no_tangent(name, *tensors) -> None:
-    dual = _T().dual
-    if any(dual(t).tangent is not None for t in tensors):
+    t = _T()
+    if t.forward_ad._current_level < 0:
+        return  # no level of the forward mode is entered, so no tensor has a tangent
+    if any(t.dual(x).tangent is not None for x in tensors):
         raise EmeansError(f"EINVAL: {name} has no forward-mode derivative (an input has a tangent)")
 
 
@@ -1083,11 +1086,25 @@ def rotary_freqs(turned: int, base: float = 10000.0, device="cuda"):
 
 def _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps):
     """The arguments that both passes of norm_rotate share, and the sizes."""
+    dev, gt, half = _rotate_checks(q, k, q_weight, k_weight, positions, freqs)
+    return dev, _rotate_list(q, k, q_weight, k_weight, positions, freqs, gt, half, eps)
+
+
+def _rotate_list(q, k, q_weight, k_weight, positions, freqs, gt, half, eps):
+    n, hq, w = q.shape
+    qs, ks = q.stride(), k.stride()
+    t = _T()
+    return (q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], t.numbers[q.dtype], n, hq,
+            k.shape[1], w, q_weight.data_ptr(), k_weight.data_ptr(), gt, positions.data_ptr(),
+            8 if positions.dtype is t.torch.int64 else 4, freqs.data_ptr(), half, eps)
+
+
+def _rotate_checks(q, k, q_weight, k_weight, positions, freqs):
     t = _T()
     dev = _device_of(q, "q")
-    dt = _number(q.dtype, "q")
-    n, hq, w, qr, qh = _heads(q, dev, "q")
-    nk, hk, wk, kr, kh = _heads(k, dev, "k", q.dtype)
+    _number(q.dtype, "q")
+    n, _, w, _, _ = _heads(q, dev, "q")
+    nk, _, wk, _, _ = _heads(k, dev, "k", q.dtype)
     if nk != n or wk != w:
         raise EmeansError(f"EINVAL: k must be {n} x heads x {w} (got {tuple(k.shape)})")
     gt = _number(q_weight.dtype, "q_weight")
@@ -1095,20 +1112,16 @@ def _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps):
     _vector(q_weight, dev, "q_weight", w, (q_weight.dtype,), names)
     _vector(k_weight, dev, "k_weight", w, (q_weight.dtype,), names)
     _vector(positions, dev, "positions", n, (t.torch.int32, t.torch.int64), "int32 or int64")
-    half = _vector(freqs, dev, "freqs", None, (t.torch.float64,), "float64")
-    return dev, (n, hq, hk, w), (
-        q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, dt, n, hq, hk, w, q_weight.data_ptr(),
-        k_weight.data_ptr(), gt, positions.data_ptr(),
-        8 if positions.dtype is t.torch.int64 else 4, freqs.data_ptr(), half, eps)
+    return dev, gt, _vector(freqs, dev, "freqs", None, (t.torch.float64,), "float64")
 
 
 def _norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps):
-    dev, (n, hq, hk, w), args = _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps)
+    dev, args = _rotate_args(q, k, q_weight, k_weight, positions, freqs, eps)
 
     def call(st):
-        empty = _T().torch.empty
-        qo = empty((n, hq, w), dtype=q.dtype, device=q.device)
-        ko = empty((n, hk, w), dtype=q.dtype, device=q.device)
+        empty, device = _T().torch.empty, q.device
+        qo = empty(q.shape, dtype=q.dtype, device=device)
+        ko = empty(k.shape, dtype=q.dtype, device=device)
         _check(lib().emeans_norm_rotate(*args, qo.data_ptr(), ko.data_ptr(), st))
         return qo, ko
 
@@ -1133,24 +1146,24 @@ def _rotate_fn():
             @staticmethod
             @torch.autograd.function.once_differentiable
             def backward(ctx, dqo, dko):
-                saved = ctx.saved_tensors
-                dev, (n, hq, hk, w), args = _rotate_args(*saved, ctx.eps)
-                q, gq = saved[0], saved[2]
-                L = lib()
+                q, k, gq, gk, positions, freqs = ctx.saved_tensors
+                L, dtype, device = lib(), q.dtype, q.device
+                args = _rotate_list(q, k, gq, gk, positions, freqs, _T().numbers[gq.dtype],
+                                    freqs.shape[0], ctx.eps)
 
                 def call(st):
                     a, b = _adjacent(dqo), _adjacent(dko)
-                    dq = torch.empty((n, hq, w), dtype=q.dtype, device=q.device)
-                    dk = torch.empty((n, hk, w), dtype=q.dtype, device=q.device)
-                    dgq, dgk = torch.empty((2, w), dtype=gq.dtype, device=q.device).unbind(0)
-                    work = _work(L.emeans_norm_rotate_work(n, w), q.device)
+                    dq, dk = (torch.empty(x.shape, dtype=dtype, device=device) for x in (q, k))
+                    dgq, dgk = (torch.empty(gq.shape, dtype=gq.dtype, device=device) for _ in "qk")
+                    work = _work(L.emeans_norm_rotate_work(q.shape[0], q.shape[2]), device)
+                    sa, sb = a.stride(), b.stride()
                     _check(L.emeans_norm_rotate_gradient(
-                        *args, a.data_ptr(), a.stride(0), a.stride(1), b.data_ptr(), b.stride(0),
-                        b.stride(1), dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(),
-                        _ptr(work), st))
+                        *args, a.data_ptr(), sa[0], sa[1], b.data_ptr(), sb[0], sb[1],
+                        dq.data_ptr(), dk.data_ptr(), dgq.data_ptr(), dgk.data_ptr(), _ptr(work),
+                        st))
                     return dq, dk, dgq, dgk
 
-                return *_run(dev, None, call), None, None, None
+                return *_run(q.get_device(), None, call), None, None, None
 
         _rotate_function = NormRotate
     return _rotate_function
@@ -1188,15 +1201,24 @@ def _aligned(t):
     return t.contiguous() if t.data_ptr() % 16 == 0 or not t.is_contiguous() else t.clone()
 
 
-def _attend_args(q, k, v, starts, k_starts, causal, scale):
-    """The arguments that both passes of attend share, and the sizes."""
+def _attend_list(q, k, v, starts, k_starts, causal, scale):
+    """The arguments that both passes of attend share."""
+    n, hq, w = q.shape
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    return (q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            _T().numbers[q.dtype], n, k.shape[0], hq, k.shape[1], w, starts.data_ptr(),
+            k_starts.data_ptr(), starts.shape[0] - 1, 1 if causal else 0,
+            w ** -0.5 if scale is None else scale)
+
+
+def _attend_checks(q, k, v, starts, k_starts):
     torch = _T().torch
     dev = _device_of(q, "q")
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise EmeansError(f"EDTYPE: q {q.dtype} not supported (bfloat16 or float16)")
-    n, hq, w, qr, qh = _heads(q, dev, "q")
-    nk, hk, wk, kr, kh = _heads(k, dev, "k", q.dtype)
-    nv, hv, wv, vr, vh = _heads(v, dev, "v", q.dtype)
+    n, hq, w, _, _ = _heads(q, dev, "q")
+    nk, hk, wk, _, _ = _heads(k, dev, "k", q.dtype)
+    nv, hv, wv, _, _ = _heads(v, dev, "v", q.dtype)
     if wk != w or (nv, hv, wv) != (nk, hk, wk):
         raise EmeansError(f"EINVAL: k and v must be rows x heads x {w} of one shape (got "
                           f"{tuple(k.shape)} and {tuple(v.shape)})")
@@ -1211,17 +1233,15 @@ def _attend_args(q, k, v, starts, k_starts, causal, scale):
         _vector(k_starts, dev, "k_starts", seqs + 1, (torch.int32,), "int32")
     elif nk != n:
         raise EmeansError(f"EINVAL: k and v must have the {n} rows of q, or k_starts be given")
-    return dev, (n, hq, w), (nk, hk, w), (
-        q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, v.data_ptr(), vr, vh,
-        BF16 if q.dtype is torch.bfloat16 else F16, n, nk, hq, hk, w, starts.data_ptr(),
-        k_starts.data_ptr(), seqs, 1 if causal else 0, w ** -0.5 if scale is None else scale)
+    return dev
 
 
 def _attend(q, k, v, starts, k_starts, causal, scale, keep):
-    dev, shape, _, args = _attend_args(q, k, v, starts, k_starts, causal, scale)
+    dev = _attend_checks(q, k, v, starts, k_starts)
+    args = _attend_list(q, k, v, starts, k_starts, causal, scale)
 
     def call(st):
-        torch = _T().torch
+        torch, shape = _T().torch, q.shape
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
         lse = rest = None
         if keep:  # what the gradients need
@@ -1245,7 +1265,6 @@ def _attend_fn():
             @staticmethod
             def forward(ctx, q, k, v, starts, k_starts, causal, scale):
                 out, lse, rest = _attend(q, k, v, starts, k_starts, causal, scale, True)
-                ctx.one = k_starts is starts
                 ctx.save_for_backward(q, k, v, starts, k_starts, out, lse, rest)
                 ctx.args = causal, scale
                 return out
@@ -1254,22 +1273,20 @@ def _attend_fn():
             @torch.autograd.function.once_differentiable
             def backward(ctx, dout):
                 q, k, v, starts, k_starts, out, lse, rest = ctx.saved_tensors
-                dev, shape, k_shape, args = _attend_args(q, k, v, starts,
-                                                         starts if ctx.one else k_starts, *ctx.args)
-                L = lib()
+                args = _attend_list(q, k, v, starts, k_starts, *ctx.args)
+                L, dtype, device, shape = lib(), q.dtype, q.device, q.shape
 
                 def call(st):
                     g = _aligned(dout)
-                    dq = torch.empty(shape, dtype=q.dtype, device=q.device)
-                    dk, dv = (torch.empty(k_shape, dtype=q.dtype, device=q.device) for _ in range(2))
-                    work = _work(L.emeans_attend_work(shape[0], shape[1]), q.device)
+                    dq, dk, dv = (torch.empty(x.shape, dtype=dtype, device=device) for x in (q, k, v))
+                    work = _work(L.emeans_attend_work(shape[0], shape[1]), device)
                     _check(L.emeans_attend_gradient(
                         *args, out.data_ptr(), lse.data_ptr(), rest.data_ptr(), g.data_ptr(),
                         g.stride(0), g.stride(1), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                         _ptr(work), st))
                     return dq, dk, dv
 
-                return *_run(dev, None, call), None, None, None, None
+                return *_run(q.get_device(), None, call), None, None, None, None
 
         _attend_function = Attend
     return _attend_function

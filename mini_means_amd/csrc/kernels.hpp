@@ -358,11 +358,6 @@ struct NormRotate {
   float* part;  // norm_rotate_groups(n) x 2 x width
   void* dgq;
   void* dgk;
-
-  __device__ float weight(const void* w, int c) const {
-    return gdt == 0 ? static_cast<const float*>(w)[c]
-                    : half_to_f32(static_cast<const uint16_t*>(w)[c], gdt == 4);
-  }
 };
 int norm_rotate_groups(int64_t n);
 hipError_t launch_norm_rotate(const NormRotate& a, hipStream_t st);

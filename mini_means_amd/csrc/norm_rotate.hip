@@ -31,19 +31,21 @@ __device__ __forceinline__ Chunk chunk_of(int j, int half, int width) {
   return {at, at + (width - 2 * half) / 2, -1};
 }
 
+// E values as they lie in memory (16 bytes, or 8 of a 16-bit type), and as numbers.
 template <int DT, int E>
-__device__ __forceinline__ void load_run(const void* base, int64_t at, float (&v)[E]) {
-  if constexpr (E == 8) {
-    load8<DT>(base, at, 8, v);
-  } else if constexpr (DT == 0) {
-    const f32x4 a = load_any<f32x4>(static_cast<const float*>(base) + at);
+using Run = std::conditional_t<DT == 0 || E == 8, u32x4, u32x2>;
+
+template <int DT, int E>
+__device__ __forceinline__ Run<DT, E> load_run(const void* base, int64_t at) {
+  return load_any<Run<DT, E>>(static_cast<const uint8_t*>(base) + at * (DT == 0 ? 4 : 2));
+}
+
+template <int DT, int E>
+__device__ __forceinline__ void numbers_of(const Run<DT, E>& w, float (&v)[E]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i];
-  } else {
-    const u32x2 a = load_any<u32x2>(static_cast<const uint16_t*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = half_to_f32((uint16_t)(a[i >> 1] >> (16 * (i & 1))), DT == 4);
-  }
+  for (int i = 0; i < E; ++i)
+    v[i] = DT == 0 ? __uint_as_float(w[i])
+                   : half_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1))), DT == 4);
 }
 
 template <int DT, int E>
@@ -59,6 +61,55 @@ __device__ __forceinline__ void store_run(void* base, int64_t at, const float (&
                          pack2<DT>(v[6], v[7])});
     else
       store_any(p, u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])});
+  }
+}
+
+// A lane's weights of both sides: E values at lo, then E at hi.
+template <int DT, int E>
+__device__ __forceinline__ void weights_of(const NormRotate& a, const Chunk& c, float (&g)[2][2 * E]) {
+  Run<DT, E> w[2][2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const void* p = s ? a.gk : a.gq;
+    w[s][0] = load_run<DT, E>(p, c.lo);
+    w[s][1] = load_run<DT, E>(p, c.hi);
+  }
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float x[E], y[E];
+    numbers_of<DT, E>(w[s][0], x);
+    numbers_of<DT, E>(w[s][1], y);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      g[s][i] = x[i];
+      g[s][E + i] = y[i];
+    }
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void all_weights(const NormRotate& a, const Chunk& c, float (&g)[2][2 * E]) {
+  if (a.gdt == 0) {
+    if constexpr (E == 4) {
+      weights_of<0, 4>(a, c, g);
+    } else {  // in two halves of 16 bytes
+      float x[2][8], y[2][8];
+      weights_of<0, 4>(a, c, x);
+      weights_of<0, 4>(a, {c.lo + 4, c.hi + 4, 0}, y);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g[s][i] = x[s][i];
+          g[s][4 + i] = y[s][i];
+          g[s][8 + i] = x[s][4 + i];
+          g[s][12 + i] = y[s][4 + i];
+        }
+    }
+  } else if (a.gdt == 1) {
+    weights_of<1, E>(a, c, g);
+  } else {
+    weights_of<4, E>(a, c, g);
   }
 }
 
@@ -126,31 +177,36 @@ __global__ __launch_bounds__(256) void norm_rotate_kernel(NormRotate a, int64_t 
   const bool on = j * E * 2 < a.width;
   const Chunk c = chunk_of<E>(on ? j : 0, a.half, a.width);
   float g[2][2 * E];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const void* w = s ? a.gk : a.gq;
-      g[s][i] = a.weight(w, c.lo + i);
-      g[s][E + i] = a.weight(w, c.hi + i);
-    }
+  all_weights<E>(a, c, g);
+  // a lane's next head is on its way while this one is worked on, and the first while the
+  // angles are made; past the last it is the last again (a whole wave takes part in the
+  // sums), and lanes past the width have the first chunk
+  const int items = tokens * heads, first = threadIdx.x / L;
+  auto head = [&](int i, int& t) {
+    const int it = min(i, items - 1);
+    t = it / heads;
+    return head_of(a, t0 + t, it - t * heads);
+  };
+  int t, next_t;
+  Head hd, next = head(first, next_t);
+  Run<DT, E> lo = load_run<DT, E>(next.x, next.at + c.lo), hi = load_run<DT, E>(next.x, next.at + c.hi);
   turns_of(a, t0, tokens, turn);
   __syncthreads();
   const float inv = 1.0f / (float)a.width;
-  const int items = tokens * heads;
-  for (int i = threadIdx.x / L; i - (int)(threadIdx.x / L) < items; i += 256 / L) {
-    const bool live = i < items;  // a whole wave takes part in the sums
-    const int it = live ? i : items - 1;
-    const int t = it / heads;
-    const Head hd = head_of(a, t0 + t, it - t * heads);
+  for (int i = first; i - first < items; i += 256 / L) {
+    const bool live = i < items;
     float x[E], y[E];
-    if (on) {
-      load_run<DT, E>(hd.x, hd.at + c.lo, x);
-      load_run<DT, E>(hd.x, hd.at + c.hi, y);
-    } else {
+    numbers_of<DT, E>(lo, x);
+    numbers_of<DT, E>(hi, y);
+    if (!on) {
 #pragma unroll
       for (int e = 0; e < E; ++e) x[e] = y[e] = 0.0f;
     }
+    hd = next;
+    t = next_t;
+    next = head(i + 256 / L, next_t);
+    lo = load_run<DT, E>(next.x, next.at + c.lo);
+    hi = load_run<DT, E>(next.x, next.at + c.hi);
     float sq = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) sq += x[e] * x[e] + y[e] * y[e];
@@ -188,15 +244,11 @@ __global__ __launch_bounds__(256) void norm_rotate_back_kernel(NormRotate a, int
   const bool on = j * E * 2 < a.width;
   const Chunk c = chunk_of<E>(on ? j : 0, a.half, a.width);
   float g[2][2 * E], dg[2][2 * E];
+  all_weights<E>(a, c, g);
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const void* w = s ? a.gk : a.gq;
-      g[s][i] = a.weight(w, c.lo + i);
-      g[s][E + i] = a.weight(w, c.hi + i);
-      dg[s][i] = dg[s][E + i] = 0.0f;
-    }
+    for (int i = 0; i < 2 * E; ++i) dg[s][i] = 0.0f;
   const float inv = 1.0f / (float)a.width;
   for (int64_t t0 = (int64_t)blockIdx.x * T; t0 < a.n; t0 += (int64_t)gridDim.x * T) {
     const int tokens = (int)min((int64_t)T, a.n - t0);
@@ -213,12 +265,15 @@ __global__ __launch_bounds__(256) void norm_rotate_back_kernel(NormRotate a, int
       const int64_t dat = hd.key ? (t0 + t) * a.dk_rs + (h - a.hq) * a.dk_hs
                                  : (t0 + t) * a.dq_rs + h * a.dq_hs;
       float x[E], y[E], u[E], v[E];
-      if (on && live) {
-        load_run<DT, E>(hd.x, hd.at + c.lo, x);
-        load_run<DT, E>(hd.x, hd.at + c.hi, y);
-        load_run<DT, E>(dy, dat + c.lo, u);
-        load_run<DT, E>(dy, dat + c.hi, v);
-      } else {
+      {
+        const Run<DT, E> xr = load_run<DT, E>(hd.x, hd.at + c.lo), yr = load_run<DT, E>(hd.x, hd.at + c.hi),
+                         ur = load_run<DT, E>(dy, dat + c.lo), vr = load_run<DT, E>(dy, dat + c.hi);
+        numbers_of<DT, E>(xr, x);
+        numbers_of<DT, E>(yr, y);
+        numbers_of<DT, E>(ur, u);
+        numbers_of<DT, E>(vr, v);
+      }
+      if (!on || !live) {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = y[e] = u[e] = v[e] = 0.0f;
       }
