@@ -1422,6 +1422,8 @@ def cache_evict(stores, table, lengths, weights, keep: int, *, recent: int = 0, 
     shape = found[0][2]
     if any(f[2][:2] != shape[:2] for f in found) or not all(f[1] for f in found):
         raise EmeansError("EINVAL: the stores must have the same pages of rows")
+    if shape[0] and len({s[0].data_ptr() for s in stores}) < len(stores):
+        raise EmeansError("EINVAL: a store is given twice")
     seqs, pages, ld, places = _places(dev, table, lengths, shape[1])
     torch = _T().torch
     wn, wd, wld = _matrix(weights, dev, "weights", (torch.float32,), "float32")

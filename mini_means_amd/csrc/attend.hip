@@ -855,7 +855,7 @@ hipError_t in_launches(int64_t wgs, GO go) {
 template <bool F16, int W>
 hipError_t forward_t(const Attend& a, hipStream_t st) {
   constexpr int NW = 4;
-  const int64_t tiles = a.n / (NW * 32) + a.seqs;
+  const int64_t tiles = a.seqs ? a.n / (NW * 32) + a.seqs : 0;
   return in_launches(tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
     attend_kernel<F16, W, NW><<<grid, NW * 64, 0, st>>>(a, wg0, tiles);
   });
@@ -868,7 +868,7 @@ hipError_t backward_t(const Attend& a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int64_t q_tiles = a.n / 128 + a.seqs, k_tiles = a.nk / 128 + a.seqs;
+  const int64_t q_tiles = a.seqs ? a.n / 128 + a.seqs : 0, k_tiles = a.seqs ? a.nk / 128 + a.seqs : 0;
   const hipError_t e = in_launches(q_tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
     query_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, q_tiles);
   });

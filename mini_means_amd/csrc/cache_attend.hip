@@ -122,16 +122,15 @@ struct Places {
 };
 
 // W: width rounded up to 64 or 128. ONE: a head lies in one block, so that its scale is a
-// factor of the score and of the softmax weight, and the store is under 4 GiB; else every
-// 16 codes have a scale of their own and rows are found with 64 bits.
+// factor of the score and of the softmax weight (and the store has under 2^32 rows); else
+// every 16 codes have a scale of their own.
 template <int DT, bool I8, int W, bool SCORES, bool ONE>
 __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
   constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3;
   constexpr int KJ = W / 64, VD = W / 16;
   typedef std::conditional_t<ONE, uint32_t, int64_t> At;
   const CacheAttend& a = s.a;
-  // per place: the row's first byte (general: its row, -1 outside the store), and for ONE
-  // both scales, the keys' times scale log2 e; the values' is 0 where there is no place.
+  // per place: its row of the store (general: -1 outside the store), and for ONE both scales, the keys' times scale log2 e; the values' is 0 where there is no place.
   // Afterwards the waves' results.
   constexpr int kRoom = kMaxPart * (ONE ? 12 : 8), kJoin = kWaves * kHeads * (W + 4) * 4;
   __shared__ __align__(16) uint8_t room[kRoom > kJoin ? kRoom : kJoin];
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
     return;
   }
   const int cnt = min(s.part, len - p0);
-  const int64_t d = (int64_t)a.hk * a.width;
+  const uint32_t d = (uint32_t)a.hk * a.width;
   const int col = kvh * a.width;
   const float c2 = a.scale * kLog2e;
   if (threadIdx.x == 0) holes = 0;
@@ -198,7 +197,7 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
       if (i >= whole) break;
       if (row[e] < 0) holes = 1;
       if constexpr (ONE) {
-        rows[i] = (uint32_t)(max(row[e], (int64_t)0) * d);
+        rows[i] = (uint32_t)max(row[e], (int64_t)0);
         k_scale[i] = scale_value(ks[e]) * c2;
         v_scale[i] = row[e] >= 0 && i < cnt ? scale_value(vs[e]) : 0.0f;
       } else {
@@ -234,7 +233,7 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
       if (!ONE) row = max(row, (At)0);
 #pragma unroll
       for (int j = 0; j < KJ; ++j) {
-        x.k[u][j] = load_any<u32x4>(a.k.codes + (ONE ? row + kc[j] : row * d + kc[j]));
+        x.k[u][j] = load_any<u32x4>(a.k.codes + (uint64_t)row * d + kc[j]);
         if constexpr (!ONE) x.ks[u][j] = a.k.scales[row * s.nb + kb[j]];
       }
     }
@@ -242,7 +241,7 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
     for (int e = 0; e < 8; ++e) {
       At row = rows[t + 16 * (e >> 2) + 4 * g + (e & 3)];
       if (!ONE) row = max(row, (At)0);
-      const uint8_t* p = a.v.codes + (ONE ? row + vc : row * d + vc);
+      const uint8_t* p = a.v.codes + (uint64_t)row * d + vc;
       if constexpr (VD == 8)
         x.v[e] = load_any<u32x2>(p);
       else
@@ -527,7 +526,7 @@ Room room_of(int64_t seqs, int64_t hq, int64_t width, int64_t parts, int64_t par
 template <int DT, bool I8, int W>
 hipError_t split_t(Split& s, int64_t wgs, bool weights, hipStream_t st) {
   // a head in one block, whichever: block a multiple of width, or width itself
-  const bool one = s.a.block % s.a.width == 0 && s.a.rows * s.a.hk * s.a.width < ((int64_t)1 << 32);
+  const bool one = s.a.block % s.a.width == 0 && s.a.rows < ((int64_t)1 << 32);
   for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
     const unsigned grid = (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups);
     s.wg0 = wg0;

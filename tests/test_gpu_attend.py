@@ -235,8 +235,10 @@ def test_attend_of_nothing_and_of_starts_outside_the_tensors(mm):
     q = torch.randn(40, 2, 64, device="cuda").bfloat16().requires_grad_()
     o = mm.attend(q, none, none, torch.tensor([0, 40], device="cuda").int(), k_starts=torch.zeros(2, device="cuda").int())
     assert not o.any() and not torch.autograd.grad(o, q, o.detach())[0].any()
-    o = mm.attend(q, q, q, zero)           # no sequence at all
-    assert not o.any()
+    for rows in (40, 300):                 # no sequence at all
+        x = torch.ones(rows, 2, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+        o = mm.attend(x, x, x, zero)
+        assert not o.any() and not torch.autograd.grad(o, x, torch.ones_like(o))[0].any()
     # starts are cut to the tensors: no row outside them is read
     for s in ([-5, 1000], [0, 50], [39, 20, 45]):
         starts = torch.tensor(s, device="cuda").int()

@@ -380,6 +380,37 @@ def test_cache_evict_of_several_stores_and_long_sequences(mm, stores):
     check_evict(mm, rng, [9000, 0, 4097], 3000, 100, 128, 16, 128, "i8", stores, columns=600)
 
 
+def test_refusals_of_the_store_calls(mm):
+    """What a caller can get wrong with tensors on the GPU: refused before any device work."""
+    import torch
+    keys, values = (mm.cache_new((4, 16), 128, block=64) for _ in range(2))
+    other = mm.cache_new((4, 8), 128, block=64)
+    i8 = mm.cache_new((4, 16), 128, block=64, dtype=torch.int8)
+    q = torch.zeros(2, 4, 64, device="cuda")
+    table, lens = torch.zeros(2, 3, device="cuda").int(), torch.zeros(2, device="cuda").int()
+    w = torch.zeros(2, 48, device="cuda")
+    attend = lambda q=q, k=keys, v=values, t=table, n=lens, **kw: mm.cache_attend(q, k, v, t, n, block=64, **kw)  # noqa: E731
+    evict = lambda s=(keys, values), t=table, n=lens, w=w, keep=5, **kw: mm.cache_evict(s, t, n, w, keep, block=64, **kw)  # noqa: E731
+    attend(weights=w)
+    evict()
+    for call, word in (
+            (lambda: attend(q=q.double()), "EDTYPE"), (lambda: attend(q=q[:, :3]), "EINVAL"),
+            (lambda: attend(q=q[:, :, :40]), "EINVAL"), (lambda: attend(q=q[:1]), "EINVAL"),
+            (lambda: attend(q=q.transpose(1, 2)), "EINVAL"), (lambda: attend(v=other), "EINVAL"),
+            (lambda: attend(v=i8), "EINVAL"), (lambda: attend(v=values[0]), "EINVAL"),
+            (lambda: attend(t=table.long()), "EDTYPE"), (lambda: attend(n=lens.long()), "EDTYPE"),
+            (lambda: attend(n=lens[:1]), "EINVAL"), (lambda: attend(weights=w[:, :40]), "EINVAL"),
+            (lambda: attend(weights=w.half()), "EDTYPE"), (lambda: attend(weights=w[:1].expand(2, 48)), "EINVAL"),
+            (lambda: attend(scale=float("nan")), "EINVAL"), (lambda: attend(k=keys[0].cpu()), "EINVAL"),
+            (lambda: attend(n=lens.cpu()), "ENOTDEVICE"),
+            (lambda: evict(s=()), "EINVAL"), (lambda: evict(s=(keys, keys)), "EINVAL"),
+            (lambda: evict(s=(keys, other)), "EINVAL"), (lambda: evict(w=w[:, 1:]), "EINVAL"),
+            (lambda: evict(keep=-1), "EINVAL"), (lambda: evict(keep=3, recent=4), "EINVAL"),
+            (lambda: evict(n=lens.cpu()), "ENOTDEVICE")):
+        with pytest.raises(mm.EmeansError, match=word):
+            call()
+
+
 # ---- streams, graphs ---------------------------------------------------------
 
 def test_on_a_given_stream_and_in_graphs(mm):
