@@ -234,15 +234,18 @@ struct Place {
 
 __device__ __forceinline__ Place place_of(const int32_t* starts, int seqs, int64_t n, int rows,
                                           int64_t tile) {
-  int lo = 0, hi = seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)(max(0, min(starts[mid], (int)n)) / rows) + mid <= tile)
-      lo = mid;
-    else
-      hi = mid;
+  const int lane = threadIdx.x & 63;
+  auto first_tile = [&](int s) { return (int64_t)(max(0, min(starts[s], (int)n)) / rows) + s; };
+  // the last sequence whose first tile is not after this one, 64 of them looked at in one
+  // read: a search by halves would be a chain of ten reads for 1000 sequences
+  int lo = 0, len = seqs;
+  while (len > 1) {
+    const int step = (len + 63) / 64, s = lane * step;
+    const int i = max(__popcll(__ballot(s < len && first_tile(lo + min(s, len - 1)) <= tile)) - 1, 0);
+    lo += i * step;
+    len = min(step, len - i * step);
   }
-  const int64_t j = tile - (max(0, min(starts[lo], (int)n)) / rows + lo);
+  const int64_t j = tile - first_tile(lo);
   return {lo, j < 0 || j * rows > 0x7FFFFFFF ? 0x7FFFFFFF : (int)(j * rows)};
 }
 
