@@ -10,12 +10,18 @@
 // summed over the query heads of a group in order): seven products instead of the
 // five that atomic sums of dQ would leave, but the same bits each time.
 //
-// Bound by the matrix unit, beside it by LDS reads and the exponentials. All products
+// Bound by the matrix unit and, as much, by the vector instructions beside it (143 for a
+// wave's 32 x 64 scores, whose 32 products take 1088 cycles). All products
 // are 32 x 32 x 16 MFMAs laid out so that nothing crosses lanes between them: with A
 // the tile's rows and B a wave's own 32 rows (kept in registers), a lane holds 16 of
 // 32 results of one own row, and these are the B operand of the next product when
 // its sum index is counted in the order in which they stand. Its A operand is the
-// tile transposed, which ds_read_b64_tr_b16 reads from the same LDS rows.
+// tile transposed, which ds_read_b64_tr_b16 reads from the same LDS rows. Two workgroups of
+// four waves share a CU: one wave's products run beside the other's exponentials.
+// Measured, 32 query and 8 key-value heads of 128 in bf16, causal: 16384 tokens 2.08 to 2.24
+// ms (980 to 1060 TFLOP/s; the library's product of 8192 a side 1223); seven sequences of
+// up to 4000 tokens 0.39 ms, dQ 0.53, dK and dV 0.85. 33 sequences of up to 500 tokens, 16
+// heads of 64 in fp16, not causal: 33 us.
 #include <type_traits>
 
 #include "block.hpp"
@@ -682,7 +688,7 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
 // dK and dV: a workgroup owns 128 key rows of a key-value head and goes over the
 // queries that see them, head by head of the group, in tiles of 32; P and dS of a tile
 // have a lane's key row as column. K stays in registers and V in LDS, which leaves room
-// for two waves on a SIMD.
+// for two waves on a SIMD (both in registers and one wave: 1.56 against 0.88 ms).
 template <bool F16, int W>
 __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
   constexpr int NW = 4, ROWS = NW * 32, R = 32;

@@ -14,6 +14,11 @@
 // places are counted in that order. fp16 and fp32 queries, and the softmax weights
 // beside them, are sums of two and three bf16 terms (16 and 24 bits), bf16 ones
 // are one term.
+//
+// Measured, 32 query and 8 key-value heads of 128, E4M3, bf16: one sequence of 131072 places
+// 51 us and 8 for the join (5.3 TB/s; a large copy 5.0), 64 sequences of up to 8192 123 and
+// 6 (4.4 TB/s), 16 of up to 4000 with weights 23 and 5. With each load in a branch of its
+// own, and none a round ahead, the first took 127 us.
 #include <type_traits>
 
 #include "block.hpp"

@@ -6,7 +6,9 @@
 //
 // Bound by HBM and by latency: a workgroup per sequence finds the threshold digit by
 // digit (the weights stay in L2) and lists the moves; then workgroups of a sequence and
-// 128 bytes of a row each go along the list.
+// 128 bytes of a row each go along the list. Measured, 16 sequences of up to 8192 rows cut to
+// 2048, two stores of 1024 codes a row: 20 us for the lists (latency: a workgroup each),
+// 18 us for the rows (5.9 TB/s; 110 us with 128 rows in flight per workgroup, not 512).
 #include <type_traits>
 
 #include "block.hpp"

@@ -6,7 +6,11 @@
 // and u = dy turned back: dx = r (g u) - x r^3 mean(g u x), dg = sum of u x r over
 // tokens and heads.
 //
-// Bound by HBM: each value is read and written once, with about ten operations.
+// Bound by HBM: each value is read and written once, with about ten operations. A
+// workgroup takes whole tokens, so that an angle is made once for all heads. Measured:
+// 16384 tokens of 40 heads of 128 in bf16 66 us (5.1 TB/s; 82 with a lane's 32 weights read
+// one by one), 5 tokens 5 us; 4099 tokens of 16 heads of 96 in fp32 13 us, their gradients
+// 17 and 4 us.
 #include <type_traits>
 
 #include "block.hpp"
