@@ -101,7 +101,7 @@ struct TileLoads {
         src = from;
         off += (uint32_t)((more - max(row0 + more + row[q] - last, 0)) * (int)rs) * 2;
       }
-      if (row[q] >= 0) lds_load16_from(scalar_base(src), off, lds + (i * NW + wave) * 1024);
+      if (row[q] >= 0) lds_load16_from(src, off, lds + (i * NW + wave) * 1024);
     }
   }
 };
@@ -717,7 +717,11 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   const int64_t full = sk.first + min(key, sk.len - 1);
   u32x4 kf[W / 16];
   own_frags<W>(static_cast<const uint16_t*>(a.k) + full * a.k_rs + kvh * a.k_hs, a.width, half, kf);
-  {
+  // query rows that see the workgroup's first key
+  const int first = a.causal ? max(at.row0 - shift, 0) / R * R : 0;
+  const int per = sq.len > first ? (sq.len - first + R - 1) / R : 0;
+  const int n_tiles = per * group;
+  if (n_tiles > 0) {  // waited for before the first tile: no load outlives the workgroup
     TileLoads<W, NW> loads;
     loads.init(a.v_rs, a.width, wave, lane);
     const uint16_t* vp = static_cast<const uint16_t*>(a.v) + sk.first * a.v_rs + kvh * a.v_hs;
@@ -727,9 +731,6 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   const float factor = F16 ? grad_factor(a) : 1.0f;
   const float lifted = factor * (F16 ? 0x1p-14f : 1.0f), unlift = F16 ? 0x1p-14f : 1.0f;
   const float c2 = a.scale * kLog2e;
-  // query rows that see the workgroup's first key
-  const int first = a.causal ? max(at.row0 - shift, 0) / R * R : 0;
-  const int per = sq.len > first ? (sq.len - first + R - 1) / R : 0;
   f32x16 dk[W / 32], dv[W / 32];
 #pragma unroll
   for (int dt = 0; dt < W / 32; ++dt)
@@ -758,7 +759,6 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   TileReads<W> reads;
   reads.init(lds, lane);
   const uint32_t v_rows = 4 * QB + wave * 32 * W * 2;  // of the wave's V beside the tile's rows
-  const int n_tiles = per * group;
   if (n_tiles > 0) fetch(0);
   int at_q = first;
   for (int j = 0; j < n_tiles; ++j, at_q = at_q + R >= sq.len ? first : at_q + R) {

@@ -419,7 +419,7 @@ __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.0f
 constexpr int kJoinHeads = 1024;
 
 template <int DT, int LANES>
-__global__ __launch_bounds__(256) void join_kernel(Split s, int joins) {
+__global__ __launch_bounds__(256) void join_kernel(Split s, int64_t joins) {
   const CacheAttend& a = s.a;
   __shared__ f32x2 ml[kJoinHeads];
   __shared__ f32x4 acc[4][LANES];
@@ -568,7 +568,7 @@ hipError_t cache_attend_t(const CacheAttend& a, hipStream_t st) {
   else
     e = a.i8 ? split_t<DT, true, 128>(s, wgs, weights, st) : split_t<DT, false, 128>(s, wgs, weights, st);
   if (e != hipSuccess || (parts == 1 && !weights)) return e;
-  const int joins = parts > 1 ? a.seqs * a.hq : 0;
+  const int64_t joins = parts > 1 ? (int64_t)a.seqs * a.hq : 0;
   const int64_t more = joins + (weights ? a.seqs * ((places + 255) / 256) : 0);
   for (int64_t wg0 = 0; wg0 < more; wg0 += kMaxGroups) {
     s.wg0 = wg0;

@@ -273,24 +273,18 @@ __device__ __forceinline__ void lds_load16(const void* src, void* lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m0), "v"(src)
                : "memory", "m0");
 }
-// The same with the address as a base in scalar registers (scalar_base) and a lane's
-// offset in bytes.
-__device__ __forceinline__ void lds_load16_from(uint64_t base, uint32_t offset, void* lds) {
+// The same with the address as a wave-uniform base (in scalar registers) and a lane's
+// offset in bytes. A vector instruction may have written the base (v_readfirstlane, or
+// v_readlane where the compiler had put it aside), and a load may read such a register
+// five wait states later at the earliest, which the backend does not see to before asm.
+__device__ __forceinline__ void lds_load16_from(const void* base, uint32_t offset, void* lds) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(offset),
-               "s"(base)
-               : "memory", "m0");
-}
-// A wave-uniform address for lds_load16_from. A vector instruction may have written it
-// (v_readfirstlane), and a load may read such a register five wait states later at
-// the earliest, which the backend does not see to inside asm.
-__device__ __forceinline__ uint64_t scalar_base(const void* p) {
-  const uint64_t at = (uint64_t)(uintptr_t)p;
+  const uint64_t at = (uint64_t)(uintptr_t)base;
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-  uint64_t base = (uint64_t)hi << 32 | lo;
-  asm volatile("s_nop 4" : "+s"(base));
-  return base;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m0), "v"(offset),
+               "s"((uint64_t)hi << 32 | lo)
+               : "memory", "m0");
 }
 __device__ __forceinline__ void lds_load4(const void* src, void* lds) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr_t)lds);

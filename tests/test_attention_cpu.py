@@ -225,3 +225,24 @@ def test_attend_gradient_refuses(L, change, word):
 def test_attend_of_nothing_is_fine(L):
     assert _packed(L, n=0, q=None, out=None) == 0 and _packed_back(L, n=0, nk=0, q=None) == 0
     assert L.emeans_attend_work(-1, 4) == 0 and L.emeans_attend_work(10, 4) >= 160
+
+
+def test_scalar_bases_of_direct_loads_are_waited_for():
+    """The shared load into LDS whose address is in scalar registers: a vector instruction may have
+    written them right before, and the hardware needs five wait states then, which only the
+    asm block itself can give."""
+    import glob
+    import os
+    import re
+    found = 0
+    for path in glob.glob(os.path.join(os.path.dirname(os.path.abspath(mm.__file__)), "csrc", "common.hpp")):
+        with open(path) as f:
+            text = f.read()
+        for block in re.findall(r'asm volatile\(\s*((?:"[^"]*"\s*)+)', text):
+            steps = [s.strip() for s in re.sub(r'"\s*"', "", block).strip('" \n').split(r"\n\t")]
+            for i, s in enumerate(steps):
+                if "_load_lds_" in s and not s.endswith("off"):
+                    found += 1
+                    waits = sum(1 + int(x.split()[1]) if x.startswith("s_nop") else 1 for x in steps[:i])
+                    assert waits >= 5, (path, steps)
+    assert found >= 1
