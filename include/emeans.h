@@ -633,10 +633,11 @@ int emeans_attend(const void* q, int64_t q_row, int64_t q_head, const void* k, i
  * and equal calls give equal bits. Weights and their gradients are rounded to dtype
  * beside the other operand. A NaN or an infinity may show anywhere in its sequence's
  * gradients.
- *   work  device, emeans_attend_work(n, hq) bytes, 16-byte aligned, or NULL (allocated
+ *   work  device, emeans_attend_work() bytes, 16-byte aligned, or NULL (allocated
  *         stream-ordered)
  * Errors: as above; ENOMEM. */
-int64_t emeans_attend_work(int64_t n, int64_t hq);
+int64_t emeans_attend_work(int64_t n, int64_t nk, int64_t hq, int64_t hk, int64_t width,
+                           int64_t seqs);
 int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
                            int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
                            int64_t v_head, int32_t dtype, int64_t n, int64_t nk, int64_t hq,

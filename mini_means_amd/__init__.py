@@ -132,7 +132,7 @@ def lib() -> ctypes.CDLL:
         attend = [c_vp, c_i64, c_i64] * 3 + [c_i32] + [c_i64] * 5 + [c_vp, c_vp, c_i64, c_i32, c_dbl]
         L.emeans_attend.argtypes = attend + [c_vp] * 4
         L.emeans_attend_gradient.argtypes = attend + [c_vp] * 4 + [c_i64, c_i64] + [c_vp] * 5
-        L.emeans_attend_work.argtypes = [c_i64, c_i64]
+        L.emeans_attend_work.argtypes = [c_i64] * 6
         L.emeans_cache_attend_work.argtypes = [c_i64] * 6 + [c_i32]
         L.emeans_cache_attend.argtypes = [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_i64,
                                           c_i64, c_i64, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64,
@@ -1279,7 +1279,8 @@ def _attend_fn():
                 def call(st):
                     g = _aligned(dout)
                     dq, dk, dv = (torch.empty(x.shape, dtype=dtype, device=device) for x in (q, k, v))
-                    work = _work(L.emeans_attend_work(shape[0], shape[1]), device)
+                    work = _work(L.emeans_attend_work(shape[0], k.shape[0], shape[1], k.shape[1],
+                                                      shape[2], starts.shape[0] - 1), device)
                     _check(L.emeans_attend_gradient(
                         *args, out.data_ptr(), lse.data_ptr(), rest.data_ptr(), g.data_ptr(),
                         g.stride(0), g.stride(1), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),

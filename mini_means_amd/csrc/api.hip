@@ -1848,9 +1848,12 @@ int emeans_attend(const void* q, int64_t q_row, int64_t q_head, const void* k, i
   return launched(launch_attend(a, static_cast<hipStream_t>(stream)), "attend");
 }
 
-int64_t emeans_attend_work(int64_t n, int64_t hq) {
-  if (n < 0 || n > kMaxLength || hq < 1 || hq > 65536) return 0;
-  return (int64_t)attend_work(n, (int)hq);
+int64_t emeans_attend_work(int64_t n, int64_t nk, int64_t hq, int64_t hk, int64_t width,
+                           int64_t seqs) {
+  if (n < 0 || n > kMaxLength || nk < 0 || nk > kMaxLength || hq < 1 || hq > 65536 || hk < 1 ||
+      hk > 65536 || width < 1 || width > 128 || seqs < 0 || seqs >= kMaxRows)
+    return 0;
+  return (int64_t)attend_work(n, nk, (int)hq, (int)hk, (int)width, seqs);
 }
 
 int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const void* k,
@@ -1884,7 +1887,7 @@ int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const v
   if ((rc = check_device(starts, "starts")) || (rc = check_device(k_starts, "k_starts"))) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   void *at, *own;
-  if ((rc = take_work(work, emeans_attend_work(n, hq), st, &at, &own))) return rc;
+  if ((rc = take_work(work, emeans_attend_work(n, nk, hq, hk, width, seqs), st, &at, &own))) return rc;
   return release(own, st, launched(launch_attend_back(a, at, st), "attend gradient"));
 }
 

@@ -689,15 +689,20 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
 // queries that see them, head by head of the group, in tiles of 32; P and dS of a tile
 // have a lane's key row as column. K stays in registers and V in LDS, which leaves room
 // for two waves on a SIMD (both in registers and one wave: 1.56 against 0.88 ms).
+// Where that leaves CUs idle, `cuts` workgroups share the list of a key tile's (head, query
+// tile) pairs and leave fp32 sums, which key_sum_kernel adds in order.
 template <bool F16, int W>
-__global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles) {
+__global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0, int64_t tiles,
+                                                          int cuts) {
   constexpr int NW = 4, ROWS = NW * 32, R = 32;
   constexpr int QB = R * W * 2, VB = ROWS * W * 2;  // bytes: of a tile of Q or dO, of V
   constexpr float kLift = F16 ? 14.0f : 0.0f;  // fp16: P times 2^14, which stays in range
   __shared__ __align__(1024) uint8_t lds[4 * QB + VB];
   __shared__ float lse[2][R], delta[2][R];
-  const int64_t b = wg0 + blockIdx.x;
+  const int64_t all = wg0 + blockIdx.x, b = all / cuts;
+  const int cut = (int)(all - b * cuts);
   if (b >= tiles * a.hk) {
+    if (b - tiles * a.hk >= kZeroGroups || cut) return;
     zero_outside(a.k_starts, a.seqs, a.nk, (int64_t)a.hk * a.width, static_cast<uint16_t*>(a.dk),
                  b - tiles * a.hk, NW * 64);
     zero_outside(a.k_starts, a.seqs, a.nk, (int64_t)a.hk * a.width, static_cast<uint16_t*>(a.dv),
@@ -720,7 +725,9 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   // query rows that see the workgroup's first key
   const int first = a.causal ? max(at.row0 - shift, 0) / R * R : 0;
   const int per = sq.len > first ? (sq.len - first + R - 1) / R : 0;
-  const int n_tiles = per * group;
+  // this workgroup's part of the list
+  const int64_t listed = (int64_t)per * group;
+  const int from = (int)(listed * cut / cuts), n_tiles = (int)(listed * (cut + 1) / cuts) - from;
   if (n_tiles > 0) {  // waited for before the first tile: no load outlives the workgroup
     TileLoads<W, NW> loads;
     loads.init(a.v_rs, a.width, wave, lane);
@@ -739,7 +746,9 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   TileLoads<W, NW, R> q_loads, g_loads;
   q_loads.init(a.q_rs, a.width, wave, lane);
   g_loads.init(a.do_rs, a.width, wave, lane);
-  int head = kvh * group, q0 = first;  // of the next tile to be fetched
+  // the next tile to be fetched
+  int head = kvh * group + (per ? from / per : 0), q0 = first + (per ? from % per : 0) * R;
+  int at_q = q0;
   auto fetch = [&](int j) {
     uint8_t* to = lds + (j & 1) * 2 * QB;
     q_loads.load(static_cast<const uint16_t*>(a.q) + sq.first * a.q_rs + head * a.q_hs, a.q_rs, q0,
@@ -760,7 +769,6 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
   reads.init(lds, lane);
   const uint32_t v_rows = 4 * QB + wave * 32 * W * 2;  // of the wave's V beside the tile's rows
   if (n_tiles > 0) fetch(0);
-  int at_q = first;
   for (int j = 0; j < n_tiles; ++j, at_q = at_q + R >= sq.len ? first : at_q + R) {
     EMK_WAIT_VMCNT(0);
     lds_barrier();
@@ -845,10 +853,52 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
     __builtin_amdgcn_s_setprio(0);
   }
   const int64_t to = (full * a.hk + kvh) * a.width;
+  if (cuts > 1) {
+    if (key >= sk.len) return;
+    const int64_t size = a.nk * a.hk * a.width;
+    float* part = a.part + cut * 2 * size + to;
+#pragma unroll
+    for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = dt * 32 + 8 * g + 4 * half;
+        if (c >= a.width) continue;
+        f32x4 x, y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = dk[dt][4 * g + i] * (a.scale / factor);
+          y[i] = dv[dt][4 * g + i] * unlift;
+        }
+        *reinterpret_cast<f32x4*>(part + c) = x;
+        *reinterpret_cast<f32x4*>(part + size + c) = y;
+      }
+    return;
+  }
   store_rows<F16, W>(dk, a.scale / factor, static_cast<uint16_t*>(a.dk) + to, nullptr, a.width,
                      half, key < sk.len);
   store_rows<F16, W>(dv, unlift, static_cast<uint16_t*>(a.dv) + to, nullptr, a.width, half,
                      key < sk.len);
+}
+
+// The sums that several workgroups left, added in order and rounded: rows of sequences, of
+// which none lies before the first start or behind the last.
+template <bool F16>
+__global__ __launch_bounds__(256) void key_sum_kernel(Attend a, int cuts) {
+  constexpr int OT = F16 ? 4 : 1;
+  const int64_t d = (int64_t)a.hk * a.width, size = a.nk * d;
+  const int64_t first = max(0, min(a.k_starts[0], (int)a.nk)) * d;
+  const int64_t last = max(0, min(a.k_starts[a.seqs], (int)a.nk)) * d;
+  for (int64_t i = first + ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < last;
+       i += (int64_t)gridDim.x * 1024) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = 0; c < cuts; ++c)
+        v += *reinterpret_cast<const f32x4*>(a.part + (2 * c + s) * size + i);
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(s ? a.dv : a.dk) + i) =
+          u32x2{pack2<OT>(v[0], v[1]), pack2<OT>(v[2], v[3])};
+    }
+  }
 }
 
 template <typename GO>
@@ -870,6 +920,14 @@ hipError_t forward_t(const Attend& a, hipStream_t st) {
   });
 }
 
+// Workgroups that share a key tile: two per CU fit, and a tile's list may be long.
+int cuts_of(int64_t nk, int64_t seqs, int hk) {
+  const int64_t wgs = (nk / 128 + seqs) * hk;
+  if (wgs < 1 || wgs >= 512) return 1;
+  const int64_t cuts = 512 / wgs;
+  return (int)(cuts > 8 ? 8 : cuts);
+}
+
 template <bool F16, int W>
 hipError_t backward_t(const Attend& a, hipStream_t st) {
   if (F16) {
@@ -878,13 +936,18 @@ hipError_t backward_t(const Attend& a, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   const int64_t q_tiles = a.seqs ? a.n / 128 + a.seqs : 0, k_tiles = a.seqs ? a.nk / 128 + a.seqs : 0;
-  const hipError_t e = in_launches(q_tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
+  hipError_t e = in_launches(q_tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
     query_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, q_tiles);
   });
   if (e != hipSuccess) return e;
-  return in_launches(k_tiles * a.hk + kZeroGroups, [&](int64_t wg0, unsigned grid) {
-    key_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, k_tiles);
+  const int cuts = cuts_of(a.nk, a.seqs, a.hk);
+  e = in_launches((k_tiles * a.hk + kZeroGroups) * cuts, [&](int64_t wg0, unsigned grid) {
+    key_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, k_tiles, cuts);
   });
+  if (e != hipSuccess || cuts == 1) return e;
+  const int64_t quads = a.nk * a.hk * a.width / 4;
+  key_sum_kernel<F16><<<(unsigned)(quads / 256 + 1 < 2048 ? quads / 256 + 1 : 2048), 256, 0, st>>>(a, cuts);
+  return hipGetLastError();
 }
 
 template <typename GO>
@@ -899,7 +962,10 @@ hipError_t by_type(const Attend& a, GO go) {
 
 }  // namespace
 
-size_t attend_work(int64_t n, int hq) { return (size_t)n * hq * 4 + 2 * kTops * 4; }
+size_t attend_work(int64_t n, int64_t nk, int hq, int hk, int width, int64_t seqs) {
+  const int cuts = cuts_of(nk, seqs, hk);
+  return 2 * kTops * 4 + (cuts > 1 ? (size_t)cuts * 2 * nk * hk * width * 4 : 0) + (size_t)n * hq * 4;
+}
 
 hipError_t launch_attend(const Attend& a, hipStream_t st) {
   return by_type(a, [&](auto f16, auto w) {
@@ -909,7 +975,9 @@ hipError_t launch_attend(const Attend& a, hipStream_t st) {
 
 hipError_t launch_attend_back(Attend a, void* work, hipStream_t st) {
   a.tops = static_cast<float*>(work);
-  a.delta = a.tops + 2 * kTops;
+  a.part = a.tops + 2 * kTops;
+  const int cuts = cuts_of(a.nk, a.seqs, a.hk);
+  a.delta = a.part + (cuts > 1 ? (int64_t)cuts * 2 * a.nk * a.hk * a.width : 0);
   return by_type(a, [&](auto f16, auto w) {
     return backward_t<decltype(f16)::value, decltype(w)::value>(a, st);
   });

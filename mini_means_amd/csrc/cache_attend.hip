@@ -53,13 +53,17 @@ __device__ __forceinline__ float xor_sum(float v) {
   return __uint_as_float(max_xor32(b, add));
 }
 
-// Four codes as bf16 values.
+// Four codes as bf16 values. int8: a byte with its sign bit turned over, u = code + 128, in
+// the last bits of 2^23 is 2^23 + u, from which 2^23 + 128 is taken: two instructions at
+// full rate, where the conversion of an integer is slower (64 sequences of up to 8192 249 us with it, 152 without).
 template <bool I8>
 __device__ __forceinline__ u32x2 values_of(uint32_t w, float s) {
   if constexpr (I8) {
+    const uint32_t u = w ^ 0x80808080u;
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = (float)(int8_t)(w >> (8 * i)) * s;
+    for (int i = 0; i < 4; ++i)
+      y[i] = (__uint_as_float(__builtin_amdgcn_perm(0x4B000000u, u, 0x070C0C00u | i)) - 8388736.0f) * s;
     return u32x2{pack2<1>(y[0], y[1]), pack2<1>(y[2], y[3])};
   } else {
     return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false)),

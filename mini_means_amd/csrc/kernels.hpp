@@ -448,10 +448,11 @@ struct Attend {
   void* dq;
   void* dk;
   void* dv;
-  float* tops;   // set by launch_attend_back
+  float* tops;   // these three are set by launch_attend_back
+  float* part;
   float* delta;
 };
-size_t attend_work(int64_t n, int hq);
+size_t attend_work(int64_t n, int64_t nk, int hq, int hk, int width, int64_t seqs);
 hipError_t launch_attend(const Attend& a, hipStream_t st);
 hipError_t launch_attend_back(Attend a, void* work, hipStream_t st);
 

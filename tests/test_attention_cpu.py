@@ -224,7 +224,7 @@ def test_attend_gradient_refuses(L, change, word):
 
 def test_attend_of_nothing_is_fine(L):
     assert _packed(L, n=0, q=None, out=None) == 0 and _packed_back(L, n=0, nk=0, q=None) == 0
-    assert L.emeans_attend_work(-1, 4) == 0 and L.emeans_attend_work(10, 4) >= 160
+    assert L.emeans_attend_work(-1, 5, 4, 2, 64, 1) == 0 and L.emeans_attend_work(10, 10, 4, 2, 64, 1) >= 160
 
 
 def test_scalar_bases_of_direct_loads_are_waited_for():
