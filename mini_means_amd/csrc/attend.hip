@@ -20,7 +20,7 @@
 // four waves share a CU: one wave's products run beside the other's exponentials.
 // Measured, 32 query and 8 key-value heads of 128 in bf16, causal: 16384 tokens 2.08 to 2.24
 // ms (980 to 1060 TFLOP/s; the library's product of 8192 a side 1223); seven sequences of
-// up to 4000 tokens 0.39 ms, dQ 0.53, dK and dV 0.85. 33 sequences of up to 500 tokens, 16
+// up to 4000 tokens 0.39 ms, dQ 0.53, dK and dV 0.82. 33 sequences of up to 500 tokens, 16
 // heads of 64 in fp16, not causal: 33 us.
 #include <type_traits>
 
@@ -688,7 +688,8 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
 // dK and dV: a workgroup owns 128 key rows of a key-value head and goes over the
 // queries that see them, head by head of the group, in tiles of 32; P and dS of a tile
 // have a lane's key row as column. K stays in registers and V in LDS, which leaves room
-// for two waves on a SIMD (both in registers and one wave: 1.56 against 0.88 ms).
+// for two waves on a SIMD (both in registers and one wave: 1.56 against 0.88 ms, seven
+// sequences of up to 4000 tokens, 32 / 8 heads of 128).
 // Where that leaves CUs idle, `cuts` workgroups share the list of a key tile's (head, query
 // tile) pairs and leave fp32 sums, which key_sum_kernel adds in order.
 template <bool F16, int W>
@@ -920,11 +921,14 @@ hipError_t forward_t(const Attend& a, hipStream_t st) {
   });
 }
 
-// Workgroups that share a key tile: two per CU fit, and a tile's list may be long.
+// Workgroups that share a key tile: two per CU fit, and a tile's list may be long. Measured:
+// one sequence of 3800 tokens, 16 / 4 heads of 128 (120 tiles), the step 845 us with one
+// each, 443 with four, 413 with eight; seven sequences of up to 4000, 32 / 8 heads (568
+// tiles), dK and dV 877 us with one each, 775 and 42 for the sums with two.
 int cuts_of(int64_t nk, int64_t seqs, int hk) {
   const int64_t wgs = (nk / 128 + seqs) * hk;
-  if (wgs < 1 || wgs >= 512) return 1;
-  const int64_t cuts = 512 / wgs;
+  if (wgs < 1 || wgs >= 1024) return 1;
+  const int64_t cuts = (1024 + wgs - 1) / wgs;
   return (int)(cuts > 8 ? 8 : cuts);
 }
 
