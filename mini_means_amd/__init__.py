@@ -1359,7 +1359,7 @@ def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=N
     added: what cache_evict goes by.
 
     The time goes by the table's columns too: pass table[:, :m] where m pages hold
-    every sequence."""
+    every sequence. The result has no gradient: `attend` is for training."""
     dev = _device_of(q, "q")
     dt = _number(q.dtype, "q")
     seqs, hq, width, qr, qh = _heads(q, dev, "q")

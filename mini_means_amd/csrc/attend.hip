@@ -20,7 +20,7 @@
 // four waves share a CU: one wave's products run beside the other's exponentials.
 // Measured, 32 query and 8 key-value heads of 128 in bf16, causal: 16384 tokens 2.08 to 2.24
 // ms (980 to 1060 TFLOP/s; the library's product of 8192 a side 1223); seven sequences of
-// up to 4000 tokens 0.39 ms, dQ 0.53, dK and dV 0.82. 33 sequences of up to 500 tokens, 16
+// up to 4000 tokens 0.39 ms, dQ 0.54, dK and dV 0.81. 33 sequences of up to 500 tokens, 16
 // heads of 64 in fp16, not causal: 33 us.
 #include <type_traits>
 
@@ -667,6 +667,8 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
         for (int r = 0; r < 16; ++r)
           if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) dp[r] = 0.0f;
       }
+      // dS (and P of dV) rounded to the inputs' type, as large an error as the result's own
+      // rounding and independent of it; two terms would take a product more
       const u32x4 ds[2] = {packed<F16>(dp, 0), packed<F16>(dp, 8)};
       __builtin_amdgcn_s_setprio(1);
       __builtin_amdgcn_sched_barrier(0);
@@ -923,8 +925,8 @@ hipError_t forward_t(const Attend& a, hipStream_t st) {
 
 // Workgroups that share a key tile: two per CU fit, and a tile's list may be long. Measured:
 // one sequence of 3800 tokens, 16 / 4 heads of 128 (120 tiles), the step 845 us with one
-// each, 443 with four, 413 with eight; seven sequences of up to 4000, 32 / 8 heads (568
-// tiles), dK and dV 877 us with one each, 775 and 42 for the sums with two.
+// each, 443 with four, 408 with eight; seven sequences of up to 4000, 32 / 8 heads (568
+// tiles), dK and dV 877 us with one each, 765 and 42 for the sums with two.
 int cuts_of(int64_t nk, int64_t seqs, int hk) {
   const int64_t wgs = (nk / 128 + seqs) * hk;
   if (wgs < 1 || wgs >= 1024) return 1;
