@@ -153,3 +153,29 @@ def attend_grad(q, k, v, do, scale, causal, dtype, top=None):
         pv_off = pv_off + mask * 2.0 ** -24 * 2.0 ** -14
     tols = (abs(scale) * off @ np.abs(k), abs(scale) * off.T @ np.abs(q), pv_off.T @ np.abs(do))
     return (dq, dk, dv), tols
+
+
+def grad_slopes(q, k, v, do, grads, scale, causal, dtype):
+    """One sequence (rows x heads x w each), for dq, dk and dv of `grads` in turn along the
+    definition's own gradient (a part that is missing or too much shows there): the change of
+    sum(o do) that they say, the one that differences of the definition give (to
+    some 1e-9 of it), and what the first may be off by."""
+    hq, group, inputs = q.shape[1], q.shape[1] // k.shape[1], [q, k, v]
+
+    def loss(x):
+        return sum((attend(x[0][:, h], x[1][:, h // group], x[2][:, h // group], scale, causal, dtype)[0] * do[:, h]).sum()
+                   for h in range(hq))
+
+    exact, tols = ([np.zeros(x.shape) for x in inputs] for _ in range(2))
+    for h in range(hq):
+        kv = h // group
+        top = np.abs(do[:, h]).max() * np.abs(v[:, kv]).max()
+        values, off = attend_grad(q[:, h], k[:, kv], v[:, kv], do[:, h], scale, causal, dtype, top)
+        for i, at in enumerate((h, kv, kv)):
+            exact[i][:, at] += values[i]
+            tols[i][:, at] += off[i]
+    for i, (g, e, t) in enumerate(zip(grads, exact, tols)):
+        way = e / np.linalg.norm(e)
+        ends = [loss([x + sign * 1e-4 * way if j == i else x for j, x in enumerate(inputs)]) for sign in (1, -1)]
+        t = t + (HALF_ULP[dtype] * 1.01 + group * SUM_ULP) * np.abs(e) + TINY[dtype]
+        yield (g * way).sum(), (ends[0] - ends[1]) / 2e-4, (np.abs(way) * t).sum()

@@ -175,6 +175,42 @@ def test_attention_gradients_are_differences():
                 assert abs((ends[0] - ends[1]) / 2e-5 - grads[i][j]) < 1e-7
 
 
+@pytest.mark.parametrize("dtype,sharp", [("bf16", 0.2), ("f16", 0.03)])
+def test_slopes_find_wrong_gradients(dtype, sharp):
+    """What the GPU's gradients are held against accepts the definition's and finds them 5% too large or
+    too small (bf16 25%: every rounding may be as large as it can be), with D left out, of another
+    mask, of one head of a group alone."""
+    rng = np.random.default_rng(6)
+    q, do = rng.normal(size=(90, 2, 64)) * 1.5, rng.normal(size=(90, 2, 64)) * 0.1
+    k, v = rng.normal(size=(2, 90, 1, 64))
+
+    def grads(causal=True, heads=(0, 1)):
+        out = [np.zeros(t.shape) for t in (q, k, v)]
+        for h in heads:
+            for o, x, at in zip(out, ref.attend_grad(q[:, h], k[:, 0], v[:, 0], do[:, h], 0.125, causal, dtype, 0.0)[0], (h, 0, 0)):
+                o[:, at] += x
+        return out
+
+    def fits(g):
+        return [abs(a - b) <= off for a, b, off in ref.grad_slopes(q, k, v, do, g, 0.125, True, dtype)]
+
+    right = grads()
+    for a, b, off in ref.grad_slopes(q, k, v, do, right, 0.125, True, dtype):
+        assert abs(a - b) <= 1e-6 * abs(b) and off <= sharp * abs(b)
+    wrong = 0.05 if dtype == "f16" else 0.25
+    assert fits([(1 + wrong) * g for g in right]) == [False] * 3
+    assert fits([(1 - wrong) * g for g in right]) == [False] * 3
+    assert fits(grads(causal=False)) == [False] * 3
+    assert fits(grads(heads=(0,)))[1:] == [False] * 2
+    without = [np.zeros(t.shape) for t in (q, k)]
+    for h in range(2):
+        p = ref.softmax(np.where(ref.seen(90, 90, True), q[:, h] @ k[:, 0].T * 0.125, -np.inf))
+        ds = p * (do[:, h] @ v[:, 0].T)
+        without[0][:, h] += 0.125 * ds @ k[:, 0]
+        without[1][:, 0] += 0.125 * ds.T @ q[:, h]
+    assert fits([*without, right[2]])[:2] == [False] * 2
+
+
 def test_attention_of_one_token_is_the_last_row_of_causal_attention():
     rng = np.random.default_rng(4)
     q, k, v = (rng.normal(size=(7, 16)) for _ in range(3))
