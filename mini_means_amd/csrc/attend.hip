@@ -500,51 +500,27 @@ __global__ __launch_bounds__(NW * 64, 2) void attend_kernel(Attend a, int64_t wg
 // Backward
 // ---------------------------------------------------------------------------
 
-// The largest |dO| and |V| of fp16 data, one pair per workgroup.
-constexpr int kTops = 256;
+// fp16 holds 2^-24 to 65504, while dS may be anything: where a product's sum runs over them, it
+// is kept times a power of two that the result's own row makes (a query of dQ, a key of dK),
+// so that nothing else in the call costs its digits. The number starts at 2^80 (|dO V^T - D|
+// is under 2^41 for fp16 data) and falls when the row's largest leaves fp16's safe range,
+// to 2^11: what is added is off by half a unit of its own or by 2^-36 of the largest. A number
+// for the whole call, made by a pass over dO and V, lost a sequence's digits to large values of
+// others and of rows outside all sequences, and took longer (seven sequences of up to 4000 tokens,
+// 32 / 8 heads of 128, the whole step 1848 us against 1753).
+constexpr float kFirstLift = 0x1p80f, kTopDs = 0x1p15f;
 
-__global__ __launch_bounds__(256) void tops_kernel(Attend a) {
-  __shared__ float tmp[4];
-  float top[2] = {0.0f, 0.0f};
+// ds (times the row's number) made to fit: true where acc, and the number, have to be
+// multiplied by `by`. Both halves of a row have the same one, as they share acc's columns.
+__device__ __forceinline__ bool outgrown(const f32x16& ds, float& by) {
+  float top = 0.0f;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const uint16_t* p = static_cast<const uint16_t*>(s ? a.v : a.dout);
-    const int64_t rs = s ? a.v_rs : a.do_rs, hs = s ? a.v_hs : a.do_hs;
-    const int heads = s ? a.hk : a.hq, chunks = a.width / 8;
-    const int64_t rows = s ? a.nk : a.n;
-    const int per = heads * chunks;
-    for (int64_t r = blockIdx.x; r < rows; r += kTops)
-      for (int i = threadIdx.x; i < per; i += 256) {
-        const int h = i / chunks, c = i - h * chunks;
-        const u32x4 w = *reinterpret_cast<const u32x4*>(p + r * rs + h * hs + c * 8);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = fabsf(f16_to_f32((uint16_t)w[e])), y = fabsf(f16_to_f32((uint16_t)(w[e] >> 16)));
-          if (x < INFINITY) top[s] = fmaxf(top[s], x);
-          if (y < INFINITY) top[s] = fmaxf(top[s], y);
-        }
-      }
-    top[s] = wave_max(top[s]);
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top[s];
-    __syncthreads();
-    if (threadIdx.x == 0)
-      a.tops[s * kTops + blockIdx.x] = fmaxf(fmaxf(tmp[0], tmp[1]), fmaxf(tmp[2], tmp[3]));
-    __syncthreads();
-  }
-}
-
-// fp16 holds 2^-24 to 65504, while dS may be anything: it is kept times a power of two
-// that leaves its bound, |dO V^T - D| <= 2 width max|dO| max|V|, at most 2^15. (The same
-// number in every workgroup: a maximum has no order.)
-__device__ __forceinline__ float grad_factor(const Attend& a) {
-  float x = 0.0f, y = 0.0f;
-  for (int i = threadIdx.x & 63; i < kTops; i += 64) {
-    x = fmaxf(x, a.tops[i]);
-    y = fmaxf(y, a.tops[kTops + i]);
-  }
-  const float bound = wave_max(x) * wave_max(y) * (2.0f * (float)a.width);
-  if (!(bound > 0.0f)) return 1.0f;
-  return __uint_as_float((uint32_t)(min(max(127 + 14 - (int)(__float_as_uint(bound) >> 23) + 127, 27), 227)) << 23);
+  for (int r = 0; r < 16; ++r) top = fmaxf(top, fabsf(ds[r]));
+  top = half_max(top);
+  const bool up = top > kTopDs;
+  // 2^(11 - exponent of top); an infinity counts as 2^128
+  by = up ? __uint_as_float((127 + 11 + 127 - (__float_as_uint(top) >> 23)) << 23) : 1.0f;
+  return __any(up);
 }
 
 // dQ: a workgroup owns 128 query rows of a head; P^T and dS^T of a tile of 64 keys have
@@ -577,7 +553,6 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
   u32x4 qf[W / 16], gf[W / 16];
   own_frags<W>(static_cast<const uint16_t*>(a.q) + full * a.q_rs + head * a.q_hs, a.width, half, qf);
   own_frags<W>(static_cast<const uint16_t*>(a.dout) + full * a.do_rs + head * a.do_hs, a.width, half, gf);
-  const float factor = F16 ? grad_factor(a) : 1.0f;
   float d = 0.0f;
   {
     // o as it was before its rounding to 16 bits: the rounding would stand in D, which all
@@ -595,9 +570,11 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
       for (int i = 0; i < 8; ++i)
         d += (number(of[ks], i) + number(rf[ks], i)) * number(gf[ks], i);
   }
-  d = half_sum(d) * factor;
+  d = half_sum(d);
   const float lse = a.lse[(int64_t)head * a.n + full];
   if (half == 0 && row < sq.len) a.delta[(int64_t)head * a.n + full] = d;
+  float factor = F16 ? kFirstLift : 1.0f;
+  d *= factor;
   const float c2 = a.scale * kLog2e;
   const int keys = max(a.causal ? min(min(at.row0 + ROWS, sq.len) + shift, sk.len) : sk.len, 0);
   const int n_tiles = (keys + kTile - 1) / kTile;
@@ -666,6 +643,19 @@ __global__ __launch_bounds__(256, 2) void query_grad_kernel(Attend a, int64_t wg
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           if (k0 + kt * 32 + (r >> 2) * 8 + 4 * half + (r & 3) >= sees) dp[r] = 0.0f;
+      }
+      if constexpr (F16) {
+        float by;
+        if (outgrown(dp, by)) {
+          factor *= by;
+          d *= by;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) dp[r] *= by;
+#pragma unroll
+          for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[dt][r] *= by;
+        }
       }
       // dS (and P of dV) rounded to the inputs' type, as large an error as the result's own
       // rounding and independent of it; two terms would take a product more
@@ -738,8 +728,9 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
     loads.load(vp, a.v_rs, at.row0, sk.len - 1, lds + 4 * QB, wave);
     loads.load(vp, a.v_rs, min(at.row0 + kTile, sk.len - 1), sk.len - 1, lds + 4 * QB + VB / 2, wave);
   }
-  const float factor = F16 ? grad_factor(a) : 1.0f;
-  const float lifted = factor * (F16 ? 0x1p-14f : 1.0f), unlift = F16 ? 0x1p-14f : 1.0f;
+  // fp16: dS is 2^14 P times (dP - D) times `factor`
+  constexpr float kUnlift = F16 ? 0x1p-14f : 1.0f;
+  float factor = F16 ? kFirstLift * kUnlift : 1.0f;
   const float c2 = a.scale * kLog2e;
   f32x16 dk[W / 32], dv[W / 32];
 #pragma unroll
@@ -828,7 +819,7 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * g + i;
         s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c2, kLift - e[i]));
-        dp[r] = s[r] * __builtin_fmaf(dp[r], lifted, -d[i] * unlift);
+        dp[r] = s[r] * __builtin_fmaf(dp[r], factor, -d[i] * factor);
       }
     }
     if (part) {
@@ -837,6 +828,18 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
       for (int r = 0; r < 16; ++r) {
         const int q = at_q + 8 * (r >> 2) + 4 * half + (r & 3);
         if (q >= sq.len || (a.causal && q + shift < key)) s[r] = dp[r] = 0.0f;
+      }
+    }
+    if constexpr (F16) {
+      float by;
+      if (outgrown(dp, by)) {
+        factor *= by;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) dp[r] *= by;
+#pragma unroll
+        for (int dt = 0; dt < W / 32; ++dt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) dk[dt][r] *= by;
       }
     }
     const u32x4 p[2] = {packed<F16>(s, 0), packed<F16>(s, 8)};
@@ -856,6 +859,7 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
     __builtin_amdgcn_s_setprio(0);
   }
   const int64_t to = (full * a.hk + kvh) * a.width;
+  const float back = a.scale / factor * kUnlift;
   if (cuts > 1) {
     if (key >= sk.len) return;
     const int64_t size = a.nk * a.hk * a.width;
@@ -869,17 +873,17 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
         f32x4 x, y;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[i] = dk[dt][4 * g + i] * (a.scale / factor);
-          y[i] = dv[dt][4 * g + i] * unlift;
+          x[i] = dk[dt][4 * g + i] * back;
+          y[i] = dv[dt][4 * g + i] * kUnlift;
         }
         *reinterpret_cast<f32x4*>(part + c) = x;
         *reinterpret_cast<f32x4*>(part + size + c) = y;
       }
     return;
   }
-  store_rows<F16, W>(dk, a.scale / factor, static_cast<uint16_t*>(a.dk) + to, nullptr, a.width,
+  store_rows<F16, W>(dk, back, static_cast<uint16_t*>(a.dk) + to, nullptr, a.width,
                      half, key < sk.len);
-  store_rows<F16, W>(dv, unlift, static_cast<uint16_t*>(a.dv) + to, nullptr, a.width, half,
+  store_rows<F16, W>(dv, kUnlift, static_cast<uint16_t*>(a.dv) + to, nullptr, a.width, half,
                      key < sk.len);
 }
 
@@ -936,11 +940,6 @@ int cuts_of(int64_t nk, int64_t seqs, int hk) {
 
 template <bool F16, int W>
 hipError_t backward_t(const Attend& a, hipStream_t st) {
-  if (F16) {
-    tops_kernel<<<kTops, 256, 0, st>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   const int64_t q_tiles = a.seqs ? a.n / 128 + a.seqs : 0, k_tiles = a.seqs ? a.nk / 128 + a.seqs : 0;
   hipError_t e = in_launches(q_tiles * a.hq + kZeroGroups, [&](int64_t wg0, unsigned grid) {
     query_grad_kernel<F16, W><<<grid, 256, 0, st>>>(a, wg0, q_tiles);
@@ -970,7 +969,7 @@ hipError_t by_type(const Attend& a, GO go) {
 
 size_t attend_work(int64_t n, int64_t nk, int hq, int hk, int width, int64_t seqs) {
   const int cuts = cuts_of(nk, seqs, hk);
-  return 2 * kTops * 4 + (cuts > 1 ? (size_t)cuts * 2 * nk * hk * width * 4 : 0) + (size_t)n * hq * 4;
+  return (cuts > 1 ? (size_t)cuts * 2 * nk * hk * width * 4 : 0) + (size_t)n * hq * 4;
 }
 
 hipError_t launch_attend(const Attend& a, hipStream_t st) {
@@ -980,8 +979,7 @@ hipError_t launch_attend(const Attend& a, hipStream_t st) {
 }
 
 hipError_t launch_attend_back(Attend a, void* work, hipStream_t st) {
-  a.tops = static_cast<float*>(work);
-  a.part = a.tops + 2 * kTops;
+  a.part = static_cast<float*>(work);
   const int cuts = cuts_of(a.nk, a.seqs, a.hk);
   a.delta = a.part + (cuts > 1 ? (int64_t)cuts * 2 * a.nk * a.hk * a.width : 0);
   return by_type(a, [&](auto f16, auto w) {

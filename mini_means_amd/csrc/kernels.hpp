@@ -448,8 +448,7 @@ struct Attend {
   void* dq;
   void* dk;
   void* dv;
-  float* tops;   // these three are set by launch_attend_back
-  float* part;
+  float* part;  // these two are set by launch_attend_back
   float* delta;
 };
 size_t attend_work(int64_t n, int64_t nk, int hq, int hk, int width, int64_t seqs);

@@ -130,8 +130,8 @@ def p_error(q, k, scale, mask, w):
 
 def attend_grad(q, k, v, do, scale, causal, dtype, top=None):
     """One head of one sequence: (dq, dk, dv) and what each may be off by. top: the largest
-    |dO| and |V| of the call, for fp16's weights' gradients: they are kept times a
-    power of two that leaves 2 w top at least 2^14 of fp16's range, in steps of 2^-24."""
+    |dO| and |V| of the call, for fp16's weights' gradients: 2^-38 of 2 w top for what the
+    step at zero takes from them (they are kept times a power of two of their row)."""
     w = q.shape[1]
     mask = seen(len(q), len(k), causal)
     p = softmax(np.where(mask, q @ k.T * scale, -np.inf))
