@@ -1198,7 +1198,8 @@ def _aligned(t):
     if (c == 1 or t.shape[2] <= 1) and a % 8 == 0 and b % 8 == 0 and t.data_ptr() % 16 == 0 \
             and a < 1 << 24:
         return t
-    return t.contiguous() if t.data_ptr() % 16 == 0 or not t.is_contiguous() else t.clone()
+    # not contiguous(): that returns t itself where what is oddly apart is one row or head
+    return t.clone(memory_format=_T().torch.contiguous_format)
 
 
 def _attend_list(q, k, v, starts, k_starts, causal, scale):
