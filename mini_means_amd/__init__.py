@@ -1217,7 +1217,7 @@ def _attend_checks(q, k, v, starts, k_starts):
     dev = _device_of(q, "q")
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise EmeansError(f"EDTYPE: q {q.dtype} not supported (bfloat16 or float16)")
-    n, hq, w, _, _ = _heads(q, dev, "q")
+    _, hq, w, _, _ = _heads(q, dev, "q")
     nk, hk, wk, _, _ = _heads(k, dev, "k", q.dtype)
     nv, hv, wv, _, _ = _heads(v, dev, "v", q.dtype)
     if wk != w or (nv, hv, wv) != (nk, hk, wk):
@@ -1232,8 +1232,6 @@ def _attend_checks(q, k, v, starts, k_starts):
         raise EmeansError("EINVAL: starts must be one more than the sequences")
     if k_starts is not starts:
         _vector(k_starts, dev, "k_starts", seqs + 1, (torch.int32,), "int32")
-    elif nk != n:
-        raise EmeansError(f"EINVAL: k and v must have the {n} rows of q, or k_starts be given")
     return dev
 
 
@@ -1318,7 +1316,11 @@ def attend(q, k, v, starts, *, k_starts=None, causal: bool = True, scale=None, s
     _no_tangent("attend", q, k, v)
     if any(t.dim() != 3 for t in (q, k, v)):
         raise EmeansError("EINVAL: q, k and v must be rows x heads x width")
-    k_starts = starts if k_starts is None else k_starts
+    if k_starts is None:
+        if k.shape[0] != q.shape[0]:
+            raise EmeansError(f"EINVAL: k and v must have the {q.shape[0]} rows of q, or k_starts be "
+                              "given")
+        k_starts = starts
     q, k, v = _aligned(q), _aligned(k), _aligned(v)
     if _T().torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _attend_fn().apply(q, k, v, starts, k_starts, causal, scale)

@@ -40,3 +40,14 @@ def test_rows_and_heads_at_any_distance_where_there_is_one(mm, rows, heads, dtyp
             assert torch.equal(mm.attend(*leaves, starts), o)
     for r in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], r))
+
+
+def test_the_same_starts_for_keys_of_a_longer_buffer(mm):  # noqa: F811
+    """k_starts given, and the same tensor as starts: keys behind the last sequence are not read."""
+    import torch
+    q, k, v, _, starts, _ = inputs([30, 9], [30, 9], 2, 1, 64, "bf16", 4, 0, 0)
+    pad = torch.full((7, 1, 64), float("nan"), device="cuda", dtype=k.dtype)
+    got = mm.attend(q, torch.cat([k, pad]), torch.cat([v, pad]), starts, k_starts=starts)
+    assert torch.equal(got, mm.attend(q, k, v, starts))
+    with pytest.raises(mm.EmeansError, match="EINVAL"):
+        mm.attend(q, torch.cat([k, pad]), torch.cat([v, pad]), starts)
