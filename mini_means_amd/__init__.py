@@ -1068,6 +1068,13 @@ def _no_tangent(name, *tensors) -> None:
         raise EmeansError(f"EINVAL: {name} has no forward-mode derivative (an input has a tangent)")
 
 
+def _no_gradient(name, *tensors) -> None:
+    """Refuse inputs that ask for a gradient that the call does not have."""
+    if _T().torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise EmeansError(f"EINVAL: {name} has no gradient (detach the input that asks for one)")
+    _no_tangent(name, *tensors)
+
+
 def _adjacent(t):
     """t with adjacent values in a row (a copy if it has not)."""
     return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
@@ -1180,12 +1187,14 @@ def norm_rotate(q, k, q_weight, k_weight, positions, freqs, *, eps: float = 1e-6
     values) are both of one number type, positions (n) int32 or int64, freqs float64
     (rotary_freqs): angles are exact products in 64 bits, so far positions turn as
     exactly as near ones. q, k and the weights have gradients (once: tangents of the
-    forward mode are refused); the weights' are sums in one order."""
+    forward mode are refused, and freqs that ask for a gradient); the weights' are sums
+    in one order."""
     _device_of(q, "q")
     if stream is not None:
         with _T().torch.cuda.stream(stream):
             return norm_rotate(q, k, q_weight, k_weight, positions, freqs, eps=eps)
     _no_tangent("norm_rotate", q, k, q_weight, k_weight)
+    _no_gradient("norm_rotate by freqs", freqs)
     if _T().torch.is_grad_enabled() and (q.requires_grad or k.requires_grad
                                          or q_weight.requires_grad or k_weight.requires_grad):
         return _rotate_fn().apply(q, k, q_weight, k_weight, positions, freqs, eps)
@@ -1362,9 +1371,11 @@ def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=N
     added: what cache_evict goes by.
 
     The time goes by the table's columns too: pass table[:, :m] where m pages hold
-    every sequence. The result has no gradient: `attend` is for training."""
+    every sequence. There is no gradient (`attend` is for training): where gradients are
+    enabled, a q or weights that ask for one are refused."""
     dev = _device_of(q, "q")
     dt = _number(q.dtype, "q")
+    _no_gradient("cache_attend", *((q,) if weights is None else (q, weights)))
     seqs, hq, width, qr, qh = _heads(q, dev, "q")
     fmt, d, shape = _paged(dev, keys, block, "keys")
     vfmt, _, vshape = _paged(dev, values, block, "values")
@@ -1433,6 +1444,7 @@ def cache_evict(stores, table, lengths, weights, keep: int, *, recent: int = 0, 
     wn, wd, wld = _matrix(weights, dev, "weights", (torch.float32,), "float32")
     if (wn, wd) != (seqs, places) or (wld < places and seqs > 1):
         raise EmeansError(f"EINVAL: weights must be {seqs} x {places}")
+    _no_gradient("cache_evict", weights)
     if not 0 <= keep < 2 ** 31 - 1023 or not 0 <= recent <= keep:
         raise EmeansError(f"EINVAL: keep or recent out of range ({keep}, {recent})")
 

@@ -51,3 +51,43 @@ def test_the_same_starts_for_keys_of_a_longer_buffer(mm):  # noqa: F811
     assert torch.equal(got, mm.attend(q, k, v, starts))
     with pytest.raises(mm.EmeansError, match="EINVAL"):
         mm.attend(q, torch.cat([k, pad]), torch.cat([v, pad]), starts)
+
+
+def small_store(mm, d=128, block=64):  # noqa: F811
+    import torch
+    store = mm.cache_new((3, 16), d, block=block)
+    mm.cache_write(randn(gen(1), 48, d), torch.arange(48, device="cuda"), *store, block=block)
+    return store
+
+
+def test_what_has_no_gradient_is_refused_for_inputs_that_ask_for_one(mm):  # noqa: F811
+    import torch
+    import torch.autograd.forward_ad as fwd
+    store, table = small_store(mm), torch.arange(3, device="cuda").int().view(1, 3)
+    lens, q = torch.tensor([40], device="cuda").int(), randn(gen(2), 1, 4, 64)
+    w = torch.zeros(1, 48, device="cuda")
+    call = lambda q, w=None: mm.cache_attend(q, store, store, table, lens, block=64, weights=w)  # noqa: E731
+    want = call(q)
+    leaf = q.clone().requires_grad_()
+    with pytest.raises(mm.EmeansError, match="EINVAL.*gradient"):
+        call(leaf)
+    with pytest.raises(mm.EmeansError, match="EINVAL.*gradient"):
+        call(q, w.clone().requires_grad_())
+    with torch.no_grad():
+        assert torch.equal(call(leaf), want) and torch.equal(call(leaf, w), want)
+    assert torch.equal(call(leaf.detach()), want)
+    with fwd.dual_level(), pytest.raises(mm.EmeansError, match="forward-mode"):
+        call(fwd.make_dual(q, torch.ones_like(q)))
+    evict = lambda w: mm.cache_evict([store], table, lens, w, 8, block=64)  # noqa: E731
+    with pytest.raises(mm.EmeansError, match="EINVAL.*gradient"):
+        evict(w.clone().requires_grad_())
+    with fwd.dual_level(), pytest.raises(mm.EmeansError, match="forward-mode"):
+        evict(fwd.make_dual(w, torch.ones_like(w)))
+    # the angles' frequencies have none either
+    x, gain, pos, f = q.expand(3, 4, 64), torch.ones(64, device="cuda"), torch.arange(3, device="cuda"), mm.rotary_freqs(64)
+    with pytest.raises(mm.EmeansError, match="EINVAL.*gradient"):
+        mm.norm_rotate(x, x, gain, gain, pos, f.clone().requires_grad_())
+    with torch.no_grad():
+        mm.norm_rotate(x, x, gain, gain, pos, f.clone().requires_grad_())
+    with fwd.dual_level(), pytest.raises(mm.EmeansError, match="forward-mode"):
+        mm.norm_rotate(x, x, gain, gain, pos, fwd.make_dual(f, torch.ones_like(f)))
