@@ -692,7 +692,8 @@ int emeans_cache_attend(const void* q, int32_t dtype, int64_t q_row, int64_t q_h
  *   new_weights    device, fp32, seqs x (table_pages * page_rows): the weights of the
  *                  rows that stay, zeros after them
  *   work           device, emeans_cache_evict_work(seqs, keep) bytes, 16-byte aligned,
- *                  or NULL (allocated stream-ordered)
+ *                  or NULL (allocated stream-ordered). Where keep >= table_pages * page_rows
+ *                  no row moves, and emeans_cache_evict_work(seqs, 0) bytes are enough
  * Errors: EINVAL, ENOTDEVICE, ENOMEM, EHIP. */
 int64_t emeans_cache_evict_work(int64_t seqs, int64_t keep);
 int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t* row_codes,

@@ -1455,7 +1455,7 @@ def cache_evict(stores, table, lengths, weights, keep: int, *, recent: int = 0, 
         kept = empty((seqs, keep), dtype=torch.int32, device=device)
         if seqs:
             L, m = lib(), len(stores)
-            work = _work(L.emeans_cache_evict_work(seqs, keep), device)
+            work = _work(L.emeans_cache_evict_work(seqs, keep if keep < places else 0), device)
             _check(L.emeans_cache_evict(
                 (c_vp * m)(*(t.data_ptr() for t in codes)),
                 (c_vp * m)(*(t.data_ptr() for t in scales)),

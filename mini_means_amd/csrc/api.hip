@@ -1955,7 +1955,7 @@ int emeans_cache_attend(const void* q, int32_t dtype, int64_t q_row, int64_t q_h
 
 int64_t emeans_cache_evict_work(int64_t seqs, int64_t keep) {
   if (seqs < 1 || seqs >= kMaxRows || keep < 0 || keep > kMaxLength) return 0;
-  return (int64_t)cache_evict_work((int)seqs, (int)keep);
+  return (int64_t)cache_evict_work((int)seqs, (int)keep, keep + 1);
 }
 
 int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t* row_codes,
@@ -2022,7 +2022,8 @@ int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t
   a.kept = kept;
   hipStream_t st = static_cast<hipStream_t>(stream);
   void *at, *own;
-  if ((rc = take_work(work, emeans_cache_evict_work(seqs, keep), st, &at, &own))) return rc;
+  if ((rc = take_work(work, (int64_t)cache_evict_work((int)seqs, (int)keep, places), st, &at, &own)))
+    return rc;
   a.work = at;
   return release(own, st, launched(launch_cache_evict(a, st), "cache evict"));
 }

@@ -24,7 +24,7 @@ struct Move {
 };
 
 struct Moves {
-  Move* list;    // seqs x keep; from or to < 0: a page outside the store
+  Move* list;    // seqs x keep (none where every row stays); from or to < 0: a page outside the store
   int32_t* span; // seqs x 2: [first rank that moves, ranks)
 };
 
@@ -266,20 +266,26 @@ __global__ __launch_bounds__(kMovers) void move_kernel(Slices s, Moves mv, int k
   }
 }
 
-size_t list_bytes(int seqs, int keep) { return ((size_t)seqs * keep * sizeof(Move) + 255) / 256 * 256; }
+// A table that holds no more than keep rows has none to move, however large keep is.
+size_t list_bytes(int seqs, int keep, int64_t places) {
+  return keep >= places ? 0 : ((size_t)seqs * keep * sizeof(Move) + 255) / 256 * 256;
+}
 
 }  // namespace
 
-size_t cache_evict_work(int seqs, int keep) { return list_bytes(seqs, keep) + (size_t)seqs * 8; }
+size_t cache_evict_work(int seqs, int keep, int64_t places) {
+  return list_bytes(seqs, keep, places) + (size_t)seqs * 8;
+}
 
 hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st) {
   if (a.seqs <= 0) return hipSuccess;
   uint8_t* work = static_cast<uint8_t*>(a.work);
+  const int64_t places = (int64_t)a.table_pages * a.page;
   const Moves mv{reinterpret_cast<Move*>(work),
-                 reinterpret_cast<int32_t*>(work + list_bytes(a.seqs, a.keep))};
+                 reinterpret_cast<int32_t*>(work + list_bytes(a.seqs, a.keep, places))};
   select_kernel<<<a.seqs, kSelect, 0, st>>>(a, mv);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.keep >= places) return e;
   Slices s{};
   for (int p = 0; p < a.planes; ++p) {
     s.plane[p] = a.plane[p];

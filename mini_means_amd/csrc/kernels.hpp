@@ -413,7 +413,7 @@ struct CacheEvict {
   int32_t* kept;       // seqs x keep
   void* work;          // cache_evict_work() bytes
 };
-size_t cache_evict_work(int seqs, int keep);
+size_t cache_evict_work(int seqs, int keep, int64_t places);
 hipError_t launch_cache_evict(const CacheEvict& a, hipStream_t st);
 
 // ---------------------------------------------------------------------------

@@ -91,3 +91,35 @@ def test_what_has_no_gradient_is_refused_for_inputs_that_ask_for_one(mm):  # noq
         mm.norm_rotate(x, x, gain, gain, pos, f.clone().requires_grad_())
     with fwd.dual_level(), pytest.raises(mm.EmeansError, match="forward-mode"):
         mm.norm_rotate(x, x, gain, gain, pos, fwd.make_dual(f, torch.ones_like(f)))
+
+
+def test_a_generous_budget_takes_no_memory(mm):  # noqa: F811
+    """keep far over what the table holds: beside the results no list of that length."""
+    import torch
+    store, table = small_store(mm), torch.arange(3, device="cuda").int().view(1, 3)
+    lens, w = torch.tensor([40], device="cuda").int(), torch.rand(1, 48, device="cuda")
+    before, keep = [s.view(torch.uint8).clone() for s in store], 40 * 10 ** 6
+    torch.cuda.synchronize()
+    at = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    new, held, kept = mm.cache_evict([store], table, lens, w, keep, recent=5, block=64)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - at <= 4 * keep + (1 << 20)
+    assert new.tolist() == [40] and torch.equal(held[:, :40], w[:, :40]) and not held[:, 40:].any()
+    assert kept.shape == (1, keep) and kept[0, :40].tolist() == list(range(40)) and bool((kept[0, 40:] == -1).all())
+    assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, store))
+
+
+@pytest.mark.parametrize("keep", [47, 48, 49, 39, 40, 41, 0, 1])
+def test_eviction_around_the_places_of_the_table(mm, keep):  # noqa: F811
+    import torch
+    store, table = small_store(mm), torch.tensor([[2, 0, 1]], device="cuda").int()
+    lens, w = torch.tensor([40], device="cuda").int(), torch.rand(1, 48, device="cuda", generator=gen(3))
+    rows = table[0].long().repeat_interleave(16) * 16 + torch.arange(48, device="cuda") % 16
+    before = [s.view(torch.uint8).flatten(0, 1)[rows].clone() for s in store]
+    new, held, kept = mm.cache_evict([store], table, lens, w, keep, block=64)
+    stay = ref.evict(f64(w[0]), 40, keep, 0)
+    assert new.tolist() == [len(stay)] and kept[0].tolist() == stay + [-1] * (keep - len(stay))
+    assert np.array_equal(f64(held[0]), np.concatenate([f64(w[0])[stay], np.zeros(48 - len(stay))]))
+    now = [s.view(torch.uint8).flatten(0, 1)[rows] for s in store]
+    assert all(torch.equal(a[stay], b[:len(stay)]) for a, b in zip(before, now))
