@@ -684,7 +684,7 @@ int emeans_cache_attend(const void* q, int32_t dtype, int64_t q_row, int64_t q_h
  * No page may be in use twice; a row whose place or new place lies in a page outside
  * [0, pages) is neither read nor written.
  *   codes, scales  host arrays of `stores` (1 to 4) device pointers; row_codes[i]
- *                  codes and row_scales[i] scales are a row of store i
+ *                  codes and row_scales[i] scales are a row of store i; no two may overlap
  *   weights        device, fp32, seqs rows weights_ld apart, at least
  *                  table_pages * page_rows each; not changed
  *   new_lengths    device, seqs int32       kept  device, seqs x keep int32: the old

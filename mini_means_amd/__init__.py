@@ -1418,7 +1418,7 @@ def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=N
 def cache_evict(stores, table, lengths, weights, keep: int, *, recent: int = 0, block: int = BLOCK,
                 stream=None):
     """Drop rows of small weight from one to four paged stores of one page layout
-    ((codes, scales) each: keys and values, say): of a sequence of more than `keep`
+    ((codes, scales) each, none of them twice: keys and values, say): of a sequence of more than `keep`
     rows stay the last `recent` and, of those before them, the keep - recent of
     largest weight (weights: seqs x places float32, as cache_attend adds them up; of
     equal ones the first, NaN counts as -infinity). They move to the sequence's first

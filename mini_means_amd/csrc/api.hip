@@ -1998,6 +1998,14 @@ int emeans_cache_evict(void* const* codes, uint8_t* const* scales, const int64_t
   if (!lengths || !new_lengths || (places > 0 && (!table || !weights || !new_weights)) ||
       (keep > 0 && !kept))
     return fail(EMEANS_EINVAL, "table, lengths, weights and results must not be NULL");
+  // rows of a plane are moved by workgroups of its own: bytes of two would be moved twice
+  typedef unsigned __int128 Wide;  // rows x bytes may pass 64 bits
+  const auto at_of = [&](int i) { return (Wide)(uintptr_t)a.plane[i]; };
+  const auto end_of = [&](int i) { return at_of(i) + (Wide)rows * (uint64_t)a.row_bytes[i]; };
+  for (int i = 0; rows > 0 && i < a.planes; ++i)
+    for (int j = 0; j < i; ++j)
+      if (at_of(i) < end_of(j) && at_of(j) < end_of(i))
+        return fail(EMEANS_EINVAL, "codes and scales of the stores must not overlap");
   if ((rc = check_device(lengths, "lengths")) || (rc = check_device(new_lengths, "new_lengths")) ||
       (keep > 0 && (rc = check_device(kept, "kept"))))
     return rc;

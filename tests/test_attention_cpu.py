@@ -134,6 +134,29 @@ def test_cache_evict_refuses(L, change, word):
     assert _evict(L, **change) == -1 and word in L.emeans_last_error()
 
 
+def test_cache_evict_refuses_planes_that_overlap(L):
+    """Before any device work: in all pairs, by a byte, and none of planes that only touch."""
+    size = 10 * 16 * 128                                   # of codes; scales are 10 x 16
+    at = [FAKE, FAKE + size, FAKE + size + 160, FAKE + 2 * size + 160]
+    planes = lambda c0, s0, c1, s1: dict(c=(ctypes.c_void_p * 2)(c0, c1), s=(ctypes.c_void_p * 2)(s0, s1))  # noqa: E731
+    assert _evict(L, **planes(*at)) != 0 and b"overlap" not in L.emeans_last_error()      # no GPU memory
+    for i in range(4):
+        for j in range(4):
+            if i != j:
+                same = list(at)
+                same[i] = at[j]
+                assert _evict(L, **planes(*same)) == -1 and b"overlap" in L.emeans_last_error()
+    for i in range(1, 4):
+        near = list(at)
+        near[i] -= 1
+        assert _evict(L, **planes(*near)) == -1 and b"overlap" in L.emeans_last_error()
+    _evict(L, pages=0)                                     # a store of no rows has none to overlap
+    assert b"overlap" not in L.emeans_last_error()
+    # lengths whose product passes 64 bits
+    assert _evict(L, **planes(*at), pages=(1 << 31) - 1, page=512, rc=(1 << 31) - 1024, wld=2048) == -1
+    assert b"overlap" in L.emeans_last_error()
+
+
 def test_nothing_to_do_is_fine(L):
     assert _rotate(L, n=0, q=None) == 0 and _attend(L, seqs=0, q=None) == 0 and _evict(L, seqs=0) == 0
     assert L.emeans_cache_evict_work(0, 5) == L.emeans_cache_attend_work(0, 4, 2, 64, 16, 4, 1) == 0

@@ -123,3 +123,19 @@ def test_eviction_around_the_places_of_the_table(mm, keep):  # noqa: F811
     assert np.array_equal(f64(held[0]), np.concatenate([f64(w[0])[stay], np.zeros(48 - len(stay))]))
     now = [s.view(torch.uint8).flatten(0, 1)[rows] for s in store]
     assert all(torch.equal(a[stay], b[:len(stay)]) for a, b in zip(before, now))
+
+
+def test_stores_that_share_memory_are_refused(mm):  # noqa: F811
+    """Rows would be moved once for each of them."""
+    import torch
+    (codes, scales), table = small_store(mm), torch.arange(3, device="cuda").int().view(1, 3)
+    lens, w = torch.tensor([40], device="cuda").int(), torch.rand(1, 48, device="cuda")
+    other, wide = codes.clone(), mm.cache_new((4, 16), 128, block=64)
+    for stores in ([(codes, scales), (other, scales)], [(codes, scales), (codes, scales.clone())],
+                   [tuple(t[:3] for t in wide), tuple(t[1:] for t in wide)]):
+        before = [t.view(torch.uint8).clone() for s in stores for t in s]
+        with pytest.raises(mm.EmeansError, match="EINVAL"):
+            mm.cache_evict(stores, table, lens, w, 8, block=64)
+        assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, (t for s in stores for t in s)))
+    halves = mm.cache_new((6, 16), 128, block=64)        # two of one allocation that do not
+    mm.cache_evict([tuple(t[:3] for t in halves), tuple(t[3:] for t in halves)], table, lens, w, 8, block=64)
