@@ -153,7 +153,7 @@ def test_cache_evict_refuses_planes_that_overlap(L):
     _evict(L, pages=0)                                     # a store of no rows has none to overlap
     assert b"overlap" not in L.emeans_last_error()
     # lengths whose product passes 64 bits
-    assert _evict(L, **planes(*at), pages=(1 << 31) - 1, page=512, rc=(1 << 31) - 1024, wld=2048) == -1
+    assert _evict(L, **planes(*at), pages=(1 << 31) - 1, page=512, rc=1 << 25, wld=2048) == -1
     assert b"overlap" in L.emeans_last_error()
 
 
