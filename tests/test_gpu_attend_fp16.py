@@ -97,3 +97,28 @@ def test_gradients_of_rows_of_any_size_side_by_side(mm, n, w, causal):  # noqa: 
         t = tols[i] + (ref.HALF_ULP["f16"] * 1.01 + 4 * ref.SUM_ULP) * np.abs(total[i]) + ref.TINY["f16"]
         off = np.abs(got[i + 1][:, 0] - total[i])
         assert np.all(off <= t), (i, np.argwhere(off > t)[:3].tolist())
+
+
+@pytest.mark.parametrize("w,at,below", [(64, 0, 15.0), (64, 4096, 15.0), (128, 2000, 12.0), (96, 70, 15.0)])
+def test_many_small_weights_keep_their_digits(mm, w, at, below):  # noqa: F811
+    """One key holds nearly all of the weight and has a value of 0; 4096 others weigh e^-12 or e^-15
+    each (2^-17.3, 2^-21.6: fp16 has its smallest normal number at 2^-14 and a step of 2^-24
+    there) and make up the result."""
+    import torch
+    n = 40
+    q, k, v = (torch.zeros(r, 1, w, device="cuda", dtype=torch.float16) for r in (n, 4097, 4097))
+    q[:, 0, 0] = 1.0
+    k[at, 0, 0] = below
+    v[:] = randn(gen(5), 1, 1, w)
+    v[at] = 0.0
+    starts, ks = (torch.tensor([0, r], device="cuda").int() for r in (n, 4097))
+    o = mm.attend(q, k, v, starts, k_starts=ks, causal=False, scale=1.0)
+    want, tol, _ = ref.attend(f64(q[:, 0]), f64(k[:, 0]), f64(v[:, 0]), 1.0, False, "f16")
+    off = np.abs(f64(o[:, 0]) - want)
+    assert np.all(off <= tol), (off / np.abs(want)).max()
+    # the gradients go by the same weights
+    do = torch.ones_like(q)
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    dv = torch.autograd.grad(mm.attend(*leaves, starts, k_starts=ks, causal=False, scale=1.0), leaves, do)[2]
+    (_, _, dv_want), (_, _, dv_tol) = ref.attend_grad(f64(q[:, 0]), f64(k[:, 0]), f64(v[:, 0]), f64(do[:, 0]), 1.0, False, "f16")
+    assert np.all(np.abs(f64(dv[:, 0]) - dv_want) <= dv_tol + ref.HALF_ULP["f16"] * 1.01 * np.abs(dv_want) + ref.TINY["f16"])
