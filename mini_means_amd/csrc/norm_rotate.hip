@@ -355,20 +355,22 @@ __global__ __launch_bounds__(256) void weight_sum_kernel(const float* part, int 
 
 // go(E, L) for the head's width: E pairs per lane, as wide as the cuts at half and
 // in the rest allow (fp32 4: 16 bytes), L lanes.
-template <typename GO>
+template <int DT, typename GO>
 hipError_t by_width(const NormRotate& a, GO go) {
-  const bool eight = a.dt != 0 && a.half % 8 == 0 && (a.width - 2 * a.half) % 16 == 0;
+  const bool eight = DT != 0 && a.half % 8 == 0 && (a.width - 2 * a.half) % 16 == 0;
   const int chunks = a.width / 2 / (eight ? 8 : 4);
 #define EMK_GO(E, L)                                                                \
   if (chunks <= L) {                                                                \
     go(std::integral_constant<int, E>(), std::integral_constant<int, L>());         \
     return hipGetLastError();                                                       \
   }
-  if (eight) {
-    EMK_GO(8, 4) EMK_GO(8, 8) EMK_GO(8, 16)
-  } else {
-    EMK_GO(4, 4) EMK_GO(4, 8) EMK_GO(4, 16) EMK_GO(4, 32)
+  if constexpr (DT != 0) {
+    if (eight) {
+      EMK_GO(8, 4) EMK_GO(8, 8) EMK_GO(8, 16)
+      return hipErrorInvalidValue;
+    }
   }
+  EMK_GO(4, 4) EMK_GO(4, 8) EMK_GO(4, 16) EMK_GO(4, 32)
 #undef EMK_GO
   return hipErrorInvalidValue;
 }
@@ -380,7 +382,7 @@ hipError_t forward_t(const NormRotate& a, hipStream_t st) {
   const int64_t wgs = (a.n + T - 1) / T;
   for (int64_t wg0 = 0; wg0 < wgs; wg0 += kMaxGroups) {
     const unsigned grid = (unsigned)(wgs - wg0 < kMaxGroups ? wgs - wg0 : kMaxGroups);
-    const hipError_t e = by_width(a, [&](auto E, auto L) {
+    const hipError_t e = by_width<DT>(a, [&](auto E, auto L) {
       norm_rotate_kernel<DT, decltype(E)::value, decltype(L)::value><<<grid, 256, 0, st>>>(a, wg0, T);
     });
     if (e != hipSuccess) return e;
@@ -392,7 +394,7 @@ template <int DT>
 hipError_t backward_t(const NormRotate& a, hipStream_t st) {
   const int groups = norm_rotate_groups(a.n);
   const int T = a.n >= 4096 ? kMaxTokens : 1;
-  const hipError_t e = by_width(a, [&](auto E, auto L) {
+  const hipError_t e = by_width<DT>(a, [&](auto E, auto L) {
     norm_rotate_back_kernel<DT, decltype(E)::value, decltype(L)::value><<<groups, 256, 0, st>>>(a, T);
   });
   if (e != hipSuccess) return e;
