@@ -654,9 +654,8 @@ int emeans_attend_gradient(const void* q, int64_t q_row, int64_t q_head, const v
  * p % page_rows, query head h with key-value head h / (hq / hk). Places in pages
  * outside [0, pages) are left out; a length is cut to 0 below and to what a table
  * row holds above; a sequence without places gives zeros. Scores, softmax and sums
- * are fp32, products exact for bf16 queries but for the softmax weights beside the
- * values, which are rounded to bf16 for bf16 queries, to 16 bits for fp16 ones and
- * to 24 for fp32 ones.
+ * are fp32, products exact but for the softmax weights beside the values, which are
+ * rounded to 16 bits (24 for fp32 queries).
  *   width    a multiple of 16, at most 128      hq  a multiple of hk
  *   q        device, seqs x hq x width, dtype   out the same (contiguous)
  *   table    device, seqs x table_pages int32, rows table_ld entries apart. A part of

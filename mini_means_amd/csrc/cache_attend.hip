@@ -11,9 +11,10 @@
 // code times its scale is exact, and nothing passes through LDS on the way: a wave
 // takes 32 places; S^T = K q^T leaves lane (h, g) the scores of places 4 g + i of
 // head h, which is what the product with the values reads as its operand if its
-// places are counted in that order. fp16 and fp32 queries, and the softmax weights
-// beside them, are sums of two and three bf16 terms (16 and 24 bits), bf16 ones
-// are one term.
+// places are counted in that order. Queries are sums of one, two and three bf16 terms for bf16,
+// fp16 and fp32 (8, 16 and 24 bits); softmax weights of two (three for fp32), as one would
+// round them to 8 bits where values cancel (its product more on a matrix unit that is 5%
+// busy: 1% of the time).
 //
 // Measured, 32 query and 8 key-value heads of 128, E4M3, bf16: one sequence of 131072 places
 // 51 us and 8 for the join (5.3 TB/s; a large copy 5.0), 64 sequences of up to 8192 123 and
@@ -135,7 +136,8 @@ struct Places {
 // every 16 codes have a scale of their own.
 template <int DT, bool I8, int W, bool SCORES, bool ONE>
 __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
-  constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3;
+  // bf16 terms of a query's values and of a softmax weight
+  constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3, NP = DT == 0 ? 3 : 2;
   constexpr int KJ = W / 64, VD = W / 16;
   typedef std::conditional_t<ONE, uint32_t, int64_t> At;
   const CacheAttend& a = s.a;
@@ -333,8 +335,8 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
       l += p[e];
       if constexpr (ONE) p[e] *= fv[e >> 2][e & 3];
     }
-    bf16x8 pf[NT];
-    terms_of<NT>(p, pf);
+    bf16x8 pf[NP];
+    terms_of<NP>(p, pf);
     u32x4 y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
                                      j & 1 ? 0x07060302u : 0x05040100u);
       const bf16x8 vf = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
-      for (int e = NT - 1; e >= 0; --e)
+      for (int e = NP - 1; e >= 0; --e)
         acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[e], acc[j], 0, 0, 0);
     }
   };

@@ -4,8 +4,9 @@ import numpy as np
 
 from block_ref import HALF_ULP, SUM_ULP, TINY, e4m3_values
 
-# bf16 terms beside a query's values and the softmax weights: 1 for bf16 queries, 2 for
-# fp16, 3 for fp32. n terms leave 2^-8n of the value (each rounding half a step, 2^-8).
+# bf16 terms that a query's values are made of: 1 for bf16 queries, 2 for fp16, 3 for fp32; the
+# softmax weights have as many, or two for bf16 ones, for which the tolerance allows one. n
+# terms leave 2^-8n of the value (each rounding half a step, 2^-8).
 TERMS = {"bf16": 1, "f16": 2, "f32": 3}
 
 

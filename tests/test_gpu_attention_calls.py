@@ -139,3 +139,37 @@ def test_stores_that_share_memory_are_refused(mm):  # noqa: F811
         assert all(torch.equal(a, b.view(torch.uint8)) for a, b in zip(before, (t for s in stores for t in s)))
     halves = mm.cache_new((6, 16), 128, block=64)        # two of one allocation that do not
     mm.cache_evict([tuple(t[:3] for t in halves), tuple(t[3:] for t in halves)], table, lens, w, 8, block=64)
+
+
+@pytest.mark.parametrize("fmt,block", [("f8", 128), ("f8", 16), ("i8", 128), ("i8", 32)])
+@pytest.mark.parametrize("width", [128, 48])
+@pytest.mark.parametrize("places", [20, 700])
+def test_softmax_weights_of_bf16_queries_keep_16_bits(mm, fmt, block, width, places):  # noqa: F811
+    """Values of both signs, so that the result is small beside the sum of its terms and the weights'
+    rounding would show: off by 2^-16 of that sum at most, beside the score's error, that
+    of the sums and the result's own rounding."""
+    import torch
+    from test_gpu_attention_store import fill, lay_out, make_store, to_gpu
+    rng = np.random.default_rng(places + width)
+    d = 2 * width
+    if block == 128:
+        block = width
+    pages, table, rows = lay_out(rng, [places], 16)
+    k, v = (make_store(rng, pages, 16, d, block, fmt) for _ in range(2))
+    for s in (k, v):
+        fill(rng, s, rows[0], fmt)
+    codes = v[0].reshape(-1, d)
+    half = rows[0][1::2]                       # each second place has the value of the one before, negative
+    prev = rows[0][:-1:2][:len(half)]
+    codes[half] = codes[prev] ^ 0x80 if fmt == "f8" else (-codes[prev].view(np.int8)).view(np.uint8)
+    v[1].reshape(-1, v[1].shape[-1])[half] = v[1].reshape(-1, v[1].shape[-1])[prev]
+    kc, vc = (ref.store_values(s[0].reshape(-1, d)[rows[0]], s[1].reshape(-1, s[1].shape[-1])[rows[0]], block, fmt)
+              .reshape(places, 2, width) for s in (k, v))
+    q = (0.02 * randn(gen(3), 1, 8, width)).bfloat16()
+    got = f64(mm.cache_attend(q, to_gpu(k, pages, 16, fmt), to_gpu(v, pages, 16, fmt), torch.from_numpy(table).cuda(),
+                              torch.tensor([places], device="cuda").int(), block=block))[0]
+    want, tol, _, _ = ref.decode(f64(q[0]), kc, vc, width ** -0.5, "bf16")
+    size = np.stack([ref.softmax(kc[:, h // 4] @ f64(q[0, h]) * width ** -0.5) @ np.abs(vc[:, h // 4]) for h in range(8)])
+    tol = tol - (2.0 ** -8 - 2.0 ** -16) * 1.01 * size
+    off = np.abs(got - want)
+    assert np.all(off <= tol), (off / size).max()
