@@ -133,9 +133,12 @@ struct Places {
 
 // W: width rounded up to 64 or 128. ONE: a head lies in one block, so that its scale is a
 // factor of the score and of the softmax weight (and the store has under 2^32 rows); else
-// every 16 codes have a scale of their own.
+// every 16 codes have a scale of their own. Three workgroups on a CU (168 registers) where that
+// holds what is in flight, else two, as spilling in the loop costs more than the third gives: heads of
+// 128, 64 sequences of up to 8192, two against three: bf16 queries over int8 142 us against 162,
+// fp16 over E4M3 133 / 159, over int8 145 / 217, fp32 134 / 205 and 150 / 297. bf16 over E4M3 fits (162).
 template <int DT, bool I8, int W, bool SCORES, bool ONE>
-__global__ __launch_bounds__(256, ONE ? 3 : 2) void split_kernel(Split s) {
+__global__ __launch_bounds__(256, ONE && (W == 64 || (DT == 1 && !I8)) ? 3 : 2) void split_kernel(Split s) {
   // bf16 terms of a query's values and of a softmax weight
   constexpr int NT = DT == 1 ? 1 : DT == 4 ? 2 : 3, NP = DT == 0 ? 3 : 2;
   constexpr int KJ = W / 64, VD = W / 16;
