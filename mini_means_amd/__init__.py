@@ -1068,11 +1068,13 @@ def _no_tangent(name, *tensors) -> None:
         raise EmeansError(f"EINVAL: {name} has no forward-mode derivative (an input has a tangent)")
 
 
-def _no_gradient(name, *tensors) -> None:
-    """Refuse inputs that ask for a gradient that the call does not have."""
-    if _T().torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+def _no_gradient(name, x) -> None:
+    """Refuse an input that asks for a gradient that the call does not have."""
+    t = _T()
+    if getattr(x, "requires_grad", False) and t.torch.is_grad_enabled():
         raise EmeansError(f"EINVAL: {name} has no gradient (detach the input that asks for one)")
-    _no_tangent(name, *tensors)
+    if t.forward_ad._current_level >= 0:
+        _no_tangent(name, x)
 
 
 def _adjacent(t):
@@ -1375,7 +1377,7 @@ def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=N
     enabled, a q or weights that ask for one are refused."""
     dev = _device_of(q, "q")
     dt = _number(q.dtype, "q")
-    _no_gradient("cache_attend", *((q,) if weights is None else (q, weights)))
+    _no_gradient("cache_attend", q)
     seqs, hq, width, qr, qh = _heads(q, dev, "q")
     fmt, d, shape = _paged(dev, keys, block, "keys")
     vfmt, _, vshape = _paged(dev, values, block, "values")
@@ -1394,6 +1396,7 @@ def cache_attend(q, keys, values, table, lengths, *, block: int = BLOCK, scale=N
     if weights is not None:
         torch = _T().torch
         wn, wd, wld = _matrix(weights, dev, "weights", (torch.float32,), "float32")
+        _no_gradient("cache_attend", weights)
         if (wn, wd) != (seqs, places) or (wld < places and seqs > 1):
             raise EmeansError(f"EINVAL: weights must be {seqs} x {places}")
 
