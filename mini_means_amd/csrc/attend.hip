@@ -18,9 +18,10 @@
 // its sum index is counted in the order in which they stand. Its A operand is the
 // tile transposed, which ds_read_b64_tr_b16 reads from the same LDS rows. Two workgroups of
 // four waves share a CU: one wave's products run beside the other's exponentials.
-// Measured, 32 query and 8 key-value heads of 128 in bf16, causal: 16384 tokens 2.08 to 2.24
-// ms (980 to 1060 TFLOP/s; the library's product of 8192 a side 1223); seven sequences of
-// up to 4000 tokens 0.39 ms, dQ 0.54, dK and dV 0.81. 33 sequences of up to 500 tokens, 16
+// Measured, 32 query and 8 key-value heads of 128 in bf16, causal: 16384 tokens 2.12 to 2.22
+// ms (990 to 1040 TFLOP/s; the library's product of 8192 a side 1223); seven sequences of
+// up to 4000 tokens 0.38 ms, dQ 0.52, dK and dV 0.73 and 0.04 for their sums (fp16 0.40, 0.57,
+// 0.79, 0.04). 33 sequences of up to 500 tokens, 16
 // heads of 64 in fp16, not causal: 33 us.
 #include <type_traits>
 
@@ -693,7 +694,8 @@ __global__ __launch_bounds__(256, 2) void key_grad_kernel(Attend a, int64_t wg0,
                                                           int cuts) {
   constexpr int NW = 4, ROWS = NW * 32, R = 32;
   constexpr int QB = R * W * 2, VB = ROWS * W * 2;  // bytes: of a tile of Q or dO, of V
-  constexpr float kLift = F16 ? 14.0f : 0.0f;  // fp16: P times 2^14, which stays in range
+  // fp16: P for dV times 2^14, in range as P <= 1; whole digits down to 2^-28, a step of 2^-38 below
+  constexpr float kLift = F16 ? 14.0f : 0.0f;
   __shared__ __align__(1024) uint8_t lds[4 * QB + VB];
   __shared__ float lse[2][R], delta[2][R];
   const int64_t all = wg0 + blockIdx.x, b = all / cuts;

@@ -13,12 +13,12 @@
 // head h, which is what the product with the values reads as its operand if its
 // places are counted in that order. Queries are sums of one, two and three bf16 terms for bf16,
 // fp16 and fp32 (8, 16 and 24 bits); softmax weights of two (three for fp32), as one would
-// round them to 8 bits where values cancel (its product more on a matrix unit that is 5%
-// busy: 1% of the time).
+// round them to 8 bits where values cancel (products more on a matrix unit that is 8% busy:
+// 1% of the time).
 //
 // Measured, 32 query and 8 key-value heads of 128, E4M3, bf16: one sequence of 131072 places
-// 51 us and 8 for the join (5.3 TB/s; a large copy 5.0), 64 sequences of up to 8192 123 and
-// 6 (4.4 TB/s), 16 of up to 4000 with weights 23 and 5. With each load in a branch of its
+// 51 us and 8 for the join (5.3 TB/s; a large copy 5.0), 64 sequences of up to 8192 124 and
+// 6 (4.4 TB/s), 16 of up to 4000 with weights 24 and 5. With each load in a branch of its
 // own, and none a round ahead, the first took 127 us.
 #include <type_traits>
 
