@@ -333,7 +333,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attend_kernel(Attend a, int64_t wg
                  b - tiles * a.hq, NW * 64);
     return;
   }
-  // causal: later rows see more keys, so the longest workgroups come first
+  // causal: later rows see more keys, so the longest workgroups of a sequence come first (the
+  // sequences themselves in packed order, from the last)
   const Place at = place_of(a.starts, a.seqs, a.n, ROWS, tiles - 1 - b / a.hq);
   const Span sq = span_of(a.starts, at.seq, a.n), sk = span_of(a.k_starts, at.seq, a.nk);
   if (at.row0 >= sq.len) return;
