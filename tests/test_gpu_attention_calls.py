@@ -173,3 +173,27 @@ def test_softmax_weights_of_bf16_queries_keep_16_bits(mm, fmt, block, width, pla
     tol = tol - (2.0 ** -8 - 2.0 ** -16) * 1.01 * size
     off = np.abs(got - want)
     assert np.all(off <= tol), (off / size).max()
+
+
+def test_gradients_with_saved_tensors_elsewhere_and_recomputed(mm):  # noqa: F811
+    """Saved tensors kept in host memory come back with strides of their own; a checkpoint makes them
+    anew."""
+    import torch
+    from torch.utils.checkpoint import checkpoint
+    base = randn(gen(7), 80, 5 * 67).half()
+    parts = [base[:, a * 67:b * 67].unflatten(1, (b - a, 67))[:, :, :64] for a, b in ((0, 3), (3, 4), (4, 5))]
+    starts, pos, f = torch.tensor([0, 50, 80], device="cuda").int(), torch.arange(80, device="cuda"), mm.rotary_freqs(64)
+    gain = torch.ones(64, device="cuda")
+
+    def layer(q, k, v, g):
+        return mm.attend(*mm.norm_rotate(q, k, g, g, pos, f), v, starts)
+
+    def grads(run, *, offload=False):
+        leaves = [t.detach().requires_grad_() for t in (*parts, gain)]
+        with torch.autograd.graph.save_on_cpu() if offload else torch.enable_grad():
+            o = run(*leaves)
+        return (o.detach(), *torch.autograd.grad(o, leaves, torch.ones_like(o)))
+
+    want = grads(layer)
+    for got in (grads(layer, offload=True), grads(lambda *a: checkpoint(layer, *a, use_reentrant=False))):
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
